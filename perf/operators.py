@@ -100,7 +100,7 @@ def work(case):
     scales = 4 * ceil_div(K, B) * ceil_div(N, B)
     if c["op"] == "matmul":
         return {"bytes": 2 * M * K + K * N + scales + 2 * M * N, "flops": 2 * M * K * N}
-    return {"bytes": 2 * M * N + 2 * M * K + K * N + scales + 2 * M * K + 4 * K * N, "flops": 4 * M * K * N}
+    return {"bytes": 2 * M * N + 2 * M * K + K * N + scales + 2 * M * K + 2 * K * N, "flops": 4 * M * K * N}
 
 
 # ---- inputs
@@ -180,7 +180,7 @@ def run(state):
         X, dY = state["X"], state["dY"]
         dX = _rows(dY) @ _weight(state["WqT"], state["s_w"].t(), dY.shape[1]).t()
         dW = _rows(X.t()) @ _rows(dY.t()).t()
-        return dX.to(X.dtype), dW
+        return dX.to(X.dtype), dW.to(X.dtype)
     return _plain_moe(state)
 
 
