@@ -1,14 +1,16 @@
 """Cases of the 8-bit floating point block-scaled operators, with their plain forms.
 
-The operators share one weight format: e4m3 codes with one fp32 scale per 128 x 128 block.
-  quantize  fp8_quantize_weight_block: a 16-bit weight to codes and scales (and the transposed codes)
+The operators share one weight format: e4m3 codes with one power-of-two scale (e8m0) per
+128 x 128 block.
+  quantize  fp8_quantize_weight_block: a 16-bit weight to codes and scales (and both transposed)
   matmul    fp8_matmul_block: Y = X W, X coded per row in groups of 128 features
   backward  fp8_matmul_block_backward: dX and dW of that product
   moe       fp8_moe_block: a mixture-of-experts layer for few tokens on 16-bit activations
 
-A group of values with the largest magnitude a has the scale s = RN32(a / 448); its codes are
-the nearest e4m3 values (ties to even) of RN32(x * RN32(448 / a)); a group of zeros has the
-scale 0.  The last group of an axis may be short.
+A group of values with the largest magnitude a has the smallest scale s = 2^e, e >= -127, with
+a <= 448 s; its codes are the nearest e4m3 values (ties to even) of x / s.  The last group of
+an axis may be short.  Rows of codes are padded with zeros to a multiple of 128, rows of scales
+to a multiple of 4 with 2^-127 (the byte 0).
 """
 import math
 
@@ -17,7 +19,7 @@ import torch
 own = False  # True: run() makes the framework's calls
 
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
-F8 = torch.float8_e4m3fn
+F8, E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 B = 128  # values of a group along each axis
 
 
@@ -27,6 +29,10 @@ def ceil_div(a, b):
 
 def padded(n):
     return ceil_div(n, B) * B
+
+
+def groups(n):
+    return ceil_div(ceil_div(n, B), 4) * 4
 
 
 # ---- cases
@@ -90,14 +96,14 @@ def work(case):
     c = case
     if c["op"] == "quantize":
         n = c["K"] * c["N"]
-        return {"bytes": 2 * n + n * (2 if c["transposed"] else 1) + 4 * ceil_div(c["K"], B) * ceil_div(c["N"], B), "flops": 2 * n}
+        return {"bytes": 2 * n + n * (2 if c["transposed"] else 1) + ceil_div(c["K"], B) * ceil_div(c["N"], B), "flops": 2 * n}
     if c["op"] == "moe":
         # the experts that T tokens with k choices each are expected to meet
         met = c["E"] * (1 - (1 - c["k"] / c["E"]) ** c["T"])
-        return {"bytes": int(met * 3 * c["H"] * c["I"] * (1 + 4 / (B * B))) + c["T"] * (4 * c["H"] + 4 * c["E"] + 8 * c["k"]),
+        return {"bytes": int(met * 3 * c["H"] * c["I"] * (1 + 1 / (B * B))) + c["T"] * (4 * c["H"] + 4 * c["E"] + 8 * c["k"]),
                 "flops": 6 * c["T"] * c["k"] * c["H"] * c["I"]}
     M, K, N = c["M"], c["K"], c["N"]
-    scales = 4 * ceil_div(K, B) * ceil_div(N, B)
+    scales = ceil_div(K, B) * ceil_div(N, B)
     if c["op"] == "matmul":
         return {"bytes": 2 * M * K + K * N + scales + 2 * M * N, "flops": 2 * M * K * N}
     return {"bytes": 2 * M * N + 2 * M * K + K * N + scales + 2 * M * K + 2 * K * N, "flops": 4 * M * K * N}
@@ -108,14 +114,18 @@ def work(case):
 def _codes(g, rows, cols, sigma, transposed=False):
     """Random codes (rows x cols, pitch padded with zeros) and block scales of a weight ~ N(0, sigma)."""
     q = torch.randn(rows, cols, generator=g, device=g.device, dtype=torch.float32).mul_(448 / 4.5).clamp_(-448, 448).to(F8)
-    s = (0.9 + 0.2 * torch.rand(ceil_div(rows, B), ceil_div(cols, B), generator=g, device=g.device)) * (sigma * 4.5 / 448)
+    most = int(math.floor(math.log2(sigma * 4.5 / 448))) + 127
+    s = torch.zeros(ceil_div(rows, B), groups(cols), dtype=torch.uint8, device=g.device)
+    s[:, :ceil_div(cols, B)] = torch.randint(most - 1, most + 1, (ceil_div(rows, B), ceil_div(cols, B)), generator=g, device=g.device)
     out = torch.zeros(rows, padded(cols), dtype=torch.uint8, device=g.device)
     out[:, :cols] = q.view(torch.uint8)
     if not transposed:
-        return out.view(F8), s
+        return out.view(F8), s.view(E8)
+    st = torch.zeros(ceil_div(cols, B), groups(rows), dtype=torch.uint8, device=g.device)
+    st[:, :ceil_div(rows, B)] = s[:, :ceil_div(cols, B)].t()
     turned = torch.zeros(cols, padded(rows), dtype=torch.uint8, device=g.device)
     turned[:, :rows] = q.view(torch.uint8).t()
-    return turned.view(F8), s
+    return turned.view(F8), st.view(E8)
 
 
 def _acts(g, M, K, dtype):
@@ -139,7 +149,7 @@ def prepare(case, seed):
     elif c["op"] == "backward":
         s["X"] = _acts(g, c["M"], c["K"], t)
         s["dY"] = torch.randn(c["M"], c["N"], generator=g, device=g.device).mul_(1e-2).to(t)
-        s["WqT"], s["s_w"] = _codes(g, c["N"], c["K"], 0.02, transposed=True)
+        s["WqT"], s["s_wT"] = _codes(g, c["N"], c["K"], 0.02, transposed=True)
     else:
         T, H, I, E = c["T"], c["H"], c["I"], c["E"]
         s["X"] = torch.randn(T, H, generator=g, device=g.device).to(t)
@@ -151,8 +161,8 @@ def prepare(case, seed):
         down = [_codes(g, H, I, 0.03) for _ in range(E)]
         s["W13q"] = torch.stack([q.view(torch.uint8) for q, _ in up]).view(F8)
         s["W2q"] = torch.stack([q.view(torch.uint8) for q, _ in down]).view(F8)
-        s["s_w13"] = torch.stack([v for _, v in up])
-        s["s_w2"] = torch.stack([v for _, v in down])
+        s["s_w13"] = torch.stack([v.view(torch.uint8) for _, v in up]).view(E8)
+        s["s_w2"] = torch.stack([v.view(torch.uint8) for _, v in down]).view(E8)
     return s
 
 
@@ -168,7 +178,7 @@ def run(state):
         if c["op"] == "matmul":
             return lm.fp8_matmul_block(state["X"], state["Wq"], state["s_w"])
         if c["op"] == "backward":
-            return lm.fp8_matmul_block_backward(state["dY"], state["X"], state["WqT"], state["s_w"])
+            return lm.fp8_matmul_block_backward(state["dY"], state["X"], state["WqT"], state["s_wT"])
         return lm.fp8_moe_block(state["X"], state["logits"], state["W13q"], state["s_w13"], state["W2q"], state["s_w2"],
                                 top_k=c["k"], renormalize=c["renormalize"])
     if c["op"] == "quantize":
@@ -178,16 +188,21 @@ def run(state):
         return (_rows(X) @ _weight(state["Wq"], state["s_w"], X.shape[1]).t()).to(X.dtype)
     if c["op"] == "backward":
         X, dY = state["X"], state["dY"]
-        dX = _rows(dY) @ _weight(state["WqT"], state["s_w"].t(), dY.shape[1]).t()
+        dX = _rows(dY) @ _weight(state["WqT"], state["s_wT"], dY.shape[1]).t()
         dW = _rows(X.t()) @ _rows(dY.t()).t()
         return dX.to(X.dtype), dW.to(X.dtype)
     return _plain_moe(state)
 
 
-def _scales(a):
-    a = torch.where(a < 2.0 ** -100, torch.zeros_like(a), a)
-    most = torch.full_like(a, 448.0)  # a tensor: division by, or of, a plain number is a product with a reciprocal
-    return a / most, torch.where(a > 0, most / a, torch.zeros_like(a))
+def _bytes(a):
+    """The e8m0 bytes (2^(byte - 127)) of groups with the largest magnitudes a: 448 = 0.875 * 2^9."""
+    m, e = torch.frexp(a)
+    e = e + (m > 0.875).to(e.dtype) - 9 + 127
+    return torch.where(a > 0, e, torch.zeros_like(e)).clamp_(min=0)
+
+
+def _power(b):
+    return b.to(torch.uint8).view(E8).float()
 
 
 def _plain_quantize(W, transposed):
@@ -195,11 +210,17 @@ def _plain_quantize(W, transposed):
     w = torch.zeros(padded(N), padded(K), dtype=torch.float32, device=W.device)
     w[:N, :K] = W.t()
     w = w.view(padded(N) // B, B, padded(K) // B, B)
-    s, inv = _scales(w.abs().amax(dim=(1, 3)))
-    q = (w * inv[:, None, :, None]).view(padded(N), padded(K)).to(F8)
+    b = _bytes(w.abs().amax(dim=(1, 3)))
+    q = (w / _power(b)[:, None, :, None]).view(padded(N), padded(K)).to(F8)
+
+    def laid(b):
+        out = torch.zeros(b.shape[0], groups(b.shape[1] * B), dtype=torch.uint8, device=W.device)
+        out[:, :b.shape[1]] = b
+        return out.view(E8)
+
     if not transposed:
-        return q[:N], s
-    return q[:N], q[:, :K].view(torch.uint8).t().contiguous().view(F8), s
+        return q[:N], laid(b)
+    return q[:N], laid(b), q[:, :K].view(torch.uint8).t().contiguous().view(F8), laid(b.t())
 
 
 def _rows(X):
@@ -208,15 +229,14 @@ def _rows(X):
     x = torch.zeros(M, padded(K), dtype=torch.float32, device=X.device)
     x[:, :K] = X
     x = x.view(M, padded(K) // B, B)
-    s, inv = _scales(x.abs().amax(dim=2))
-    q = (x * inv[:, :, None]).to(F8).float()
-    return (q * s[:, :, None]).view(M, padded(K))[:, :K]
+    s = _power(_bytes(x.abs().amax(dim=2)))[:, :, None]
+    return ((x / s).to(F8).float() * s).view(M, padded(K))[:, :K]
 
 
 def _weight(q, s, cols):
     """The values that codes (R x pitch) with block scales stand for: R x cols, fp32."""
     R = q.shape[-2]
-    wide = s.repeat_interleave(B, dim=-1)[..., :cols].repeat_interleave(B, dim=-2)[..., :R, :]
+    wide = s.float().repeat_interleave(B, dim=-1)[..., :cols].repeat_interleave(B, dim=-2)[..., :R, :]
     return q[..., :cols].float() * wide
 
 
@@ -232,9 +252,9 @@ def _plain_moe(state):
     p = torch.where(open_, e / total, torch.zeros_like(e))
     if T * k <= E:  # the chosen experts' weights alone
         at, x = ids.reshape(-1), X.float().repeat_interleave(k, dim=0)[:, :, None]
-        gu = torch.bmm(_weight(state["W13q"].view(torch.uint8)[at].view(F8), state["s_w13"][at], H), x)
+        gu = torch.bmm(_weight(state["W13q"].view(torch.uint8)[at].view(F8), state["s_w13"].view(torch.uint8)[at].view(E8), H), x)
         h = (gu[:, :I] * torch.sigmoid(gu[:, :I]) * gu[:, I:]).to(X.dtype).float()
-        y = torch.bmm(_weight(state["W2q"].view(torch.uint8)[at].view(F8), state["s_w2"][at], I), h).view(T, k, H)
+        y = torch.bmm(_weight(state["W2q"].view(torch.uint8)[at].view(F8), state["s_w2"].view(torch.uint8)[at].view(E8), I), h).view(T, k, H)
         y = (y * p[:, :, None]).sum(dim=1)
     else:  # every expert on every token
         gu = torch.matmul(_weight(state["W13q"], state["s_w13"], H), X.float().t())
@@ -255,21 +275,19 @@ def _e4m3(v):
     return torch.round(v / step) * step
 
 
+def _scale(a):
+    """The scales of groups with the largest magnitudes a."""
+    e = torch.ceil(torch.log2(torch.where(a > 0, a, torch.ones_like(a)) / 448.0))
+    return torch.exp2(torch.where(a > 0, e, torch.full_like(e, -127)).clamp(min=-127))
+
+
 def _coded(x, dim):
-    """(codes, scales) of 64-bit x in groups of 128 along dim, with the definition's roundings to 32 bits."""
-    n = x.shape[dim]
-    codes, scales = [], []
+    """The values of 64-bit x after coding in groups of 128 along dim."""
+    parts = []
     for part in x.split(B, dim=dim):
-        a = part.abs().amax(dim=dim, keepdim=True)
-        inv = torch.where(a > 0, 448.0 / a, torch.zeros_like(a)).float().double()
-        codes.append(_e4m3((part * inv).float().double()))
-        scales.append((a / 448.0).float().double())
-    assert sum(p.shape[dim] for p in codes) == n
-    return codes, scales
-
-
-def _turned(codes, scales, dim):
-    return torch.cat([q * s for q, s in zip(codes, scales)], dim=dim)
+        s = _scale(part.abs().amax(dim=dim, keepdim=True))
+        parts.append(_e4m3(part / s) * s)
+    return torch.cat(parts, dim=dim)
 
 
 def exact(case, seed):
@@ -278,34 +296,33 @@ def exact(case, seed):
         W = s["W"]
         K, N = c["K"], c["N"]
         q = torch.zeros(N, padded(K), dtype=F8, device=W.device)
-        sw = torch.zeros(ceil_div(N, B), ceil_div(K, B), dtype=torch.float64, device=W.device)
+        sw = torch.full((ceil_div(N, B), groups(K)), 2.0 ** -127, dtype=torch.float64, device=W.device)
         for b in range(ceil_div(K, B)):
             w = torch.zeros(B, padded(N), dtype=torch.float64, device=W.device)
             w[: min(B, K - b * B), :N] = W[b * B:(b + 1) * B]
             w = w.view(B, padded(N) // B, B)
-            a = w.abs().amax(dim=(0, 2))
-            inv = torch.where(a > 0, 448.0 / a, torch.zeros_like(a)).float().double()
-            sw[:, b] = a / 448.0
-            codes = _e4m3((w * inv[None, :, None]).float().double())
+            sw[:, b] = _scale(w.abs().amax(dim=(0, 2)))
+            codes = _e4m3(w / sw[:, b][None, :, None])
             q[:, b * B:(b + 1) * B] = codes.view(B, padded(N))[:, :N].t().float().to(F8)
         if not c["transposed"]:
             return q, sw
         t = torch.zeros(K, padded(N), dtype=torch.uint8, device=W.device)
         t[:, :N] = q.view(torch.uint8)[:, :K].t()
-        return q, t.view(F8), sw
+        swt = torch.full((ceil_div(K, B), groups(N)), 2.0 ** -127, dtype=torch.float64, device=W.device)
+        swt[:, :ceil_div(N, B)] = sw[:, :ceil_div(K, B)].t()
+        return q, sw, t.view(F8), swt
 
     def weight(q, sc, cols):
         at_r = torch.arange(q.shape[0], device=q.device) // B
         at_c = torch.arange(cols, device=q.device) // B
-        return q[:, :cols].float().double() * sc.double()[at_r][:, at_c]
+        return q[:, :cols].float().double() * sc.float().double()[at_r][:, at_c]
 
     if c["op"] == "matmul":
-        x = _turned(*_coded(s["X"].double(), 1), 1)
-        return x @ weight(s["Wq"], s["s_w"], c["K"]).t()
+        return _coded(s["X"].double(), 1) @ weight(s["Wq"], s["s_w"], c["K"]).t()
     if c["op"] == "backward":
         x, dy = s["X"].double(), s["dY"].double()
-        dx = _turned(*_coded(dy, 1), 1) @ weight(s["WqT"], s["s_w"].t(), c["N"]).t()
-        dw = _turned(*_coded(x, 0), 0).t().contiguous() @ _turned(*_coded(dy, 0), 0)
+        dx = _coded(dy, 1) @ weight(s["WqT"], s["s_wT"], c["N"]).t()
+        dw = _coded(x, 0).t().contiguous() @ _coded(dy, 0)
         return dx, dw
     T, I, k = c["T"], c["I"], c["k"]
     x, logits = s["X"].double(), s["logits"].double()
