@@ -58,7 +58,8 @@
  *                            stats_copy, stats_sync, stats_copy_cols, group_colmax,
  *                            quantize_weight_groups, group_xpass, gemm_group,
  *                            gemm_group_small, fill_zero, block_quantize, block_dequantize,
- *                            scratch_symbol).
+ *                            scratch_symbol, fp8_weight, fp8_rows, fp8_gemm, fp8_cols_dy,
+ *                            fp8_cols_x, fp8_gemm_dx, fp8_gemm_dw, fp8_moe).
  */
 #ifndef LLMINT8_H
 #define LLMINT8_H
@@ -314,6 +315,108 @@ int int8_matmul_group_products(int64_t M, int64_t K, int dtype, int64_t group, c
 #define LLMINT8_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)
 int int8_matmul_noalloc(const void* X, int64_t M, int64_t K, int dtype, const int8_t* Wq, const float* w_scale,
                         int64_t N, float threshold, void* Y, void* stream);
+
+/*
+ * 8-bit floating point (e4m3) with one power-of-two scale per block of 128: a weight format
+ * beside the int8 ones above, its product, the product's gradient, and a mixture-of-experts
+ * layer on weights of this format.
+ *
+ * The format.  A group of values with the largest magnitude a has the scale s = 2^e, the
+ * smallest power of two >= 2^-127 with a <= 448 s, kept as its e8m0 byte e + 127.  The code of
+ * x is the e4m3 value (the finite-only kind, largest 448) nearest to x / s, ties to even; it
+ * stands for code * s.  A code has four significant bits whatever its scale, and the division
+ * by a power of two is exact, so that is the only rounding.  Groups:
+ *   weights      blocks of 128 x 128 of W,
+ *   activations  128 consecutive features of a row (the sum's axis), coded inside each call;
+ * the last group of an axis may be short.  Layouts:
+ *   a row of codes over n values     fp8_code_pitch(n) bytes: n rounded up to a multiple of
+ *                                    128, zero past n;
+ *   a row of scales over n values    fp8_scale_pitch(n) bytes: ceil(n / 128) rounded up to a
+ *                                    multiple of 4, zero past the last group.
+ * Non-finite values are outside the contract of the results, but not of the memory accesses:
+ * one makes every output whose sum it enters not finite, the finite values of its group are
+ * coded with its scale (as good as zero), and nothing else changes.
+ *
+ * Shapes and conventions as above (K a multiple of 16, N of 8), with a bound of 2^22 on the
+ * length of a sum in place of the int32 one (LLMINT8_ERANGE).
+ */
+int64_t fp8_code_pitch(int64_t n);
+int64_t fp8_scale_pitch(int64_t n);
+
+/*
+ * Weight conversion (data-free, one pass).
+ *   W         in : K x N, dtype, row-major.
+ *   Wq        out: N rows of codes over K (16-byte aligned).
+ *   w_scale   out: ceil(N/128) rows of scales over K (4-byte aligned).
+ *   WqT       out, may be NULL with wT_scale: K rows of codes over N, the same codes transposed,
+ *             which the input gradient sums over.
+ *   wT_scale  out: ceil(K/128) rows of scales over N.
+ * K = 0 or N = 0 is a no-op.
+ */
+int fp8_quantize_weight_block(const void* W, int64_t K, int64_t N, int dtype, uint8_t* Wq, uint8_t* w_scale,
+                              uint8_t* WqT, uint8_t* wT_scale, void* stream);
+
+/*
+ * Y = X W on that format:
+ *   Y[m,n] = RN_T( sum over groups g of s_x[m,g] s_w[n/128,g] sum over k in g of
+ *                  Xq[m,k] Wq[n,k] ),
+ * X coded per row in groups of 128 features, products and sums in fp32 on the scaled matrix
+ * instruction (which adds each run of 8 products at 13 bits below the largest of them, then
+ * fp32; a sum of products is off by less than 2^-10 of the sum of their magnitudes).
+ *   Y          out: M x N, dtype, 16-byte aligned.
+ *   workspace  fp8_matmul_block_workspace_bytes(M, K, N) bytes, 16-byte aligned.
+ * M = 0 or N = 0 is a no-op; K = 0 gives Y = 0 (no workspace needed).  Outputs and workspace
+ * overlap nothing (LLMINT8_EINVAL).  ceil(M/64) is at most 65535 (LLMINT8_ERANGE).
+ */
+size_t fp8_matmul_block_workspace_bytes(int64_t M, int64_t K, int64_t N);
+int fp8_matmul_block(const void* X, int64_t M, int64_t K, int dtype, const uint8_t* Wq, const uint8_t* w_scale,
+                     int64_t N, void* Y, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The gradient of Y = X W (W its values after coding, dY the gradient of Y):
+ *   dX[m,k] = RN_T( sum_n dYhat[m,n] What[k,n] )     dYhat: dY coded per row in groups of 128
+ *                                                    along N;
+ *   dW[k,n] = RN_T( sum_m Xhat[m,k] dYhat'[m,n] )    Xhat, dYhat': coded per column in groups of
+ *                                                    128 tokens (rows).
+ *   dX  out, M x K, dtype, 16-byte aligned; NULL: not wanted (WqT and wT_scale may be NULL then).
+ *   dW  out, K x N, dtype, 16-byte aligned; NULL: not wanted (X may be NULL then).
+ *   workspace  fp8_matmul_block_backward_workspace_bytes(M, K, N, dX != NULL, dW != NULL) bytes,
+ *              16-byte aligned.
+ * An empty sum (N = 0 for dX, M = 0 for dW) gives zeros.  M and N are at most 2^22
+ * (LLMINT8_ERANGE).
+ */
+size_t fp8_matmul_block_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int need_dx, int need_dw);
+int fp8_matmul_block_backward(const void* dY, const void* X, int64_t M, int64_t K, int64_t N, int dtype,
+                              const uint8_t* WqT, const uint8_t* wT_scale, void* dX, void* dW, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * A mixture-of-experts layer for few tokens (a decoding step).  With few tokens the layer is
+ * bound by the bytes of the experts it meets, so X stays in 16 bits: only the weights are coded.
+ * For each token x with its E gate logits l:
+ *   the experts e_0, e_1, ... are those of the top_k largest logits, largest first, equal ones by
+ *   ascending index; a logit of -infinity or NaN is never taken, +infinity counts as the largest
+ *   finite number;
+ *   p_j = exp(l[e_j] - l[e_0]) / Z, Z summing over the chosen experts (renormalize != 0) or over
+ *   all E;
+ *   h_j = RN_T( silu(g) * u ),  [g; u] = W13hat[e_j] x,  y = RN_T( sum_j p_j W2hat[e_j] h_j ).
+ * A token with fewer than top_k logits above -infinity gets that many experts; with none, y = 0.
+ *   X         in : T x H, dtype (T <= 128, else LLMINT8_ERANGE; H and I multiples of 16).
+ *   logits    in : T x E fp32 (E <= 1024, top_k <= 16, else LLMINT8_ERANGE).
+ *   W13q, w13_scale  in : E times the conversion of an H x 2I weight, gate columns first.
+ *   W2q, w2_scale    in : E times the conversion of an I x H weight.
+ *   Y             out: T x H, dtype.
+ *   topk_ids      out: T x top_k int32, the chosen experts, -1 where there is none.
+ *   topk_weights  out: T x top_k fp32, p_j, 0 where there is none.
+ *   workspace     fp8_moe_block_workspace_bytes(...) bytes (0 for invalid arguments), 16-byte
+ *                 aligned.
+ * T = 0 or H = 0 is a no-op; I = 0 gives Y = 0.
+ */
+size_t fp8_moe_block_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
+int fp8_moe_block(const void* X, int64_t T, int64_t H, int dtype, const float* logits, int64_t E, int64_t top_k,
+                  int renormalize, const uint8_t* W13q, const uint8_t* w13_scale, const uint8_t* W2q,
+                  const uint8_t* w2_scale, int64_t I, void* Y, int32_t* topk_ids, float* topk_weights, void* workspace,
+                  size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -9,9 +9,19 @@ is no fallback, and importing fails loudly when the library has not been built
     Wq, s_w = int8_quantize_weight(W)                  # offline, W: K x N
     Y = int8_matmul(X, Wq, s_w, threshold=6.0)          # X: M x K -> Y: M x N
     n_outliers, cols = int8_matmul_stats(X, 6.0)
+
+8-bit floating point with a power-of-two scale per block of 128 (codes float8_e4m3fn, scales
+float8_e8m0fnu): a product, its gradient, and a mixture-of-experts layer for few tokens
+
+    Wq, s_w = fp8_quantize_weight_block(W)              # W: K x N
+    Y = fp8_matmul_block(X, Wq, s_w)
+    Wq, s_w, WqT, s_wT = fp8_quantize_weight_block(W, transposed=True)
+    dX, dW = fp8_matmul_block_backward(dY, X, WqT, s_wT)
+    Y, ids, p = fp8_moe_block(X, logits, W13q, s_w13, W2q, s_w2, top_k=8)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -68,6 +78,15 @@ _SIGNATURES = {
     "int8_matmul_group": (_I, [_P, _I64, _I64, _I, _I64, _P, _P, _I64, _P, _P, _SZ, _P]),
     "int8_matmul_group_prepare": (_I, [_P, _I64, _I64, _I, _I64, _P, _SZ, _P]),
     "int8_matmul_group_products": (_I, [_I64, _I64, _I, _I64, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "fp8_code_pitch": (_I64, [_I64]),
+    "fp8_scale_pitch": (_I64, [_I64]),
+    "fp8_quantize_weight_block": (_I, [_P, _I64, _I64, _I, _P, _P, _P, _P, _P]),
+    "fp8_matmul_block_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "fp8_matmul_block": (_I, [_P, _I64, _I64, _I, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "fp8_matmul_block_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _I]),
+    "fp8_matmul_block_backward": (_I, [_P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "fp8_moe_block_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "fp8_moe_block": (_I, [_P, _I64, _I64, _I, _P, _I64, _I64, _I, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
 }
 
 _lib = None
@@ -469,10 +488,204 @@ def group_workspace_views(ws: torch.Tensor, M: int, K: int, group: int) -> dict:
     }
 
 
+# ---- 8-bit floating point with a power-of-two scale per block of 128
+
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_E8M0 = (torch.float8_e8m0fnu, torch.uint8)
+_T16 = (torch.float16, torch.bfloat16)
+
+
+def fp8_code_pitch(n: int) -> int:
+    """Bytes of a row of codes over n values: n rounded up to a multiple of 128."""
+    return -(-n // 128) * 128
+
+
+def fp8_scale_pitch(n: int) -> int:
+    """Bytes of a row of scales over n values: a byte per 128, rounded up to a multiple of 4."""
+    return -(-n // 512) * 4
+
+
+def _fp8_arg(t, name: str, dtypes, shape=None, device=None) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t
+
+
+def _fp8_on(device: torch.device, stream):
+    """The context in which a call allocates and enqueues: the tensors' device, and the given
+    stream where it is not that device's current one (what is allocated then belongs to it)."""
+    if stream is None:
+        return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(getattr(stream, "cuda_stream", stream) or 0)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _fp8_workspace(ws, nbytes: int, device) -> torch.Tensor:
+    if ws is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    return _fp8_arg(ws, "workspace", (torch.uint8,), device=device)
+
+
+def fp8_quantize_weight_block(W: torch.Tensor, transposed: bool = False, stream=None) -> Tuple[torch.Tensor, ...]:
+    """W (K x N, fp16/bf16) -> (Wq N x code_pitch(K) e4m3, w_scale ceil(N/128) x scale_pitch(K)
+    e8m0); with transposed also (WqT K x code_pitch(N), wT_scale ceil(K/128) x scale_pitch(N))."""
+    if _fp8_arg(W, "W", _T16).dim() != 2:
+        raise ValueError("W must be 2-D")
+    K, N = W.shape
+    dev = W.device
+    with _fp8_on(dev, stream):
+        out = [torch.empty((N, fp8_code_pitch(K)), dtype=_E4M3[0], device=dev),
+               torch.empty((-(-N // 128), fp8_scale_pitch(K)), dtype=_E8M0[0], device=dev)]
+        if transposed:
+            out += [torch.empty((K, fp8_code_pitch(N)), dtype=_E4M3[0], device=dev),
+                    torch.empty((-(-K // 128), fp8_scale_pitch(N)), dtype=_E8M0[0], device=dev)]
+        ptrs = [t.data_ptr() for t in out] + [None] * (4 - len(out))
+        _check(lib().fp8_quantize_weight_block(W.data_ptr(), K, N, _DT[W.dtype], *ptrs,
+                                               torch._C._cuda_getCurrentRawStream(dev.index)),
+               "fp8_quantize_weight_block")
+    return tuple(out)
+
+
+def fp8_matmul_block_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().fp8_matmul_block_workspace_bytes(M, K, N))
+
+
+def fp8_matmul_block(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, Y: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y = X W (M x N) of X (M x K, fp16/bf16), coded per row in groups of 128, with a converted weight."""
+    if _fp8_arg(X, "X", _T16).dim() != 2:
+        raise ValueError("X must be 2-D")
+    M, K = X.shape
+    dev = X.device
+    if _fp8_arg(Wq, "Wq", _E4M3, device=dev).dim() != 2 or Wq.shape[1] != fp8_code_pitch(K):
+        raise ValueError(f"Wq must be N x {fp8_code_pitch(K)} for K = {K}, got {tuple(Wq.shape)}")
+    N = Wq.shape[0]
+    _fp8_arg(w_scale, "w_scale", _E8M0, (-(-N // 128), fp8_scale_pitch(K)), dev)
+    L = lib()
+    with _fp8_on(dev, stream):
+        if Y is None:
+            Y = torch.empty((M, N), dtype=X.dtype, device=dev)
+        else:
+            _fp8_arg(Y, "Y", (X.dtype,), (M, N), dev)
+        ws = _fp8_workspace(workspace, L.fp8_matmul_block_workspace_bytes(M, K, N), dev)
+        rc = L.fp8_matmul_block(X.data_ptr(), M, K, _DT[X.dtype], Wq.data_ptr(), w_scale.data_ptr(), N, Y.data_ptr(),
+                                ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev.index))
+    _check(rc, "fp8_matmul_block")
+    return Y
+
+
+def fp8_matmul_block_backward_workspace_bytes(M: int, K: int, N: int, need_dx: bool = True, need_dw: bool = True) -> int:
+    return int(lib().fp8_matmul_block_backward_workspace_bytes(M, K, N, int(need_dx), int(need_dw)))
+
+
+def fp8_matmul_block_backward(dY: torch.Tensor, X: Optional[torch.Tensor], WqT: Optional[torch.Tensor],
+                              wT_scale: Optional[torch.Tensor], need_dx: bool = True, need_dw: bool = True,
+                              dX: Optional[torch.Tensor] = None, dW: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dX M x K, dW K x N) of fp8_matmul_block; one that is not needed is None, and its operands
+    (WqT and wT_scale for dX, X for dW) may be None then."""
+    if _fp8_arg(dY, "dY", _T16).dim() != 2:
+        raise ValueError("dY must be 2-D")
+    M, N = dY.shape
+    dev, t = dY.device, dY.dtype
+    if not need_dx and not need_dw:
+        return None, None
+    if need_dw:
+        if _fp8_arg(X, "X", (t,), device=dev).dim() != 2 or X.shape[0] != M:
+            raise ValueError(f"X must be {M} x K, got {tuple(X.shape)}")
+        K = X.shape[1]
+    if need_dx:
+        if _fp8_arg(WqT, "WqT", _E4M3, device=dev).dim() != 2 or WqT.shape[1] != fp8_code_pitch(N):
+            raise ValueError(f"WqT must be K x {fp8_code_pitch(N)} for N = {N}, got {tuple(WqT.shape)}")
+        if need_dw and WqT.shape[0] != K:
+            raise ValueError(f"WqT must have {K} rows, got {WqT.shape[0]}")
+        K = WqT.shape[0]
+        _fp8_arg(wT_scale, "wT_scale", _E8M0, (-(-K // 128), fp8_scale_pitch(N)), dev)
+    L = lib()
+    with _fp8_on(dev, stream):
+        if not need_dx:
+            dX = None
+        elif dX is None:
+            dX = torch.empty((M, K), dtype=t, device=dev)
+        else:
+            _fp8_arg(dX, "dX", (t,), (M, K), dev)
+        if not need_dw:
+            dW = None
+        elif dW is None:
+            dW = torch.empty((K, N), dtype=t, device=dev)
+        else:
+            _fp8_arg(dW, "dW", (t,), (K, N), dev)
+        ws = _fp8_workspace(workspace, L.fp8_matmul_block_backward_workspace_bytes(M, K, N, int(need_dx), int(need_dw)), dev)
+        rc = L.fp8_matmul_block_backward(dY.data_ptr(), X.data_ptr() if need_dw else None, M, K, N, _DT[t],
+                                         WqT.data_ptr() if need_dx else None, wT_scale.data_ptr() if need_dx else None,
+                                         dX.data_ptr() if need_dx else None, dW.data_ptr() if need_dw else None,
+                                         ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev.index))
+    _check(rc, "fp8_matmul_block_backward")
+    return dX, dW
+
+
+def fp8_moe_block_workspace_bytes(T: int, H: int, I: int, E: int, top_k: int) -> int:
+    return int(lib().fp8_moe_block_workspace_bytes(T, H, I, E, top_k))
+
+
+def fp8_moe_block(X: torch.Tensor, logits: torch.Tensor, W13q: torch.Tensor, w13_scale: torch.Tensor,
+                  W2q: torch.Tensor, w2_scale: torch.Tensor, top_k: int, renormalize: bool = True,
+                  Y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(Y T x H, topk_ids T x top_k int32, topk_weights T x top_k fp32) of a mixture-of-experts
+    layer on X (T x H, at most 128 tokens) with gate logits (T x E fp32); W13q E x 2I x
+    code_pitch(H) (gate rows first) and W2q E x H x code_pitch(I) with their scales: E conversions
+    by fp8_quantize_weight_block, stacked.  I is W13q.shape[1] / 2."""
+    if _fp8_arg(X, "X", _T16).dim() != 2:
+        raise ValueError("X must be 2-D")
+    T, H = X.shape
+    dev = X.device
+    if _fp8_arg(logits, "logits", (torch.float32,), device=dev).dim() != 2 or logits.shape[0] != T:
+        raise ValueError(f"logits must be {T} x E, got {tuple(logits.shape)}")
+    E = logits.shape[1]
+    if _fp8_arg(W13q, "W13q", _E4M3, device=dev).dim() != 3 or W13q.shape[1] % 2:
+        raise ValueError("W13q must be E x 2I x code_pitch(H)")
+    I = W13q.shape[1] // 2
+    _fp8_arg(W13q, "W13q", _E4M3, (E, 2 * I, fp8_code_pitch(H)), dev)
+    _fp8_arg(w13_scale, "w13_scale", _E8M0, (E, -(-2 * I // 128), fp8_scale_pitch(H)), dev)
+    _fp8_arg(W2q, "W2q", _E4M3, (E, H, fp8_code_pitch(I)), dev)
+    _fp8_arg(w2_scale, "w2_scale", _E8M0, (E, -(-H // 128), fp8_scale_pitch(I)), dev)
+    L = lib()
+    with _fp8_on(dev, stream):
+        if Y is None:
+            Y = torch.empty((T, H), dtype=X.dtype, device=dev)
+        else:
+            _fp8_arg(Y, "Y", (X.dtype,), (T, H), dev)
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        p = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        ws = _fp8_workspace(workspace, L.fp8_moe_block_workspace_bytes(T, H, I, E, top_k), dev)
+        rc = L.fp8_moe_block(X.data_ptr(), T, H, _DT[X.dtype], logits.data_ptr(), E, top_k, int(renormalize),
+                             W13q.data_ptr(), w13_scale.data_ptr(), W2q.data_ptr(), w2_scale.data_ptr(), I,
+                             Y.data_ptr(), ids.data_ptr(), p.data_ptr(), ws.data_ptr(), ws.numel(),
+                             torch._C._cuda_getCurrentRawStream(dev.index))
+    _check(rc, "fp8_moe_block")
+    return Y, ids, p
+
+
 __all__ = [
     "int8_quantize_weight", "int8_matmul", "int8_matmul_noalloc", "int8_matmul_stats", "int8_matmul_prepare", "int8_matmul_products", "int8_matmul_workspace_bytes",
     "int8_matmul_workspace_layout", "int8_matmul_accumulators", "workspace_views", "LLMInt8Error", "lib",
     "int8_blockwise_quantize", "int8_blockwise_dequantize", "int8_quantize_weight_fixed", "int8_matmul_fixed",
     "status_string", "int8_quantize_weight_group", "int8_matmul_group", "int8_matmul_group_workspace_bytes",
     "group_workspace_views", "int8_matmul_group_small_batch", "int8_matmul_group_prepare", "int8_matmul_group_products",
+    "fp8_code_pitch", "fp8_scale_pitch", "fp8_quantize_weight_block", "fp8_matmul_block",
+    "fp8_matmul_block_workspace_bytes", "fp8_matmul_block_backward", "fp8_matmul_block_backward_workspace_bytes",
+    "fp8_moe_block", "fp8_moe_block_workspace_bytes",
 ]

@@ -28,7 +28,7 @@ LIB = os.path.join(HERE, "libllmint8.so")
 PROBE_LIB = os.path.join(HERE, "libllmint8_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 SOURCES = ["api.hip", "xpass.hip", "weight.hip", "gemm.hip", "gemm_small.hip", "codec.hip", "gemm_group.hip",
-           "gemm_group_small.hip"]
+           "gemm_group_small.hip", "api_fp8.hip", "fp8_codec.hip", "fp8_gemm.hip", "fp8_moe.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -194,4 +194,45 @@ hipError_t launch_gemm_group_small(int dt, const int8_t* Xq, const int8_t* Xqb, 
                                    const float* s_w, int64_t M, int64_t N, int64_t K, int64_t G, void* Y,
                                    hipStream_t stream);
 
+// ---- e4m3 codes with power-of-two block scales (the format: fp8_common.hpp)
+// Wq N x pitch(K), s_w ceil(N/128) x sp(K); with WqT also K x pitch(N), s_wT ceil(K/128) x sp(N)
+hipError_t launch_fp8_weight(int dt, const void* W, int64_t K, int64_t N, uint8_t* Wq, uint8_t* s_w, uint8_t* WqT,
+                             uint8_t* s_wT, hipStream_t stream);
+// q M x pitch(K), s M x sp(K): a scale per row and group of 128 columns
+hipError_t launch_fp8_rows(int dt, const void* X, int64_t M, int64_t K, uint8_t* q, uint8_t* s, hipStream_t stream);
+// qt C x pitch(R), st C x sp(R): a scale per column of A (R x C) and group of 128 rows, the
+// codes transposed; q, s (both or neither): launch_fp8_rows of the same matrix
+hipError_t launch_fp8_cols(int dt, const void* A, int64_t R, int64_t C, uint8_t* qt, uint8_t* st, uint8_t* q, uint8_t* s,
+                           hipStream_t stream);
+
+struct Fp8GemmArgs {
+    const uint8_t* A;  // M rows of codes
+    const uint8_t* B;  // N rows of codes
+    int64_t M, N, pitch;  // pitch: bytes of a row of codes, a multiple of 128
+    const uint8_t* sa;  // scale rows: one per row of A, one per (n >> bshift) of B
+    const uint8_t* sb;
+    int64_t spitch;     // bytes of a scale row, a multiple of 4
+    int bshift;         // 7: B has one scale per 128 rows; 0: one per row
+    uint16_t* Y;        // M x N
+};
+hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& p, hipStream_t stream);
+
+struct Fp8MoeArgs {
+    const uint16_t* X;
+    int64_t T, H;
+    const float* logits;
+    int64_t E;
+    int k, renormalize;
+    const uint8_t* W13;  // E x 2I x pitch(H): rows 0 .. I-1 gate, I .. 2I-1 up
+    const uint8_t* s13;  // E x ceil(2I/128) x sp(H)
+    const uint8_t* W2;   // E x H x pitch(I)
+    const uint8_t* s2;   // E x ceil(H/128) x sp(I)
+    int64_t I;
+    uint16_t* Y;
+    int32_t* ids;    // T x k
+    float* weights;  // T x k
+    uint16_t* h;     // (T k) x I
+};
+hipError_t launch_fp8_moe(int dt, const Fp8MoeArgs& p, hipStream_t stream);
+
 }  // namespace llmint8

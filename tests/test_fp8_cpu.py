@@ -1,0 +1,169 @@
+"""The boundary of the e4m3 block-scaled operators on the CPU: argument checks (which come before
+any GPU work), layouts, the stages of a dry run, and the reference's own pins."""
+import re
+
+import pytest
+import torch
+
+import int8_quantized_matmul_rowwise_amd as lm
+from tests import fp8_ref as ref
+
+MB = 0x100000
+A, B, C, D, E, F, G, H_, W_ = (MB * 4096 * i for i in range(1, 10))  # fake device addresses, never dereferenced
+BIG = 1 << 40
+
+
+def quant(**kw):
+    a = dict(W=A, K=64, N=72, dt=0, Wq=B, s=C, WqT=D, sT=E)
+    a.update(kw)
+    return lm.lib().fp8_quantize_weight_block(a["W"], a["K"], a["N"], a["dt"], a["Wq"], a["s"], a["WqT"], a["sT"], None)
+
+
+def mm(**kw):
+    a = dict(X=A, M=4, K=64, dt=0, Wq=B, s=C, N=72, Y=D, ws=E, wsb=BIG >> 10)
+    a.update(kw)
+    return lm.lib().fp8_matmul_block(a["X"], a["M"], a["K"], a["dt"], a["Wq"], a["s"], a["N"], a["Y"], a["ws"], a["wsb"], None)
+
+
+def back(**kw):
+    a = dict(dY=A, X=B, M=4, K=64, N=72, dt=0, WqT=C, sT=D, dX=E, dW=F, ws=G, wsb=BIG >> 10)
+    a.update(kw)
+    return lm.lib().fp8_matmul_block_backward(a["dY"], a["X"], a["M"], a["K"], a["N"], a["dt"], a["WqT"], a["sT"],
+                                              a["dX"], a["dW"], a["ws"], a["wsb"], None)
+
+
+def moe(**kw):
+    a = dict(X=A, T=3, H=64, dt=0, l=A + MB, E=4, k=2, W13=B, s13=C, W2=D, s2=E, I=48, Y=F, ids=G, p=G + MB, ws=H_, wsb=MB)
+    a.update(kw)
+    return lm.lib().fp8_moe_block(a["X"], a["T"], a["H"], a["dt"], a["l"], a["E"], a["k"], 1, a["W13"], a["s13"],
+                                  a["W2"], a["s2"], a["I"], a["Y"], a["ids"], a["p"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=2), lm.EINVAL), (dict(K=-16), lm.EINVAL), (dict(K=24), lm.EINVAL), (dict(N=12), lm.EINVAL),
+    (dict(K=(1 << 22) + 16), lm.ERANGE), (dict(N=(1 << 22) + 8), lm.ERANGE), (dict(W=None), lm.EINVAL),
+    (dict(W=A + 8), lm.EINVAL), (dict(Wq=None), lm.EINVAL), (dict(Wq=B + 4), lm.EINVAL), (dict(s=None), lm.EINVAL),
+    (dict(s=C + 2), lm.EINVAL), (dict(WqT=None), lm.EINVAL), (dict(sT=None), lm.EINVAL), (dict(WqT=D + 8), lm.EINVAL),
+    (dict(Wq=A), lm.EINVAL), (dict(WqT=B + 128), lm.EINVAL), (dict(s=B), lm.EINVAL), (dict(sT=C), lm.EINVAL),
+    (dict(K=0, W=None, Wq=None), lm.OK), (dict(N=0, W=None), lm.OK),
+])
+def test_quantize_refuses(kw, code):
+    assert quant(**kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=-1), lm.EINVAL), (dict(M=-1), lm.EINVAL), (dict(K=24), lm.EINVAL), (dict(N=12), lm.EINVAL),
+    (dict(K=(1 << 22) + 16), lm.ERANGE), (dict(M=1 << 31), lm.EINVAL), (dict(M=64 * 65535 + 1), lm.ERANGE),
+    (dict(X=None), lm.EINVAL), (dict(X=A + 8), lm.EINVAL), (dict(Wq=None), lm.EINVAL), (dict(Wq=B + 8), lm.EINVAL),
+    (dict(s=None), lm.EINVAL), (dict(s=C + 1), lm.EINVAL), (dict(Y=None), lm.EINVAL), (dict(Y=D + 2), lm.EINVAL),
+    (dict(ws=None), lm.EWORKSPACE), (dict(ws=E + 8), lm.EWORKSPACE), (dict(wsb=100), lm.EWORKSPACE),
+    (dict(Y=A), lm.EINVAL), (dict(Y=B), lm.EINVAL), (dict(Y=E), lm.EINVAL), (dict(ws=A), lm.EINVAL), (dict(ws=B), lm.EINVAL),
+    (dict(M=0, X=None, ws=None), lm.OK), (dict(N=0, Y=None, Wq=None), lm.OK),
+])
+def test_matmul_refuses(kw, code):
+    assert mm(**kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=3), lm.EINVAL), (dict(K=8), lm.EINVAL), (dict(N=4), lm.EINVAL), (dict(M=(1 << 22) + 1), lm.ERANGE),
+    (dict(N=(1 << 22) + 8), lm.ERANGE), (dict(K=(1 << 22) + 16), lm.ERANGE), (dict(dY=None), lm.EINVAL),
+    (dict(dY=A + 8), lm.EINVAL), (dict(X=None), lm.EINVAL), (dict(WqT=None), lm.EINVAL), (dict(sT=None), lm.EINVAL),
+    (dict(dX=E + 8), lm.EINVAL), (dict(dW=F + 8), lm.EINVAL), (dict(ws=None), lm.EWORKSPACE), (dict(wsb=64), lm.EWORKSPACE),
+    (dict(dX=F), lm.EINVAL), (dict(dX=A), lm.EINVAL), (dict(dW=B), lm.EINVAL), (dict(ws=C), lm.EINVAL), (dict(dW=G), lm.EINVAL),
+    (dict(dX=None, dW=None, dY=None, ws=None), lm.OK),
+])
+def test_backward_refuses(kw, code):
+    assert back(**kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=2), lm.EINVAL), (dict(T=-1), lm.EINVAL), (dict(H=24), lm.EINVAL), (dict(I=8), lm.EINVAL), (dict(E=0), lm.EINVAL),
+    (dict(k=0), lm.EINVAL), (dict(k=5), lm.EINVAL), (dict(T=129), lm.ERANGE), (dict(E=1025), lm.ERANGE),
+    (dict(E=32, k=17), lm.ERANGE), (dict(H=(1 << 22) + 16), lm.ERANGE), (dict(l=None), lm.EINVAL), (dict(l=A + MB + 2), lm.EINVAL),
+    (dict(X=None), lm.EINVAL), (dict(X=A + 8), lm.EINVAL), (dict(W13=None), lm.EINVAL), (dict(W2=D + 8), lm.EINVAL),
+    (dict(s13=None), lm.EINVAL), (dict(s2=None), lm.EINVAL), (dict(Y=None), lm.EINVAL), (dict(ids=None), lm.EINVAL),
+    (dict(p=None), lm.EINVAL), (dict(ws=None), lm.EWORKSPACE), (dict(wsb=16), lm.EWORKSPACE), (dict(Y=A), lm.EINVAL),
+    (dict(ids=F), lm.EINVAL), (dict(p=G), lm.EINVAL), (dict(ws=D), lm.EINVAL), (dict(Y=B), lm.EINVAL),
+    (dict(T=0, X=None, ws=None), lm.OK), (dict(H=0, X=None), lm.OK),
+])
+def test_moe_refuses(kw, code):
+    assert moe(**kw) == code
+
+
+def test_sizes():
+    for n in (0, 1, 16, 127, 128, 129, 512, 513, 4096, 12288):
+        assert lm.lib().fp8_code_pitch(n) == lm.fp8_code_pitch(n) == ref.pitch(n)
+        assert lm.lib().fp8_scale_pitch(n) == lm.fp8_scale_pitch(n) == ref.sp(n)
+    assert lm.lib().fp8_code_pitch(-1) == 0 and lm.lib().fp8_scale_pitch(-1) == 0
+    assert lm.fp8_matmul_block_workspace_bytes(-1, 16, 8) == 0
+    assert lm.fp8_matmul_block_backward_workspace_bytes(4, -16, 8) == 0
+    assert lm.fp8_moe_block_workspace_bytes(1, 64, 64, 4, 5) == 0
+    for dx in (False, True):
+        for dw in (False, True):
+            assert lm.fp8_matmul_block_backward_workspace_bytes(130, 272, 136, dx, dw) >= dx * 130 * 256 + dw * (136 + 272) * 256
+
+
+def _calls():
+    return {
+        "quantize": (lambda: quant(), ["fp8_weight"]),
+        "matmul": (lambda: mm(M=300, K=1024, N=520), ["fp8_rows", "fp8_gemm"]),
+        "matmul_k0": (lambda: mm(K=0), ["fill_zero"]),
+        "backward": (lambda: back(M=300, K=1024, N=520), ["fp8_cols_dy", "fp8_cols_x", "fp8_gemm_dx", "fp8_gemm_dw"]),
+        "backward_dx": (lambda: back(M=300, dW=None), ["fp8_rows", "fp8_gemm_dx"]),
+        "backward_dw": (lambda: back(M=300, dX=None), ["fp8_cols_dy", "fp8_cols_x", "fp8_gemm_dw"]),
+        "backward_no_tokens": (lambda: back(M=0, ws=None), ["fill_zero"]),
+        "backward_n0": (lambda: back(N=0, ws=None, dY=None), ["fill_zero"]),
+        "moe": (lambda: moe(), ["fp8_moe"]),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(_calls()))
+def test_stages_and_their_failures(name, monkeypatch, capfd):
+    fn, want = _calls()[name]
+    monkeypatch.setenv("LLMINT8_LOG", "1")
+
+    def run(fault):
+        monkeypatch.setenv("LLMINT8_FAULT", fault)
+        capfd.readouterr()
+        rc = fn()
+        return rc, re.findall(r"^\[llmint8\]   stage (\w+)", capfd.readouterr().err, flags=re.M)
+
+    assert run("no_such_stage") == (lm.OK, want)
+    for i, st in enumerate(want):
+        assert run(st) == (lm.EHIP, want[: i + 1])
+
+
+def test_binding_refuses_what_is_not_on_the_gpu():
+    x = torch.zeros(4, 64, dtype=torch.float16)
+    with pytest.raises(TypeError):
+        lm.fp8_matmul_block(x, x, x)
+    with pytest.raises(TypeError):
+        lm.fp8_quantize_weight_block(x)
+    with pytest.raises(TypeError):
+        lm.fp8_matmul_block_backward(x, x, x, x)
+    with pytest.raises(TypeError):
+        lm.fp8_moe_block(x, x, x, x, x, x, top_k=1)
+
+
+def test_reference_rounds_as_the_type_does():
+    """The reference's e4m3 against torch's conversion, over every code, the midpoints between
+    neighbours and their surroundings."""
+    codes = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    mid = (codes[1:] + codes[:-1]) / 2
+    v = torch.cat([codes, mid, mid * (1 + 2.0 ** -20), mid * (1 - 2.0 ** -20)])
+    v = torch.cat([v, -v])
+    assert torch.equal(ref.e4m3(v), v.float().to(torch.float8_e4m3fn).double())
+
+
+def test_reference_scales():
+    a = torch.tensor([448.0, 448.0001, 447.9, 1.75, 1.7500001, 0.0, 2.0 ** -140, 224.0, 224.0001], dtype=torch.float64)
+    e = ref.power_of(a)
+    assert e.tolist() == [0, 1, 0, -8, -7, -127, -127, -1, 0]
+    assert (a <= 448 * torch.exp2(e.double())).all()
+
+
+def test_reference_on_a_case_by_hand():
+    """One group: 448 * 2^-2 = 112 >= 100, so the scale is 2^-2; 100 / 2^-2 = 400 lies between the
+    codes 384 and 416, at their middle: the even one is taken."""
+    v, q, b = ref.coded_rows(torch.tensor([[1.0, 100.0]]))
+    assert b[0, 0] == 127 - 2 and q[0, :2].tolist() == [4.0, 384.0] and v[0].tolist() == [1.0, 96.0]

@@ -1,0 +1,460 @@
+"""The e4m3 block-scaled operators on the GPU against the 64-bit reference (fp8_ref): weight
+conversion and its transposed form bit for bit, the product and its gradient on lattices whose
+sums are exact (bit for bit) and on random data (derived bounds), and the mixture-of-experts
+layer; captured, on another stream, in caller-owned buffers between canaries."""
+import math
+
+import pytest
+import torch
+
+import int8_quantized_matmul_rowwise_amd as lm
+from tests import fp8_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DTS = [torch.float16, torch.bfloat16]
+F8, E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape):
+    return torch.randn(*shape, generator=g)
+
+
+def outliers(g, x):
+    """A few columns far larger, one row of zeros, one group of zeros."""
+    x = x.clone()
+    x[:, torch.randint(0, x.shape[1], (3,), generator=g)] *= 30
+    if x.shape[0] > 2:
+        x[1] = 0
+    x[0, :128] = 0
+    return x
+
+
+def u8(t):
+    return t.view(torch.uint8).cpu()
+
+
+def codes_equal(got, want_values, what):
+    assert torch.equal(got.cpu().view(F8).float().double(), want_values), f"{what}: codes differ"
+
+
+# ---- weight conversion
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("K,N", [(16, 8), (128, 128), (144, 136), (2064, 520), (400, 1032), (528, 8), (16, 1288)])
+def test_quantize_weight(K, N, dt):
+    print(f"\n[case] quantize {dt} {K}x{N}", flush=True)
+    g = gen(K + N)
+    W = (randn(g, K, N) * 0.02 * torch.exp2(torch.randint(-6, 3, (K, 1), generator=g).float()))
+    W[: min(K, 128), : min(N, 128)] *= 0  # a block of zeros
+    W = W.to(dt)
+    Wd = W.cuda()
+    Wq, s, WqT, sT = lm.fp8_quantize_weight_block(Wd, transposed=True)
+    q1, s1 = lm.fp8_quantize_weight_block(Wd)
+    _, rq, rs, rqt, rst = ref.coded_weight(W)
+    codes_equal(Wq, rq, "Wq")
+    codes_equal(WqT, rqt, "WqT")
+    assert torch.equal(u8(s), rs) and torch.equal(u8(sT), rst)
+    assert torch.equal(u8(q1), u8(Wq)) and torch.equal(u8(s1), u8(s))
+
+
+@pytest.mark.parametrize("dt", DTS)
+def test_quantize_border_values(dt):
+    """Blocks whose largest magnitude is 448 times a power of two, one step to either side of it,
+    the type's largest and smallest numbers, and every tie between two codes."""
+    fi = torch.finfo(dt)
+    step = torch.finfo(dt).eps
+    tops = [448.0, 448.0 * (1 + step), 448.0 * (1 - step / 2), 1.75, 3.5 * 2.0 ** -9, fi.max, fi.tiny,
+            fi.smallest_normal * step, 1.0, 0.0]
+    cols = []
+    for a in tops:
+        v = torch.linspace(-1, 1, 128, dtype=torch.float64) * a
+        v[0], v[1] = a, -a
+        cols.append(v)
+    grid = torch.tensor([m * 2.0 ** e for e in range(-9, 9) for m in (1.0, 1.0625, 1.1875, 1.3125, 1.4375, 1.5625, 1.6875)]
+                        + [448.0, 0.0], dtype=torch.float64)  # ties at the odd sixteenths
+    cols.append(grid[-128:])
+    # one block per value: 128 equal columns each
+    W = torch.cat([c[:, None].expand(128, 128) for c in cols], dim=1).to(dt).contiguous()
+    Wq, s = lm.fp8_quantize_weight_block(W.cuda())
+    _, rq, rs, _, _ = ref.coded_weight(W)
+    codes_equal(Wq, rq, "Wq")
+    assert torch.equal(u8(s), rs)
+
+
+# ---- product
+
+def lattice(g, *shape, dt, spread=0):
+    """Whole numbers -3 .. 3 times a power of two per row: their codes are exact, and so is every
+    sum of their products here."""
+    x = torch.randint(-3, 4, shape, generator=g).double()
+    if spread:
+        x = x * torch.exp2(torch.randint(0, spread + 1, (shape[0], 1), generator=g).double())
+    return x.to(dt)
+
+
+SHAPES = [(1, 16, 8), (1, 4096, 264), (3, 144, 1032), (16, 272, 520), (17, 1040, 264), (33, 528, 136), (64, 1664, 72),
+          (65, 256, 136), (100, 640, 2056), (128, 2064, 264), (129, 128, 264), (300, 1040, 520), (257, 400, 1288),
+          (520, 144, 776)]
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_matmul_exact_lattice(M, K, N, dt):
+    print(f"\n[case] matmul lattice {dt} {M}x{K}x{N}", flush=True)
+    g = gen(M + K + N)
+    X = lattice(g, M, K, dt=dt, spread=3)
+    W = lattice(g, N, K, dt=dt, spread=3).t().contiguous()
+    Wq, s = lm.fp8_quantize_weight_block(W.cuda())
+    Y = lm.fp8_matmul_block(X.cuda(), Wq, s)
+    want = (X.double() @ W.double()).float().to(dt)
+    assert torch.equal(Y.cpu(), want)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_matmul_random(M, K, N, dt):
+    print(f"\n[case] matmul random {dt} {M}x{K}x{N}", flush=True)
+    g = gen(M * 3 + K + N)
+    X = outliers(g, randn(g, M, K)).to(dt)
+    W = (randn(g, K, N) * 0.02 * torch.exp2(torch.randint(-3, 3, (K, 1), generator=g).float())).to(dt)
+    Wq, s = lm.fp8_quantize_weight_block(W.cuda())
+    Y = lm.fp8_matmul_block(X.cuda(), Wq, s)
+    xh, what = ref.coded_rows(X)[0], ref.coded_weight(W)[0]
+    y, err = ref.product(xh, what.t())
+    ref.assert_close(Y, y, err, "Y")
+    # far below the bound on the whole: the output's rounding (at most u of the norm), and the
+    # dropped bits, which are independent from run to run of 8 products: about 2^-13 of the norm
+    assert (Y.double().cpu() - y).norm() <= (ref.U[dt] + 2.0 ** -12) * y.norm()
+
+
+@pytest.mark.parametrize("dt", DTS)
+def test_matmul_rows_do_not_meet(dt):
+    """A row that is not finite leaves the others as they were, bit for bit, whatever its place."""
+    M, K, N = 37, 400, 264
+    g = gen(5)
+    X, W = randn(g, M, K).to(dt), (randn(g, K, N) * 0.02).to(dt)
+    Wq, s = lm.fp8_quantize_weight_block(W.cuda())
+    Y = lm.fp8_matmul_block(X.cuda(), Wq, s).cpu()
+    for row, v in ((0, math.nan), (36, math.inf), (16, -math.inf)):
+        X2 = X.clone()
+        X2[row, 7] = v
+        Y2 = lm.fp8_matmul_block(X2.cuda(), Wq, s).cpu()
+        keep = torch.arange(M) != row
+        assert torch.equal(Y2[keep], Y[keep])
+        assert not torch.isfinite(Y2[row].float()).any()
+
+
+@pytest.mark.parametrize("dt", DTS)
+def test_matmul_far_scales(dt):
+    """Rows and blocks at the ends of the type's range: the scales are applied without a
+    detour through values that overflow or vanish."""
+    M, K, N = 20, 256, 136
+    g = gen(6)
+    lo, hi = (-12, 8) if dt == torch.float16 else (-90, 90)
+    X = lattice(g, M, K, dt=torch.float64)
+    e = torch.linspace(lo, hi, M).round().double()
+    X = (X * torch.exp2(e)[:, None]).to(dt)
+    W = (lattice(g, K, N, dt=torch.float64) * 2.0 ** (-4 if dt == torch.float16 else -20)).to(dt)
+    Wq, s = lm.fp8_quantize_weight_block(W.cuda())
+    Y = lm.fp8_matmul_block(X.cuda(), Wq, s)
+    assert torch.equal(Y.cpu(), (X.double() @ W.double()).float().to(dt))
+
+
+def test_matmul_empty():
+    Wq, s = lm.fp8_quantize_weight_block(torch.zeros(0, 64, dtype=torch.float16, device="cuda"))
+    Y = lm.fp8_matmul_block(torch.zeros(5, 0, dtype=torch.float16, device="cuda"), Wq, s)
+    assert Y.shape == (5, 64) and not Y.any()
+    Wq, s = lm.fp8_quantize_weight_block(torch.zeros(64, 8, dtype=torch.float16, device="cuda"))
+    assert lm.fp8_matmul_block(torch.zeros(0, 64, dtype=torch.float16, device="cuda"), Wq, s).shape == (0, 8)
+
+
+def framed(shape, dt, fill=3.0):
+    """(view, whole): a buffer of the shape between canaries."""
+    n = math.prod(shape)
+    whole = torch.full((n + 512,), fill, dtype=dt, device="cuda")
+    return whole[256: 256 + n].view(shape), whole
+
+
+def frame_untouched(whole, n, fill=3.0):
+    return bool((whole[:256] == fill).all()) and bool((whole[256 + n:] == fill).all())
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 144, 72), (19, 272, 136), (70, 400, 264), (300, 1040, 520)])
+def test_matmul_writes_its_output_alone(M, K, N):
+    g = gen(7)
+    X, W = randn(g, M, K).half().cuda(), randn(g, K, N).half().cuda()
+    Wq, s = lm.fp8_quantize_weight_block(W)
+    Y, yw = framed((M, N), torch.float16)
+    nb = lm.fp8_matmul_block_workspace_bytes(M, K, N)
+    ws, wsw = framed((nb,), torch.uint8, 90)
+    lm.fp8_matmul_block(X, Wq, s, Y=Y, workspace=ws)
+    torch.cuda.synchronize()
+    assert frame_untouched(yw, M * N) and frame_untouched(wsw, nb, 90)
+    # the workspace's old contents do not matter, and equal calls give equal bits
+    ws.fill_(255)
+    assert torch.equal(lm.fp8_matmul_block(X, Wq, s, workspace=ws), Y)
+
+
+# ---- gradient
+
+BACK = [(1, 16, 8), (5, 144, 136), (128, 256, 128), (130, 272, 264), (333, 1040, 520), (64, 2064, 72), (700, 400, 1288)]
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M,K,N", BACK)
+def test_backward_exact_lattice(M, K, N, dt):
+    print(f"\n[case] backward lattice {dt} {M}x{K}x{N}", flush=True)
+    g = gen(M + K + N)
+    X, W, dY = lattice(g, M, K, dt=dt), lattice(g, K, N, dt=dt), lattice(g, M, N, dt=dt)
+    _, _, WqT, sT = lm.fp8_quantize_weight_block(W.cuda(), transposed=True)
+    dX, dW = lm.fp8_matmul_block_backward(dY.cuda(), X.cuda(), WqT, sT)
+    assert torch.equal(dX.cpu(), (dY.double() @ W.double().t()).float().to(dt))
+    assert torch.equal(dW.cpu(), (X.double().t() @ dY.double()).float().to(dt))
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M,K,N", BACK)
+def test_backward_random(M, K, N, dt):
+    print(f"\n[case] backward random {dt} {M}x{K}x{N}", flush=True)
+    g = gen(M + K * 2 + N)
+    X = outliers(g, randn(g, M, K)).to(dt)
+    W = (randn(g, K, N) * 0.02).to(dt)
+    dY = (randn(g, M, N) * 0.01 * torch.exp2(torch.randint(-4, 4, (M, 1), generator=g).float())).to(dt)
+    _, _, WqT, sT = lm.fp8_quantize_weight_block(W.cuda(), transposed=True)
+    dX, dW = lm.fp8_matmul_block_backward(dY.cuda(), X.cuda(), WqT, sT)
+    x, err = ref.product(ref.coded_rows(dY)[0], ref.coded_weight(W)[0])
+    ref.assert_close(dX, x, err, "dX")
+    w, err = ref.product(ref.coded_rows(X.t())[0], ref.coded_rows(dY.t())[0])
+    ref.assert_close(dW, w, err, "dW")
+
+
+def test_backward_against_differences():
+    """<dY, Y(X + D) - Y(X)> = <dX, D> and <dY, Y(W + D) - Y(W)> = <dW, D>: on whole numbers
+    -1 .. 1 the codes, the outputs and both gradients are exact, and Y is linear."""
+    M, K, N, dt = 70, 272, 136, torch.float16
+    g = gen(9)
+
+    def trits(*shape):
+        return torch.randint(-1, 2, shape, generator=g).to(dt)
+
+    X, W, dY, DX, DW = trits(M, K), trits(K, N), trits(M, N), trits(M, K), trits(K, N)
+
+    def forward(X, W):
+        return lm.fp8_matmul_block(X.cuda(), *lm.fp8_quantize_weight_block(W.cuda())).cpu().double()
+
+    _, _, WqT, sT = lm.fp8_quantize_weight_block(W.cuda(), transposed=True)
+    dX, dW = (t.cpu().double() for t in lm.fp8_matmul_block_backward(dY.cuda(), X.cuda(), WqT, sT))
+    Y = forward(X, W)
+    assert (dY.double() * (forward(X + DX, W) - Y)).sum() == (dX * DX.double()).sum()
+    assert (dY.double() * (forward(X, W + DW) - Y)).sum() == (dW * DW.double()).sum()
+
+
+def test_backward_one_of_the_two_and_empty_sums():
+    M, K, N = 130, 272, 136
+    g = gen(10)
+    X, W, dY = randn(g, M, K).half().cuda(), randn(g, K, N).half().cuda(), randn(g, M, N).half().cuda()
+    _, _, WqT, sT = lm.fp8_quantize_weight_block(W, transposed=True)
+    dX, dW = lm.fp8_matmul_block_backward(dY, X, WqT, sT)
+    a, none = lm.fp8_matmul_block_backward(dY, None, WqT, sT, need_dw=False)
+    assert none is None and torch.equal(a, dX)
+    none, b = lm.fp8_matmul_block_backward(dY, X, None, None, need_dx=False)
+    assert none is None and torch.equal(b, dW)
+    assert lm.fp8_matmul_block_backward(dY, None, None, None, need_dx=False, need_dw=False) == (None, None)
+    e, z = lm.fp8_matmul_block_backward(dY[:0], X[:0], WqT, sT)  # no tokens
+    assert e.shape == (0, K) and z.shape == (K, N) and not z.any()
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 144, 72), (200, 400, 264)])
+def test_backward_writes_its_outputs_alone(M, K, N):
+    g = gen(11)
+    X, W, dY = randn(g, M, K).bfloat16().cuda(), randn(g, K, N).bfloat16().cuda(), randn(g, M, N).bfloat16().cuda()
+    _, _, WqT, sT = lm.fp8_quantize_weight_block(W, transposed=True)
+    dX, xw = framed((M, K), torch.bfloat16)
+    dW, ww = framed((K, N), torch.bfloat16)
+    nb = lm.fp8_matmul_block_backward_workspace_bytes(M, K, N)
+    ws, wsw = framed((nb,), torch.uint8, 90)
+    lm.fp8_matmul_block_backward(dY, X, WqT, sT, dX=dX, dW=dW, workspace=ws)
+    torch.cuda.synchronize()
+    assert frame_untouched(xw, M * K) and frame_untouched(ww, K * N) and frame_untouched(wsw, nb, 90)
+    ws.fill_(255)
+    a, b = lm.fp8_matmul_block_backward(dY, X, WqT, sT, workspace=ws)
+    assert torch.equal(a, dX) and torch.equal(b, dW)
+
+
+# ---- mixture of experts
+
+def experts(g, E, H, I, dt):
+    up = [lm.fp8_quantize_weight_block((randn(g, H, 2 * I) * 0.05).to(dt).cuda()) for _ in range(E)]
+    down = [lm.fp8_quantize_weight_block((randn(g, I, H) * 0.05).to(dt).cuda()) for _ in range(E)]
+
+    def stacked(ts, t):
+        return torch.stack([x.view(torch.uint8) for x in ts]).view(t)
+
+    return (stacked([q for q, _ in up], F8), stacked([s for _, s in up], E8), stacked([q for q, _ in down], F8),
+            stacked([s for _, s in down], E8))
+
+
+def moe_check(X, logits, w, k, renormalize):
+    W13q, s13, W2q, s2 = w
+    E, I, (T, H) = W13q.shape[0], W13q.shape[1] // 2, X.shape
+    Y, ids, p = lm.fp8_moe_block(X.cuda(), logits.cuda(), *w, top_k=k, renormalize=renormalize)
+    W13 = torch.stack([ref.weight_values(W13q[e].cpu(), s13[e].cpu(), H) for e in range(E)])
+    W2 = torch.stack([ref.weight_values(W2q[e].cpu(), s2[e].cpu(), I) for e in range(E)])
+    y, err, rids, rp = ref.moe(X, logits, W13, W2, k, renormalize)
+    assert torch.equal(ids.cpu(), rids)
+    # exp and a sum of at most 1024 of them, a division: 64 steps are ample for top_k <= 16,
+    # and E steps more where all experts are summed
+    assert ((p.cpu().double() - rp).abs() <= (64 + (0 if renormalize else E)) * 2.0 ** -24 * rp + 2.0 ** -140).all()
+    ref.assert_close(Y, y, err + y.abs() * (64 + E) * 2.0 ** -24, "y")
+    return Y, ids, p
+
+
+MOE = [(1, 16, 16, 1, 1), (1, 256, 128, 8, 2), (1, 272, 144, 64, 8), (2, 528, 400, 12, 3), (4, 384, 272, 5, 5),
+       (9, 256, 144, 70, 4), (17, 272, 208, 6, 2), (40, 144, 272, 9, 4), (64, 256, 128, 130, 8), (128, 128, 144, 4, 2),
+       (33, 128, 128, 3, 1), (5, 1040, 64, 20, 16)]
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("T,H,I,E,k", MOE)
+def test_moe(T, H, I, E, k, dt):
+    for renormalize in (True, False):
+        print(f"\n[case] moe {dt} T={T} H={H} I={I} E={E} k={k} renormalize={renormalize}", flush=True)
+        g = gen(T + H + I + E + k)
+        X = randn(g, T, H).to(dt)
+        logits = 2 * randn(g, T, E)
+        moe_check(X, logits, experts(g, E, H, I, dt), k, renormalize)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("T", [3, 20, 100])
+def test_moe_masks_ties_and_odd_logits(T, dt):
+    """Closed experts, rows of padding, ties, NaN and infinities in the logits; every token on one
+    expert, and an expert without tokens."""
+    H, I, E, k = 144, 80, 11, 3
+    g = gen(T)
+    X = randn(g, T, H).to(dt)
+    w = experts(g, E, H, I, dt)
+    l = 2 * randn(g, T, E)
+    l[torch.rand(T, E, generator=g) < 0.4] = -math.inf
+    l[0] = -math.inf           # no expert at all
+    l[1] = 0.5                 # all equal
+    l[2] = -math.inf
+    l[2, 7] = -3.0             # a single one
+    l[T - 1] = -math.inf
+    if T > 10:
+        l[3, 4] = math.nan
+        l[4] = math.nan
+        l[5, 2] = math.inf
+        l[6, 2] = l[6, 5] = math.inf
+        l[7] = torch.finfo(torch.float32).min
+        l[8] = torch.arange(E).float() * 90
+        X[0] = math.nan        # padding may hold anything
+    for renormalize in (True, False):
+        Y, ids, p = moe_check(X if T <= 10 else torch.where(torch.isnan(X), torch.zeros_like(X), X), l, w, k, renormalize)
+        assert not Y[0].any() and (ids[0] == -1).all() and not p[0].any()
+        if T > 10:
+            Y2, ids2, p2 = lm.fp8_moe_block(X.cuda(), l.cuda(), *w, top_k=k, renormalize=renormalize)
+            assert torch.equal(Y2, Y) and torch.equal(ids2, ids) and torch.equal(p2, p)
+    one = torch.full((T, E), -1.0)
+    one[:, 6] = 1.0
+    moe_check(torch.nan_to_num(X), one, w, 1, True)
+
+
+def test_moe_writes_its_outputs_alone():
+    T, H, I, E, k = 7, 272, 144, 6, 2
+    g = gen(12)
+    X, logits, w = randn(g, T, H).half().cuda(), randn(g, T, E).cuda(), experts(g, E, H, I, torch.float16)
+    Y, yw = framed((T, H), torch.float16)
+    nb = lm.fp8_moe_block_workspace_bytes(T, H, I, E, k)
+    ws, wsw = framed((nb,), torch.uint8, 90)
+    lm.fp8_moe_block(X, logits, *w, top_k=k, Y=Y, workspace=ws)
+    torch.cuda.synchronize()
+    assert frame_untouched(yw, T * H) and frame_untouched(wsw, nb, 90)
+    ws.fill_(255)
+    assert torch.equal(lm.fp8_moe_block(X, logits, *w, top_k=k, workspace=ws)[0], Y)
+
+
+# ---- together, captured, and on another stream
+
+def block_forward(X, gate, proj, moe_w, k):
+    """A projection, then the expert layer on its output: the operators as a decoding step uses them."""
+    Y = lm.fp8_matmul_block(X, *proj)
+    return lm.fp8_moe_block(Y, (Y.float() @ gate), *moe_w, top_k=k)
+
+
+@pytest.mark.parametrize("T", [1, 6, 48])
+def test_together_captured_and_replayed(T):
+    K, H, I, E, k = 272, 256, 144, 12, 3
+    g = gen(T)
+    dt = torch.bfloat16
+    proj = lm.fp8_quantize_weight_block((randn(g, K, H) * 0.05).to(dt).cuda())
+    gate, moe_w = (randn(g, H, E) * 0.2).cuda(), experts(g, E, H, I, dt)
+    X = randn(g, T, K).to(dt).cuda()
+    block_forward(X, gate, proj, moe_w, k)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = block_forward(X, gate, proj, moe_w, k)
+    for r in range(4):
+        X.copy_(randn(g, T, K).to(dt))
+        want = block_forward(X, gate, proj, moe_w, k)
+        torch.cuda.synchronize()
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b), r
+
+
+def test_two_captured_graphs_and_a_training_step():
+    M, K, N = 130, 272, 264
+    g = gen(13)
+    W = (randn(g, K, N) * 0.05).half().cuda()
+    X, dY = randn(g, M, K).half().cuda(), randn(g, M, N).half().cuda()
+
+    def step():
+        Wq, s, WqT, sT = lm.fp8_quantize_weight_block(W, transposed=True)
+        Y = lm.fp8_matmul_block(X, Wq, s)
+        return (Y,) + lm.fp8_matmul_block_backward(dY, X, WqT, sT)
+
+    step()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        graphs.append((graph, out))
+    for r in range(3):
+        X.copy_(randn(g, M, K).half())
+        W.copy_((randn(g, K, N) * 0.05).half())
+        want = step()
+        for graph, out in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            for a, b in zip(out, want):
+                assert torch.equal(a, b), r
+
+
+def test_on_another_stream():
+    M, K, N = 40, 272, 264
+    g = gen(14)
+    X, W = randn(g, M, K).half().cuda(), randn(g, K, N).half().cuda()
+    Wq, s = lm.fp8_quantize_weight_block(W)
+    want = lm.fp8_matmul_block(X, Wq, s)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = [lm.fp8_matmul_block(X, Wq, s, stream=side if i % 2 else side.cuda_stream) for i in range(8)]
+    side.synchronize()
+    for o in outs:
+        assert torch.equal(o, want)
+    assert torch.cuda.current_stream() != side
