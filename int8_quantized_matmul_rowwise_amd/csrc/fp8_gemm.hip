@@ -3,6 +3,27 @@
 // g over groups of 128 along K; ea per row, eb per row (n >> 0) or per 128 rows (n >> 7).
 // The forward product, the input gradient (b: the transposed weight codes) and the weight
 // gradient (both operands per row, the sum over the tokens) are all this product.
+//
+// The scaled matrix instruction v_mfma_scale_f32_16x16x128_f8f6f4 takes one group at a time and
+// applies both scales itself, so the sums stay in the accumulators: no fold of partial sums.
+// n is its row side and m its column side: a lane's four results are neighbours along n.
+//
+// Tiled kernel: BM x BN outputs per workgroup, waves in WM x WN, each 64 rows m (MF = 4 pieces
+// of 16) by 16 NF columns n.  A stage is one group: a 128-byte line per row of each operand,
+// loaded straight into LDS (16-byte chunk c of row r at chunk c ^ swz(r), so that 8 lanes
+// reading one chunk of 8 rows meet all banks), A one stage ahead (2 slots) and B two (3 slots).
+// Within a stage the n pieces stream from LDS two ahead of their MFMAs, the m pieces of the
+// stage stay in registers.  The workgroup meets once per stage, after the stage's last LDS read
+// and before the MFMAs of its last two n pieces; under those the next stage's m pieces and first
+// n pieces are read.  The barrier waits for all but the newest B loads (counted), so the loads
+// in flight are never drained.
+// The scales come as dwords, one per row and four groups (instruction operands that select one
+// of four bytes): the stages are unrolled by four, and the next four groups' dwords are loaded
+// at the first of them.
+// Persistent over the XCD's run of tiles, as the int8 product kernels: the next tile's first
+// loads are in flight during a tile's last stages and its output.
+#include <type_traits>
+
 #include "fp8_common.hpp"
 #include "launch.hpp"
 
@@ -10,52 +31,332 @@ namespace llmint8 {
 
 namespace {
 
-// One workgroup per 64 x 64 outputs, each wave 16 columns n by 64 rows m; operands from global
-// memory straight into the matrix unit's registers (16x16x128: lane l holds row l % 16, bytes
-// 32 (l / 16) .. + 31 of the group).  n is the instruction's row side, so a lane's four results
-// are four neighbours along n of one row m.
-template <int DT>
-__global__ __launch_bounds__(256) void fp8_gemm_kernel(Fp8GemmArgs p) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+constexpr int MF = 4;
+constexpr int BK = 128;
+constexpr int kXcds = 8;
+constexpr int kGroupM = 8;
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)bytes, 0x00020000);
+}
+
+// by value: a choice between the variables themselves would put them into memory
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t pick(int d, __amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b,
+                                                       __amdgpu_buffer_rsrc_t c) {
+    return d == 0 ? a : (d == 1 ? b : c);
+}
+
+__host__ __device__ constexpr int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+#define LLMINT8_FP8_INLINE __attribute__((always_inline))
+// wait for this wave's LDS reads and all but the N newest loads, then the bare barrier
+#define LLMINT8_FP8_WAIT_BARRIER(N)                                        \
+    do {                                                                   \
+        __builtin_amdgcn_s_waitcnt(0xC07F);                                \
+        asm volatile("s_waitcnt vmcnt(" #N ")\n\ts_barrier" ::: "memory"); \
+    } while (0)
+
+struct TiledParams {
+    Fp8GemmArgs a;
+    int tiles_m, tiles_n;
+};
+
+// U: the byte of the scale dwords (the group's place among four)
+template <int U>
+__device__ __forceinline__ v4f mfma_fp8(const v8i& n, const v8i& m, const v4f& c, int sn, int sm) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(n, m, c, 0, 0, U, sn, U, sm);
+}
+
+// ROWB: B has a scale per row (else per 128 rows, one for a wave's columns)
+template <int DT, int WM, int WN, int NF, bool ROWB>
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams tp) {
+    constexpr int kWaves = WM * WN;
+    constexpr int BM = 16 * MF * WM, BN = 16 * NF * WN;
+    constexpr int kSlotA = BM * BK, kSlotB = BN * BK;
+    constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = BN / 8 / kWaves;
+    constexpr int NS = ROWB ? NF : 1;  // scale dwords of a wave's columns
+    constexpr int kYPitch = 16 * NF + 8;  // staged output row, 16-bit elements
+    static_assert(kLoadsA == 4 && kLoadsB == 4, "the barrier's wait leaves the four newest loads (B) in flight");
+    static_assert((kWaves / 2) * 16 * kYPitch * 2 <= kSlotA && (kWaves / 2) * 16 * kYPitch * 2 <= kSlotB, "staging");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kSlotA + 3 * kSlotB];
+    const Fp8GemmArgs& p = tp.a;
+    const int tid = threadIdx.x, lane = tid & 63, wu = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wu % WM, wn = wu / WM;
     const int li = lane & 15, q = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 64 + 16 * w, m0 = (int64_t)blockIdx.y * 64;
-    const int64_t n = n0 + li < p.N ? n0 + li : p.N - 1;
-    const uint8_t* b = p.B + n * p.pitch + 32 * q;
-    const uint8_t* sb = p.sb + (n >> p.bshift) * p.spitch;
-    const uint8_t* a[4];
-    const uint8_t* sa[4];
+    const int nk = (int)(p.pitch / BK);
+
+    // ---- this workgroup's tiles: a strided part of its XCD's contiguous run (ids congruent mod
+    // 8 share an XCD), in groups of kGroupM row tiles
+    const int T = tp.tiles_m * tp.tiles_n;
+    const int bid = blockIdx.x, nwg = gridDim.x;
+    const int xcd = bid % kXcds, local = bid / kXcds;
+    const int per = T / kXcds, rem = T % kXcds;
+    const int x_start = xcd * per + (xcd < rem ? xcd : rem), x_cnt = per + (xcd < rem ? 1 : 0);
+    const int on_xcd = (nwg - xcd + kXcds - 1) / kXcds;
+    const int my_tiles = local < x_cnt ? (x_cnt - local + on_xcd - 1) / on_xcd : 0;
+    if (my_tiles == 0) return;  // the same for every wave
+    auto tile_origin = [&](int i, int64_t& m0, int64_t& n0) LLMINT8_FP8_INLINE {
+        const int t = x_start + local + i * on_xcd;
+        const int in_group = kGroupM * tp.tiles_n;
+        const int first_m = (t / in_group) * kGroupM;
+        const int gm = tp.tiles_m - first_m < kGroupM ? tp.tiles_m - first_m : kGroupM;
+        m0 = (int64_t)(first_m + (t % in_group) % gm) * BM;
+        n0 = (int64_t)((t % in_group) / gm) * BN;
+    };
+
+    // ---- operand loads: rows past M or N lie past the resources and read zero, as do all of
+    // those past the last tile (they land in slots that no stage reads)
+    auto tile_rsrc = [&](int i, __amdgpu_buffer_rsrc_t& ra, __amdgpu_buffer_rsrc_t& rb) LLMINT8_FP8_INLINE {
+        int64_t m0 = 0, n0 = 0, rows_a = 0, rows_b = 0;
+        if (i < my_tiles) {
+            tile_origin(i, m0, n0);
+            rows_a = p.M - m0 < BM ? p.M - m0 : BM;
+            rows_b = p.N - n0 < BN ? p.N - n0 : BN;
+        }
+        ra = buffer_rsrc(p.A + m0 * p.pitch, rows_a * p.pitch);
+        rb = buffer_rsrc(p.B + n0 * p.pitch, rows_b * p.pitch);
+    };
+    __amdgpu_buffer_rsrc_t ra0, rb0, ra1, rb1, ra2, rb2;
+    tile_rsrc(0, ra0, rb0);
+    tile_rsrc(1, ra1, rb1);
+    tile_rsrc(2, ra2, rb2);
+    uint32_t off[4];  // of both operands: row 8 (4 wu + j) + lane / 8, its chunk lane % 8
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + 16 * j + li < p.M ? m0 + 16 * j + li : p.M - 1;
-        a[j] = p.A + m * p.pitch + 32 * q;
-        sa[j] = p.sa + m * p.spitch;
+        const int r = 8 * (4 * wu + j) + lane / 8;
+        off[j] = (uint32_t)(r * p.pitch + (((lane & 7) ^ swz(r)) << 4));
     }
-    v4f acc[4] = {};
-    for (int64_t g = 0; g < p.pitch / 128; ++g) {
-        const v8i fb = *(const v8i*)(b + g * 128);
-        const int eb = sb[g];
+    auto slot_a = [&](int s) LLMINT8_FP8_INLINE { return smem + s * kSlotA; };
+    auto slot_b = [&](int s) LLMINT8_FP8_INLINE { return smem + 2 * kSlotA + s * kSlotB; };
+    auto issue = [&](__amdgpu_buffer_rsrc_t rs, uint8_t* slot, int k, int j) LLMINT8_FP8_INLINE {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(slot + (4 * wu + j) * 1024), 16, (int)off[j], k * BK, 0, 0);
+    };
+
+    // ---- scale dwords of four groups (past the last group of the last tile: zeros)
+    auto load_scales = [&](int i, int g4, int (&sm)[MF], int (&sn)[NS]) LLMINT8_FP8_INLINE {
+        int64_t m0 = 0, n0 = 0, rows_a = 0, rows_b = 0;
+        if (i < my_tiles) {
+            tile_origin(i, m0, n0);
+            rows_a = p.M - m0 < BM ? p.M - m0 : BM;
+            rows_b = p.N - n0 < BN ? p.N - n0 : BN;
+        }
+        const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(p.sa + m0 * p.spitch, rows_a * p.spitch);
+        const int sp = (int)p.spitch;
+        int li = lane & 15;  // opaque: the offsets are computed here, not held in registers
+        asm volatile("" : "+v"(li));
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, *(const v8i*)(a[j] + g * 128), acc[j], 0, 0, 0,
-                                                                      eb, 0, (int)sa[j][g]);
+        for (int j = 0; j < MF; ++j)
+            sm[j] = (int)__builtin_amdgcn_raw_buffer_load_b32(ra, (uint32_t)((64 * wm + 16 * j + li) * sp), 4 * g4, 0);
+        if constexpr (ROWB) {
+            const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.sb + n0 * p.spitch, rows_b * p.spitch);
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                sn[f] = (int)__builtin_amdgcn_raw_buffer_load_b32(rb, (uint32_t)((16 * NF * wn + 16 * f + li) * sp), 4 * g4, 0);
+        } else {
+            const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.sb + (n0 >> 7) * p.spitch, ((rows_b + 127) >> 7) * p.spitch);
+            sn[0] = (int)__builtin_amdgcn_raw_buffer_load_b32(rb, (uint32_t)(((16 * NF * wn) >> 7) * sp), 4 * g4, 0);
+        }
+    };
+
+    // ---- operand reads: piece f of a slot holds rows 16 f + li, chunks 2q and 2q + 1
+    const int rd = li * BK + (((2 * q) ^ swz(li)) << 4);
+    auto read = [&](const uint8_t* slot, int f) LLMINT8_FP8_INLINE {
+        const v4i lo = *(const v4i*)(slot + f * 16 * BK + rd), hi = *(const v4i*)(slot + f * 16 * BK + (rd ^ 16));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+
+    v4f acc[NF][MF];
+    v8i fm[2][MF], fn[2];      // m pieces of the stage and of the next, the next stage's first n pieces
+    int sm[MF], sn[NS], nsm[MF], nsn[NS];
+
+    // Stage kt of tile ti, in slots sa, sb; U = kt % 4.
+    auto stage = [&](auto utag, int sa, int sb, int kt, int ti) LLMINT8_FP8_INLINE {
+        constexpr int U = decltype(utag)::value, P = U & 1;
+        const int da = __builtin_amdgcn_readfirstlane(kt + 1 < nk ? 0 : 1);
+        const int ka = kt + 1 - da * nk;
+        const int db = __builtin_amdgcn_readfirstlane(kt + 2 < nk ? 0 : (kt + 2 < 2 * nk ? 1 : 2));
+        const int kb = kt + 2 - db * nk;
+        const __amdgpu_buffer_rsrc_t rs_a = pick(da, ra0, ra1, ra1), rs_b = pick(db, rb0, rb1, rb2);
+        uint8_t* to_a = slot_a(sa ^ 1);
+        uint8_t* to_b = slot_b(sb == 0 ? 2 : sb - 1);
+        const uint8_t* An = slot_a(sa ^ 1) + wm * (16 * MF * BK);
+        const uint8_t* Bc = slot_b(sb) + wn * (16 * NF * BK);
+        const uint8_t* Bn = slot_b(sb == 2 ? 0 : sb + 1) + wn * (16 * NF * BK);
+        v8i w[NF];
+        w[0] = fn[0];
+        w[1] = fn[1];
+        auto mfma_row = [&](int f) LLMINT8_FP8_INLINE {
+#pragma unroll
+            for (int j = 0; j < MF; ++j) acc[f][j] = mfma_fp8<U>(w[f], fm[P][j], acc[f][j], sn[ROWB ? f : 0], sm[j]);
+        };
+        constexpr int kPhases = NF - 2;
+#pragma unroll
+        for (int f = 0; f < kPhases; ++f) {
+#pragma unroll
+            for (int l = 0; l < 8; ++l)  // the loads, spread over the phases: A, then B
+                if (l * kPhases / 8 == f) {
+                    if (l < 4) issue(rs_a, to_a, ka, l);
+                    else issue(rs_b, to_b, kb, l - 4);
+                }
+            w[f + 2] = read(Bc, f + 2);
+            mfma_row(f);
+            __builtin_amdgcn_sched_barrier(0);
+            // the next four groups' scales: after A, before B
+            if constexpr (U == 0)
+                if (f == kPhases / 2 - 1) {
+                    const int last = 4 * (kt / 4 + 1) >= nk;
+                    load_scales(ti + last, last ? 0 : kt / 4 + 1, nsm, nsn);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        }
+        LLMINT8_FP8_WAIT_BARRIER(4);
+        fn[0] = read(Bn, 0);
+#pragma unroll
+        for (int j = 0; j < MF; ++j) fm[P ^ 1][j] = read(An, j);
+        fn[1] = read(Bn, 1);
+        mfma_row(NF - 2);
+        mfma_row(NF - 1);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    // ---- output of tile ti, through the slots its last stage freed (A: the first half of the
+    // waves, B: the second), 16 rows m of a wave at a time
+    auto output = [&](int ti, int sa, int sb) LLMINT8_FP8_INLINE {
+        int lane = tid & 63;  // opaque: nothing derived from it here is held through the stages
+        asm volatile("" : "+v"(lane));
+        const int li = lane & 15, q = lane >> 4;
+        int64_t m0, n0;
+        tile_origin(ti, m0, n0);
+        constexpr int kArea = 16 * kYPitch * 2;
+        uint16_t* ys = (uint16_t*)(wu < kWaves / 2 ? slot_a(sa) + wu * kArea : slot_b(sb) + (wu - kWaves / 2) * kArea);
+        const int64_t wm0 = m0 + 64 * wm, wn0 = n0 + 16 * NF * wn;
+        constexpr int kLanes = 2 * NF;  // 16-byte pieces of a staged row
+#pragma unroll
+        for (int j = 0; j < MF; ++j) {
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                u32x2 v;
+                v[0] = (uint32_t)from_f32<DT>(acc[f][j][0]) | ((uint32_t)from_f32<DT>(acc[f][j][1]) << 16);
+                v[1] = (uint32_t)from_f32<DT>(acc[f][j][2]) | ((uint32_t)from_f32<DT>(acc[f][j][3]) << 16);
+                *(u32x2*)(ys + li * kYPitch + 16 * f + 4 * q) = v;
+            }
+#pragma unroll
+            for (int it = 0; it < 16 * kLanes / 64; ++it) {
+                const int row = it * (64 / kLanes) + lane / kLanes, ch = lane % kLanes;
+                const u32x4 v = *(const u32x4*)(ys + row * kYPitch + 8 * ch);
+                const int64_t m = wm0 + 16 * j + row, n = wn0 + 8 * ch;
+                if (m < p.M && n < p.N) *(u32x4*)(p.Y + m * p.N + n) = v;
+            }
+        }
+    };
+
+    // ---- prologue: A of stage 0, B of stages 0 and 1, the first scales
+    load_scales(0, 0, sm, sn);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) issue(ra0, slot_a(0), 0, j);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) issue(rb0, slot_b(0), 0, j);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) issue(pick(nk > 1 ? 0 : 1, rb0, rb1, rb1), slot_b(1), nk > 1 ? 1 : 0, j);
+    LLMINT8_FP8_WAIT_BARRIER(4);
+    auto first_reads = [&](int sa, int sb) LLMINT8_FP8_INLINE {
+        fn[0] = read(slot_b(sb) + wn * (16 * NF * BK), 0);
+#pragma unroll
+        for (int j = 0; j < MF; ++j) fm[0][j] = read(slot_a(sa) + wm * (16 * MF * BK), j);
+        fn[1] = read(slot_b(sb) + wn * (16 * NF * BK), 1);
+    };
+    first_reads(0, 0);
+    int sa = 0, sb = 0;
+    auto advance = [&]() LLMINT8_FP8_INLINE {
+        sa ^= 1;
+        sb = sb == 2 ? 0 : sb + 1;
+    };
+    auto next_scales = [&]() LLMINT8_FP8_INLINE {
+#pragma unroll
+        for (int j = 0; j < MF; ++j) sm[j] = nsm[j];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) sn[j] = nsn[j];
+    };
+    for (int ti = 0; ti < my_tiles; ++ti) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int j = 0; j < MF; ++j) acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        int kt = 0;
+        for (; kt + 4 <= nk; kt += 4) {
+            stage(std::integral_constant<int, 0>{}, sa, sb, kt, ti);
+            advance();
+            stage(std::integral_constant<int, 1>{}, sa, sb, kt + 1, ti);
+            advance();
+            stage(std::integral_constant<int, 2>{}, sa, sb, kt + 2, ti);
+            advance();
+            stage(std::integral_constant<int, 3>{}, sa, sb, kt + 3, ti);
+            advance();
+            next_scales();
+        }
+        if (kt < nk) {
+            stage(std::integral_constant<int, 0>{}, sa, sb, kt, ti);
+            advance();
+            if (kt + 1 < nk) {
+                stage(std::integral_constant<int, 1>{}, sa, sb, kt + 1, ti);
+                advance();
+            }
+            if (kt + 2 < nk) {
+                stage(std::integral_constant<int, 2>{}, sa, sb, kt + 2, ti);
+                advance();
+            }
+            next_scales();
+        }
+        // the slots of the stage before (sa, sb): freed by it
+        output(ti, sa ^ 1, sb == 0 ? 2 : sb - 1);
+        if (ti + 1 < my_tiles) {
+            ra0 = ra1;
+            rb0 = rb1;
+            ra1 = ra2;
+            rb1 = rb2;
+            tile_rsrc(ti + 3, ra2, rb2);
+            if (nk & 1) {
+#pragma unroll
+                for (int j = 0; j < MF; ++j) fm[0][j] = fm[1][j];
+            }
+            // every wave is done with its staging area: the next stage's loads go there
+            __builtin_amdgcn_s_waitcnt(0xC07F);
+            __builtin_amdgcn_s_barrier();
+        }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + 16 * j + li;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (m < p.M && n0 + 4 * q + e < p.N) p.Y[m * p.N + n0 + 4 * q + e] = from_f32<DT>(acc[j][e]);
-    }
+    // no load into this workgroup's LDS may outlive it
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+template <int DT, int WM, int WN, int NF, bool ROWB>
+hipError_t tiled_launch(const Fp8GemmArgs& a, hipStream_t stream) {
+    constexpr int BM = 16 * MF * WM, BN = 16 * NF * WN;
+    TiledParams p{a, (int)ceil_div(a.M, BM), (int)ceil_div(a.N, BN)};
+    int dev = 0, cus = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess) return e;
+    const int64_t T = (int64_t)p.tiles_m * p.tiles_n, G = (int64_t)(cus > 0 ? cus : 1) * (8 / (WM * WN));
+    fp8_tiled_kernel<DT, WM, WN, NF, ROWB><<<(unsigned)(T < G ? T : G), 64 * WM * WN, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+template <int WM, int WN, int NF>
+hipError_t tiled(int dt, const Fp8GemmArgs& a, hipStream_t stream) {
+    if (a.bshift == 0)
+        return dt == F16 ? tiled_launch<F16, WM, WN, NF, true>(a, stream) : tiled_launch<BF16, WM, WN, NF, true>(a, stream);
+    return dt == F16 ? tiled_launch<F16, WM, WN, NF, false>(a, stream) : tiled_launch<BF16, WM, WN, NF, false>(a, stream);
 }
 
 }  // namespace
 
-hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& p, hipStream_t stream) {
-    if (p.M == 0 || p.N == 0) return hipSuccess;
-    const dim3 g((unsigned)ceil_div(p.N, 64), (unsigned)ceil_div(p.M, 64));
-    if (dt == F16) fp8_gemm_kernel<F16><<<g, 256, 0, stream>>>(p);
-    else fp8_gemm_kernel<BF16><<<g, 256, 0, stream>>>(p);
-    return hipGetLastError();
+hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& a, hipStream_t stream) {
+    if (a.M == 0 || a.N == 0) return hipSuccess;
+    // 256 x 256 tiles where they fill the compute units, else 128 x 128
+    if (ceil_div(a.M, 256) * ceil_div(a.N, 256) >= 256) return tiled<4, 2, 8>(dt, a, stream);
+    return tiled<2, 2, 4>(dt, a, stream);
 }
 
 }  // namespace llmint8

@@ -117,6 +117,33 @@ def test_matmul_exact_lattice(M, K, N, dt):
     assert torch.equal(Y.cpu(), want)
 
 
+# many tiles, several per workgroup, with few and many groups along K (the sums of the lattice are
+# exact in 64 bits on the GPU too)
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M,K,N", [(4100, 16, 4104), (4100, 128, 4104), (4100, 256, 4104), (4100, 272, 4360), (4100, 512, 4104),
+                                   (4100, 640, 4104), (5000, 1040, 4104), (3800, 16, 4000), (3800, 144, 4000),
+                                   (3800, 400, 4000), (3800, 1664, 4000), (2049, 912, 8200)])
+def test_matmul_many_tiles(M, K, N, dt):
+    print(f"\n[case] matmul many tiles {dt} {M}x{K}x{N}", flush=True)
+    g = gen(M + K + N)
+    X = lattice(g, M, K, dt=dt, spread=3).cuda()
+    W = lattice(g, N, K, dt=dt, spread=3).t().contiguous().cuda()
+    Y = lm.fp8_matmul_block(X, *lm.fp8_quantize_weight_block(W))
+    assert torch.equal(Y, (X.double() @ W.double()).float().to(dt))
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M,K,N", [(130, 4112, 4104), (700, 4112, 4104), (4100, 4112, 520), (520, 1040, 8200)])
+def test_backward_many_tiles(M, K, N, dt):
+    print(f"\n[case] backward many tiles {dt} {M}x{K}x{N}", flush=True)
+    g = gen(M + K + N)
+    X, W, dY = (lattice(g, *sh, dt=dt).cuda() for sh in ((M, K), (K, N), (M, N)))
+    _, _, WqT, sT = lm.fp8_quantize_weight_block(W, transposed=True)
+    dX, dW = lm.fp8_matmul_block_backward(dY, X, WqT, sT)
+    assert torch.equal(dX, (dY.double() @ W.double().t()).float().to(dt))
+    assert torch.equal(dW, (X.double().t() @ dY.double()).float().to(dt))
+
+
 @pytest.mark.parametrize("dt", DTS)
 @pytest.mark.parametrize("M,K,N", SHAPES)
 def test_matmul_random(M, K, N, dt):
