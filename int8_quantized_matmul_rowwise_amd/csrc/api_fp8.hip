@@ -78,7 +78,7 @@ Fp8Layout fp8_layout(int64_t M, int64_t K, int64_t N) {
     Fp8Layout L;
     L.xq = 0;
     L.s_x = align_up(code_bytes(M, K));
-    L.total = align_up(L.s_x + scale_bytes(M, K));
+    L.total = align_up(L.s_x + (size_t)fp8_row_scale_bytes(M, K));
     return L;
 }
 
@@ -116,7 +116,7 @@ LLMINT8_API int fp8_matmul_block(const void* X, int64_t M, int64_t K, int dtype,
     hipError_t e = stage("fp8_rows", [&] { return launch_fp8_rows(dtype, X, M, K, ws + L.xq, ws + L.s_x, st); });
     if (e == hipSuccess)
         e = stage("fp8_gemm", [&] {
-            const Fp8GemmArgs a{ws + L.xq, Wq, M, N, fp8_pitch(K), ws + L.s_x, w_scale, fp8_scale_pitch_of(K), 7, (uint16_t*)Y};
+            const Fp8GemmArgs a{ws + L.xq, Wq, M, N, fp8_pitch(K), ws + L.s_x, w_scale, fp8_scale_pitch_of(K), (uint16_t*)Y};
             return launch_fp8_gemm(dtype, a, st);
         });
     return hip_status(e);
@@ -139,11 +139,11 @@ Fp8BackwardLayout fp8_backward_layout(int64_t M, int64_t K, int64_t N, bool dx, 
         return at;
     };
     L.dyq = take(dx ? code_bytes(M, N) : 0);
-    L.s_dy = take(dx ? scale_bytes(M, N) : 0);
+    L.s_dy = take(dx ? (size_t)fp8_row_scale_bytes(M, N) : 0);
     L.dyt = take(dw ? code_bytes(N, M) : 0);
-    L.s_dyt = take(dw ? scale_bytes(N, M) : 0);
+    L.s_dyt = take(dw ? (size_t)fp8_row_scale_bytes(N, M) : 0);
     L.xt = take(dw ? code_bytes(K, M) : 0);
-    L.s_xt = take(dw ? scale_bytes(K, M) : 0);
+    L.s_xt = take(dw ? (size_t)fp8_row_scale_bytes(K, M) : 0);
     L.total = off;
     return L;
 }
@@ -196,13 +196,13 @@ LLMINT8_API int fp8_matmul_block_backward(const void* dY, const void* X, int64_t
         e = stage("fp8_cols_x", [&] { return launch_fp8_cols(dtype, X, M, K, ws + L.xt, ws + L.s_xt, nullptr, nullptr, st); });
     if (e == hipSuccess && out_x)
         e = sum_x ? stage("fp8_gemm_dx", [&] {
-                        const Fp8GemmArgs a{ws + L.dyq, WqT, M, K, fp8_pitch(N), ws + L.s_dy, wT_scale, fp8_scale_pitch_of(N), 7, (uint16_t*)dX};
+                        const Fp8GemmArgs a{ws + L.dyq, WqT, M, K, fp8_pitch(N), ws + L.s_dy, wT_scale, fp8_scale_pitch_of(N), (uint16_t*)dX};
                         return launch_fp8_gemm(dtype, a, st);
                     })
                   : stage("fill_zero", [&] { return launch_fill_zero((float*)dX, M * K / 2, st); });
     if (e == hipSuccess && out_w)
         e = sum_w ? stage("fp8_gemm_dw", [&] {
-                        const Fp8GemmArgs a{ws + L.xt, ws + L.dyt, K, N, fp8_pitch(M), ws + L.s_xt, ws + L.s_dyt, fp8_scale_pitch_of(M), 0, (uint16_t*)dW};
+                        const Fp8GemmArgs a{ws + L.xt, ws + L.dyt, K, N, fp8_pitch(M), ws + L.s_xt, ws + L.s_dyt, 0, (uint16_t*)dW};
                         return launch_fp8_gemm(dtype, a, st);
                     })
                   : stage("fill_zero", [&] { return launch_fill_zero((float*)dW, K * N / 2, st); });

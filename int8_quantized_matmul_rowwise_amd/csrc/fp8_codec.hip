@@ -11,7 +11,7 @@
 //   The transposed codes pass through LDS, where piece p (8 rows) of a column sits at piece
 //   p ^ (column / 8 % 16): the 8-byte writes of the 16 lanes of a row and the 16-byte reads of
 //   a column then spread over all banks.
-// Code rows are padded with zeros to a multiple of 128, scale rows with zeros to one of 4.
+// Code rows are padded with zeros to a multiple of 128, a weight's scale rows to one of 4.
 #include "fp8_common.hpp"
 #include "launch.hpp"
 
@@ -22,11 +22,11 @@ namespace {
 template <int DT>
 __global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t K,
                                                        uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
-    const int64_t kp = fp8_pitch(K), sp = fp8_scale_pitch_of(K);
-    const int64_t total = M * sp;  // every byte of the scale rows, those past the last group too
+    const int64_t kp = fp8_pitch(K), ng = ceil_div(K, 128);
+    const int64_t total = M * ng;
     const int sl = threadIdx.x & 15;
     for (int64_t b = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4; b < total; b += (int64_t)gridDim.x * 16) {
-        const int64_t row = b / sp, g = b - row * sp;
+        const int64_t row = b / ng, g = b - row * ng;
         const int64_t k = g * 128 + 8 * sl;
         u32x4 v = {0u, 0u, 0u, 0u};
         if (k < K) v = *(const u32x4*)(X + row * K + k);  // K is a multiple of 8
@@ -37,8 +37,8 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* __restric
             m = m > o ? m : o;
         }
         const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)m));
-        if (k < kp) *(u32x2*)(q + row * kp + k) = e4m3x8<DT>(v, e8m0_inverse(e));
-        if (sl == 0) s[b] = (uint8_t)e;
+        *(u32x2*)(q + row * kp + k) = e4m3x8<DT>(v, e8m0_value(e));
+        if (sl == 0) s[fp8_row_scale_at(row, g, M)] = (uint8_t)e;
     }
 }
 
@@ -46,9 +46,9 @@ struct TileParams {
     const uint16_t* A;  // R x C, row-major
     int64_t R, C;
     uint8_t* q;   // codes in order: R x pitch(C), or NULL
-    uint8_t* s;   // their scales: BLOCK ceil(R/128) x sp(C), ROWS R x sp(C)
+    uint8_t* s;   // their scales: BLOCK ceil(R/128) x sp(C), ROWS fp8_row_scale_at
     uint8_t* qt;  // codes transposed: C x pitch(R)
-    uint8_t* st;  // their scales: BLOCK ceil(C/128) x sp(R), COLS C x sp(R)
+    uint8_t* st;  // their scales: BLOCK ceil(C/128) x sp(R), COLS fp8_row_scale_at
 };
 
 // MODE 0: BLOCK, transposed codes; 1: BLOCK, both; 2: COLS; 3: COLS and ROWS
@@ -85,18 +85,13 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(TileParams p) {
             const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)m));
             const int64_t r = r0 + 8 * rr + u;
             if (r < p.R) {
-                *(u32x2*)(p.q + r * cpitch + c) = e4m3x8<DT>(v[u], e8m0_inverse(e));
-                if (cc == 0) {
-                    p.s[r * csp + tc] = (uint8_t)e;
-                    if (last_c)
-                        for (int64_t i = tc + 1; i < csp; ++i) p.s[r * csp + i] = 0;
-                }
+                *(u32x2*)(p.q + r * cpitch + c) = e4m3x8<DT>(v[u], e8m0_value(e));
+                if (cc == 0) p.s[fp8_row_scale_at(r, tc, p.R)] = (uint8_t)e;
             }
         }
     }
     // ---- the scales of the transposed codes: largest patterns of the tile or of its columns
-    float inv[8];
-    uint32_t byte[8];
+    float sv[8];
     if constexpr (BLOCK) {
         uint32_t m = 0;
 #pragma unroll
@@ -110,19 +105,15 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(TileParams p) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = m > red[i][0] ? m : red[i][0];
-        byte[0] = e8m0_of(to_f32<DT>((uint16_t)m));
-        inv[0] = e8m0_inverse(byte[0]);
+        const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)m));
 #pragma unroll
-        for (int j = 1; j < 8; ++j) {
-            inv[j] = inv[0];
-            byte[j] = byte[0];
-        }
+        for (int j = 0; j < 8; ++j) sv[j] = e8m0_value(e);
         if (tid == 0) {
-            p.st[tc * rsp + tr] = (uint8_t)byte[0];
+            p.st[tc * rsp + tr] = (uint8_t)e;
             if (last_r)
                 for (int64_t i = tr + 1; i < rsp; ++i) p.st[tc * rsp + i] = 0;
             if constexpr (MODE == 1) {
-                p.s[tr * csp + tc] = (uint8_t)byte[0];
+                p.s[tr * csp + tc] = (uint8_t)e;
                 if (last_c)
                     for (int64_t i = tc + 1; i < csp; ++i) p.s[tr * csp + i] = 0;
             }
@@ -152,32 +143,26 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(TileParams p) {
                 const uint32_t o = red[i][8 * cc + j];
                 m[j] = m[j] > o ? m[j] : o;
             }
-            byte[j] = e8m0_of(to_f32<DT>((uint16_t)m[j]));
-            inv[j] = e8m0_inverse(byte[j]);
-            if (rr == 0 && c + j < p.C) {
-                p.st[(c + j) * rsp + tr] = (uint8_t)byte[j];
-                if (last_r)
-                    for (int64_t i = tr + 1; i < rsp; ++i) p.st[(c + j) * rsp + i] = 0;
-            }
+            const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)m[j]));
+            sv[j] = e8m0_value(e);
+            if (rr == 0 && c + j < p.C) p.st[fp8_row_scale_at(c + j, tr, p.C)] = (uint8_t)e;
         }
     }
     if constexpr (MODE == 1) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const int64_t r = r0 + 8 * rr + u;
-            if (r < p.R) *(u32x2*)(p.q + r * cpitch + c) = e4m3x8<DT>(v[u], inv[0]);
+            if (r < p.R) *(u32x2*)(p.q + r * cpitch + c) = e4m3x8<DT>(v[u], sv[0]);
         }
     }
     // ---- codes transposed: 8 rows of a column are 8 bytes of its output row
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        float f[8];
+        u32x4 col;  // the column's 8 rows
 #pragma unroll
-        for (int u = 0; u < 8; ++u) f[u] = __fmul_rn(to_f32<DT>((uint16_t)(v[u][j >> 1] >> (16 * (j & 1)))), inv[j]);
-        u32x2 q;
-        q[0] = e4m3x4(f[0], f[1], f[2], f[3]);
-        q[1] = e4m3x4(f[4], f[5], f[6], f[7]);
-        *(u32x2*)(tile + (8 * cc + j) * 128 + ((rr ^ cc) << 3)) = q;
+        for (int u = 0; u < 4; ++u)  // v_perm: bytes 0-3 of the second operand, 4-7 of the first
+            col[u] = __builtin_amdgcn_perm(v[2 * u + 1][j >> 1], v[2 * u][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+        *(u32x2*)(tile + (8 * cc + j) * 128 + ((rr ^ cc) << 3)) = e4m3x8<DT>(col, sv[j]);
     }
     __syncthreads();
 #pragma unroll

@@ -17,23 +17,25 @@ constexpr int kFp8Block = 128;  // values of a group along each axis
 __host__ __device__ constexpr int64_t fp8_pitch(int64_t n) { return round_up(n, 128); }
 __host__ __device__ constexpr int64_t fp8_scale_pitch_of(int64_t n) { return round_up(ceil_div(n, 128), 4); }
 
+// The scales of coded activations, one per row and group, as the product kernels take them: for
+// each group, for each 64 rows, a dword per row mod 16 that holds the bytes of the four rows
+// 16 apart -- the matrix instruction picks a byte of its scale operand, so one dword per lane
+// scales four pieces of 16 rows.  Bytes of rows past the last are not written.
+__host__ __device__ constexpr int64_t fp8_row_scale_at(int64_t r, int64_t g, int64_t rows) {
+    return (g * ceil_div(rows, 64) + (r >> 6)) * 64 + (r & 15) * 4 + ((r >> 4) & 3);
+}
+__host__ __device__ constexpr int64_t fp8_row_scale_bytes(int64_t rows, int64_t sum) {
+    return ceil_div(sum, 128) * round_up(rows, 64);
+}
+
 // The scale's byte from the largest magnitude: 448 = 1.75 * 2^8, so the exponent of a is
 // raised by one where its mantissa is above 1.75, and lowered by 8.
 __device__ __forceinline__ uint32_t e8m0_of(float a) {
     const int b = (int)((__builtin_bit_cast(uint32_t, a) + 0x1fffffu) >> 23) - 8;
     return b > 0 ? (uint32_t)b : 0u;
 }
-// 1 / s (a byte is at most 248: the exponent stays in range), and s itself
-__device__ __forceinline__ float e8m0_inverse(uint32_t b) { return __builtin_bit_cast(float, (254u - b) << 23); }
 __device__ __forceinline__ float e8m0_value(uint32_t b) {
     return __builtin_bit_cast(float, b ? b << 23 : 0x00400000u);
-}
-
-// Four codes, the first in the low byte.  |v| <= 448 or not finite (which gives NaN).
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-    int p = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    p = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, p, true);
-    return (uint32_t)p;
 }
 
 // Eight 16-bit values (one 16-byte piece): their magnitudes as patterns, whose unsigned order
@@ -49,14 +51,24 @@ __device__ __forceinline__ uint32_t max_pattern(const u32x4& v, uint32_t m) {
     return m;
 }
 
+// Codes of two 16-bit values (a pattern pair) at the scale's value s, into half HI of `old`: the
+// instruction divides by the power of two and rounds once (not finite: NaN).
+template <int DT, bool HI>
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t old, uint32_t v, float s) {
+    typedef short v2s __attribute__((ext_vector_type(2)));
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    v2s o = __builtin_bit_cast(v2s, old);
+    if constexpr (DT == F16) o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(o, __builtin_bit_cast(v2h, v), s, HI);
+    else o = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(o, __builtin_bit_cast(v2bf, v), s, HI);
+    return __builtin_bit_cast(uint32_t, o);
+}
+
 template <int DT>
-__device__ __forceinline__ u32x2 e4m3x8(const u32x4& v, float inv) {
-    float f[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(to_f32<DT>((uint16_t)(v[k >> 1] >> (16 * (k & 1)))), inv);
+__device__ __forceinline__ u32x2 e4m3x8(const u32x4& v, float s) {
     u32x2 q;
-    q[0] = e4m3x4(f[0], f[1], f[2], f[3]);
-    q[1] = e4m3x4(f[4], f[5], f[6], f[7]);
+    q[0] = e4m3x2<DT, true>(e4m3x2<DT, false>(0u, v[0], s), v[1], s);
+    q[1] = e4m3x2<DT, true>(e4m3x2<DT, false>(0u, v[2], s), v[3], s);
     return q;
 }
 

@@ -1,6 +1,6 @@
 // Products of e4m3 codes with power-of-two block scales:
 //   Y[m,n] = RN_T( sum_g 2^(ea[m,g] + eb[n,g]) sum_{k in g} a[m,k] b[n,k] ),
-// g over groups of 128 along K; ea per row, eb per row (n >> 0) or per 128 rows (n >> 7).
+// g over groups of 128 along K; ea per row, eb per row or per 128 rows.
 // The forward product, the input gradient (b: the transposed weight codes) and the weight
 // gradient (both operands per row, the sum over the tokens) are all this product.
 //
@@ -11,15 +11,16 @@
 // Tiled kernel: BM x BN outputs per workgroup, waves in WM x WN, each 64 rows m (MF = 4 pieces
 // of 16) by 16 NF columns n.  A stage is one group: a 128-byte line per row of each operand,
 // loaded straight into LDS (16-byte chunk c of row r at chunk c ^ swz(r), so that 8 lanes
-// reading one chunk of 8 rows meet all banks), A one stage ahead (2 slots) and B two (3 slots).
+// reading one chunk of 8 rows meet all banks), B two stages ahead (3 slots), A as soon as the
+// stage two before is read (2 slots).
 // Within a stage the n pieces stream from LDS two ahead of their MFMAs, the m pieces of the
 // stage stay in registers.  The workgroup meets once per stage, after the stage's last LDS read
 // and before the MFMAs of its last two n pieces; under those the next stage's m pieces and first
 // n pieces are read.  The barrier waits for all but the newest B loads (counted), so the loads
 // in flight are never drained.
-// The scales come as dwords, one per row and four groups (instruction operands that select one
-// of four bytes): the stages are unrolled by four, and the next four groups' dwords are loaded
-// at the first of them.
+// The scales of a row-scaled operand come as one dword per four pieces of 16 rows (the layout is
+// the instruction's choice of a byte), one load per stage, a stage ahead; a block-scaled B's is
+// one byte for all of a wave's columns.
 // Persistent over the XCD's run of tiles, as the int8 product kernels: the next tile's first
 // loads are in flight during a tile's last stages and its output.
 #include <type_traits>
@@ -48,6 +49,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t pick(int d, __amdgpu_buffer_rs
     return d == 0 ? a : (d == 1 ? b : c);
 }
 
+__device__ __forceinline__ int pick(int d, int a, int b) { return d == 0 ? a : b; }
+
 __host__ __device__ constexpr int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 #define LLMINT8_FP8_INLINE __attribute__((always_inline))
@@ -63,10 +66,15 @@ struct TiledParams {
     int tiles_m, tiles_n;
 };
 
-// U: the byte of the scale dwords (the group's place among four)
-template <int U>
-__device__ __forceinline__ v4f mfma_fp8(const v8i& n, const v8i& m, const v4f& c, int sn, int sm) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(n, m, c, 0, 0, U, sn, U, sm);
+// the instruction with bytes bn, bm of the scale dwords (constants after unrolling)
+__device__ __forceinline__ v4f mfma_fp8(const v8i& n, const v8i& m, const v4f& c, int sn, int bn, int sm, int bm) {
+#define LLMINT8_MFMA(BN_, BM_) \
+    if (bn == BN_ && bm == BM_) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(n, m, c, 0, 0, BN_, sn, BM_, sm);
+#define LLMINT8_MFMA4(BN_) LLMINT8_MFMA(BN_, 0) LLMINT8_MFMA(BN_, 1) LLMINT8_MFMA(BN_, 2) LLMINT8_MFMA(BN_, 3)
+    LLMINT8_MFMA4(0) LLMINT8_MFMA4(1) LLMINT8_MFMA4(2) LLMINT8_MFMA4(3)
+#undef LLMINT8_MFMA4
+#undef LLMINT8_MFMA
+    return c;
 }
 
 // ROWB: B has a scale per row (else per 128 rows, one for a wave's columns)
@@ -76,10 +84,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
     constexpr int BM = 16 * MF * WM, BN = 16 * NF * WN;
     constexpr int kSlotA = BM * BK, kSlotB = BN * BK;
     constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = BN / 8 / kWaves;
-    constexpr int NS = ROWB ? NF : 1;  // scale dwords of a wave's columns
-    constexpr int kYPitch = 16 * NF + 8;  // staged output row, 16-bit elements
+    constexpr int NS = ROWB ? NF / 4 : 1;  // scale dwords of a wave's columns
+    static_assert(NF % 4 == 0 && 16 * MF == 64, "a scale dword serves four pieces");
     static_assert(kLoadsA == 4 && kLoadsB == 4, "the barrier's wait leaves the four newest loads (B) in flight");
-    static_assert((kWaves / 2) * 16 * kYPitch * 2 <= kSlotA && (kWaves / 2) * 16 * kYPitch * 2 <= kSlotB, "staging");
+    static_assert(kWaves * 16 * 32 * NF <= kSlotB, "output staging");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kSlotA + 3 * kSlotB];
     const Fp8GemmArgs& p = tp.a;
     const int tid = threadIdx.x, lane = tid & 63, wu = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -134,29 +142,37 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(slot + (4 * wu + j) * 1024), 16, (int)off[j], k * BK, 0, 0);
     };
 
-    // ---- scale dwords of four groups (past the last group of the last tile: zeros)
-    auto load_scales = [&](int i, int g4, int (&sm)[MF], int (&sn)[NS]) LLMINT8_FP8_INLINE {
+    // ---- the scales of a stage: offsets and bytes of this tile's and the next tile's, held as
+    // scalars (past the last tile: none, the loads return zeros)
+    const int ta = (int)round_up(p.M, 64), tb = ROWB ? (int)round_up(p.N, 64) : 0;  // bytes of a group's scales
+    int a_at0, a_at1, a_n0, a_n1, b_at0, b_at1, b_n0, b_n1;
+    auto scale_range = [&](int i, int& a_at, int& a_n, int& b_at, int& b_n) LLMINT8_FP8_INLINE {
         int64_t m0 = 0, n0 = 0, rows_a = 0, rows_b = 0;
         if (i < my_tiles) {
             tile_origin(i, m0, n0);
             rows_a = p.M - m0 < BM ? p.M - m0 : BM;
             rows_b = p.N - n0 < BN ? p.N - n0 : BN;
         }
-        const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(p.sa + m0 * p.spitch, rows_a * p.spitch);
-        const int sp = (int)p.spitch;
+        a_at = (int)m0;
+        a_n = (int)round_up(rows_a, 64);
+        b_at = ROWB ? (int)n0 : (int)(n0 >> 7);
+        b_n = ROWB ? (int)round_up(rows_b, 64) : (int)ceil_div(rows_b, 128);
+    };
+    scale_range(0, a_at0, a_n0, b_at0, b_n0);
+    scale_range(1, a_at1, a_n1, b_at1, b_n1);
+    auto load_scales = [&](int next, int k, int& sm, int (&sn)[NS]) LLMINT8_FP8_INLINE {
         int li = lane & 15;  // opaque: the offsets are computed here, not held in registers
         asm volatile("" : "+v"(li));
-#pragma unroll
-        for (int j = 0; j < MF; ++j)
-            sm[j] = (int)__builtin_amdgcn_raw_buffer_load_b32(ra, (uint32_t)((64 * wm + 16 * j + li) * sp), 4 * g4, 0);
+        const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(p.sa + (int64_t)k * ta + pick(next, a_at0, a_at1), pick(next, a_n0, a_n1));
+        sm = (int)__builtin_amdgcn_raw_buffer_load_b32(ra, (uint32_t)(64 * wm + 4 * li), 0, 0);
         if constexpr (ROWB) {
-            const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.sb + n0 * p.spitch, rows_b * p.spitch);
+            const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.sb + (int64_t)k * tb + pick(next, b_at0, b_at1), pick(next, b_n0, b_n1));
 #pragma unroll
-            for (int f = 0; f < NF; ++f)
-                sn[f] = (int)__builtin_amdgcn_raw_buffer_load_b32(rb, (uint32_t)((16 * NF * wn + 16 * f + li) * sp), 4 * g4, 0);
+            for (int f = 0; f < NS; ++f)
+                sn[f] = (int)__builtin_amdgcn_raw_buffer_load_b32(rb, (uint32_t)(16 * NF * wn + 64 * f + 4 * li), 0, 0);
         } else {
-            const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.sb + (n0 >> 7) * p.spitch, ((rows_b + 127) >> 7) * p.spitch);
-            sn[0] = (int)__builtin_amdgcn_raw_buffer_load_b32(rb, (uint32_t)(((16 * NF * wn) >> 7) * sp), 4 * g4, 0);
+            const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.sb + pick(next, b_at0, b_at1) * p.spitch, pick(next, b_n0, b_n1) * p.spitch);
+            sn[0] = (int)__builtin_amdgcn_raw_buffer_load_b8(rb, (uint32_t)(((16 * NF * wn) >> 7) * (int)p.spitch + k), 0, 0);
         }
     };
 
@@ -169,17 +185,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
 
     v4f acc[NF][MF];
     v8i fm[2][MF], fn[2];      // m pieces of the stage and of the next, the next stage's first n pieces
-    int sm[MF], sn[NS], nsm[MF], nsn[NS];
+    int sm, sn[NS], nsm, nsn[NS];  // scales of the stage and of the next
 
-    // Stage kt of tile ti, in slots sa, sb; U = kt % 4.
-    auto stage = [&](auto utag, int sa, int sb, int kt, int ti) LLMINT8_FP8_INLINE {
-        constexpr int U = decltype(utag)::value, P = U & 1;
-        const int da = __builtin_amdgcn_readfirstlane(kt + 1 < nk ? 0 : 1);
-        const int ka = kt + 1 - da * nk;
-        const int db = __builtin_amdgcn_readfirstlane(kt + 2 < nk ? 0 : (kt + 2 < 2 * nk ? 1 : 2));
-        const int kb = kt + 2 - db * nk;
-        const __amdgpu_buffer_rsrc_t rs_a = pick(da, ra0, ra1, ra1), rs_b = pick(db, rb0, rb1, rb2);
-        uint8_t* to_a = slot_a(sa ^ 1);
+    // Stage kt of a tile, in slots sa, sb; P = kt % 2.
+    auto stage = [&](auto ptag, int sa, int sb, int kt) LLMINT8_FP8_INLINE {
+        constexpr int P = decltype(ptag)::value;
+        // both operands' loads are two stages ahead: stage k2 of the tile d ahead
+        const int d = __builtin_amdgcn_readfirstlane(kt + 2 < nk ? 0 : (kt + 2 < 2 * nk ? 1 : 2));
+        const int k2 = kt + 2 - d * nk;
+        const __amdgpu_buffer_rsrc_t rs_a = pick(d, ra0, ra1, ra2), rs_b = pick(d, rb0, rb1, rb2);
         uint8_t* to_b = slot_b(sb == 0 ? 2 : sb - 1);
         const uint8_t* An = slot_a(sa ^ 1) + wm * (16 * MF * BK);
         const uint8_t* Bc = slot_b(sb) + wn * (16 * NF * BK);
@@ -189,50 +203,53 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
         w[1] = fn[1];
         auto mfma_row = [&](int f) LLMINT8_FP8_INLINE {
 #pragma unroll
-            for (int j = 0; j < MF; ++j) acc[f][j] = mfma_fp8<U>(w[f], fm[P][j], acc[f][j], sn[ROWB ? f : 0], sm[j]);
+            for (int j = 0; j < MF; ++j) acc[f][j] = mfma_fp8(w[f], fm[P][j], acc[f][j], sn[ROWB ? f / 4 : 0], ROWB ? f % 4 : 0, sm, j);
         };
+        // the next stage's scales (before B's loads, which the barrier leaves in flight)
+        const int next = __builtin_amdgcn_readfirstlane(kt + 1 < nk ? 0 : 1);
+        load_scales(next, next ? 0 : kt + 1, nsm, nsn);
+        __builtin_amdgcn_sched_barrier(0);
         constexpr int kPhases = NF - 2;
 #pragma unroll
         for (int f = 0; f < kPhases; ++f) {
 #pragma unroll
-            for (int l = 0; l < 8; ++l)  // the loads, spread over the phases: A, then B
-                if (l * kPhases / 8 == f) {
-                    if (l < 4) issue(rs_a, to_a, ka, l);
-                    else issue(rs_b, to_b, kb, l - 4);
-                }
+            for (int l = 0; l < 4; ++l)
+                if (l * kPhases / 4 == f) issue(rs_b, to_b, k2, l);
             w[f + 2] = read(Bc, f + 2);
             mfma_row(f);
             __builtin_amdgcn_sched_barrier(0);
-            // the next four groups' scales: after A, before B
-            if constexpr (U == 0)
-                if (f == kPhases / 2 - 1) {
-                    const int last = 4 * (kt / 4 + 1) >= nk;
-                    load_scales(ti + last, last ? 0 : kt / 4 + 1, nsm, nsn);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
         }
         LLMINT8_FP8_WAIT_BARRIER(4);
         fn[0] = read(Bn, 0);
+        fm[P ^ 1][0] = read(An, 0);
+        fm[P ^ 1][1] = read(An, 1);
 #pragma unroll
-        for (int j = 0; j < MF; ++j) fm[P ^ 1][j] = read(An, j);
-        fn[1] = read(Bn, 1);
+        for (int l = 0; l < 2; ++l) issue(rs_a, slot_a(sa), k2, l);
         mfma_row(NF - 2);
+        __builtin_amdgcn_sched_barrier(0);
+        fm[P ^ 1][2] = read(An, 2);
+        fm[P ^ 1][3] = read(An, 3);
+        fn[1] = read(Bn, 1);
+#pragma unroll
+        for (int l = 2; l < 4; ++l) issue(rs_a, slot_a(sa), k2, l);
         mfma_row(NF - 1);
         __builtin_amdgcn_sched_barrier(0);
+        sm = nsm;
+#pragma unroll
+        for (int f = 0; f < NS; ++f) sn[f] = nsn[f];
     };
 
-    // ---- output of tile ti, through the slots its last stage freed (A: the first half of the
-    // waves, B: the second), 16 rows m of a wave at a time
-    auto output = [&](int ti, int sa, int sb) LLMINT8_FP8_INLINE {
+    // ---- output of tile ti, through the B slot its last stage freed, 16 rows m of a wave at a
+    // time: row r's 16-byte piece c sits at piece c ^ r (mod the pieces of a row)
+    auto output = [&](int ti, int sb) LLMINT8_FP8_INLINE {
         int lane = tid & 63;  // opaque: nothing derived from it here is held through the stages
         asm volatile("" : "+v"(lane));
         const int li = lane & 15, q = lane >> 4;
         int64_t m0, n0;
         tile_origin(ti, m0, n0);
-        constexpr int kArea = 16 * kYPitch * 2;
-        uint16_t* ys = (uint16_t*)(wu < kWaves / 2 ? slot_a(sa) + wu * kArea : slot_b(sb) + (wu - kWaves / 2) * kArea);
+        constexpr int kPieces = 2 * NF;
+        uint8_t* ys = slot_b(sb) + wu * (16 * 16 * kPieces);
         const int64_t wm0 = m0 + 64 * wm, wn0 = n0 + 16 * NF * wn;
-        constexpr int kLanes = 2 * NF;  // 16-byte pieces of a staged row
 #pragma unroll
         for (int j = 0; j < MF; ++j) {
 #pragma unroll
@@ -240,27 +257,31 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
                 u32x2 v;
                 v[0] = (uint32_t)from_f32<DT>(acc[f][j][0]) | ((uint32_t)from_f32<DT>(acc[f][j][1]) << 16);
                 v[1] = (uint32_t)from_f32<DT>(acc[f][j][2]) | ((uint32_t)from_f32<DT>(acc[f][j][3]) << 16);
-                *(u32x2*)(ys + li * kYPitch + 16 * f + 4 * q) = v;
+                const int c = (2 * f + (q >> 1)) ^ (li & (kPieces - 1));
+                *(u32x2*)(ys + (li * kPieces + c) * 16 + 8 * (q & 1)) = v;
             }
 #pragma unroll
-            for (int it = 0; it < 16 * kLanes / 64; ++it) {
-                const int row = it * (64 / kLanes) + lane / kLanes, ch = lane % kLanes;
-                const u32x4 v = *(const u32x4*)(ys + row * kYPitch + 8 * ch);
+            for (int it = 0; it < 16 * kPieces / 64; ++it) {
+                const int row = it * (64 / kPieces) + lane / kPieces, ch = lane % kPieces;
+                const u32x4 v = *(const u32x4*)(ys + (row * kPieces + (ch ^ (row & (kPieces - 1)))) * 16);
                 const int64_t m = wm0 + 16 * j + row, n = wn0 + 8 * ch;
                 if (m < p.M && n < p.N) *(u32x4*)(p.Y + m * p.N + n) = v;
             }
         }
     };
 
-    // ---- prologue: A of stage 0, B of stages 0 and 1, the first scales
+    // ---- prologue: stages 0 and 1 of both operands, the first scales
     load_scales(0, 0, sm, sn);
 #pragma unroll
     for (int j = 0; j < 4; ++j) issue(ra0, slot_a(0), 0, j);
 #pragma unroll
     for (int j = 0; j < 4; ++j) issue(rb0, slot_b(0), 0, j);
+    const int d1 = nk > 1 ? 0 : 1, k1 = 1 - d1;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) issue(pick(nk > 1 ? 0 : 1, rb0, rb1, rb1), slot_b(1), nk > 1 ? 1 : 0, j);
-    LLMINT8_FP8_WAIT_BARRIER(4);
+    for (int j = 0; j < 4; ++j) issue(pick(d1, rb0, rb1, rb1), slot_b(1), k1, j);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) issue(pick(d1, ra0, ra1, ra1), slot_a(1), k1, j);
+    LLMINT8_FP8_WAIT_BARRIER(8);
     auto first_reads = [&](int sa, int sb) LLMINT8_FP8_INLINE {
         fn[0] = read(slot_b(sb) + wn * (16 * NF * BK), 0);
 #pragma unroll
@@ -273,50 +294,34 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
         sa ^= 1;
         sb = sb == 2 ? 0 : sb + 1;
     };
-    auto next_scales = [&]() LLMINT8_FP8_INLINE {
-#pragma unroll
-        for (int j = 0; j < MF; ++j) sm[j] = nsm[j];
-#pragma unroll
-        for (int j = 0; j < NS; ++j) sn[j] = nsn[j];
-    };
     for (int ti = 0; ti < my_tiles; ++ti) {
 #pragma unroll
         for (int f = 0; f < NF; ++f)
 #pragma unroll
             for (int j = 0; j < MF; ++j) acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         int kt = 0;
-        for (; kt + 4 <= nk; kt += 4) {
-            stage(std::integral_constant<int, 0>{}, sa, sb, kt, ti);
+        for (; kt + 2 <= nk; kt += 2) {
+            stage(std::integral_constant<int, 0>{}, sa, sb, kt);
             advance();
-            stage(std::integral_constant<int, 1>{}, sa, sb, kt + 1, ti);
+            stage(std::integral_constant<int, 1>{}, sa, sb, kt + 1);
             advance();
-            stage(std::integral_constant<int, 2>{}, sa, sb, kt + 2, ti);
-            advance();
-            stage(std::integral_constant<int, 3>{}, sa, sb, kt + 3, ti);
-            advance();
-            next_scales();
         }
         if (kt < nk) {
-            stage(std::integral_constant<int, 0>{}, sa, sb, kt, ti);
+            stage(std::integral_constant<int, 0>{}, sa, sb, kt);
             advance();
-            if (kt + 1 < nk) {
-                stage(std::integral_constant<int, 1>{}, sa, sb, kt + 1, ti);
-                advance();
-            }
-            if (kt + 2 < nk) {
-                stage(std::integral_constant<int, 2>{}, sa, sb, kt + 2, ti);
-                advance();
-            }
-            next_scales();
         }
-        // the slots of the stage before (sa, sb): freed by it
-        output(ti, sa ^ 1, sb == 0 ? 2 : sb - 1);
+        output(ti, sb == 0 ? 2 : sb - 1);  // the slot of the last stage
         if (ti + 1 < my_tiles) {
             ra0 = ra1;
             rb0 = rb1;
             ra1 = ra2;
             rb1 = rb2;
             tile_rsrc(ti + 3, ra2, rb2);
+            a_at0 = a_at1;
+            a_n0 = a_n1;
+            b_at0 = b_at1;
+            b_n0 = b_n1;
+            scale_range(ti + 2, a_at1, a_n1, b_at1, b_n1);
             if (nk & 1) {
 #pragma unroll
                 for (int j = 0; j < MF; ++j) fm[0][j] = fm[1][j];
@@ -345,7 +350,7 @@ hipError_t tiled_launch(const Fp8GemmArgs& a, hipStream_t stream) {
 
 template <int WM, int WN, int NF>
 hipError_t tiled(int dt, const Fp8GemmArgs& a, hipStream_t stream) {
-    if (a.bshift == 0)
+    if (a.spitch == 0)
         return dt == F16 ? tiled_launch<F16, WM, WN, NF, true>(a, stream) : tiled_launch<BF16, WM, WN, NF, true>(a, stream);
     return dt == F16 ? tiled_launch<F16, WM, WN, NF, false>(a, stream) : tiled_launch<BF16, WM, WN, NF, false>(a, stream);
 }

@@ -198,10 +198,10 @@ hipError_t launch_gemm_group_small(int dt, const int8_t* Xq, const int8_t* Xqb, 
 // Wq N x pitch(K), s_w ceil(N/128) x sp(K); with WqT also K x pitch(N), s_wT ceil(K/128) x sp(N)
 hipError_t launch_fp8_weight(int dt, const void* W, int64_t K, int64_t N, uint8_t* Wq, uint8_t* s_w, uint8_t* WqT,
                              uint8_t* s_wT, hipStream_t stream);
-// q M x pitch(K), s M x sp(K): a scale per row and group of 128 columns
+// q M x pitch(K); s: a scale per row and group of 128 columns (at fp8_row_scale_at)
 hipError_t launch_fp8_rows(int dt, const void* X, int64_t M, int64_t K, uint8_t* q, uint8_t* s, hipStream_t stream);
-// qt C x pitch(R), st C x sp(R): a scale per column of A (R x C) and group of 128 rows, the
-// codes transposed; q, s (both or neither): launch_fp8_rows of the same matrix
+// qt C x pitch(R): the codes of A (R x C) transposed, with a scale st per column of A and group
+// of 128 rows (at fp8_row_scale_at); q, s (both or neither): launch_fp8_rows of the same matrix
 hipError_t launch_fp8_cols(int dt, const void* A, int64_t R, int64_t C, uint8_t* qt, uint8_t* st, uint8_t* q, uint8_t* s,
                            hipStream_t stream);
 
@@ -209,10 +209,9 @@ struct Fp8GemmArgs {
     const uint8_t* A;  // M rows of codes
     const uint8_t* B;  // N rows of codes
     int64_t M, N, pitch;  // pitch: bytes of a row of codes, a multiple of 128
-    const uint8_t* sa;  // scale rows: one per row of A, one per (n >> bshift) of B
-    const uint8_t* sb;
-    int64_t spitch;     // bytes of a scale row, a multiple of 4
-    int bshift;         // 7: B has one scale per 128 rows; 0: one per row
+    const uint8_t* sa;  // scales of A, one per row and group (fp8_row_scale_at)
+    const uint8_t* sb;  // scales of B: as A's, or ceil(N/128) rows, one scale per 128 rows of B
+    int64_t spitch;     // bytes of such a scale row; 0: B has a scale per row
     uint16_t* Y;        // M x N
 };
 hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& p, hipStream_t stream);
