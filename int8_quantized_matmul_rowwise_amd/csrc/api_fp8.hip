@@ -219,17 +219,29 @@ int check_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
     if (T < 0 || H < 0 || I < 0 || E < 1 || k < 1 || k > E) return LLMINT8_EINVAL;
     if (H % 16 != 0 || I % 16 != 0) return LLMINT8_EINVAL;
     if (T > kMoeMaxTokens || E > kMoeMaxExperts || k > kMoeMaxTopK) return LLMINT8_ERANGE;
-    if (H > kMaxSum || I > kMaxSum / 2) return LLMINT8_ERANGE;
+    if (H > kMaxSum || I > kMaxSum / 2 || T * k * I >= (int64_t)1 << 30) return LLMINT8_ERANGE;
     return LLMINT8_OK;
 }
 
-size_t moe_workspace(int64_t T, int64_t I, int64_t k) { return align_up((size_t)T * (size_t)k * (size_t)I * 2); }
+struct MoeLayout {
+    size_t h, table, pairs, total;
+};
+
+MoeLayout moe_layout(int64_t T, int64_t I, int64_t k) {
+    MoeLayout L;
+    const size_t n = (size_t)T * (size_t)k;
+    L.h = 0;
+    L.table = align_up(n * (size_t)I * 2);
+    L.pairs = align_up(L.table + (1 + 3 * n) * 4);
+    L.total = align_up(L.pairs + n * 4);
+    return L;
+}
 
 }  // namespace
 
 LLMINT8_API size_t fp8_moe_block_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
     if (check_moe(T, H, I, E, top_k)) return 0;
-    return moe_workspace(T, I, top_k);
+    return moe_layout(T, I, top_k).total;
 }
 
 LLMINT8_API int fp8_moe_block(const void* X, int64_t T, int64_t H, int dtype, const float* logits, int64_t E,
@@ -246,13 +258,13 @@ LLMINT8_API int fp8_moe_block(const void* X, int64_t T, int64_t H, int dtype, co
     if (I > 0 && (!W13q || !aligned(W13q, 16) || !w13_scale || !aligned(w13_scale, 4) || !W2q || !aligned(W2q, 16) ||
                   !w2_scale || !aligned(w2_scale, 4)))
         return LLMINT8_EINVAL;
-    const size_t wb = moe_workspace(T, I, top_k);
-    if (I > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < wb)) return LLMINT8_EWORKSPACE;
+    const MoeLayout L = moe_layout(T, I, top_k);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < L.total) return LLMINT8_EWORKSPACE;
     const size_t e = (size_t)E, pairs = (size_t)T * (size_t)top_k;
     const Range r[] = {{Y, (size_t)T * (size_t)H * 2},
                        {topk_ids, pairs * 4},
                        {topk_weights, pairs * 4},
-                       {workspace, wb},
+                       {workspace, L.total},
                        {X, (size_t)T * (size_t)H * 2},
                        {logits, (size_t)T * e * 4},
                        {W13q, e * code_bytes(2 * I, H)},
@@ -261,7 +273,9 @@ LLMINT8_API int fp8_moe_block(const void* X, int64_t T, int64_t H, int dtype, co
                        {w2_scale, e * scale_bytes(ceil_div(H, 128), I)}};
     if (clash(r, 4, 10)) return LLMINT8_EINVAL;
     log_call("fp8_moe_block", T, H, I, dtype, NAN, "fp8_moe");
+    uint8_t* ws = (uint8_t*)workspace;
     const Fp8MoeArgs a{(const uint16_t*)X, T, H, logits, E, (int)top_k, renormalize != 0, W13q, w13_scale, W2q, w2_scale,
-                       I, (uint16_t*)Y, topk_ids, topk_weights, (uint16_t*)workspace};
+                       I, (uint16_t*)Y, topk_ids, topk_weights, (uint16_t*)(ws + L.h), (int32_t*)(ws + L.table),
+                       (int32_t*)(ws + L.pairs)};
     return hip_status(stage("fp8_moe", [&] { return launch_fp8_moe(dtype, a, (hipStream_t)stream); }));
 }

@@ -72,4 +72,8 @@ __device__ __forceinline__ u32x2 e4m3x8(const u32x4& v, float s) {
     return q;
 }
 
+// After a loop of matrix instructions, before their results are read: the wait states the reader
+// needs, which the compiler (ROCm 7.2) has been seen to leave out across a branch.
+__device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
 }  // namespace llmint8

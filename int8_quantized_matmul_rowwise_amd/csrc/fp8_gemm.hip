@@ -310,6 +310,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
             stage(std::integral_constant<int, 0>{}, sa, sb, kt);
             advance();
         }
+        mfma_settle();
         output(ti, sb == 0 ? 2 : sb - 1);  // the slot of the last stage
         if (ti + 1 < my_tiles) {
             ra0 = ra1;

@@ -230,7 +230,10 @@ struct Fp8MoeArgs {
     uint16_t* Y;
     int32_t* ids;    // T x k
     float* weights;  // T x k
+    // workspace
     uint16_t* h;     // (T k) x I
+    int32_t* table;  // 1 + 3 T k: the entries of the second launch
+    int32_t* pairs;  // T k: their pairs of token and choice
 };
 hipError_t launch_fp8_moe(int dt, const Fp8MoeArgs& p, hipStream_t stream);
 
