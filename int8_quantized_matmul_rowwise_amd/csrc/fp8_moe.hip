@@ -48,57 +48,78 @@ __device__ __forceinline__ float usable_logit(float l) {  // NaN as -inf, +inf a
     return l != l ? -__builtin_inff() : fminf(l, 3.4028234663852886e38f);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-    return v;
+// Reductions over a wave with lane-to-lane operands (about 8 cycles a step; a shuffle takes about
+// 100): the result comes from lane 63.
+template <class F>
+__device__ __forceinline__ float wave_reduce(float v, float none, F&& f) {
+#define LLMINT8_DPP(CTRL, ROWS)                                                                                   \
+    v = f(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v), \
+                                                                   CTRL, ROWS, 0xf, false)))
+    LLMINT8_DPP(0x111, 0xf);  // from the lane 1, 2, 4, 8 below in the row of 16
+    LLMINT8_DPP(0x112, 0xf);
+    LLMINT8_DPP(0x114, 0xf);
+    LLMINT8_DPP(0x118, 0xf);
+    LLMINT8_DPP(0x142, 0xa);  // row 0's last lane to row 1, row 2's to row 3
+    LLMINT8_DPP(0x143, 0xc);  // lane 31 to the upper rows
+#undef LLMINT8_DPP
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
-// The experts and weights of one token, by one wave; lane j < k returns choice j.
-__device__ __forceinline__ void route_token(const float* __restrict__ l, int E, int k, int renormalize, int& id, float& p) {
+// The experts and weights of one token, by one wave; lane j < k returns choice j.  A lane holds C
+// neighbouring experts, so that among equal values the lowest lane, and in it the first expert,
+// is the lowest index.
+template <int C>
+__device__ __forceinline__ void route_lanes(const float* __restrict__ l, int E, int k, int renormalize, int& id, float& p) {
+    const float kNone = -__builtin_inff();
     const int lane = threadIdx.x & 63;
-    float prev = __builtin_inff(), top = 0.0f, chosen = 0.0f;
-    int prev_e = -1;
+    float v[C], all[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        v[i] = C * lane + i < E ? usable_logit(l[C * lane + i]) : kNone;
+        all[i] = v[i];
+    }
+    float top = 0.0f, chosen = 0.0f;
     id = -1;
     p = 0.0f;
     for (int j = 0; j < k; ++j) {
-        // the best of those after (prev, prev_e) in the order (value descending, index ascending)
-        float best = -__builtin_inff();
-        int at = 0x7fffffff;
-        for (int e = lane; e < E; e += kWave) {
-            const float v = usable_logit(l[e]);
-            if ((v < prev || (v == prev && e > prev_e)) && v > best) {
-                best = v;
-                at = e;
-            }
-        }
+        float best = v[0];
 #pragma unroll
-        for (int off = 32; off > 0; off >>= 1) {
-            const float v = __shfl_xor(best, off, kWave);
-            const int e = __shfl_xor(at, off, kWave);
-            if (v > best || (v == best && e < at)) {
-                best = v;
-                at = e;
-            }
+        for (int i = 1; i < C; ++i) best = v[i] > best ? v[i] : best;
+        const float most = wave_reduce(best, kNone, [](float a, float b) { return a > b ? a : b; });
+        if (!(most > kNone)) break;  // the same in every lane
+        const int from = __builtin_ctzll(__ballot(best == most));
+        int at = 0;
+        bool taken = false;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {  // the first of the winning lane's experts with that value
+            const bool it = lane == from && !taken && v[i] == most;
+            at = it ? i : at;
+            v[i] = it ? kNone : v[i];
+            taken = taken || it;
         }
-        if (!(best > -__builtin_inff())) break;  // the same in every lane
-        if (j == 0) top = best;
-        const float x = expf(best - top);
+        at = C * from + __builtin_amdgcn_readlane(at, from);
+        if (j == 0) top = most;
+        const float x = expf(most - top);
         chosen += x;
         if (lane == j) {
             id = at;
             p = x;
         }
-        prev = best;
-        prev_e = at;
     }
     float z = chosen;
     if (!renormalize) {
-        z = 0.0f;
-        for (int e = lane; e < E; e += kWave) z += expf(usable_logit(l[e]) - top);
-        z = wave_sum(z);
+        float own = 0.0f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) own += expf(all[i] - top);
+        z = wave_reduce(own, 0.0f, [](float a, float b) { return a + b; });
     }
     if (id >= 0) p /= z;
+}
+
+__device__ __forceinline__ void route_token(const float* __restrict__ l, int E, int k, int renormalize, int& id, float& p) {
+    if (E <= 64) route_lanes<1>(l, E, k, renormalize, id, p);
+    else if (E <= 256) route_lanes<4>(l, E, k, renormalize, id, p);
+    else route_lanes<16>(l, E, k, renormalize, id, p);
 }
 
 __global__ __launch_bounds__(64) void moe_route_kernel(Fp8MoeArgs p) {
@@ -215,12 +236,14 @@ __device__ __forceinline__ void group_product(const u32x4 (&w)[2], float s, cons
     }
 }
 
-// ---- gate, up and SwiGLU: a workgroup takes 16 columns of I of one expert (16 gate rows and 16
-// up rows), its waves split the groups of H.  Workgroup 0 writes the table.  by_pair: workgroups
-// go by pair of token and choice (each expert at its first pair), else by expert.
+// ---- gate, up and SwiGLU: a workgroup takes `span` tiles of 16 columns of I of one expert (16
+// gate rows and 16 up rows each), its waves split the groups of H.  A wave's groups, tile after
+// tile, run through D sets of registers, so that the next tile's weights are on their way while
+// a tile's sums meet.  Workgroup 0 writes the table.  by_pair: workgroups go by pair of token and
+// choice (each expert at its first pair), else by expert.
 template <int DT, int MG, bool ROUTE>
-__global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(Fp8MoeArgs p, int tiles, int by_pair) {
-    constexpr int WV = kUpWaves, U = MG == 1 ? 2 : 1;
+__global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(Fp8MoeArgs p, int spans, int span, int by_pair) {
+    constexpr int WV = kUpWaves, D = 2;
     union Shared {
         v4f red[WV][2 * MG][64];
         struct {
@@ -236,6 +259,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(Fp8MoeArgs p, int
     const int li = lane & 15, q = lane >> 4;
     const int T = (int)p.T, E = (int)p.E, k = p.k;
     const int32_t* ids = p.ids;
+    if (tid == 0) dup = 0;
     if constexpr (ROUTE) {
         if (w < T) {
             int id;
@@ -250,21 +274,19 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(Fp8MoeArgs p, int
             }
         }
         ids = own_ids;
-        __syncthreads();
     }
+    __syncthreads();
     if (blockIdx.x == 0) {
         build_table(ids, T, E, k, 16 * MG, p.table, p.pairs, sh.t.mask, sh.t.first);
         return;
     }
-    const int y = (int)(blockIdx.x - 1) / tiles, tile = (int)(blockIdx.x - 1) % tiles;
+    const int y = (int)(blockIdx.x - 1) / spans, tile0 = (int)(blockIdx.x - 1) % spans * span;
     int e = y;
     if (by_pair) {
         e = ids[y];
         if (e < 0) return;
     }
     // the expert's tokens, ascending: list[place] = token * k + choice
-    if (tid == 0) dup = 0;
-    __syncthreads();
     int mine = -1;
     if (tid < 128 && tid < T)
         for (int j = 0; j < k; ++j)
@@ -279,13 +301,12 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(Fp8MoeArgs p, int
     __syncthreads();
 
     const int64_t hp = fp8_pitch(p.H), hsp = fp8_scale_pitch_of(p.H);
-    const int i0 = 16 * tile, ng = (int)(hp / 128);
+    const int tiles = (int)(p.I / 16), ng = (int)(hp / 128);
+    const int my_tiles = tiles - tile0 < span ? tiles - tile0 : span;
+    const int gw = (ng + WV - 1) / WV;  // groups of a wave (its last may lie past H: zeros)
+    const int steps = my_tiles * gw;
     const uint8_t* W = p.W13 + (int64_t)e * 2 * p.I * hp;
     const uint8_t* S = p.s13 + (int64_t)e * ceil_div(2 * p.I, 128) * hsp;
-    const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(W + (int64_t)i0 * hp, 16 * hp);
-    const __amdgpu_buffer_rsrc_t ru = buffer_rsrc(W + (p.I + i0) * hp, 16 * hp);
-    const uint8_t* sg = S + (int64_t)(i0 >> 7) * hsp;
-    const uint8_t* su = S + ((p.I + i0) >> 7) * hsp;  // I is a multiple of 16: one block
     const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(p.X, p.T * p.H * 2);
     const uint32_t w_off = (uint32_t)(li * hp + 32 * q);
 
@@ -300,167 +321,196 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(Fp8MoeArgs p, int
             const int i = c0 + 16 * j + li;
             x_off[j] = i < count ? (uint32_t)((list[i] / k) * p.H + 32 * q) * 2 : kFar;
         }
-        auto load = [&](int g, Group& r) LLMINT8_MOE_INLINE {
-            const uint32_t far = g < ng ? 0u : kFar;
+        int lt = 0, lg = w;  // the next load's tile and group
+        auto load = [&](Group& r) LLMINT8_MOE_INLINE {
+            const bool in = lt < my_tiles && lg < ng;
+            const uint32_t far = in ? 0u : kFar;
+            const int64_t i0 = 16 * (int64_t)(lt < my_tiles ? tile0 + lt : tile0);
+            const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(W + i0 * hp, 16 * hp), ru = buffer_rsrc(W + (p.I + i0) * hp, 16 * hp);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t off = (w_off + (uint32_t)(g * 128 + 16 * h)) | far;
+                const uint32_t off = (w_off + (uint32_t)(lg * 128 + 16 * h)) | far;
                 r.g[h] = load16(rg, off);
                 r.u[h] = load16(ru, off);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t out = g * 128 + 32 * q + 8 * i < p.H ? far : kFar;  // past H: the next row's
+                const uint32_t out = lg * 128 + 32 * q + 8 * i < p.H ? far : kFar;  // past H: the next row's
 #pragma unroll
-                for (int j = 0; j < MG; ++j)
-                    r.x[j][i] = load16(rx, (x_off[j] + (uint32_t)(g * 128 + 8 * i) * 2) | out);
+                for (int j = 0; j < MG; ++j) r.x[j][i] = load16(rx, (x_off[j] + (uint32_t)(lg * 128 + 8 * i) * 2) | out);
             }
-            r.eg = g < ng ? e8m0_value(sg[g]) : 0.0f;
-            r.eu = g < ng ? e8m0_value(su[g]) : 0.0f;
+            // the scales of the 16 rows (I is a multiple of 16: one block of rows each)
+            r.eg = in ? e8m0_value(S[(i0 >> 7) * hsp + lg]) : 0.0f;
+            r.eu = in ? e8m0_value(S[((p.I + i0) >> 7) * hsp + lg]) : 0.0f;
+            lg += WV;
+            if (lg >= gw * WV) {
+                lg = w;
+                ++lt;
+            }
         };
         v4f ag[MG] = {}, au[MG] = {};
-        auto multiply = [&](const Group& r) LLMINT8_MOE_INLINE {
-            group_product<DT, MG>(r.g, r.eg, r.x, ag);
-            group_product<DT, MG>(r.u, r.eu, r.x, au);
+        int tile = tile0, done = 0;
+        // after a tile's last group: the waves' sums meet, SwiGLU, h
+        auto finish = [&]() LLMINT8_MOE_INLINE {
+            mfma_settle();
+#pragma unroll
+            for (int j = 0; j < MG; ++j) {
+                sh.red[w][j][lane] = ag[j];
+                sh.red[w][MG + j][lane] = au[j];
+                ag[j] = au[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+            __syncthreads();
+            if (w < MG) {  // piece w: sums in the order of the waves
+                v4f sgate = sh.red[0][w][lane], sup = sh.red[0][MG + w][lane];
+#pragma unroll
+                for (int i = 1; i < WV; ++i) {
+                    sgate += sh.red[i][w][lane];
+                    sup += sh.red[i][MG + w][lane];
+                }
+                const int i = c0 + 16 * w + li;
+                if (i < count) {
+                    uint16_t h[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) h[r] = from_f32<DT>(sgate[r] / (1.0f + expf(-sgate[r])) * sup[r]);
+                    u32x2 v;
+                    v[0] = (uint32_t)h[0] | ((uint32_t)h[1] << 16);
+                    v[1] = (uint32_t)h[2] | ((uint32_t)h[3] << 16);
+                    *(u32x2*)(p.h + (int64_t)list[i] * p.I + 16 * tile + 4 * q) = v;
+                }
+            }
+            __syncthreads();
+            ++tile;
         };
-        Group a[U], b[U];
-        int g = w;
+        Group r[D];
 #pragma unroll
-        for (int u = 0; u < U; ++u) load(g + u * WV, a[u]);
-        while (g < ng) {
-            g += U * WV;
+        for (int d = 0; d < D; ++d) load(r[d]);
+        for (int s = 0; s < steps; s += D) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) load(g + u * WV, b[u]);
-#pragma unroll
-            for (int u = 0; u < U; ++u) multiply(a[u]);
-            if (g >= ng) break;
-            g += U * WV;
-#pragma unroll
-            for (int u = 0; u < U; ++u) load(g + u * WV, a[u]);
-#pragma unroll
-            for (int u = 0; u < U; ++u) multiply(b[u]);
-        }
-        mfma_settle();
-#pragma unroll
-        for (int j = 0; j < MG; ++j) {
-            sh.red[w][j][lane] = ag[j];
-            sh.red[w][MG + j][lane] = au[j];
-        }
-        __syncthreads();
-        if (w < MG) {  // piece w: sums in the order of the waves
-            v4f sgate = sh.red[0][w][lane], sup = sh.red[0][MG + w][lane];
-#pragma unroll
-            for (int i = 1; i < WV; ++i) {
-                sgate += sh.red[i][w][lane];
-                sup += sh.red[i][MG + w][lane];
-            }
-            const int i = c0 + 16 * w + li;
-            if (i < count) {
-                uint16_t h[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) h[r] = from_f32<DT>(sgate[r] / (1.0f + expf(-sgate[r])) * sup[r]);
-                u32x2 v;
-                v[0] = (uint32_t)h[0] | ((uint32_t)h[1] << 16);
-                v[1] = (uint32_t)h[2] | ((uint32_t)h[3] << 16);
-                *(u32x2*)(p.h + (int64_t)list[i] * p.I + i0 + 4 * q) = v;
+            for (int d = 0; d < D; ++d) {
+                if (s + d >= steps) break;
+                group_product<DT, MG>(r[d].g, r[d].eg, r[d].x, ag);
+                group_product<DT, MG>(r[d].u, r[d].eu, r[d].x, au);
+                load(r[d]);
+                if (++done == gw) {
+                    done = 0;
+                    finish();
+                }
             }
         }
-        __syncthreads();
     }
 }
 
 // ---- down and the weighted sum: a workgroup takes 16 columns of H of all entries.  Their groups
-// of I, entry after entry, are split evenly over the waves; a wave ends an entry (or its share of
-// it) by adding p times its sums to its own rows of token sums in LDS.
-template <int DT, int MG, int WV>
+// of I, entry after entry, are split evenly over the waves and run through D sets of registers;
+// a wave ends an entry (or its share of it) by adding p times its sums to its own rows of token
+// sums in LDS.
+template <int DT, int MG, int MAXT, int WV>
 __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
-    extern __shared__ v4f ysum[];  // [WV][T][4] quads: a wave's sums of 16 columns per token
+    constexpr int D = MG == 1 ? (WV == 8 ? 4 : 3) : 2, MAXN = MAXT * kMaxTopK;
+    __shared__ v4f ysum[WV][MAXT][4];  // a wave's sums of 16 columns per token
+    __shared__ int32_t table[3 * MAXN], pairs[MAXN];
+    __shared__ float weights[MAXN];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, q = lane >> 4;
-    const int T = (int)p.T, k = p.k;
+    const int T = (int)p.T, k = p.k, n = T * k;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int64_t ip = fp8_pitch(p.I), isp = fp8_scale_pitch_of(p.I);
     const int ng = (int)(ip / 128);
     const int entries = __builtin_amdgcn_readfirstlane(p.table[0]);
-    for (int i = tid; i < WV * T * 4; i += 64 * WV) ysum[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = tid; i < 3 * n; i += 64 * WV) table[i] = p.table[1 + i];  // past the entries: unread
+    for (int i = tid; i < n; i += 64 * WV) {
+        pairs[i] = p.pairs[i];
+        weights[i] = p.weights[i];
+    }
+    for (int i = tid; i < WV * T * 4; i += 64 * WV) ysum[i / (4 * T)][(i >> 2) % T][i & 3] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     __syncthreads();
     const int64_t total = (int64_t)entries * ng;
     const int64_t from = total * w / WV, to = total * (w + 1) / WV;
-    const uint32_t w_off = (uint32_t)(li * ip + 32 * q);
-    const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, p.T * k * p.I * 2);
-    v4f* mine = ysum + (int64_t)w * T * 4;
-    for (int64_t at = from; at < to;) {
-        const int entry = __builtin_amdgcn_readfirstlane((int)(at / ng));
-        const int g0 = (int)(at - (int64_t)entry * ng);
-        const int g1 = to - at < ng - g0 ? g0 + (int)(to - at) : ng;
-        const int e = __builtin_amdgcn_readfirstlane(p.table[1 + 3 * entry]);
-        const int off = __builtin_amdgcn_readfirstlane(p.table[2 + 3 * entry]);
-        const int count = __builtin_amdgcn_readfirstlane(p.table[3 + 3 * entry]);
-        uint32_t h_off[MG];
-        int token[MG];
-        float pt[MG];
-#pragma unroll
-        for (int j = 0; j < MG; ++j) {
-            const int i = 16 * j + li;
-            const int pair = i < count ? p.pairs[off + i] : -1;
-            token[j] = pair >= 0 ? pair / k : -1;
-            pt[j] = pair >= 0 ? p.weights[pair] : 0.0f;
-            h_off[j] = pair >= 0 ? (uint32_t)(pair * p.I + 32 * q) * 2 : kFar;
-        }
-        const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(p.W2 + ((int64_t)e * p.H + n0) * ip, 16 * ip);
-        const uint8_t* s = p.s2 + ((int64_t)e * ceil_div(p.H, 128) + (n0 >> 7)) * isp;
+    if (from < to) {
+        const uint32_t w_off = (uint32_t)(li * ip + 32 * q);
+        const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, (int64_t)n * p.I * 2);
+        const int64_t scale_rows = ceil_div(p.H, 128);
         struct Group {
             u32x4 w[2], x[MG][4];
             float s;
         };
-        auto load = [&](int g, Group& r) LLMINT8_MOE_INLINE {
-            const uint32_t far = g < g1 ? 0u : kFar;
+        // the next load's entry and group, and that entry's expert and rows of h
+        int le = (int)(from / ng), lg = (int)(from - (int64_t)le * ng), expert = 0;
+        int64_t left = to - from;
+        uint32_t h_off[MG];
+        auto open = [&]() LLMINT8_MOE_INLINE {
+            if (le >= entries) return;
+            expert = __builtin_amdgcn_readfirstlane(table[3 * le]);
+            const int first = table[3 * le + 1], count = table[3 * le + 2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) r.w[h] = load16(rw, (w_off + (uint32_t)(g * 128 + 16 * h)) | far);
+            for (int j = 0; j < MG; ++j) {
+                const int i = 16 * j + li;
+                h_off[j] = i < count ? (uint32_t)(pairs[first + i] * p.I + 32 * q) * 2 : kFar;
+            }
+        };
+        auto load = [&](Group& r) LLMINT8_MOE_INLINE {
+            const bool in = left > 0;
+            const uint32_t far = in ? 0u : kFar;
+            const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(p.W2 + ((int64_t)expert * p.H + n0) * ip, 16 * ip);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) r.w[h] = load16(rw, (w_off + (uint32_t)(lg * 128 + 16 * h)) | far);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t out = g * 128 + 32 * q + 8 * i < p.I ? far : kFar;
+                const uint32_t out = lg * 128 + 32 * q + 8 * i < p.I ? far : kFar;  // past I: the next row's
 #pragma unroll
-                for (int j = 0; j < MG; ++j)
-                    r.x[j][i] = load16(rh, (h_off[j] + (uint32_t)(g * 128 + 8 * i) * 2) | out);
+                for (int j = 0; j < MG; ++j) r.x[j][i] = load16(rh, (h_off[j] + (uint32_t)(lg * 128 + 8 * i) * 2) | out);
             }
-            r.s = g < g1 ? e8m0_value(s[g]) : 0.0f;
+            r.s = in ? e8m0_value(p.s2[(expert * scale_rows + (n0 >> 7)) * isp + lg]) : 0.0f;
+            --left;
+            if (++lg == ng) {
+                lg = 0;
+                ++le;
+                open();
+            }
         };
-        constexpr int U = MG <= 2 ? 2 : 1;
         v4f acc[MG] = {};
-        Group a[U], b[U];
-        int g = g0;
+        int ce = le, cg = lg;  // the entry and group being multiplied
+        auto flush = [&]() LLMINT8_MOE_INLINE {
+            mfma_settle();
+            const int first = table[3 * ce + 1], count = table[3 * ce + 2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) load(g + u, a[u]);
-        while (g < g1) {
-            g += U;
+            for (int j = 0; j < MG; ++j) {
+                const int i = 16 * j + li;
+                if (i < count) {
+                    const int pair = pairs[first + i];
+                    const float pt = weights[pair];
+                    v4f y = ysum[w][pair / k][q];
 #pragma unroll
-            for (int u = 0; u < U; ++u) load(g + u, b[u]);
-#pragma unroll
-            for (int u = 0; u < U; ++u) group_product<DT, MG>(a[u].w, a[u].s, a[u].x, acc);
-            if (g >= g1) break;
-            g += U;
-#pragma unroll
-            for (int u = 0; u < U; ++u) load(g + u, a[u]);
-#pragma unroll
-            for (int u = 0; u < U; ++u) group_product<DT, MG>(b[u].w, b[u].s, b[u].x, acc);
-        }
-        mfma_settle();
-#pragma unroll
-        for (int j = 0; j < MG; ++j)
-            if (token[j] >= 0) {
-                v4f y = mine[token[j] * 4 + q];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(pt[j], acc[j][r], y[r]);
-                mine[token[j] * 4 + q] = y;
+                    for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(pt, acc[j][r], y[r]);
+                    ysum[w][pair / k][q] = y;
+                }
+                acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
             }
-        at += g1 - g0;
+        };
+        Group r[D];
+        open();
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(r[d]);
+        const int steps = (int)(to - from);
+        for (int s = 0; s < steps; s += D) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (s + d >= steps) break;
+                group_product<DT, MG>(r[d].w, r[d].s, r[d].x, acc);
+                load(r[d]);
+                if (++cg == ng || s + d + 1 == steps) {
+                    flush();
+                    cg = 0;
+                    ++ce;
+                }
+            }
+        }
     }
     __syncthreads();
     for (int i = tid; i < T * 4; i += 64 * WV) {
-        v4f y = ysum[i];
+        v4f y = ysum[0][i >> 2][i & 3];
 #pragma unroll
-        for (int v = 1; v < WV; ++v) y += ysum[v * T * 4 + i];
+        for (int v = 1; v < WV; ++v) y += ysum[v][i >> 2][i & 3];
         u32x2 o;
         o[0] = (uint32_t)from_f32<DT>(y[0]) | ((uint32_t)from_f32<DT>(y[1]) << 16);
         o[1] = (uint32_t)from_f32<DT>(y[2]) | ((uint32_t)from_f32<DT>(y[3]) << 16);
@@ -470,22 +520,43 @@ __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
 
 template <int DT, int MG>
 hipError_t moe_launch(const Fp8MoeArgs& p, hipStream_t stream) {
-    const bool route = p.T <= kRouteTokens;
     const int by_pair = p.T * p.k < p.E;
-    const int tiles = (int)(p.I / 16);
-    const int64_t grid = 1 + (int64_t)tiles * (by_pair ? p.T * p.k : p.E);
-    if (!route) moe_route_kernel<<<(unsigned)p.T, 64, 0, stream>>>(p);
-    if (route && MG == 1) moe_up_kernel<DT, MG, MG == 1><<<(unsigned)grid, 64 * kUpWaves, 0, stream>>>(p, tiles, by_pair);
-    else moe_up_kernel<DT, MG, false><<<(unsigned)grid, 64 * kUpWaves, 0, stream>>>(p, tiles, by_pair);
-    constexpr int WV = 8;
-    moe_down_kernel<DT, MG, WV><<<(unsigned)(p.H / 16), 64 * WV, WV * p.T * 64, stream>>>(p);
+    const int64_t rows = by_pair ? p.T * p.k : p.E, tiles = p.I / 16;
+    // tiles of a workgroup: its setup (choosing the experts or reading them, the list) is paid
+    // once, as long as enough workgroups are left
+    int64_t span = tiles * rows / 1024;
+    span = span < 1 ? 1 : (span > 8 ? 8 : span);
+    const int64_t spans = ceil_div(tiles, span), grid = 1 + spans * rows;
+    if (MG == 1 && p.T <= kRouteTokens && grid <= 2048) {
+        moe_up_kernel<DT, MG, MG == 1><<<(unsigned)grid, 64 * kUpWaves, 0, stream>>>(p, (int)spans, (int)span, by_pair);
+    } else {
+        moe_route_kernel<<<(unsigned)p.T, 64, 0, stream>>>(p);
+        moe_up_kernel<DT, MG, false><<<(unsigned)grid, 64 * kUpWaves, 0, stream>>>(p, (int)spans, (int)span, by_pair);
+    }
+    const unsigned cols = (unsigned)(p.H / 16);
+    if constexpr (MG == 1) {
+        if (p.T <= 16) {
+            moe_down_kernel<DT, MG, 16, 16><<<cols, 1024, 0, stream>>>(p);
+            return hipGetLastError();
+        }
+    }
+    if constexpr (MG < 4) {
+        if (p.T <= 64) {
+            moe_down_kernel<DT, MG, 64, 16><<<cols, 1024, 0, stream>>>(p);
+            return hipGetLastError();
+        }
+    }
+    moe_down_kernel<DT, MG, 128, 8><<<cols, 512, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 template <int DT>
 hipError_t moe_pieces(const Fp8MoeArgs& p, hipStream_t stream) {
-    if (p.T <= 16) return moe_launch<DT, 1>(p, stream);
-    if (p.T <= 32) return moe_launch<DT, 2>(p, stream);
+    // pieces of 16 tokens multiplied at once: by the tokens that an expert has on average (one
+    // that has more is read once per 16 MG of them)
+    const int64_t mean16 = 16 * p.T * p.k / p.E;
+    if (mean16 <= 12 * 16 || p.T <= 16) return moe_launch<DT, 1>(p, stream);
+    if (mean16 <= 28 * 16 || p.T <= 32) return moe_launch<DT, 2>(p, stream);
     return moe_launch<DT, 4>(p, stream);
 }
 
