@@ -337,8 +337,8 @@ int int8_matmul_noalloc(const void* X, int64_t M, int64_t K, int dtype, const in
  * one makes every output whose sum it enters not finite, the finite values of its group are
  * coded with its scale (as good as zero), and nothing else changes.
  *
- * Shapes and conventions as above (K a multiple of 16, N of 8), with a bound of 2^22 on the
- * length of a sum in place of the int32 one (LLMINT8_ERANGE).
+ * Shapes and conventions as above (K a multiple of 16, N of 8), with a bound of 2^22 on M and
+ * on the length of a sum in place of the int32 one (LLMINT8_ERANGE).
  */
 int64_t fp8_code_pitch(int64_t n);
 int64_t fp8_scale_pitch(int64_t n);
@@ -366,7 +366,8 @@ int fp8_quantize_weight_block(const void* W, int64_t K, int64_t N, int dtype, ui
  *   Y          out: M x N, dtype, 16-byte aligned.
  *   workspace  fp8_matmul_block_workspace_bytes(M, K, N) bytes, 16-byte aligned.
  * M = 0 or N = 0 is a no-op; K = 0 gives Y = 0 (no workspace needed).  Outputs and workspace
- * overlap nothing (LLMINT8_EINVAL).  ceil(M/64) is at most 65535 (LLMINT8_ERANGE).
+ * overlap nothing (LLMINT8_EINVAL).  The workspace is free for other uses between calls (nothing
+ * in it has to survive, or to be zero); calls that may run at the same time need one each.
  */
 size_t fp8_matmul_block_workspace_bytes(int64_t M, int64_t K, int64_t N);
 int fp8_matmul_block(const void* X, int64_t M, int64_t K, int dtype, const uint8_t* Wq, const uint8_t* w_scale,
@@ -382,8 +383,8 @@ int fp8_matmul_block(const void* X, int64_t M, int64_t K, int dtype, const uint8
  *   dW  out, K x N, dtype, 16-byte aligned; NULL: not wanted (X may be NULL then).
  *   workspace  fp8_matmul_block_backward_workspace_bytes(M, K, N, dX != NULL, dW != NULL) bytes,
  *              16-byte aligned.
- * An empty sum (N = 0 for dX, M = 0 for dW) gives zeros.  M and N are at most 2^22
- * (LLMINT8_ERANGE).
+ * An empty sum (N = 0 for dX, M = 0 for dW) gives zeros (no workspace needed).  M, K and N are at
+ * most 2^22 (LLMINT8_ERANGE).
  */
 size_t fp8_matmul_block_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int need_dx, int need_dw);
 int fp8_matmul_block_backward(const void* dY, const void* X, int64_t M, int64_t K, int64_t N, int dtype,

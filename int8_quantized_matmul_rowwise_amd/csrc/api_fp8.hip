@@ -18,12 +18,10 @@ int check_fp8_shape(int64_t M, int64_t K, int64_t N, int dtype) {
     if (dtype != LLMINT8_F16 && dtype != LLMINT8_BF16) return LLMINT8_EINVAL;
     if (M < 0 || K < 0 || N < 0 || M > kMaxDim || N > kMaxDim) return LLMINT8_EINVAL;
     if (K % 16 != 0 || N % 8 != 0) return LLMINT8_EINVAL;
-    if (K > kMaxSum) return LLMINT8_ERANGE;
+    if (K > kMaxSum || M > kMaxSum) return LLMINT8_ERANGE;
+    if (ceil_div(M, 128) * ceil_div(N, 128) > kMaxDim) return LLMINT8_ERANGE;  // the product's grid
     return LLMINT8_OK;
 }
-
-// The product's grids: one workgroup per tile of 64 x 64 at the least.
-bool grid_ok(int64_t M, int64_t N) { return ceil_div(M, 64) * ceil_div(N, 64) <= kMaxDim && ceil_div(M, 64) <= 65535; }
 
 size_t code_bytes(int64_t rows, int64_t sum) { return (size_t)rows * (size_t)fp8_pitch(sum); }
 size_t scale_bytes(int64_t rows, int64_t sum) { return (size_t)rows * (size_t)fp8_scale_pitch_of(sum); }
@@ -70,22 +68,35 @@ LLMINT8_API int fp8_quantize_weight_block(const void* W, int64_t K, int64_t N, i
 namespace {
 
 struct Fp8Layout {
-    size_t xq, s_x, total;
+    Fp8Plan plan;
+    size_t xq, s_x, counters, partial, total;
 };
 
 Fp8Layout fp8_layout(int64_t M, int64_t K, int64_t N) {
-    (void)N;
     Fp8Layout L;
+    L.plan = fp8_plan(M, N, ceil_div(K, 128), true, false);
+    const bool fused = L.plan.kind == Fp8Plan::kFused;
     L.xq = 0;
-    L.s_x = align_up(code_bytes(M, K));
-    L.total = align_up(L.s_x + (size_t)fp8_row_scale_bytes(M, K));
+    L.s_x = align_up(fused ? 0 : code_bytes(M, K));
+    L.counters = align_up(L.s_x + (fused ? 0 : (size_t)fp8_row_scale_bytes(M, K)));
+    L.partial = align_up(L.counters + (L.plan.split > 1 ? (size_t)L.plan.tiles * 4 : 0));
+    L.total = align_up(L.partial + (size_t)L.plan.partial_bytes);
     return L;
+}
+
+const char* plan_name(const Fp8Plan& p) {
+    switch (p.kind) {
+        case Fp8Plan::kTile256: return p.split > 1 ? "fp8_tile256_split" : "fp8_tile256";
+        case Fp8Plan::kTile128: return p.split > 1 ? "fp8_tile128_split" : "fp8_tile128";
+        case Fp8Plan::kSmall: return p.split > 1 ? "fp8_small_split" : "fp8_small";
+        default: return "fp8_small_fused";
+    }
 }
 
 }  // namespace
 
 LLMINT8_API size_t fp8_matmul_block_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-    if (M < 0 || K < 0 || N < 0) return 0;
+    if (check_fp8_shape(M, K, N, LLMINT8_F16) || M == 0 || N == 0 || K == 0) return 0;
     return fp8_layout(M, K, N).total;
 }
 
@@ -94,7 +105,6 @@ LLMINT8_API int fp8_matmul_block(const void* X, int64_t M, int64_t K, int dtype,
                                  void* stream) {
     int rc = check_fp8_shape(M, K, N, dtype);
     if (rc) return rc;
-    if (!grid_ok(M, N)) return LLMINT8_ERANGE;
     if (M == 0 || N == 0) return LLMINT8_OK;
     if (!Y || !aligned(Y, 16)) return LLMINT8_EINVAL;
     hipStream_t st = (hipStream_t)stream;
@@ -104,20 +114,26 @@ LLMINT8_API int fp8_matmul_block(const void* X, int64_t M, int64_t K, int dtype,
     }
     if (!X || !aligned(X, 16) || !Wq || !aligned(Wq, 16) || !w_scale || !aligned(w_scale, 4)) return LLMINT8_EINVAL;
     const Fp8Layout L = fp8_layout(M, K, N);
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < L.total) return LLMINT8_EWORKSPACE;
+    if (L.total > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < L.total)) return LLMINT8_EWORKSPACE;
     const Range r[] = {{Y, (size_t)M * (size_t)N * 2},
                        {workspace, L.total},
                        {X, (size_t)M * (size_t)K * 2},
                        {Wq, code_bytes(N, K)},
                        {w_scale, scale_bytes(ceil_div(N, 128), K)}};
     if (clash(r, 2, 5)) return LLMINT8_EINVAL;
-    log_call("fp8_matmul_block", M, K, N, dtype, NAN, "fp8_tiled");
+    log_call("fp8_matmul_block", M, K, N, dtype, NAN, plan_name(L.plan));
     uint8_t* ws = (uint8_t*)workspace;
-    hipError_t e = stage("fp8_rows", [&] { return launch_fp8_rows(dtype, X, M, K, ws + L.xq, ws + L.s_x, st); });
+    int32_t* counters = L.plan.split > 1 ? (int32_t*)(ws + L.counters) : nullptr;
+    hipError_t e = hipSuccess;
+    if (L.plan.kind != Fp8Plan::kFused)
+        e = stage("fp8_rows", [&] {
+            return launch_fp8_rows(dtype, X, M, K, ws + L.xq, ws + L.s_x, counters, counters ? L.plan.tiles : 0, st);
+        });
     if (e == hipSuccess)
         e = stage("fp8_gemm", [&] {
-            const Fp8GemmArgs a{ws + L.xq, Wq, M, N, fp8_pitch(K), ws + L.s_x, w_scale, fp8_scale_pitch_of(K), (uint16_t*)Y};
-            return launch_fp8_gemm(dtype, a, st);
+            const Fp8GemmArgs a{ws + L.xq, Wq, M, N, fp8_pitch(K), ws + L.s_x, w_scale, fp8_scale_pitch_of(K), (uint16_t*)Y,
+                                (const uint16_t*)X, K, counters, (float*)(ws + L.partial)};
+            return launch_fp8_gemm(dtype, a, L.plan, st);
         });
     return hip_status(e);
 }
@@ -127,11 +143,14 @@ LLMINT8_API int fp8_matmul_block(const void* X, int64_t M, int64_t K, int dtype,
 namespace {
 
 struct Fp8BackwardLayout {
-    size_t dyq, s_dy, dyt, s_dyt, xt, s_xt, total;
+    Fp8Plan dx, dw;
+    size_t dyq, s_dy, dyt, s_dyt, xt, s_xt, counters, partial, total;
 };
 
 Fp8BackwardLayout fp8_backward_layout(int64_t M, int64_t K, int64_t N, bool dx, bool dw) {
-    Fp8BackwardLayout L;
+    Fp8BackwardLayout L{};
+    if (dx) L.dx = fp8_plan(M, K, ceil_div(N, 128), false, false);
+    if (dw) L.dw = fp8_plan(K, N, ceil_div(M, 128), false, true);
     size_t off = 0;
     auto take = [&](size_t n) {
         const size_t at = off;
@@ -144,6 +163,10 @@ Fp8BackwardLayout fp8_backward_layout(int64_t M, int64_t K, int64_t N, bool dx, 
     L.s_dyt = take(dw ? (size_t)fp8_row_scale_bytes(N, M) : 0);
     L.xt = take(dw ? code_bytes(K, M) : 0);
     L.s_xt = take(dw ? (size_t)fp8_row_scale_bytes(K, M) : 0);
+    // one product after the other: the partial sums share their place
+    L.counters = take((L.dx.split > 1 ? (size_t)L.dx.tiles * 4 : 0) + (L.dw.split > 1 ? (size_t)L.dw.tiles * 4 : 0));
+    const size_t px = (size_t)L.dx.partial_bytes, pw = (size_t)L.dw.partial_bytes;
+    L.partial = take(px > pw ? px : pw);
     L.total = off;
     return L;
 }
@@ -151,7 +174,7 @@ Fp8BackwardLayout fp8_backward_layout(int64_t M, int64_t K, int64_t N, bool dx, 
 }  // namespace
 
 LLMINT8_API size_t fp8_matmul_block_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int need_dx, int need_dw) {
-    if (M < 0 || K < 0 || N < 0) return 0;
+    if (check_fp8_shape(M, K, N, LLMINT8_F16) || M > kMaxSum || N > kMaxSum || M == 0 || K == 0 || N == 0) return 0;
     return fp8_backward_layout(M, K, N, need_dx != 0, need_dw != 0).total;
 }
 
@@ -162,7 +185,6 @@ LLMINT8_API int fp8_matmul_block_backward(const void* dY, const void* X, int64_t
     if (rc) return rc;
     const bool dx = dX != nullptr, dw = dW != nullptr;
     if (M > kMaxSum || N > kMaxSum) return LLMINT8_ERANGE;
-    if (!grid_ok(M, K) || !grid_ok(K, N)) return LLMINT8_ERANGE;
     if (!dx && !dw) return LLMINT8_OK;
     const bool out_x = dx && M > 0 && K > 0, out_w = dw && K > 0 && N > 0;
     if (!out_x && !out_w) return LLMINT8_OK;
@@ -171,7 +193,7 @@ LLMINT8_API int fp8_matmul_block_backward(const void* dY, const void* X, int64_t
     if ((sum_x || sum_w) && (!dY || !aligned(dY, 16))) return LLMINT8_EINVAL;
     if (sum_w && (!X || !aligned(X, 16))) return LLMINT8_EINVAL;
     if (sum_x && (!WqT || !aligned(WqT, 16) || !wT_scale || !aligned(wT_scale, 4))) return LLMINT8_EINVAL;
-    const Fp8BackwardLayout L = fp8_backward_layout(M, K, N, dx, dw);
+    const Fp8BackwardLayout L = fp8_backward_layout(M, K, N, sum_x, sum_w);
     if ((sum_x || sum_w) && (!workspace || !aligned(workspace, 16) || workspace_bytes < L.total)) return LLMINT8_EWORKSPACE;
     const Range r[] = {{dX, out_x ? (size_t)M * (size_t)K * 2 : 0},
                        {dW, out_w ? (size_t)K * (size_t)N * 2 : 0},
@@ -184,26 +206,33 @@ LLMINT8_API int fp8_matmul_block_backward(const void* dY, const void* X, int64_t
     log_call("fp8_matmul_block_backward", M, K, N, dtype, NAN, dx ? (dw ? "fp8_dx_dw" : "fp8_dx") : "fp8_dw");
     hipStream_t st = (hipStream_t)stream;
     uint8_t* ws = (uint8_t*)workspace;
+    int32_t* counters = (int32_t*)(ws + L.counters);
+    const int64_t n_dx = L.dx.split > 1 ? L.dx.tiles : 0, n_dw = L.dw.split > 1 ? L.dw.tiles : 0;
+    float* partial = (float*)(ws + L.partial);
     hipError_t e = hipSuccess;
     if (sum_w)
         e = stage("fp8_cols_dy", [&] {
             return launch_fp8_cols(dtype, dY, M, N, ws + L.dyt, ws + L.s_dyt, sum_x ? ws + L.dyq : nullptr,
-                                   sum_x ? ws + L.s_dy : nullptr, st);
+                                   sum_x ? ws + L.s_dy : nullptr, counters, n_dx + n_dw, st);
         });
     else if (sum_x)
-        e = stage("fp8_rows", [&] { return launch_fp8_rows(dtype, dY, M, N, ws + L.dyq, ws + L.s_dy, st); });
+        e = stage("fp8_rows", [&] { return launch_fp8_rows(dtype, dY, M, N, ws + L.dyq, ws + L.s_dy, counters, n_dx, st); });
     if (e == hipSuccess && sum_w)
-        e = stage("fp8_cols_x", [&] { return launch_fp8_cols(dtype, X, M, K, ws + L.xt, ws + L.s_xt, nullptr, nullptr, st); });
+        e = stage("fp8_cols_x", [&] {
+            return launch_fp8_cols(dtype, X, M, K, ws + L.xt, ws + L.s_xt, nullptr, nullptr, nullptr, 0, st);
+        });
     if (e == hipSuccess && out_x)
         e = sum_x ? stage("fp8_gemm_dx", [&] {
-                        const Fp8GemmArgs a{ws + L.dyq, WqT, M, K, fp8_pitch(N), ws + L.s_dy, wT_scale, fp8_scale_pitch_of(N), (uint16_t*)dX};
-                        return launch_fp8_gemm(dtype, a, st);
+                        const Fp8GemmArgs a{ws + L.dyq, WqT, M, K, fp8_pitch(N), ws + L.s_dy, wT_scale, fp8_scale_pitch_of(N), (uint16_t*)dX,
+                                            nullptr, 0, counters, partial};
+                        return launch_fp8_gemm(dtype, a, L.dx, st);
                     })
                   : stage("fill_zero", [&] { return launch_fill_zero((float*)dX, M * K / 2, st); });
     if (e == hipSuccess && out_w)
         e = sum_w ? stage("fp8_gemm_dw", [&] {
-                        const Fp8GemmArgs a{ws + L.xt, ws + L.dyt, K, N, fp8_pitch(M), ws + L.s_xt, ws + L.s_dyt, 0, (uint16_t*)dW};
-                        return launch_fp8_gemm(dtype, a, st);
+                        const Fp8GemmArgs a{ws + L.xt, ws + L.dyt, K, N, fp8_pitch(M), ws + L.s_xt, ws + L.s_dyt, 0, (uint16_t*)dW,
+                                            nullptr, 0, counters + n_dx, partial};
+                        return launch_fp8_gemm(dtype, a, L.dw, st);
                     })
                   : stage("fill_zero", [&] { return launch_fill_zero((float*)dW, K * N / 2, st); });
     return hip_status(e);

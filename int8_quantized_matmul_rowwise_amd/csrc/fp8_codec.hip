@@ -21,7 +21,9 @@ namespace {
 
 template <int DT>
 __global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t K,
-                                                       uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
+                                                       uint8_t* __restrict__ q, uint8_t* __restrict__ s,
+                                                       int32_t* __restrict__ zero, int64_t n_zero) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n_zero; i += (int64_t)gridDim.x * 256) zero[i] = 0;
     const int64_t kp = fp8_pitch(K), ng = ceil_div(K, 128);
     const int64_t total = M * ng;
     const int sl = threadIdx.x & 15;
@@ -49,6 +51,8 @@ struct TileParams {
     uint8_t* s;   // their scales: BLOCK ceil(R/128) x sp(C), ROWS fp8_row_scale_at
     uint8_t* qt;  // codes transposed: C x pitch(R)
     uint8_t* st;  // their scales: BLOCK ceil(C/128) x sp(R), COLS fp8_row_scale_at
+    int32_t* zero;
+    int64_t n_zero;
 };
 
 // MODE 0: BLOCK, transposed codes; 1: BLOCK, both; 2: COLS; 3: COLS and ROWS
@@ -60,6 +64,10 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(TileParams p) {
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int cc = tid & 15, rr = tid >> 4;  // columns 8 cc .. + 7, rows 8 rr .. + 7 of the tile
     const int64_t tc = blockIdx.x, tr = blockIdx.y;
+    if constexpr (!BLOCK) {
+        const int64_t id = (tr * gridDim.x + tc) * 256 + tid;
+        for (int64_t i = id; i < p.n_zero; i += (int64_t)gridDim.x * gridDim.y * 256) p.zero[i] = 0;
+    }
     const int64_t c0 = tc * 128, r0 = tr * 128;
     const int64_t cpitch = fp8_pitch(p.C), rpitch = fp8_pitch(p.R);
     const int64_t csp = fp8_scale_pitch_of(p.C), rsp = fp8_scale_pitch_of(p.R);
@@ -188,23 +196,24 @@ hipError_t tile_launch(int dt, const TileParams& p, hipStream_t stream) {
 hipError_t launch_fp8_weight(int dt, const void* W, int64_t K, int64_t N, uint8_t* Wq, uint8_t* s_w, uint8_t* WqT,
                              uint8_t* s_wT, hipStream_t stream) {
     if (K == 0 || N == 0) return hipSuccess;
-    const TileParams p{(const uint16_t*)W, K, N, WqT, s_wT, Wq, s_w};
+    const TileParams p{(const uint16_t*)W, K, N, WqT, s_wT, Wq, s_w, nullptr, 0};
     return WqT ? tile_launch<1>(dt, p, stream) : tile_launch<0>(dt, p, stream);
 }
 
-hipError_t launch_fp8_rows(int dt, const void* X, int64_t M, int64_t K, uint8_t* q, uint8_t* s, hipStream_t stream) {
+hipError_t launch_fp8_rows(int dt, const void* X, int64_t M, int64_t K, uint8_t* q, uint8_t* s, int32_t* zero,
+                           int64_t n_zero, hipStream_t stream) {
     if (M == 0 || K == 0) return hipSuccess;
-    const int64_t need = ceil_div(M * fp8_scale_pitch_of(K), 16);
+    const int64_t need = ceil_div(M * ceil_div(K, 128), 16);
     const unsigned grid = (unsigned)(need < 16384 ? need : 16384);
-    if (dt == F16) fp8_rows_kernel<F16><<<grid, 256, 0, stream>>>((const uint16_t*)X, M, K, q, s);
-    else fp8_rows_kernel<BF16><<<grid, 256, 0, stream>>>((const uint16_t*)X, M, K, q, s);
+    if (dt == F16) fp8_rows_kernel<F16><<<grid, 256, 0, stream>>>((const uint16_t*)X, M, K, q, s, zero, n_zero);
+    else fp8_rows_kernel<BF16><<<grid, 256, 0, stream>>>((const uint16_t*)X, M, K, q, s, zero, n_zero);
     return hipGetLastError();
 }
 
 hipError_t launch_fp8_cols(int dt, const void* A, int64_t R, int64_t C, uint8_t* qt, uint8_t* st, uint8_t* q, uint8_t* s,
-                           hipStream_t stream) {
+                           int32_t* zero, int64_t n_zero, hipStream_t stream) {
     if (R == 0 || C == 0) return hipSuccess;
-    const TileParams p{(const uint16_t*)A, R, C, q, s, qt, st};
+    const TileParams p{(const uint16_t*)A, R, C, q, s, qt, st, zero, n_zero};
     return q ? tile_launch<3>(dt, p, stream) : tile_launch<2>(dt, p, stream);
 }
 

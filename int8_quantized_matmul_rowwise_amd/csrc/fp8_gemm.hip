@@ -64,7 +64,32 @@ __host__ __device__ constexpr int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); 
 struct TiledParams {
     Fp8GemmArgs a;
     int tiles_m, tiles_n;
+    int split, part;  // parts of the sum and the stages of one (split 1: all of them)
 };
+
+constexpr int kCoherent = 16;  // cache policy: coherent across the XCDs, past their L2s
+
+// A workgroup's share of a tile's sums is in memory (stores of every wave issued): true for the
+// one that finds all `parts` in, which leaves the counter at zero.  flag: a word of LDS.
+__device__ __forceinline__ bool last_part(int32_t* counter, int parts, int* flag) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const int done = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
+        *flag = done == parts;
+        if (done == parts) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    const bool last = *flag != 0;
+    __syncthreads();  // before the word is used again
+    return last;
+}
+__device__ __forceinline__ v4f load_part(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t at) {
+    return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off, at, kCoherent));
+}
+__device__ __forceinline__ void store_part(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t at, const v4f& v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, off, at, kCoherent);
+}
 
 // the instruction with bytes bn, bm of the scale dwords (constants after unrolling)
 __device__ __forceinline__ v4f mfma_fp8(const v8i& n, const v8i& m, const v4f& c, int sn, int bn, int sm, int bm) {
@@ -77,8 +102,10 @@ __device__ __forceinline__ v4f mfma_fp8(const v8i& n, const v8i& m, const v4f& c
     return c;
 }
 
-// ROWB: B has a scale per row (else per 128 rows, one for a wave's columns)
-template <int DT, int WM, int WN, int NF, bool ROWB>
+// ROWB: B has a scale per row (else per 128 rows, one for a wave's columns).  SPLIT: few tiles; a
+// workgroup takes one part of one tile's stages, dumps its sums, and the last of the tile's parts
+// to end adds them up in their order and writes the output.
+template <int DT, int WM, int WN, int NF, bool ROWB, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams tp) {
     constexpr int kWaves = WM * WN;
     constexpr int BM = 16 * MF * WM, BN = 16 * NF * WN;
@@ -93,11 +120,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
     const int tid = threadIdx.x, lane = tid & 63, wu = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wu % WM, wn = wu / WM;
     const int li = lane & 15, q = lane >> 4;
-    const int nk = (int)(p.pitch / BK);
 
     // ---- this workgroup's tiles: a strided part of its XCD's contiguous run (ids congruent mod
     // 8 share an XCD), in groups of kGroupM row tiles
-    const int T = tp.tiles_m * tp.tiles_n;
+    const int T1 = tp.tiles_m * tp.tiles_n, T = SPLIT ? T1 * tp.split : T1;  // SPLIT: part after part
     const int bid = blockIdx.x, nwg = gridDim.x;
     const int xcd = bid % kXcds, local = bid / kXcds;
     const int per = T / kXcds, rem = T % kXcds;
@@ -105,8 +131,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
     const int on_xcd = (nwg - xcd + kXcds - 1) / kXcds;
     const int my_tiles = local < x_cnt ? (x_cnt - local + on_xcd - 1) / on_xcd : 0;
     if (my_tiles == 0) return;  // the same for every wave
+    // SPLIT: one tile (T workgroups), its stages from k0
+    const int part = SPLIT ? (x_start + local) / T1 : 0, k0 = SPLIT ? part * tp.part : 0;
+    const int all = (int)(p.pitch / BK), nk = SPLIT ? (all - k0 < tp.part ? all - k0 : tp.part) : all;
     auto tile_origin = [&](int i, int64_t& m0, int64_t& n0) LLMINT8_FP8_INLINE {
-        const int t = x_start + local + i * on_xcd;
+        const int t = SPLIT ? (x_start + local) - part * T1 : x_start + local + i * on_xcd;
         const int in_group = kGroupM * tp.tiles_n;
         const int first_m = (t / in_group) * kGroupM;
         const int gm = tp.tiles_m - first_m < kGroupM ? tp.tiles_m - first_m : kGroupM;
@@ -139,7 +168,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
     auto slot_a = [&](int s) LLMINT8_FP8_INLINE { return smem + s * kSlotA; };
     auto slot_b = [&](int s) LLMINT8_FP8_INLINE { return smem + 2 * kSlotA + s * kSlotB; };
     auto issue = [&](__amdgpu_buffer_rsrc_t rs, uint8_t* slot, int k, int j) LLMINT8_FP8_INLINE {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(slot + (4 * wu + j) * 1024), 16, (int)off[j], k * BK, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(slot + (4 * wu + j) * 1024), 16, (int)off[j], (k0 + k) * BK, 0, 0);
     };
 
     // ---- the scales of a stage: offsets and bytes of this tile's and the next tile's, held as
@@ -160,7 +189,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
     };
     scale_range(0, a_at0, a_n0, b_at0, b_n0);
     scale_range(1, a_at1, a_n1, b_at1, b_n1);
-    auto load_scales = [&](int next, int k, int& sm, int (&sn)[NS]) LLMINT8_FP8_INLINE {
+    auto load_scales = [&](int next, int kt, int& sm, int (&sn)[NS]) LLMINT8_FP8_INLINE {
+        const int k = k0 + kt;
         int li = lane & 15;  // opaque: the offsets are computed here, not held in registers
         asm volatile("" : "+v"(li));
         const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(p.sa + (int64_t)k * ta + pick(next, a_at0, a_at1), pick(next, a_n0, a_n1));
@@ -311,6 +341,34 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
             advance();
         }
         mfma_settle();
+        if constexpr (SPLIT) {
+            constexpr uint32_t kStep = 64 * kWaves * 16;  // bytes of one quad of every thread
+            const int tile = x_start + local - part * T1;
+            auto slot = [&](int i) LLMINT8_FP8_INLINE {
+                return buffer_rsrc(p.partial + ((int64_t)tile * tp.split + i) * (BM * BN), (int64_t)BM * BN * 4);
+            };
+            const __amdgpu_buffer_rsrc_t own = slot(part);
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int j = 0; j < MF; ++j) store_part(own, 16 * tid, (f * MF + j) * kStep, acc[f][j]);
+            if (!last_part(p.counters + tile, tp.split, (int*)slot_b(sb == 0 ? 2 : sb - 1))) break;
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int j = 0; j < MF; ++j) acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < tp.split; ++i) {
+                const __amdgpu_buffer_rsrc_t rs = slot(i);
+#pragma unroll
+                for (int f = 0; f < NF; ++f) {
+                    v4f v[MF];
+#pragma unroll
+                    for (int j = 0; j < MF; ++j) v[j] = load_part(rs, 16 * tid, (f * MF + j) * kStep);
+#pragma unroll
+                    for (int j = 0; j < MF; ++j) acc[f][j] += v[j];
+                }
+            }
+        }
         output(ti, sb == 0 ? 2 : sb - 1);  // the slot of the last stage
         if (ti + 1 < my_tiles) {
             ra0 = ra1;
@@ -337,32 +395,241 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
 }
 
 template <int DT, int WM, int WN, int NF, bool ROWB>
-hipError_t tiled_launch(const Fp8GemmArgs& a, hipStream_t stream) {
+hipError_t tiled_launch(const Fp8GemmArgs& a, int split, hipStream_t stream) {
     constexpr int BM = 16 * MF * WM, BN = 16 * NF * WN;
-    TiledParams p{a, (int)ceil_div(a.M, BM), (int)ceil_div(a.N, BN)};
+    const int nk = (int)(a.pitch / BK);
+    TiledParams p{a, (int)ceil_div(a.M, BM), (int)ceil_div(a.N, BN), split, (int)ceil_div(nk, split)};
+    const int64_t T = (int64_t)p.tiles_m * p.tiles_n;
+    if (split > 1) {
+        fp8_tiled_kernel<DT, WM, WN, NF, ROWB, true><<<(unsigned)(T * split), 64 * WM * WN, 0, stream>>>(p);
+        return hipGetLastError();
+    }
     int dev = 0, cus = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
     if (e != hipSuccess) return e;
-    const int64_t T = (int64_t)p.tiles_m * p.tiles_n, G = (int64_t)(cus > 0 ? cus : 1) * (8 / (WM * WN));
-    fp8_tiled_kernel<DT, WM, WN, NF, ROWB><<<(unsigned)(T < G ? T : G), 64 * WM * WN, 0, stream>>>(p);
+    const int64_t G = (int64_t)(cus > 0 ? cus : 1) * (8 / (WM * WN));
+    fp8_tiled_kernel<DT, WM, WN, NF, ROWB, false><<<(unsigned)(T < G ? T : G), 64 * WM * WN, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 template <int WM, int WN, int NF>
-hipError_t tiled(int dt, const Fp8GemmArgs& a, hipStream_t stream) {
+hipError_t tiled(int dt, const Fp8GemmArgs& a, int split, hipStream_t stream) {
     if (a.spitch == 0)
-        return dt == F16 ? tiled_launch<F16, WM, WN, NF, true>(a, stream) : tiled_launch<BF16, WM, WN, NF, true>(a, stream);
-    return dt == F16 ? tiled_launch<F16, WM, WN, NF, false>(a, stream) : tiled_launch<BF16, WM, WN, NF, false>(a, stream);
+        return dt == F16 ? tiled_launch<F16, WM, WN, NF, true>(a, split, stream) : tiled_launch<BF16, WM, WN, NF, true>(a, split, stream);
+    return dt == F16 ? tiled_launch<F16, WM, WN, NF, false>(a, split, stream) : tiled_launch<BF16, WM, WN, NF, false>(a, split, stream);
+}
+
+// ---- few rows (M <= 64): the product is bound by B's bytes, each read once straight into
+// registers.  A workgroup takes 16 NF columns n; its WV waves split the groups (wave w: w, w + WV,
+// ...), U of them in flight while U are multiplied, and their fp32 sums meet in LDS in the order of
+// the waves.  With FUSED (one piece of 16 rows), A is the 16-bit X itself: a lane codes its 32
+// values of the group (the row's largest magnitude over four lanes), which costs less than the
+// launch and the round trip of a separate coding pass while there are few rows.
+// With few columns the groups are split over `split` workgroups too (grid.y, `part` groups each):
+// their sums go through memory and the last one adds them up in their order.
+template <int DT, int MG, int NF, int WV, bool FUSED, int U, int OCC>
+__global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, int split, int part) {
+    static_assert(!FUSED || MG == 1, "one piece of rows");
+    constexpr int NA = FUSED ? 4 : 2 * MG;  // 16-byte pieces of A per lane and group
+    __shared__ v4f red[WV][NF * MG][64];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, q = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * NF);
+    const int all = (int)(p.pitch / BK), g0 = blockIdx.y * part, nk = all - g0 < part ? all : g0 + part;
+    const int64_t K = p.K;
+    const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.B + n0 * p.pitch, (p.N - n0 < 16 * NF ? p.N - n0 : 16 * NF) * p.pitch);
+    const uint8_t* sb = p.sb + (n0 >> 7) * p.spitch;  // 16 NF divides 128: one block of columns
+    const __amdgpu_buffer_rsrc_t ra = FUSED ? buffer_rsrc(p.X, p.M * K * 2) : buffer_rsrc(p.A, p.M * p.pitch);
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(p.sa, FUSED ? 0 : (int64_t)all * 64);
+    uint32_t b_off[NF], a_off[MG];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) b_off[f] = (uint32_t)((16 * f + li) * p.pitch + 32 * q);
+#pragma unroll
+    for (int j = 0; j < MG; ++j) a_off[j] = (uint32_t)(FUSED ? (li * K + 32 * q) * 2 : (16 * j + li) * p.pitch + 32 * q);
+
+    struct Group {
+        u32x4 b[NF][2], a[NA];
+        int eb, ea;
+    };
+    // group g (past the last: nothing in reach, zeros)
+    auto load = [&](int g, Group& r) LLMINT8_FP8_INLINE {
+        const bool in = g < nk;
+        const uint32_t far = in ? 0u : 0x80000000u;  // past every resource
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                r.b[f][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, (b_off[f] + (uint32_t)(g * BK + 16 * h)) | far, 0, 0));
+        if constexpr (FUSED) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t k = (int64_t)g * BK + 32 * q + 8 * i;  // past K: the next row's, or nothing
+                const uint32_t off = (a_off[0] + (uint32_t)(g * BK + 8 * i) * 2) | (in && k < K && li < p.M ? 0u : 0x80000000u);
+                r.a[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, off, 0, 0));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < MG; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    r.a[2 * j + h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, (a_off[j] + (uint32_t)(g * BK + 16 * h)) | far, 0, 0));
+            r.ea = (int)__builtin_amdgcn_raw_buffer_load_b32(rs, (uint32_t)(g * 64 + 4 * li) | far, 0, 0);
+        }
+        r.eb = in ? sb[g] : 0;
+    };
+    v4f acc[NF][MG] = {};
+    auto wide = [](const u32x4& lo, const u32x4& hi) LLMINT8_FP8_INLINE {
+        return __builtin_bit_cast(v8i, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    auto multiply = [&](const Group& r) LLMINT8_FP8_INLINE {
+        v8i a[MG];
+        int ea = r.ea;
+        if constexpr (FUSED) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = max_pattern(r.a[i], m);
+#pragma unroll
+            for (int off = 16; off <= 32; off <<= 1) {
+                const uint32_t o = (uint32_t)__shfl_xor((int)m, off, kWave);
+                m = m > o ? m : o;
+            }
+            ea = (int)e8m0_of(to_f32<DT>((uint16_t)m));
+            const float s = e8m0_value((uint32_t)ea);
+            u32x2 c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = e4m3x8<DT>(r.a[i], s);
+            a[0] = v8i{(int)c[0][0], (int)c[0][1], (int)c[1][0], (int)c[1][1], (int)c[2][0], (int)c[2][1], (int)c[3][0], (int)c[3][1]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < MG; ++j) a[j] = wide(r.a[2 * j], r.a[2 * j + 1]);
+        }
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int j = 0; j < MG; ++j) acc[f][j] = mfma_fp8(wide(r.b[f][0], r.b[f][1]), a[j], acc[f][j], r.eb, 0, ea, FUSED ? 0 : j);
+    };
+    Group x[U], y[U];
+    int g = g0 + w;
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(g + u * WV, x[u]);
+    while (g < nk) {  // the groups are taken U at a time, two sets in turn
+        g += U * WV;
+#pragma unroll
+        for (int u = 0; u < U; ++u) load(g + u * WV, y[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) multiply(x[u]);
+        if (g >= nk) break;
+        g += U * WV;
+#pragma unroll
+        for (int u = 0; u < U; ++u) load(g + u * WV, x[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) multiply(y[u]);
+    }
+    mfma_settle();
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int j = 0; j < MG; ++j) red[w][f * MG + j][lane] = acc[f][j];
+    __syncthreads();
+    auto sum = [&](int t) LLMINT8_FP8_INLINE {
+        v4f s = red[0][t][lane];
+#pragma unroll
+        for (int i = 1; i < WV; ++i) s += red[i][t][lane];
+        return s;
+    };
+    auto store = [&](int t, const v4f& s) LLMINT8_FP8_INLINE {
+        const int64_t m = 16 * (t % MG) + li, n = n0 + 16 * (t / MG) + 4 * q;
+        if (m < p.M && n < p.N) {  // N is a multiple of 8
+            u32x2 v;
+            v[0] = (uint32_t)from_f32<DT>(s[0]) | ((uint32_t)from_f32<DT>(s[1]) << 16);
+            v[1] = (uint32_t)from_f32<DT>(s[2]) | ((uint32_t)from_f32<DT>(s[3]) << 16);
+            *(u32x2*)(p.Y + m * p.N + n) = v;
+        }
+    };
+    constexpr int kTiles = NF * MG;
+    if (split == 1) {
+        for (int t = w; t < kTiles; t += WV) store(t, sum(t));
+        return;
+    }
+    const __amdgpu_buffer_rsrc_t rp = buffer_rsrc(p.partial + (int64_t)blockIdx.x * split * (kTiles * 256), (int64_t)split * kTiles * 1024);
+    for (int t = w; t < kTiles; t += WV) store_part(rp, 16 * lane, (uint32_t)((blockIdx.y * kTiles + t) * 1024), sum(t));
+    __shared__ int flag;
+    if (!last_part(p.counters + blockIdx.x, split, &flag)) return;
+    for (int t = w; t < kTiles; t += WV) {
+        v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < split; ++i) s += load_part(rp, 16 * lane, (uint32_t)((i * kTiles + t) * 1024));
+        store(t, s);
+    }
+}
+
+template <int DT, int MG, int NF, int WV, bool FUSED, int U, int OCC>
+hipError_t small_launch(const Fp8GemmArgs& a, int split, hipStream_t stream) {
+    const int part = (int)ceil_div(a.pitch / BK, split);
+    const dim3 g((unsigned)ceil_div(a.N, 16 * NF), (unsigned)split);
+    fp8_small_kernel<DT, MG, NF, WV, FUSED, U, OCC><<<g, 64 * WV, 0, stream>>>(a, split, part);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t small(const Fp8GemmArgs& a, const Fp8Plan& plan, hipStream_t stream) {
+    if (plan.kind == Fp8Plan::kFused) return small_launch<DT, 1, 1, 8, true, 1, 4>(a, plan.split, stream);
+    switch (4 * plan.pieces + plan.columns) {
+        case 4 + 1: return small_launch<DT, 1, 1, 4, false, 2, 4>(a, plan.split, stream);
+        case 4 + 2: return small_launch<DT, 1, 2, 4, false, 1, 4>(a, plan.split, stream);
+        case 8 + 1: return small_launch<DT, 2, 1, 4, false, 1, 4>(a, plan.split, stream);
+        case 8 + 2: return small_launch<DT, 2, 2, 8, false, 1, 2>(a, plan.split, stream);
+        case 16 + 1: return small_launch<DT, 4, 1, 4, false, 1, 4>(a, plan.split, stream);
+        default: return small_launch<DT, 4, 4, 8, false, 1, 2>(a, plan.split, stream);
+    }
+}
+
+// parts of `groups` groups such that none is empty and each has at least `least`
+int parts(int64_t groups, int64_t wanted, int64_t least) {
+    int64_t s = groups / least < wanted ? groups / least : wanted;
+    if (s < 2) return 1;
+    const int64_t part = ceil_div(groups, s);
+    return (int)ceil_div(groups, part);
 }
 
 }  // namespace
 
-hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& a, hipStream_t stream) {
+Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb) {
+    Fp8Plan p{Fp8Plan::kTile256, 0, 0, 1, 0, 0};
+    int64_t out = 256 * 256;
+    if (M <= 64 && !rowb) {
+        const bool fused = x16 && M <= 4 && N * nk <= (int64_t)1 << 17;
+        p.kind = fused ? Fp8Plan::kFused : Fp8Plan::kSmall;
+        p.pieces = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
+        p.columns = fused ? 1 : (p.pieces == 1 ? (N >= 12288 ? 2 : 1) : (p.pieces == 2 ? (N >= 8192 ? 2 : 1) : (N >= 12288 ? 4 : 1)));
+        p.tiles = ceil_div(N, 16 * p.columns);
+        if (!fused && p.tiles < 128) p.split = parts(nk, 256 / p.tiles, 8);
+        out = 256 * p.columns * p.pieces;
+    } else {
+        const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256), t128 = ceil_div(M, 128) * ceil_div(N, 128);
+        if (t256 < 256) {
+            p.kind = Fp8Plan::kTile128;
+            out = 128 * 128;
+            p.tiles = t128;
+            if (M > 128 && t256 <= 128 && nk >= 32) {
+                p.kind = Fp8Plan::kTile256;
+                out = 256 * 256;
+                p.tiles = t256;
+                p.split = parts(nk, 256 / t256, 8);
+            } else if (t128 <= 256) {
+                p.split = parts(nk, 512 / t128, 8);
+            }
+        }
+    }
+    p.partial_bytes = p.split > 1 ? p.tiles * p.split * out * 4 : 0;
+    return p;
+}
+
+hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& a, const Fp8Plan& plan, hipStream_t stream) {
     if (a.M == 0 || a.N == 0) return hipSuccess;
-    // 256 x 256 tiles where they fill the compute units, else 128 x 128
-    if (ceil_div(a.M, 256) * ceil_div(a.N, 256) >= 256) return tiled<4, 2, 8>(dt, a, stream);
-    return tiled<2, 2, 4>(dt, a, stream);
+    if (plan.kind == Fp8Plan::kTile256) return tiled<4, 2, 8>(dt, a, plan.split, stream);
+    if (plan.kind == Fp8Plan::kTile128) return tiled<2, 2, 4>(dt, a, plan.split, stream);
+    return dt == F16 ? small<F16>(a, plan, stream) : small<BF16>(a, plan, stream);
 }
 
 }  // namespace llmint8

@@ -199,11 +199,26 @@ hipError_t launch_gemm_group_small(int dt, const int8_t* Xq, const int8_t* Xqb, 
 hipError_t launch_fp8_weight(int dt, const void* W, int64_t K, int64_t N, uint8_t* Wq, uint8_t* s_w, uint8_t* WqT,
                              uint8_t* s_wT, hipStream_t stream);
 // q M x pitch(K); s: a scale per row and group of 128 columns (at fp8_row_scale_at)
-hipError_t launch_fp8_rows(int dt, const void* X, int64_t M, int64_t K, uint8_t* q, uint8_t* s, hipStream_t stream);
+// (also zeroes zero[0, n_zero): the counters of the products' split sums)
+hipError_t launch_fp8_rows(int dt, const void* X, int64_t M, int64_t K, uint8_t* q, uint8_t* s, int32_t* zero,
+                           int64_t n_zero, hipStream_t stream);
 // qt C x pitch(R): the codes of A (R x C) transposed, with a scale st per column of A and group
 // of 128 rows (at fp8_row_scale_at); q, s (both or neither): launch_fp8_rows of the same matrix
+// (and zeroes zero[0, n_zero) as above)
 hipError_t launch_fp8_cols(int dt, const void* A, int64_t R, int64_t C, uint8_t* qt, uint8_t* st, uint8_t* q, uint8_t* s,
-                           hipStream_t stream);
+                           int32_t* zero, int64_t n_zero, hipStream_t stream);
+
+// How a product of M x N outputs over nk groups runs.
+struct Fp8Plan {
+    enum Kind { kTile256, kTile128, kSmall, kFused } kind;
+    int pieces;   // kSmall: pieces of 16 rows m (1, 2 or 4); kFused: 1
+    int columns;  // kSmall, kFused: pieces of 16 columns of a workgroup
+    int split;    // parts of the sum, each a workgroup's; their partial sums go through memory
+    int64_t tiles;  // counters when split > 1
+    int64_t partial_bytes;
+};
+// x16: A is at hand in 16 bits (it may be coded in the product kernel); rowb: B has a scale per row
+Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb);
 
 struct Fp8GemmArgs {
     const uint8_t* A;  // M rows of codes
@@ -213,8 +228,12 @@ struct Fp8GemmArgs {
     const uint8_t* sb;  // scales of B: as A's, or ceil(N/128) rows, one scale per 128 rows of B
     int64_t spitch;     // bytes of such a scale row; 0: B has a scale per row
     uint16_t* Y;        // M x N
+    const uint16_t* X;  // kFused: A's values, M x K
+    int64_t K;
+    int32_t* counters;  // split > 1: one per tile, zero; the product leaves them so
+    float* partial;
 };
-hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& p, hipStream_t stream);
+hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& p, const Fp8Plan& plan, hipStream_t stream);
 
 struct Fp8MoeArgs {
     const uint16_t* X;

@@ -20,7 +20,7 @@ def quant(**kw):
 
 
 def mm(**kw):
-    a = dict(X=A, M=4, K=64, dt=0, Wq=B, s=C, N=72, Y=D, ws=E, wsb=BIG >> 10)
+    a = dict(X=A, M=100, K=64, dt=0, Wq=B, s=C, N=72, Y=D, ws=E, wsb=BIG >> 10)
     a.update(kw)
     return lm.lib().fp8_matmul_block(a["X"], a["M"], a["K"], a["dt"], a["Wq"], a["s"], a["N"], a["Y"], a["ws"], a["wsb"], None)
 
@@ -53,7 +53,7 @@ def test_quantize_refuses(kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=-1), lm.EINVAL), (dict(M=-1), lm.EINVAL), (dict(K=24), lm.EINVAL), (dict(N=12), lm.EINVAL),
-    (dict(K=(1 << 22) + 16), lm.ERANGE), (dict(M=1 << 31), lm.EINVAL), (dict(M=64 * 65535 + 1), lm.ERANGE),
+    (dict(K=(1 << 22) + 16), lm.ERANGE), (dict(M=1 << 31), lm.EINVAL), (dict(M=(1 << 22) + 1), lm.ERANGE),
     (dict(X=None), lm.EINVAL), (dict(X=A + 8), lm.EINVAL), (dict(Wq=None), lm.EINVAL), (dict(Wq=B + 8), lm.EINVAL),
     (dict(s=None), lm.EINVAL), (dict(s=C + 1), lm.EINVAL), (dict(Y=None), lm.EINVAL), (dict(Y=D + 2), lm.EINVAL),
     (dict(ws=None), lm.EWORKSPACE), (dict(ws=E + 8), lm.EWORKSPACE), (dict(wsb=100), lm.EWORKSPACE),
@@ -101,12 +101,15 @@ def test_sizes():
     for dx in (False, True):
         for dw in (False, True):
             assert lm.fp8_matmul_block_backward_workspace_bytes(130, 272, 136, dx, dw) >= dx * 130 * 256 + dw * (136 + 272) * 256
+    assert lm.fp8_matmul_block_workspace_bytes(130, 272, 136) >= 130 * 384
+    assert lm.fp8_matmul_block_workspace_bytes(0, 272, 136) == lm.fp8_matmul_block_workspace_bytes(130, 0, 136) == 0
 
 
 def _calls():
     return {
         "quantize": (lambda: quant(), ["fp8_weight"]),
         "matmul": (lambda: mm(M=300, K=1024, N=520), ["fp8_rows", "fp8_gemm"]),
+        "matmul_fused": (lambda: mm(M=2, K=1024, N=520, ws=None, wsb=0), ["fp8_gemm"]),
         "matmul_k0": (lambda: mm(K=0), ["fill_zero"]),
         "backward": (lambda: back(M=300, K=1024, N=520), ["fp8_cols_dy", "fp8_cols_x", "fp8_gemm_dx", "fp8_gemm_dw"]),
         "backward_dx": (lambda: back(M=300, dW=None), ["fp8_rows", "fp8_gemm_dx"]),

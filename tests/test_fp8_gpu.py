@@ -101,7 +101,10 @@ def lattice(g, *shape, dt, spread=0):
 
 SHAPES = [(1, 16, 8), (1, 4096, 264), (3, 144, 1032), (16, 272, 520), (17, 1040, 264), (33, 528, 136), (64, 1664, 72),
           (65, 256, 136), (100, 640, 2056), (128, 2064, 264), (129, 128, 264), (300, 1040, 520), (257, 400, 1288),
-          (520, 144, 776)]
+          (520, 144, 776),
+          # split sums: few columns and many groups, with parts of unequal length
+          (2, 16384, 520), (16, 4240, 264), (30, 8208, 72), (64, 2192, 264), (40, 4096, 8200), (64, 1040, 12296),
+          (100, 4240, 264), (300, 8208, 520), (260, 4240, 2056), (6, 1040, 16392), (4, 16400, 8200)]
 
 
 @pytest.mark.parametrize("dt", DTS)
@@ -231,7 +234,7 @@ def test_matmul_writes_its_output_alone(M, K, N):
 
 # ---- gradient
 
-BACK = [(1, 16, 8), (5, 144, 136), (128, 256, 128), (130, 272, 264), (333, 1040, 520), (64, 2064, 72), (700, 400, 1288)]
+BACK = [(40, 264 * 16, 136), (2100, 272, 264), (300, 272, 4360), (24, 400, 6152), (1, 16, 8), (5, 144, 136), (128, 256, 128), (130, 272, 264), (333, 1040, 520), (64, 2064, 72), (700, 400, 1288)]
 
 
 @pytest.mark.parametrize("dt", DTS)
