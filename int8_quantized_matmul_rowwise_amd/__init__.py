@@ -21,7 +21,6 @@ float8_e8m0fnu): a product, its gradient, and a mixture-of-experts layer for few
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -520,10 +519,11 @@ def _fp8_arg(t, name: str, dtypes, shape=None, device=None) -> torch.Tensor:
 
 
 def _fp8_on(device: torch.device, stream):
-    """The context in which a call allocates and enqueues: the tensors' device, and the given
-    stream where it is not that device's current one (what is allocated then belongs to it)."""
+    """None where a call allocates and enqueues as things stand (the current device, its current
+    stream), else the context to do it in: the tensors' device, and the given stream (what is
+    allocated then belongs to it)."""
     if stream is None:
-        return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         raw = int(getattr(stream, "cuda_stream", stream) or 0)
         stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
@@ -532,10 +532,15 @@ def _fp8_on(device: torch.device, stream):
     return torch.cuda.stream(stream)
 
 
-def _fp8_workspace(ws, nbytes: int, device) -> torch.Tensor:
+def _fp8_workspace(ws, nbytes: int, device):
+    """(the workspace, its address, its bytes)"""
     if ws is None:
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    return _fp8_arg(ws, "workspace", (torch.uint8,), device=device)
+        if nbytes == 0:
+            return None, None, 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        _fp8_arg(ws, "workspace", (torch.uint8,), device=device)
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def fp8_quantize_weight_block(W: torch.Tensor, transposed: bool = False, stream=None) -> Tuple[torch.Tensor, ...]:
@@ -545,16 +550,18 @@ def fp8_quantize_weight_block(W: torch.Tensor, transposed: bool = False, stream=
         raise ValueError("W must be 2-D")
     K, N = W.shape
     dev = W.device
-    with _fp8_on(dev, stream):
-        out = [torch.empty((N, fp8_code_pitch(K)), dtype=_E4M3[0], device=dev),
-               torch.empty((-(-N // 128), fp8_scale_pitch(K)), dtype=_E8M0[0], device=dev)]
-        if transposed:
-            out += [torch.empty((K, fp8_code_pitch(N)), dtype=_E4M3[0], device=dev),
-                    torch.empty((-(-K // 128), fp8_scale_pitch(N)), dtype=_E8M0[0], device=dev)]
-        ptrs = [t.data_ptr() for t in out] + [None] * (4 - len(out))
-        _check(lib().fp8_quantize_weight_block(W.data_ptr(), K, N, _DT[W.dtype], *ptrs,
-                                               torch._C._cuda_getCurrentRawStream(dev.index)),
-               "fp8_quantize_weight_block")
+    on = _fp8_on(dev, stream)
+    if on is not None:
+        with on:
+            return fp8_quantize_weight_block(W, transposed)
+    out = [torch.empty((N, fp8_code_pitch(K)), dtype=_E4M3[0], device=dev),
+           torch.empty((-(-N // 128), fp8_scale_pitch(K)), dtype=_E8M0[0], device=dev)]
+    if transposed:
+        out += [torch.empty((K, fp8_code_pitch(N)), dtype=_E4M3[0], device=dev),
+                torch.empty((-(-K // 128), fp8_scale_pitch(N)), dtype=_E8M0[0], device=dev)]
+    ptrs = [t.data_ptr() for t in out] + [None] * (4 - len(out))
+    _check(lib().fp8_quantize_weight_block(W.data_ptr(), K, N, _DT[W.dtype], *ptrs,
+                                           torch._C._cuda_getCurrentRawStream(dev.index)), "fp8_quantize_weight_block")
     return tuple(out)
 
 
@@ -569,20 +576,24 @@ def fp8_matmul_block(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, Y
         raise ValueError("X must be 2-D")
     M, K = X.shape
     dev = X.device
+    on = _fp8_on(dev, stream)
+    if on is not None:
+        with on:
+            return fp8_matmul_block(X, Wq, w_scale, Y, workspace)
     if _fp8_arg(Wq, "Wq", _E4M3, device=dev).dim() != 2 or Wq.shape[1] != fp8_code_pitch(K):
         raise ValueError(f"Wq must be N x {fp8_code_pitch(K)} for K = {K}, got {tuple(Wq.shape)}")
     N = Wq.shape[0]
     _fp8_arg(w_scale, "w_scale", _E8M0, (-(-N // 128), fp8_scale_pitch(K)), dev)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=X.dtype, device=dev)
+    else:
+        _fp8_arg(Y, "Y", (X.dtype,), (M, N), dev)
     L = lib()
-    with _fp8_on(dev, stream):
-        if Y is None:
-            Y = torch.empty((M, N), dtype=X.dtype, device=dev)
-        else:
-            _fp8_arg(Y, "Y", (X.dtype,), (M, N), dev)
-        ws = _fp8_workspace(workspace, L.fp8_matmul_block_workspace_bytes(M, K, N), dev)
-        rc = L.fp8_matmul_block(X.data_ptr(), M, K, _DT[X.dtype], Wq.data_ptr(), w_scale.data_ptr(), N, Y.data_ptr(),
-                                ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev.index))
-    _check(rc, "fp8_matmul_block")
+    ws, at, size = _fp8_workspace(workspace, L.fp8_matmul_block_workspace_bytes(M, K, N), dev)
+    rc = L.fp8_matmul_block(X.data_ptr(), M, K, _DT[X.dtype], Wq.data_ptr(), w_scale.data_ptr(), N, Y.data_ptr(),
+                            at, size, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "fp8_matmul_block")
     return Y
 
 
@@ -600,6 +611,10 @@ def fp8_matmul_block_backward(dY: torch.Tensor, X: Optional[torch.Tensor], WqT: 
         raise ValueError("dY must be 2-D")
     M, N = dY.shape
     dev, t = dY.device, dY.dtype
+    on = _fp8_on(dev, stream)
+    if on is not None:
+        with on:
+            return fp8_matmul_block_backward(dY, X, WqT, wT_scale, need_dx, need_dw, dX, dW, workspace)
     if not need_dx and not need_dw:
         return None, None
     if need_dw:
@@ -614,25 +629,23 @@ def fp8_matmul_block_backward(dY: torch.Tensor, X: Optional[torch.Tensor], WqT: 
         K = WqT.shape[0]
         _fp8_arg(wT_scale, "wT_scale", _E8M0, (-(-K // 128), fp8_scale_pitch(N)), dev)
     L = lib()
-    with _fp8_on(dev, stream):
-        if not need_dx:
-            dX = None
-        elif dX is None:
-            dX = torch.empty((M, K), dtype=t, device=dev)
-        else:
-            _fp8_arg(dX, "dX", (t,), (M, K), dev)
-        if not need_dw:
-            dW = None
-        elif dW is None:
-            dW = torch.empty((K, N), dtype=t, device=dev)
-        else:
-            _fp8_arg(dW, "dW", (t,), (K, N), dev)
-        ws = _fp8_workspace(workspace, L.fp8_matmul_block_backward_workspace_bytes(M, K, N, int(need_dx), int(need_dw)), dev)
-        rc = L.fp8_matmul_block_backward(dY.data_ptr(), X.data_ptr() if need_dw else None, M, K, N, _DT[t],
-                                         WqT.data_ptr() if need_dx else None, wT_scale.data_ptr() if need_dx else None,
-                                         dX.data_ptr() if need_dx else None, dW.data_ptr() if need_dw else None,
-                                         ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev.index))
-    _check(rc, "fp8_matmul_block_backward")
+    if not need_dx:
+        dX = None
+    elif dX is None:
+        dX = torch.empty((M, K), dtype=t, device=dev)
+    else:
+        _fp8_arg(dX, "dX", (t,), (M, K), dev)
+    if not need_dw:
+        dW = None
+    elif dW is None:
+        dW = torch.empty((K, N), dtype=t, device=dev)
+    else:
+        _fp8_arg(dW, "dW", (t,), (K, N), dev)
+    ws, at, size = _fp8_workspace(workspace, L.fp8_matmul_block_backward_workspace_bytes(M, K, N, int(need_dx), int(need_dw)), dev)
+    _check(L.fp8_matmul_block_backward(dY.data_ptr(), X.data_ptr() if need_dw else None, M, K, N, _DT[t],
+                                       WqT.data_ptr() if need_dx else None, wT_scale.data_ptr() if need_dx else None,
+                                       dX.data_ptr() if need_dx else None, dW.data_ptr() if need_dw else None,
+                                       at, size, torch._C._cuda_getCurrentRawStream(dev.index)), "fp8_matmul_block_backward")
     return dX, dW
 
 
@@ -652,30 +665,37 @@ def fp8_moe_block(X: torch.Tensor, logits: torch.Tensor, W13q: torch.Tensor, w13
         raise ValueError("X must be 2-D")
     T, H = X.shape
     dev = X.device
+    on = _fp8_on(dev, stream)
+    if on is not None:
+        with on:
+            return fp8_moe_block(X, logits, W13q, w13_scale, W2q, w2_scale, top_k, renormalize, Y, workspace)
     if _fp8_arg(logits, "logits", (torch.float32,), device=dev).dim() != 2 or logits.shape[0] != T:
         raise ValueError(f"logits must be {T} x E, got {tuple(logits.shape)}")
     E = logits.shape[1]
-    if _fp8_arg(W13q, "W13q", _E4M3, device=dev).dim() != 3 or W13q.shape[1] % 2:
+    if not isinstance(W13q, torch.Tensor) or W13q.dim() != 3 or W13q.shape[1] % 2:
         raise ValueError("W13q must be E x 2I x code_pitch(H)")
     I = W13q.shape[1] // 2
     _fp8_arg(W13q, "W13q", _E4M3, (E, 2 * I, fp8_code_pitch(H)), dev)
     _fp8_arg(w13_scale, "w13_scale", _E8M0, (E, -(-2 * I // 128), fp8_scale_pitch(H)), dev)
     _fp8_arg(W2q, "W2q", _E4M3, (E, H, fp8_code_pitch(I)), dev)
     _fp8_arg(w2_scale, "w2_scale", _E8M0, (E, -(-H // 128), fp8_scale_pitch(I)), dev)
+    if Y is None:
+        Y = torch.empty((T, H), dtype=X.dtype, device=dev)
+    else:
+        _fp8_arg(Y, "Y", (X.dtype,), (T, H), dev)
+    top_k = int(top_k)
+    if not 0 < top_k <= E:
+        raise ValueError(f"top_k must be in 1 .. {E}, got {top_k}")
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    p = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     L = lib()
-    with _fp8_on(dev, stream):
-        if Y is None:
-            Y = torch.empty((T, H), dtype=X.dtype, device=dev)
-        else:
-            _fp8_arg(Y, "Y", (X.dtype,), (T, H), dev)
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-        p = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-        ws = _fp8_workspace(workspace, L.fp8_moe_block_workspace_bytes(T, H, I, E, top_k), dev)
-        rc = L.fp8_moe_block(X.data_ptr(), T, H, _DT[X.dtype], logits.data_ptr(), E, top_k, int(renormalize),
-                             W13q.data_ptr(), w13_scale.data_ptr(), W2q.data_ptr(), w2_scale.data_ptr(), I,
-                             Y.data_ptr(), ids.data_ptr(), p.data_ptr(), ws.data_ptr(), ws.numel(),
-                             torch._C._cuda_getCurrentRawStream(dev.index))
-    _check(rc, "fp8_moe_block")
+    ws, at, size = _fp8_workspace(workspace, L.fp8_moe_block_workspace_bytes(T, H, I, E, top_k), dev)
+    rc = L.fp8_moe_block(X.data_ptr(), T, H, _DT[X.dtype], logits.data_ptr(), E, top_k, int(renormalize),
+                         W13q.data_ptr(), w13_scale.data_ptr(), W2q.data_ptr(), w2_scale.data_ptr(), I,
+                         Y.data_ptr(), ids.data_ptr(), p.data_ptr(), at, size,
+                         torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "fp8_moe_block")
     return Y, ids, p
 
 

@@ -439,7 +439,7 @@ __global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, 
     const int all = (int)(p.pitch / BK), g0 = blockIdx.y * part, nk = all - g0 < part ? all : g0 + part;
     const int64_t K = p.K;
     const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.B + n0 * p.pitch, (p.N - n0 < 16 * NF ? p.N - n0 : 16 * NF) * p.pitch);
-    const uint8_t* sb = p.sb + (n0 >> 7) * p.spitch;  // 16 NF divides 128: one block of columns
+    const __amdgpu_buffer_rsrc_t rsb = buffer_rsrc(p.sb + (n0 >> 7) * p.spitch, p.spitch);  // 16 NF divides 128: one block
     const __amdgpu_buffer_rsrc_t ra = FUSED ? buffer_rsrc(p.X, p.M * K * 2) : buffer_rsrc(p.A, p.M * p.pitch);
     const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(p.sa, FUSED ? 0 : (int64_t)all * 64);
     uint32_t b_off[NF], a_off[MG];
@@ -450,7 +450,7 @@ __global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, 
 
     struct Group {
         u32x4 b[NF][2], a[NA];
-        int eb, ea;
+        int eb, ea, shift;
     };
     // group g (past the last: nothing in reach, zeros)
     auto load = [&](int g, Group& r) LLMINT8_FP8_INLINE {
@@ -476,7 +476,10 @@ __global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, 
                     r.a[2 * j + h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, (a_off[j] + (uint32_t)(g * BK + 16 * h)) | far, 0, 0));
             r.ea = (int)__builtin_amdgcn_raw_buffer_load_b32(rs, (uint32_t)(g * 64 + 4 * li) | far, 0, 0);
         }
-        r.eb = in ? sb[g] : 0;
+        // the dword that holds the byte (of a byte load the compiler widens the value at once, and
+        // waits for it there); the byte is shifted down where it is used
+        r.eb = (int)__builtin_amdgcn_raw_buffer_load_b32(rsb, (uint32_t)(g & ~3) | far, 0, 0);
+        r.shift = 8 * (g & 3);
     };
     v4f acc[NF][MG] = {};
     auto wide = [](const u32x4& lo, const u32x4& hi) LLMINT8_FP8_INLINE {
@@ -484,7 +487,9 @@ __global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, 
     };
     auto multiply = [&](const Group& r) LLMINT8_FP8_INLINE {
         v8i a[MG];
-        int ea = r.ea;
+        int ea = r.ea, eb = r.eb;
+        asm volatile("" : "+v"(eb));
+        eb = (int)((uint32_t)eb >> r.shift);
         if constexpr (FUSED) {
             uint32_t m = 0;
 #pragma unroll
@@ -507,7 +512,7 @@ __global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, 
 #pragma unroll
         for (int f = 0; f < NF; ++f)
 #pragma unroll
-            for (int j = 0; j < MG; ++j) acc[f][j] = mfma_fp8(wide(r.b[f][0], r.b[f][1]), a[j], acc[f][j], r.eb, 0, ea, FUSED ? 0 : j);
+            for (int j = 0; j < MG; ++j) acc[f][j] = mfma_fp8(wide(r.b[f][0], r.b[f][1]), a[j], acc[f][j], eb, 0, ea, FUSED ? 0 : j);
     };
     Group x[U], y[U];
     int g = g0 + w;
@@ -533,9 +538,13 @@ __global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, 
         for (int j = 0; j < MG; ++j) red[w][f * MG + j][lane] = acc[f][j];
     __syncthreads();
     auto sum = [&](int t) LLMINT8_FP8_INLINE {
-        v4f s = red[0][t][lane];
+        v4f v[WV];  // all reads first
 #pragma unroll
-        for (int i = 1; i < WV; ++i) s += red[i][t][lane];
+        for (int i = 0; i < WV; ++i) v[i] = red[i][t][lane];
+        __builtin_amdgcn_sched_barrier(0);
+        v4f s = v[0];
+#pragma unroll
+        for (int i = 1; i < WV; ++i) s += v[i];
         return s;
     };
     auto store = [&](int t, const v4f& s) LLMINT8_FP8_INLINE {
@@ -579,8 +588,9 @@ hipError_t small(const Fp8GemmArgs& a, const Fp8Plan& plan, hipStream_t stream) 
         case 4 + 2: return small_launch<DT, 1, 2, 4, false, 1, 4>(a, plan.split, stream);
         case 8 + 1: return small_launch<DT, 2, 1, 4, false, 1, 4>(a, plan.split, stream);
         case 8 + 2: return small_launch<DT, 2, 2, 8, false, 1, 2>(a, plan.split, stream);
+        case 8 + 4: return small_launch<DT, 2, 4, 4, false, 1, 2>(a, plan.split, stream);
         case 16 + 1: return small_launch<DT, 4, 1, 4, false, 1, 4>(a, plan.split, stream);
-        default: return small_launch<DT, 4, 4, 8, false, 1, 2>(a, plan.split, stream);
+        default: return small_launch<DT, 4, 2, 4, false, 1, 2>(a, plan.split, stream);
     }
 }
 
@@ -601,7 +611,7 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb) {
         const bool fused = x16 && M <= 4 && N * nk <= (int64_t)1 << 17;
         p.kind = fused ? Fp8Plan::kFused : Fp8Plan::kSmall;
         p.pieces = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
-        p.columns = fused ? 1 : (p.pieces == 1 ? (N >= 12288 ? 2 : 1) : (p.pieces == 2 ? (N >= 8192 ? 2 : 1) : (N >= 12288 ? 4 : 1)));
+        p.columns = fused || N < 8192 ? 1 : (p.pieces == 2 && N >= 12288 ? 4 : (p.pieces == 1 && N < 12288 ? 1 : 2));
         p.tiles = ceil_div(N, 16 * p.columns);
         if (!fused && p.tiles < 128) p.split = parts(nk, 256 / p.tiles, 8);
         out = 256 * p.columns * p.pieces;
