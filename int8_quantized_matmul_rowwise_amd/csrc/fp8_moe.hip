@@ -6,21 +6,26 @@
 //     (renormalize) or over all;
 //   [g; u] = W13hat_e x (2I values), h = RN_T(silu(g) u), y = RN_T(sum_j p_j W2hat_e h).
 //
-// Bound by the bytes of the experts met, each read once (once per kMaxPieces * 16 tokens of one
-// expert).  Two launches: gate, up and SwiGLU (h goes to the workspace), then down and the
-// weighted sum; with more than kRouteTokens tokens a third one before them chooses the experts,
-// which otherwise every workgroup of the first does for itself (that costs less than a launch).
+// Bound by the bytes of the experts met, each read once (once per 16 MG tokens of one expert).  Two
+// launches: gate, up and SwiGLU (h goes to the workspace), then down and the weighted sum; a third
+// one before them chooses the experts where every workgroup of the first doing it for itself would
+// cost more than a launch (more than kRouteTokens tokens, or many workgroups).
 //
 // The products run on 16-bit matrix instructions (16x16x32): a code is exact in either 16-bit
 // type, so nothing is lost against the coded weight, and the activations keep their 16 bits --
 // few tokens leave the matrix units idle anyway.  Weights are the row side (16 rows), an expert's
-// tokens the column side, 16 to a piece; lane l holds bytes 32 (l / 16) .. + 31 of its row's
-// group of 128, and instruction s of a group takes 8 s .. 8 s + 7 of them from both operands (the
-// order of a sum's terms is free, as long as both agree).  bf16 takes the scale in the
-// conversion (an exact shift of the exponent); fp16 could not hold it, so there each group's sum
-// is added with its scale.  Sums are fp32; the waves of a workgroup split them and meet in LDS in
-// a fixed order, and every token has a column of its own, so neither the order of atomics nor a
-// token's neighbours change its bits.
+// tokens the column side, 16 to a piece; a group of 128 takes four instructions, whose order of
+// the terms is free as long as both operands agree.  bf16 takes the scale in the conversion (an
+// exact shift of the exponent); fp16 could not hold it, so there each group's sum is added with its
+// scale.  Sums are fp32; the waves of a workgroup split them and meet in LDS in a fixed order, and
+// every token has a column of its own, so neither the order of atomics nor a token's neighbours
+// change its bits.
+//
+// Two forms of both launches.  Where experts have few tokens (a mean of kLightMean at most) the
+// work is cut finer, so that small layers fill the compute units: the 16 rows of an instruction
+// are 8 gate and the same 8 up columns in the first launch, and 8 columns of two experts in the
+// second, whose tokens are the two halves of its columns (the products of one expert's rows with
+// the other's tokens are not used).  Otherwise 16 columns and MG pieces of tokens.
 #include "fp8_common.hpp"
 #include "launch.hpp"
 
@@ -31,18 +36,33 @@ namespace {
 constexpr int kMaxTokens = 128;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 16;
-constexpr int kUpWaves = 8;
-constexpr int kRouteTokens = kUpWaves;  // a wave per token
+constexpr int kUpWaves = 8, kLightUpWaves = 4;
+constexpr int kRouteTokens = kLightUpWaves;  // one a wave
+constexpr int kLightMean = 6;
 
 #define LLMINT8_MOE_INLINE __attribute__((always_inline))
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)bytes, 0x00020000);
 }
-__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t off, int at = 0) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, at, 0));
 }
 constexpr uint32_t kFar = 0x80000000u;  // an offset past every resource: reads zero
+
+// The scale of group g of a row of scales: the dword that holds its byte, and the number where it
+// is used (of a byte load the compiler widens the value at once, and waits for it there).
+struct Scale {
+    int dword, shift;
+};
+__device__ __forceinline__ Scale load_scale(const uint8_t* row, int g) {
+    return Scale{*(const int*)(row + (g & ~3)), 8 * (g & 3)};
+}
+__device__ __forceinline__ float scale_here(const Scale& s) {
+    int d = s.dword;
+    asm volatile("" : "+v"(d));
+    return e8m0_value(((uint32_t)d >> s.shift) & 0xffu);
+}
 
 __device__ __forceinline__ float usable_logit(float l) {  // NaN as -inf, +inf as the largest number
     return l != l ? -__builtin_inff() : fminf(l, 3.4028234663852886e38f);
@@ -188,6 +208,10 @@ __device__ __forceinline__ void build_table(const int32_t* ids, int T, int E, in
 }
 
 // ---- the group product.  A weight row's 32 bytes against a token's 32 values: four steps of 8.
+// Lane quarter q holds bytes 16 q .. and 64 + 16 q .. of the group, so that one load of 16 rows
+// takes half a line of each; step i's values start at 16 q plus
+__host__ __device__ constexpr int at_step(int i) { return 64 * (i >> 1) + 8 * (i & 1); }
+
 template <int DT>
 __device__ __forceinline__ u32x4 codes8(uint32_t lo, uint32_t hi, float s) {  // 8 codes as 16-bit values, times s
     u32x4 r;
@@ -236,13 +260,67 @@ __device__ __forceinline__ void group_product(const u32x4 (&w)[2], float s, cons
     }
 }
 
+template <int DT>
+__device__ __forceinline__ uint16_t swiglu(float gate, float up) {
+    return from_f32<DT>(gate / (1.0f + expf(-gate)) * up);
+}
+
+// ---- what a workgroup of the first launch sets up: the choices (ROUTE: it makes them itself,
+// workgroup 0 writes them down) and its expert's tokens
+template <bool ROUTE>
+struct UpSetup {
+    int32_t own[ROUTE ? kRouteTokens * kMaxTopK : 1];
+    int list[kMaxTokens];  // the expert's tokens, ascending, as token * top_k + choice
+    int part[2], dup;
+
+    template <int WV>
+    __device__ __forceinline__ const int32_t* route(const Fp8MoeArgs& p) {
+        if (threadIdx.x == 0) dup = 0;
+        if constexpr (ROUTE) {
+            const int lane = threadIdx.x & 63;
+            for (int t = threadIdx.x >> 6; t < p.T; t += WV) {
+                int id;
+                float wt;
+                route_token(p.logits + t * p.E, (int)p.E, p.k, p.renormalize, id, wt);
+                if (lane < p.k) {
+                    own[t * p.k + lane] = id;
+                    if (blockIdx.x == 0) {
+                        p.ids[t * p.k + lane] = id;
+                        p.weights[t * p.k + lane] = wt;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        return ROUTE ? own : p.ids;
+    }
+    // The tokens of this workgroup's expert: of pair y (by_pair; none if an earlier pair has the
+    // same expert, whose workgroups do it), or of expert y.
+    __device__ __forceinline__ int find(const Fp8MoeArgs& p, const int32_t* ids, int y, int by_pair, int& e) {
+        const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+        e = by_pair ? ids[y] : y;
+        int mine = -1;
+        if (tid < 128 && tid < p.T)
+            for (int j = 0; j < p.k; ++j)
+                if (ids[tid * p.k + j] == e) mine = tid * p.k + j;
+        if (e < 0) mine = -1;
+        if (by_pair && mine >= 0 && mine < y) dup = 1;
+        const uint64_t have = __ballot(mine >= 0);
+        if (w < 2 && lane == 0) part[w] = __popcll(have);
+        __syncthreads();
+        const int count = dup ? 0 : part[0] + part[1];
+        if (mine >= 0) list[(w == 1 ? part[0] : 0) + __popcll(have & ((1ull << lane) - 1ull))] = mine;
+        __syncthreads();
+        return count;
+    }
+};
+
 // ---- gate, up and SwiGLU: a workgroup takes `span` tiles of 16 columns of I of one expert (16
 // gate rows and 16 up rows each), its waves split the groups of H.  A wave's groups, tile after
 // tile, run through D sets of registers, so that the next tile's weights are on their way while
-// a tile's sums meet.  Workgroup 0 writes the table.  by_pair: workgroups go by pair of token and
-// choice (each expert at its first pair), else by expert.
-template <int DT, int MG, bool ROUTE>
-__global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(Fp8MoeArgs p, int spans, int span, int by_pair) {
+// a tile's sums meet.  Workgroup 0 writes the table.
+template <int DT, int MG>
+__global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(Fp8MoeArgs p, int spans, int span, int by_pair, int chunk) {
     constexpr int WV = kUpWaves, D = 2;
     union Shared {
         v4f red[WV][2 * MG][64];
@@ -252,53 +330,20 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
         } t;
     };
     __shared__ Shared sh;
-    __shared__ int32_t own_ids[ROUTE ? kRouteTokens * kMaxTopK : 1];
-    __shared__ int list[kMaxTokens];
-    __shared__ int part[2], dup;
+    __shared__ UpSetup<false> setup;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, q = lane >> 4;
-    const int T = (int)p.T, E = (int)p.E, k = p.k;
-    const int32_t* ids = p.ids;
-    if (tid == 0) dup = 0;
-    if constexpr (ROUTE) {
-        if (w < T) {
-            int id;
-            float wt;
-            route_token(p.logits + (int64_t)w * E, E, k, p.renormalize, id, wt);
-            if (lane < k) {
-                own_ids[w * k + lane] = id;
-                if (blockIdx.x == 0) {
-                    p.ids[w * k + lane] = id;
-                    p.weights[w * k + lane] = wt;
-                }
-            }
-        }
-        ids = own_ids;
-    }
-    __syncthreads();
+    const int k = p.k;
+    const int32_t* ids = setup.template route<WV>(p);
     if (blockIdx.x == 0) {
-        build_table(ids, T, E, k, 16 * MG, p.table, p.pairs, sh.t.mask, sh.t.first);
+        build_table(ids, (int)p.T, (int)p.E, k, chunk, p.table, p.pairs, sh.t.mask, sh.t.first);
         return;
     }
     const int y = (int)(blockIdx.x - 1) / spans, tile0 = (int)(blockIdx.x - 1) % spans * span;
-    int e = y;
-    if (by_pair) {
-        e = ids[y];
-        if (e < 0) return;
-    }
-    // the expert's tokens, ascending: list[place] = token * k + choice
-    int mine = -1;
-    if (tid < 128 && tid < T)
-        for (int j = 0; j < k; ++j)
-            if (ids[tid * k + j] == e) mine = tid * k + j;
-    if (by_pair && mine >= 0 && mine < y) dup = 1;  // an earlier pair's workgroups do this expert
-    const uint64_t have = __ballot(mine >= 0);
-    if (w < 2 && lane == 0) part[w] = __popcll(have);
-    __syncthreads();
-    const int count = part[0] + part[1];
-    if (count == 0 || dup) return;  // the same in every thread
-    if (mine >= 0) list[(w == 1 ? part[0] : 0) + __popcll(have & ((1ull << lane) - 1ull))] = mine;
-    __syncthreads();
+    int e;
+    const int count = setup.find(p, ids, y, by_pair, e);
+    if (count == 0) return;  // the same in every thread
+    const int* list = setup.list;
 
     const int64_t hp = fp8_pitch(p.H), hsp = fp8_scale_pitch_of(p.H);
     const int tiles = (int)(p.I / 16), ng = (int)(hp / 128);
@@ -308,45 +353,46 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
     const uint8_t* W = p.W13 + (int64_t)e * 2 * p.I * hp;
     const uint8_t* S = p.s13 + (int64_t)e * ceil_div(2 * p.I, 128) * hsp;
     const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(p.X, p.T * p.H * 2);
-    const uint32_t w_off = (uint32_t)(li * hp + 32 * q);
+    const uint32_t w_off = (uint32_t)(li * hp + 16 * q);
 
     struct Group {
         u32x4 g[2], u[2], x[MG][4];
-        float eg, eu;
+        Scale eg, eu;
     };
     for (int c0 = 0; c0 < count; c0 += 16 * MG) {
         uint32_t x_off[MG];
 #pragma unroll
         for (int j = 0; j < MG; ++j) {
             const int i = c0 + 16 * j + li;
-            x_off[j] = i < count ? (uint32_t)((list[i] / k) * p.H + 32 * q) * 2 : kFar;
+            x_off[j] = i < count ? (uint32_t)((list[i] / k) * p.H + 16 * q) * 2 : kFar;
         }
         int lt = 0, lg = w;  // the next load's tile and group
         auto load = [&](Group& r) LLMINT8_MOE_INLINE {
-            const bool in = lt < my_tiles && lg < ng;
-            const uint32_t far = in ? 0u : kFar;
+            const uint32_t far = lt < my_tiles && lg < ng ? 0u : kFar;  // no group: any weights times zeros
             const int64_t i0 = 16 * (int64_t)(lt < my_tiles ? tile0 + lt : tile0);
+            const int wg = lg < ng ? lg : ng - 1;
             const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(W + i0 * hp, 16 * hp), ru = buffer_rsrc(W + (p.I + i0) * hp, 16 * hp);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t off = (w_off + (uint32_t)(lg * 128 + 16 * h)) | far;
-                r.g[h] = load16(rg, off);
-                r.u[h] = load16(ru, off);
+                r.g[h] = load16(rg, w_off + 64 * h, wg * 128);
+                r.u[h] = load16(ru, w_off + 64 * h, wg * 128);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t out = lg * 128 + 32 * q + 8 * i < p.H ? far : kFar;  // past H: the next row's
+                const int at = lg * 128 + at_step(i);
+                const uint32_t out = at + 16 * q < p.H ? far : kFar;  // past H: the next row's
 #pragma unroll
-                for (int j = 0; j < MG; ++j) r.x[j][i] = load16(rx, (x_off[j] + (uint32_t)(lg * 128 + 8 * i) * 2) | out);
+                for (int j = 0; j < MG; ++j) r.x[j][i] = load16(rx, (x_off[j] + (uint32_t)at * 2) | out);
             }
             // the scales of the 16 rows (I is a multiple of 16: one block of rows each)
-            r.eg = in ? e8m0_value(S[(i0 >> 7) * hsp + lg]) : 0.0f;
-            r.eu = in ? e8m0_value(S[((p.I + i0) >> 7) * hsp + lg]) : 0.0f;
+            r.eg = load_scale(S + (i0 >> 7) * hsp, wg);
+            r.eu = load_scale(S + ((p.I + i0) >> 7) * hsp, wg);
             lg += WV;
             if (lg >= gw * WV) {
                 lg = w;
                 ++lt;
             }
+            __builtin_amdgcn_sched_barrier(0);  // the sets are issued, and so waited for, one after the other
         };
         v4f ag[MG] = {}, au[MG] = {};
         int tile = tile0, done = 0;
@@ -360,23 +406,23 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
                 ag[j] = au[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
             }
             __syncthreads();
-            if (w < MG) {  // piece w: sums in the order of the waves
-                v4f sgate = sh.red[0][w][lane], sup = sh.red[0][MG + w][lane];
+            // an output a thread: the waves' sums in their order
+            const float* red = (const float*)sh.red;
+            for (int o = tid; o < 256 * MG; o += 64 * WV) {
+                float a[WV], b[WV];
+#pragma unroll
+                for (int i = 0; i < WV; ++i) {
+                    a[i] = red[i * (512 * MG) + o];
+                    b[i] = red[i * (512 * MG) + 256 * MG + o];
+                }
+                float gate = a[0], up = b[0];
 #pragma unroll
                 for (int i = 1; i < WV; ++i) {
-                    sgate += sh.red[i][w][lane];
-                    sup += sh.red[i][MG + w][lane];
+                    gate += a[i];
+                    up += b[i];
                 }
-                const int i = c0 + 16 * w + li;
-                if (i < count) {
-                    uint16_t h[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) h[r] = from_f32<DT>(sgate[r] / (1.0f + expf(-sgate[r])) * sup[r]);
-                    u32x2 v;
-                    v[0] = (uint32_t)h[0] | ((uint32_t)h[1] << 16);
-                    v[1] = (uint32_t)h[2] | ((uint32_t)h[3] << 16);
-                    *(u32x2*)(p.h + (int64_t)list[i] * p.I + 16 * tile + 4 * q) = v;
-                }
+                const int l = (o >> 2) & 63, i = c0 + 16 * (o >> 8) + (l & 15);
+                if (i < count) p.h[(int64_t)list[i] * p.I + 16 * tile + 4 * (l >> 4) + (o & 3)] = swiglu<DT>(gate, up);
             }
             __syncthreads();
             ++tile;
@@ -384,14 +430,119 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
         Group r[D];
 #pragma unroll
         for (int d = 0; d < D; ++d) load(r[d]);
+        // (whole rounds of D steps: a way out between them would make the compiler wait, at the top,
+        // for every set instead of the first; steps past the last multiply zeros)
         for (int s = 0; s < steps; s += D) {
 #pragma unroll
             for (int d = 0; d < D; ++d) {
-                if (s + d >= steps) break;
-                group_product<DT, MG>(r[d].g, r[d].eg, r[d].x, ag);
-                group_product<DT, MG>(r[d].u, r[d].eu, r[d].x, au);
+                group_product<DT, MG>(r[d].g, scale_here(r[d].eg), r[d].x, ag);
+                group_product<DT, MG>(r[d].u, scale_here(r[d].eu), r[d].x, au);
                 load(r[d]);
-                if (++done == gw) {
+                if (s + d < steps && ++done == gw) {
+                    done = 0;
+                    finish();
+                }
+            }
+        }
+    }
+}
+
+// ---- the same in the light form: 8 columns of I a tile, rows 0 .. 7 of the instruction gate and
+// 8 .. 15 up.
+template <int DT, bool ROUTE>
+__global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8MoeArgs p, int spans, int span, int by_pair, int chunk) {
+    constexpr int WV = kLightUpWaves, D = 2;
+    union Shared {
+        v4f red[WV][64];
+        struct {
+            uint32_t mask[kMaxExperts][4];
+            int first[kMaxExperts];
+        } t;
+    };
+    __shared__ Shared sh;
+    __shared__ UpSetup<ROUTE> setup;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, q = lane >> 4;
+    const int32_t* ids = setup.template route<WV>(p);
+    if (blockIdx.x == 0) {
+        build_table(ids, (int)p.T, (int)p.E, p.k, chunk, p.table, p.pairs, sh.t.mask, sh.t.first);
+        return;
+    }
+    const int y = (int)(blockIdx.x - 1) / spans, tile0 = (int)(blockIdx.x - 1) % spans * span;
+    int e;
+    const int count = setup.find(p, ids, y, by_pair, e);
+    if (count == 0) return;  // the same in every thread
+
+    const int64_t hp = fp8_pitch(p.H), hsp = fp8_scale_pitch_of(p.H);
+    const int tiles = (int)(p.I / 8), ng = (int)(hp / 128);
+    const int my_tiles = tiles - tile0 < span ? tiles - tile0 : span;
+    const int gw = (ng + WV - 1) / WV;  // groups of a wave (its last may lie past H: zeros)
+    const int steps = my_tiles * gw;
+    // this lane's row of the first tile, and its scales: of the row that it converts (bf16), or of
+    // the row of the results that it adds up (fp16)
+    const int64_t row0 = 8 * (int64_t)tile0 + (li & 7) + (li >= 8 ? p.I : 0);
+    const int64_t srow0 = 8 * (int64_t)tile0 + ((DT == F16 ? q >= 2 : li >= 8) ? p.I : 0);
+    const uint8_t* W = p.W13 + ((int64_t)e * 2 * p.I + row0) * hp + 16 * q;
+    const uint8_t* S = p.s13 + (int64_t)e * ceil_div(2 * p.I, 128) * hsp;
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(p.X, p.T * p.H * 2);
+    struct Group {
+        u32x4 w[2], x[1][4];
+        Scale e;
+    };
+    for (int c0 = 0; c0 < count; c0 += 16) {
+        const uint32_t x_off = c0 + li < count ? (uint32_t)((setup.list[c0 + li] / p.k) * p.H + 16 * q) * 2 : kFar;
+        int lt = 0, lg = w;  // the next load's tile and group
+        auto load = [&](Group& r) LLMINT8_MOE_INLINE {
+            const uint32_t far = lt < my_tiles && lg < ng ? 0u : kFar;  // no group: any weights times zeros
+            const int t = lt < my_tiles ? lt : 0, wg = lg < ng ? lg : ng - 1;
+            const uint8_t* at = W + 8 * t * hp + wg * 128;
+            r.w[0] = *(const u32x4*)at;
+            r.w[1] = *(const u32x4*)(at + 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = lg * 128 + at_step(i);
+                const uint32_t out = k + 16 * q < p.H ? far : kFar;  // past H: the next row's
+                r.x[0][i] = load16(rx, (x_off + (uint32_t)k * 2) | out);
+            }
+            r.e = load_scale(S + ((srow0 + 8 * t) >> 7) * hsp, wg);  // I is a multiple of 16: one block
+            lg += WV;
+            if (lg >= gw * WV) {
+                lg = w;
+                ++lt;
+            }
+            __builtin_amdgcn_sched_barrier(0);  // as above
+        };
+        v4f acc[1] = {};
+        int tile = tile0, done = 0;
+        auto finish = [&]() LLMINT8_MOE_INLINE {
+            mfma_settle();
+            sh.red[w][lane] = acc[0];
+            acc[0] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            __syncthreads();
+            if (tid < 128) {  // an output a thread (up: two lane quarters on)
+                const float* red = (const float*)sh.red;
+                float gate = red[tid], up = red[128 + tid];
+#pragma unroll
+                for (int i = 1; i < WV; ++i) {
+                    gate += red[256 * i + tid];
+                    up += red[256 * i + 128 + tid];
+                }
+                const int l = tid >> 2, i = c0 + (l & 15);
+                if (i < count)
+                    p.h[(int64_t)setup.list[i] * p.I + 8 * tile + 4 * (l >> 4) + (tid & 3)] = swiglu<DT>(gate, up);
+            }
+            __syncthreads();
+            ++tile;
+        };
+        Group r[D];
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(r[d]);
+        for (int s = 0; s < steps; s += D) {  // whole rounds, as above
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                group_product<DT, 1>(r[d].w, scale_here(r[d].e), r[d].x, acc);
+                load(r[d]);
+                if (s + d < steps && ++done == gw) {
                     done = 0;
                     finish();
                 }
@@ -424,19 +575,17 @@ __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
     }
     for (int i = tid; i < WV * T * 4; i += 64 * WV) ysum[i / (4 * T)][(i >> 2) % T][i & 3] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     __syncthreads();
-    const int64_t total = (int64_t)entries * ng;
-    const int64_t from = total * w / WV, to = total * (w + 1) / WV;
+    const int total = entries * ng, from = (int)((int64_t)total * w / WV), to = (int)((int64_t)total * (w + 1) / WV);
     if (from < to) {
-        const uint32_t w_off = (uint32_t)(li * ip + 32 * q);
+        const uint32_t w_off = (uint32_t)(li * ip + 16 * q);
         const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, (int64_t)n * p.I * 2);
         const int64_t scale_rows = ceil_div(p.H, 128);
         struct Group {
             u32x4 w[2], x[MG][4];
-            float s;
+            Scale s;
         };
         // the next load's entry and group, and that entry's expert and rows of h
-        int le = (int)(from / ng), lg = (int)(from - (int64_t)le * ng), expert = 0;
-        int64_t left = to - from;
+        int le = from / ng, lg = from - le * ng, expert = 0, left = to - from;
         uint32_t h_off[MG];
         auto open = [&]() LLMINT8_MOE_INLINE {
             if (le >= entries) return;
@@ -445,22 +594,23 @@ __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
 #pragma unroll
             for (int j = 0; j < MG; ++j) {
                 const int i = 16 * j + li;
-                h_off[j] = i < count ? (uint32_t)(pairs[first + i] * p.I + 32 * q) * 2 : kFar;
+                h_off[j] = i < count ? (uint32_t)(pairs[first + i] * p.I + 16 * q) * 2 : kFar;
             }
         };
         auto load = [&](Group& r) LLMINT8_MOE_INLINE {
-            const bool in = left > 0;
-            const uint32_t far = in ? 0u : kFar;
+            const uint32_t far = left > 0 ? 0u : kFar;  // past the share: any weights times zeros
             const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(p.W2 + ((int64_t)expert * p.H + n0) * ip, 16 * ip);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) r.w[h] = load16(rw, (w_off + (uint32_t)(lg * 128 + 16 * h)) | far);
+            for (int h = 0; h < 2; ++h) r.w[h] = load16(rw, w_off + 64 * h, lg * 128);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t out = lg * 128 + 32 * q + 8 * i < p.I ? far : kFar;  // past I: the next row's
+                const int at = lg * 128 + at_step(i);
+                const uint32_t out = at + 16 * q < p.I ? far : kFar;  // past I: the next row's
 #pragma unroll
-                for (int j = 0; j < MG; ++j) r.x[j][i] = load16(rh, (h_off[j] + (uint32_t)(lg * 128 + 8 * i) * 2) | out);
+                for (int j = 0; j < MG; ++j) r.x[j][i] = load16(rh, (h_off[j] + (uint32_t)at * 2) | out);
             }
-            r.s = in ? e8m0_value(p.s2[(expert * scale_rows + (n0 >> 7)) * isp + lg]) : 0.0f;
+            r.s = load_scale(p.s2 + (expert * scale_rows + (n0 >> 7)) * isp, lg);
+            __builtin_amdgcn_sched_barrier(0);  // as above
             --left;
             if (++lg == ng) {
                 lg = 0;
@@ -491,14 +641,13 @@ __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
         open();
 #pragma unroll
         for (int d = 0; d < D; ++d) load(r[d]);
-        const int steps = (int)(to - from);
-        for (int s = 0; s < steps; s += D) {
+        const int steps = to - from;
+        for (int s = 0; s < steps; s += D) {  // whole rounds, as above
 #pragma unroll
             for (int d = 0; d < D; ++d) {
-                if (s + d >= steps) break;
-                group_product<DT, MG>(r[d].w, r[d].s, r[d].x, acc);
+                group_product<DT, MG>(r[d].w, scale_here(r[d].s), r[d].x, acc);
                 load(r[d]);
-                if (++cg == ng || s + d + 1 == steps) {
+                if (s + d < steps && (++cg == ng || s + d + 1 == steps)) {
                     flush();
                     cg = 0;
                     ++ce;
@@ -518,52 +667,205 @@ __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
     }
 }
 
+// ---- the same in the light form: 8 columns of H, two entries (of up to 8 tokens) at a time, the
+// even one in rows and columns 0 .. 7 of the instruction, the odd one in 8 .. 15.
+template <int DT, int MAXT, int WV>
+__global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
+    constexpr int D = 3, MAXN = MAXT * kMaxTopK;
+    __shared__ v4f ysum[WV][MAXT][2];  // a wave's sums of 8 columns per token
+    __shared__ int32_t table[3 * MAXN], pairs[MAXN];
+    __shared__ float weights[MAXN];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, q = lane >> 4, half = li >> 3;
+    const int T = (int)p.T, k = p.k, n = T * k;
+    const int64_t n0 = (int64_t)blockIdx.x * 8;
+    const int64_t ip = fp8_pitch(p.I), isp = fp8_scale_pitch_of(p.I);
+    const int ng = (int)(ip / 128);
+    const int entries = __builtin_amdgcn_readfirstlane(p.table[0]), twos = (entries + 1) / 2;
+    for (int i = tid; i < 3 * n; i += 64 * WV) table[i] = p.table[1 + i];  // past the entries: unread
+    for (int i = tid; i < n; i += 64 * WV) {
+        pairs[i] = p.pairs[i];
+        weights[i] = p.weights[i];
+    }
+    for (int i = tid; i < WV * T * 2; i += 64 * WV) ysum[i / (2 * T)][(i >> 1) % T][i & 1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    __syncthreads();
+    const int total = twos * ng, from = (int)((int64_t)total * w / WV), to = (int)((int64_t)total * (w + 1) / WV);
+    if (from < to) {
+        const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, (int64_t)n * p.I * 2);
+        const int64_t scale_rows = ceil_div(p.H, 128);
+        struct Group {
+            u32x4 w[2], x[1][4];
+            Scale s;
+        };
+        // the next load's two entries and group; of this lane's entry its row of W2, its scales
+        // and its token's row of h (an odd count: the last entry's weights times zeros)
+        int le = from / ng, lg = from - le * ng, left = to - from;
+        const uint8_t *row = nullptr, *scales = nullptr;
+        uint32_t h_off = kFar;
+        auto open = [&]() LLMINT8_MOE_INLINE {
+            const int mine = 2 * le + half, at = mine < entries ? mine : entries - 1;
+            const int e = table[3 * at], first = table[3 * at + 1], count = mine < entries ? table[3 * at + 2] : 0;
+            row = p.W2 + ((int64_t)e * p.H + n0 + (li & 7)) * ip + 16 * q;
+            scales = p.s2 + (e * scale_rows + (n0 >> 7)) * isp;
+            h_off = (li & 7) < count ? (uint32_t)(pairs[first + (li & 7)] * p.I + 16 * q) * 2 : kFar;
+        };
+        auto load = [&](Group& r) LLMINT8_MOE_INLINE {
+            const uint32_t far = left > 0 ? 0u : kFar;  // past the share: any weights times zeros
+            r.w[0] = *(const u32x4*)(row + lg * 128);
+            r.w[1] = *(const u32x4*)(row + lg * 128 + 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = lg * 128 + at_step(i);
+                const uint32_t out = at + 16 * q < p.I ? far : kFar;  // past I: the next row's
+                r.x[0][i] = load16(rh, (h_off + (uint32_t)at * 2) | out);
+            }
+            r.s = load_scale(scales, lg);
+            __builtin_amdgcn_sched_barrier(0);  // as above
+            --left;
+            if (++lg == ng) {
+                lg = 0;
+                ++le;
+                if (le < twos) open();
+            }
+        };
+        v4f acc[1] = {};
+        int ce = le, cg = lg;  // the entries and group being multiplied
+        // The results of an entry's rows with its own tokens; the even entry first, then the odd one:
+        // a token may be in both.
+        auto flush = [&]() LLMINT8_MOE_INLINE {
+            mfma_settle();
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int at = 2 * ce + t;
+                if (half == t && (q >> 1) == t && at < entries && (li & 7) < table[3 * at + 2]) {
+                    const int pair = pairs[table[3 * at + 1] + (li & 7)];
+                    const float pt = weights[pair];
+                    v4f y = ysum[w][pair / k][q & 1];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(pt, acc[0][r], y[r]);
+                    ysum[w][pair / k][q & 1] = y;
+                }
+            }
+            acc[0] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        };
+        Group r[D];
+        open();
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(r[d]);
+        const int steps = to - from;
+        for (int s = 0; s < steps; s += D) {  // whole rounds, as above
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                group_product<DT, 1>(r[d].w, scale_here(r[d].s), r[d].x, acc);
+                load(r[d]);
+                if (s + d < steps && (++cg == ng || s + d + 1 == steps)) {
+                    flush();
+                    cg = 0;
+                    ++ce;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < T * 2; i += 64 * WV) {
+        v4f y = ysum[0][i >> 1][i & 1];
+#pragma unroll
+        for (int v = 1; v < WV; ++v) y += ysum[v][i >> 1][i & 1];
+        u32x2 o;
+        o[0] = (uint32_t)from_f32<DT>(y[0]) | ((uint32_t)from_f32<DT>(y[1]) << 16);
+        o[1] = (uint32_t)from_f32<DT>(y[2]) | ((uint32_t)from_f32<DT>(y[3]) << 16);
+        *(u32x2*)(p.Y + (int64_t)(i >> 1) * p.H + n0 + 4 * (i & 1)) = o;
+    }
+}
+
+// The first launch's grid: workgroup 0 (the table), then `rows` (pairs or experts) of `spans` spans
+// of `span` tiles.  A workgroup's setup (choosing the experts or reading them, the list) is paid
+// once per span, as long as about `enough` workgroups are left: 4 tokens, 64 experts of 2048 x 768,
+// top 8: 25.5 us with spans of 3, 32.6 with single tiles; longer ones gain nothing (8 tokens, 128
+// such experts: 48.3 us with spans of 3, 47.3 with 6, 59.6 with 1; 16 tokens, top 4: 38.6, 44.9, 47.2).
+struct UpGrid {
+    int by_pair, spans, span;
+    int64_t grid;
+};
+UpGrid up_grid(const Fp8MoeArgs& p, int columns, int64_t enough, int64_t longest) {
+    UpGrid g;
+    g.by_pair = p.T * p.k < p.E;
+    const int64_t rows = g.by_pair ? p.T * p.k : p.E, tiles = p.I / columns;
+    int64_t span = tiles * rows / enough;
+    span = span < 1 ? 1 : (span > longest ? longest : span);
+    g.span = (int)span;
+    g.spans = (int)ceil_div(tiles, span);
+    g.grid = 1 + g.spans * rows;
+    return g;
+}
+
+// MG: pieces of 16 tokens multiplied at once; 0: the light form
 template <int DT, int MG>
-hipError_t moe_launch(const Fp8MoeArgs& p, hipStream_t stream) {
-    const int by_pair = p.T * p.k < p.E;
-    const int64_t rows = by_pair ? p.T * p.k : p.E, tiles = p.I / 16;
-    // tiles of a workgroup: its setup (choosing the experts or reading them, the list) is paid
-    // once, as long as enough workgroups are left
-    int64_t span = tiles * rows / 1024;
-    span = span < 1 ? 1 : (span > 8 ? 8 : span);
-    const int64_t spans = ceil_div(tiles, span), grid = 1 + spans * rows;
-    if (MG == 1 && p.T <= kRouteTokens && grid <= 2048) {
-        moe_up_kernel<DT, MG, MG == 1><<<(unsigned)grid, 64 * kUpWaves, 0, stream>>>(p, (int)spans, (int)span, by_pair);
+hipError_t launch_up(const Fp8MoeArgs& p, int chunk, hipStream_t stream) {
+    if constexpr (MG == 0) {
+        const UpGrid g = up_grid(p, 8, 1024, 3);
+        constexpr int kThreads = 64 * kLightUpWaves;
+        if (p.T <= kRouteTokens) {
+            moe_up_light_kernel<DT, true><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk);
+        } else {
+            moe_route_kernel<<<(unsigned)p.T, 64, 0, stream>>>(p);
+            moe_up_light_kernel<DT, false><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk);
+        }
     } else {
+        const UpGrid g = up_grid(p, 16, 1024, 8);
         moe_route_kernel<<<(unsigned)p.T, 64, 0, stream>>>(p);
-        moe_up_kernel<DT, MG, false><<<(unsigned)grid, 64 * kUpWaves, 0, stream>>>(p, (int)spans, (int)span, by_pair);
+        moe_up_kernel<DT, MG><<<(unsigned)g.grid, 64 * kUpWaves, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk);
     }
-    const unsigned cols = (unsigned)(p.H / 16);
-    if constexpr (MG == 1) {
-        if (p.T <= 16) {
-            moe_down_kernel<DT, MG, 16, 16><<<cols, 1024, 0, stream>>>(p);
-            return hipGetLastError();
+    return hipGetLastError();
+}
+
+template <int DT, int MG>
+hipError_t launch_down(const Fp8MoeArgs& p, hipStream_t stream) {
+    if constexpr (MG == 0) {
+        const unsigned cols = (unsigned)(p.H / 8);
+        if (p.T <= 16) moe_down_light_kernel<DT, 16, 8><<<cols, 512, 0, stream>>>(p);
+        else moe_down_light_kernel<DT, 128, 8><<<cols, 512, 0, stream>>>(p);
+    } else {
+        const unsigned cols = (unsigned)(p.H / 16);
+        if constexpr (MG < 4) {
+            if (p.T <= 64) {
+                moe_down_kernel<DT, MG, 64, 16><<<cols, 1024, 0, stream>>>(p);
+                return hipGetLastError();
+            }
         }
+        moe_down_kernel<DT, MG, 128, 8><<<cols, 512, 0, stream>>>(p);
     }
-    if constexpr (MG < 4) {
-        if (p.T <= 64) {
-            moe_down_kernel<DT, MG, 64, 16><<<cols, 1024, 0, stream>>>(p);
-            return hipGetLastError();
-        }
-    }
-    moe_down_kernel<DT, MG, 128, 8><<<cols, 512, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 template <int DT>
-hipError_t moe_pieces(const Fp8MoeArgs& p, hipStream_t stream) {
-    // pieces of 16 tokens multiplied at once: by the tokens that an expert has on average (one
-    // that has more is read once per 16 MG of them)
+hipError_t moe_launch(const Fp8MoeArgs& p, hipStream_t stream) {
+    // pieces by the tokens that an expert has on average (one that has more is read once per 16 MG
+    // of them); with few, the light forms where the others would leave compute units idle: 16
+    // tokens, 60 experts of 2064 x 1424, top 4: up 74 us light, 83 not, down 51 and 50; 8 tokens, 8
+    // experts of 4096 x 14336, top 2: up 192 light, 171 not, down 103 and 94; 1 token, 64 experts of
+    // 2048 x 768, top 8: up 9.5 and 12.7, down 7.4 and 10.6
     const int64_t mean16 = 16 * p.T * p.k / p.E;
-    if (mean16 <= 12 * 16 || p.T <= 16) return moe_launch<DT, 1>(p, stream);
-    if (mean16 <= 28 * 16 || p.T <= 32) return moe_launch<DT, 2>(p, stream);
-    return moe_launch<DT, 4>(p, stream);
+    const int mg = mean16 <= 12 * 16 || p.T <= 16 ? 1 : (mean16 <= 28 * 16 || p.T <= 32 ? 2 : 4);
+    const bool few = p.T <= 8 || mean16 <= kLightMean * 16;
+    const int64_t rows = p.T * p.k < p.E ? p.T * p.k : p.E;
+    const bool light_up = few && (p.I / 16) * rows <= 4096, light_down = few && p.H / 16 < 256;
+    const int chunk = light_down ? 8 : 16 * mg;  // tokens of an entry
+    hipError_t e = light_up    ? launch_up<DT, 0>(p, chunk, stream)
+                   : mg == 1   ? launch_up<DT, 1>(p, chunk, stream)
+                   : mg == 2   ? launch_up<DT, 2>(p, chunk, stream)
+                               : launch_up<DT, 4>(p, chunk, stream);
+    if (e != hipSuccess) return e;
+    return light_down ? launch_down<DT, 0>(p, stream)
+           : mg == 1  ? launch_down<DT, 1>(p, stream)
+           : mg == 2  ? launch_down<DT, 2>(p, stream)
+                      : launch_down<DT, 4>(p, stream);
 }
 
 }  // namespace
 
 hipError_t launch_fp8_moe(int dt, const Fp8MoeArgs& p, hipStream_t stream) {
-    return dt == F16 ? moe_pieces<F16>(p, stream) : moe_pieces<BF16>(p, stream);
+    return dt == F16 ? moe_launch<F16>(p, stream) : moe_launch<BF16>(p, stream);
 }
 
 }  // namespace llmint8

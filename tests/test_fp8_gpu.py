@@ -346,7 +346,9 @@ def moe_check(X, logits, w, k, renormalize):
     return Y, ids, p
 
 
-MOE = [(1, 16, 16, 1, 1), (1, 256, 128, 8, 2), (1, 272, 144, 64, 8), (2, 528, 400, 12, 3), (4, 384, 272, 5, 5),
+MOE = [(1, 4352, 144, 8, 2), (12, 4112, 80, 9, 2), (3, 272, 1040, 600, 4), (70, 272, 144, 64, 5), (128, 144, 272, 16, 2),
+       (50, 4128, 64, 6, 2), (20, 144, 80, 3, 2), (2, 64, 33 * 128, 520, 16), (128, 64, 48, 1024, 16),
+       (1, 16, 16, 1, 1), (1, 256, 128, 8, 2), (1, 272, 144, 64, 8), (2, 528, 400, 12, 3), (4, 384, 272, 5, 5),
        (9, 256, 144, 70, 4), (17, 272, 208, 6, 2), (40, 144, 272, 9, 4), (64, 256, 128, 130, 8), (128, 128, 144, 4, 2),
        (33, 128, 128, 3, 1), (5, 1040, 64, 20, 16)]
 
