@@ -248,7 +248,7 @@ int check_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
     if (T < 0 || H < 0 || I < 0 || E < 1 || k < 1 || k > E) return LLMINT8_EINVAL;
     if (H % 16 != 0 || I % 16 != 0) return LLMINT8_EINVAL;
     if (T > kMoeMaxTokens || E > kMoeMaxExperts || k > kMoeMaxTopK) return LLMINT8_ERANGE;
-    if (H > kMaxSum || I > kMaxSum / 2 || T * k * I >= (int64_t)1 << 30) return LLMINT8_ERANGE;
+    if (H > kMaxSum || I > kMaxSum / 2 || T * k * fp8_pitch(I) >= (int64_t)1 << 30) return LLMINT8_ERANGE;
     return LLMINT8_OK;
 }
 
@@ -260,7 +260,7 @@ MoeLayout moe_layout(int64_t T, int64_t I, int64_t k) {
     MoeLayout L;
     const size_t n = (size_t)T * (size_t)k;
     L.h = 0;
-    L.table = align_up(n * (size_t)I * 2);
+    L.table = align_up(n * (size_t)fp8_pitch(I) * 2);
     L.pairs = align_up(L.table + (1 + 3 * n) * 4);
     L.total = align_up(L.pairs + n * 4);
     return L;

@@ -50,6 +50,10 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t off,
 }
 constexpr uint32_t kFar = 0x80000000u;  // an offset past every resource: reads zero
 
+// A step's instructions bound these kernels before its bytes do, so what a step computes is kept
+// short: the group's place rides in the scalar offset, a step without a group has empty resources
+// (it reads zeros), and only the last group of a ragged H selects other offsets per lane.
+
 // The scale of group g of a row of scales: the dword that holds its byte, and the number where it
 // is used (of a byte load the compiler widens the value at once, and waits for it there).
 struct Scale {
@@ -57,6 +61,9 @@ struct Scale {
 };
 __device__ __forceinline__ Scale load_scale(const uint8_t* row, int g) {
     return Scale{*(const int*)(row + (g & ~3)), 8 * (g & 3)};
+}
+__device__ __forceinline__ Scale load_scale(__amdgpu_buffer_rsrc_t rs, uint32_t row, int g) {
+    return Scale{(int)__builtin_amdgcn_raw_buffer_load_b32(rs, row, g & ~3, 0), 8 * (g & 3)};
 }
 __device__ __forceinline__ float scale_here(const Scale& s) {
     int d = s.dword;
@@ -208,9 +215,8 @@ __device__ __forceinline__ void build_table(const int32_t* ids, int T, int E, in
 }
 
 // ---- the group product.  A weight row's 32 bytes against a token's 32 values: four steps of 8.
-// Lane quarter q holds bytes 16 q .. and 64 + 16 q .. of the group, so that one load of 16 rows
-// takes half a line of each; step i's values start at 16 q plus
-__host__ __device__ constexpr int at_step(int i) { return 64 * (i >> 1) + 8 * (i & 1); }
+// Lane quarter q holds bytes 16 q .. + 15 and 64 + 16 q .. + 15 of the group, so that one load of
+// 16 rows takes half a line of each.
 
 template <int DT>
 __device__ __forceinline__ u32x4 codes8(uint32_t lo, uint32_t hi, float s) {  // 8 codes as 16-bit values, times s
@@ -227,6 +233,25 @@ __device__ __forceinline__ u32x4 codes8(uint32_t lo, uint32_t hi, float s) {  //
         r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true));
     }
     return r;
+}
+
+// Byte offsets of this lane's values of a row of `n` (at `row`, kFar: none) in the first group, in its
+// first and second half; past `n` in the last group the next row's are left out.
+struct RowAt {
+    uint32_t lo, hi, last_lo, last_hi;
+    __device__ __forceinline__ void set(uint32_t row, int n, int ng, int q) {
+        lo = row + 32 * q;
+        hi = lo + 128;
+        last_lo = 128 * (ng - 1) + 16 * q < n ? lo : kFar;
+        last_hi = 128 * (ng - 1) + 64 + 16 * q < n ? hi : kFar;
+    }
+};
+__device__ __forceinline__ void load_row(__amdgpu_buffer_rsrc_t rs, const RowAt& a, int g, bool last, u32x4 (&x)[4]) {
+    const uint32_t lo = last ? a.last_lo : a.lo, hi = last ? a.last_hi : a.hi;
+    x[0] = load16(rs, lo, 256 * g);
+    x[1] = load16(rs, lo + 16, 256 * g);
+    x[2] = load16(rs, hi, 256 * g);
+    x[3] = load16(rs, hi + 16, 256 * g);
 }
 
 template <int DT>
@@ -263,6 +288,13 @@ __device__ __forceinline__ void group_product(const u32x4 (&w)[2], float s, cons
 template <int DT>
 __device__ __forceinline__ uint16_t swiglu(float gate, float up) {
     return from_f32<DT>(gate / (1.0f + expf(-gate)) * up);
+}
+
+// The rows of h are padded with zeros to whole groups: by the workgroup of the last tile.
+__device__ __forceinline__ void pad_rows(const Fp8MoeArgs& p, const int* list, int from, int to, int64_t ip) {
+    const int pad = (int)(ip - p.I);
+    if (pad == 0) return;
+    for (int i = threadIdx.x; i < (to - from) * pad; i += blockDim.x) p.h[(int64_t)list[from + i / pad] * ip + p.I + i % pad] = 0;
 }
 
 // ---- what a workgroup of the first launch sets up: the choices (ROUTE: it makes them itself,
@@ -352,7 +384,7 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
     const int steps = my_tiles * gw;
     const uint8_t* W = p.W13 + (int64_t)e * 2 * p.I * hp;
     const uint8_t* S = p.s13 + (int64_t)e * ceil_div(2 * p.I, 128) * hsp;
-    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(p.X, p.T * p.H * 2);
+    const int64_t ip = fp8_pitch(p.I);
     const uint32_t w_off = (uint32_t)(li * hp + 16 * q);
 
     struct Group {
@@ -360,30 +392,26 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
         Scale eg, eu;
     };
     for (int c0 = 0; c0 < count; c0 += 16 * MG) {
-        uint32_t x_off[MG];
+        RowAt x_at[MG];
 #pragma unroll
         for (int j = 0; j < MG; ++j) {
             const int i = c0 + 16 * j + li;
-            x_off[j] = i < count ? (uint32_t)((list[i] / k) * p.H + 16 * q) * 2 : kFar;
+            x_at[j].set(i < count ? (uint32_t)((list[i] / k) * p.H) * 2 : kFar, (int)p.H, ng, q);
         }
         int lt = 0, lg = w;  // the next load's tile and group
         auto load = [&](Group& r) LLMINT8_MOE_INLINE {
-            const uint32_t far = lt < my_tiles && lg < ng ? 0u : kFar;  // no group: any weights times zeros
-            const int64_t i0 = 16 * (int64_t)(lt < my_tiles ? tile0 + lt : tile0);
-            const int wg = lg < ng ? lg : ng - 1;
-            const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(W + i0 * hp, 16 * hp), ru = buffer_rsrc(W + (p.I + i0) * hp, 16 * hp);
+            const bool in = lt < my_tiles && lg < ng;
+            const int64_t i0 = 16 * (int64_t)(in ? tile0 + lt : tile0);
+            const int wg = in ? lg : 0, bytes = in ? 16 * (int)hp : 0;
+            const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(W + i0 * hp, bytes), ru = buffer_rsrc(W + (p.I + i0) * hp, bytes);
+            const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(p.X, in ? p.T * p.H * 2 : 0);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 r.g[h] = load16(rg, w_off + 64 * h, wg * 128);
                 r.u[h] = load16(ru, w_off + 64 * h, wg * 128);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = lg * 128 + at_step(i);
-                const uint32_t out = at + 16 * q < p.H ? far : kFar;  // past H: the next row's
-#pragma unroll
-                for (int j = 0; j < MG; ++j) r.x[j][i] = load16(rx, (x_off[j] + (uint32_t)at * 2) | out);
-            }
+            for (int j = 0; j < MG; ++j) load_row(rx, x_at[j], wg, lg == ng - 1, r.x[j]);
             // the scales of the 16 rows (I is a multiple of 16: one block of rows each)
             r.eg = load_scale(S + (i0 >> 7) * hsp, wg);
             r.eu = load_scale(S + ((p.I + i0) >> 7) * hsp, wg);
@@ -422,8 +450,9 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
                     up += b[i];
                 }
                 const int l = (o >> 2) & 63, i = c0 + 16 * (o >> 8) + (l & 15);
-                if (i < count) p.h[(int64_t)list[i] * p.I + 16 * tile + 4 * (l >> 4) + (o & 3)] = swiglu<DT>(gate, up);
+                if (i < count) p.h[(int64_t)list[i] * ip + 16 * tile + 4 * (l >> 4) + (o & 3)] = swiglu<DT>(gate, up);
             }
+            if (tile == tiles - 1) pad_rows(p, list, c0, count < c0 + 16 * MG ? count : c0 + 16 * MG, ip);
             __syncthreads();
             ++tile;
         };
@@ -478,33 +507,31 @@ __global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8
     const int my_tiles = tiles - tile0 < span ? tiles - tile0 : span;
     const int gw = (ng + WV - 1) / WV;  // groups of a wave (its last may lie past H: zeros)
     const int steps = my_tiles * gw;
-    // this lane's row of the first tile, and its scales: of the row that it converts (bf16), or of
-    // the row of the results that it adds up (fp16)
+    // this lane's row of the first tile; its scale is the one of the row that it converts (bf16), or
+    // of the row of the results that it adds up (fp16)
     const int64_t row0 = 8 * (int64_t)tile0 + (li & 7) + (li >= 8 ? p.I : 0);
-    const int64_t srow0 = 8 * (int64_t)tile0 + ((DT == F16 ? q >= 2 : li >= 8) ? p.I : 0);
     const uint8_t* W = p.W13 + ((int64_t)e * 2 * p.I + row0) * hp + 16 * q;
-    const uint8_t* S = p.s13 + (int64_t)e * ceil_div(2 * p.I, 128) * hsp;
-    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(p.X, p.T * p.H * 2);
+    const int64_t s_bytes = ceil_div(2 * p.I, 128) * hsp, ip = fp8_pitch(p.I);
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(p.s13 + (int64_t)e * s_bytes, s_bytes);
+    const bool up_scale = DT == F16 ? q >= 2 : li >= 8;
     struct Group {
         u32x4 w[2], x[1][4];
         Scale e;
     };
     for (int c0 = 0; c0 < count; c0 += 16) {
-        const uint32_t x_off = c0 + li < count ? (uint32_t)((setup.list[c0 + li] / p.k) * p.H + 16 * q) * 2 : kFar;
+        RowAt x_at;
+        x_at.set(c0 + li < count ? (uint32_t)((setup.list[c0 + li] / p.k) * p.H) * 2 : kFar, (int)p.H, ng, q);
         int lt = 0, lg = w;  // the next load's tile and group
         auto load = [&](Group& r) LLMINT8_MOE_INLINE {
-            const uint32_t far = lt < my_tiles && lg < ng ? 0u : kFar;  // no group: any weights times zeros
-            const int t = lt < my_tiles ? lt : 0, wg = lg < ng ? lg : ng - 1;
-            const uint8_t* at = W + 8 * t * hp + wg * 128;
+            const bool in = lt < my_tiles && lg < ng;  // else: one line of weights times zeros
+            const int t = in ? lt : 0, wg = in ? lg : 0;
+            const uint8_t* at = in ? W + 8 * t * hp + wg * 128 : p.W13;
             r.w[0] = *(const u32x4*)at;
             r.w[1] = *(const u32x4*)(at + 64);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = lg * 128 + at_step(i);
-                const uint32_t out = k + 16 * q < p.H ? far : kFar;  // past H: the next row's
-                r.x[0][i] = load16(rx, (x_off + (uint32_t)k * 2) | out);
-            }
-            r.e = load_scale(S + ((srow0 + 8 * t) >> 7) * hsp, wg);  // I is a multiple of 16: one block
+            load_row(buffer_rsrc(p.X, in ? p.T * p.H * 2 : 0), x_at, wg, lg == ng - 1, r.x[0]);
+            // (I is a multiple of 16: a tile's gate rows, and its up rows, lie in one block)
+            const int64_t i0 = 8 * (int64_t)(tile0 + t);
+            r.e = load_scale(rs, up_scale ? (uint32_t)(((p.I + i0) >> 7) * hsp) : (uint32_t)((i0 >> 7) * hsp), wg);
             lg += WV;
             if (lg >= gw * WV) {
                 lg = w;
@@ -529,8 +556,9 @@ __global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8
                 }
                 const int l = tid >> 2, i = c0 + (l & 15);
                 if (i < count)
-                    p.h[(int64_t)setup.list[i] * p.I + 8 * tile + 4 * (l >> 4) + (tid & 3)] = swiglu<DT>(gate, up);
+                    p.h[(int64_t)setup.list[i] * ip + 8 * tile + 4 * (l >> 4) + (tid & 3)] = swiglu<DT>(gate, up);
             }
+            if (tile == tiles - 1) pad_rows(p, setup.list, c0, count < c0 + 16 ? count : c0 + 16, ip);
             __syncthreads();
             ++tile;
         };
@@ -578,7 +606,7 @@ __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
     const int total = entries * ng, from = (int)((int64_t)total * w / WV), to = (int)((int64_t)total * (w + 1) / WV);
     if (from < to) {
         const uint32_t w_off = (uint32_t)(li * ip + 16 * q);
-        const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, (int64_t)n * p.I * 2);
+        const int64_t h_bytes = (int64_t)n * ip * 2;
         const int64_t scale_rows = ceil_div(p.H, 128);
         struct Group {
             u32x4 w[2], x[MG][4];
@@ -594,21 +622,20 @@ __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
 #pragma unroll
             for (int j = 0; j < MG; ++j) {
                 const int i = 16 * j + li;
-                h_off[j] = i < count ? (uint32_t)(pairs[first + i] * p.I + 16 * q) * 2 : kFar;
+                h_off[j] = i < count ? (uint32_t)(pairs[first + i] * ip + 16 * q) * 2 : kFar;
             }
         };
         auto load = [&](Group& r) LLMINT8_MOE_INLINE {
-            const uint32_t far = left > 0 ? 0u : kFar;  // past the share: any weights times zeros
-            const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(p.W2 + ((int64_t)expert * p.H + n0) * ip, 16 * ip);
+            const bool in = left > 0;  // past the share: zeros
+            const int g = in ? lg : 0;  // (an empty resource takes no scalar offset: the check subtracts it)
+            const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(p.W2 + ((int64_t)expert * p.H + n0) * ip, in ? 16 * ip : 0);
+            const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, in ? h_bytes : 0);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) r.w[h] = load16(rw, w_off + 64 * h, lg * 128);
+            for (int h = 0; h < 2; ++h) r.w[h] = load16(rw, w_off + 64 * h, g * 128);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = lg * 128 + at_step(i);
-                const uint32_t out = at + 16 * q < p.I ? far : kFar;  // past I: the next row's
+            for (int j = 0; j < MG; ++j)
 #pragma unroll
-                for (int j = 0; j < MG; ++j) r.x[j][i] = load16(rh, (h_off[j] + (uint32_t)at * 2) | out);
-            }
+                for (int i = 0; i < 4; ++i) r.x[j][i] = load16(rh, h_off[j] + 128 * (i >> 1) + 16 * (i & 1), g * 256);
             r.s = load_scale(p.s2 + (expert * scale_rows + (n0 >> 7)) * isp, lg);
             __builtin_amdgcn_sched_barrier(0);  // as above
             --left;
@@ -669,9 +696,9 @@ __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
 
 // ---- the same in the light form: 8 columns of H, two entries (of up to 8 tokens) at a time, the
 // even one in rows and columns 0 .. 7 of the instruction, the odd one in 8 .. 15.
-template <int DT, int MAXT, int WV>
+template <int DT, int MAXT, int WV, int C, int D>
 __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
-    constexpr int D = 3, MAXN = MAXT * kMaxTopK;
+    constexpr int MAXN = MAXT * kMaxTopK;
     __shared__ v4f ysum[WV][MAXT][2];  // a wave's sums of 8 columns per token
     __shared__ int32_t table[3 * MAXN], pairs[MAXN];
     __shared__ float weights[MAXN];
@@ -689,9 +716,12 @@ __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
     }
     for (int i = tid; i < WV * T * 2; i += 64 * WV) ysum[i / (2 * T)][(i >> 1) % T][i & 1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     __syncthreads();
-    const int total = twos * ng, from = (int)((int64_t)total * w / WV), to = (int)((int64_t)total * (w + 1) / WV);
-    if (from < to) {
-        const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, (int64_t)n * p.I * 2);
+    // the steps (groups of I, two entries after two entries) go round the waves C at a time, so that
+    // what the workgroup reads at a time lies together
+    const int total = twos * ng, round = WV * C, own = total - total / round * round - w * C;
+    const int steps = total / round * C + (own < 0 ? 0 : (own < C ? own : C));
+    if (steps > 0) {
+        const int64_t h_bytes = (int64_t)n * ip * 2;
         const int64_t scale_rows = ceil_div(p.H, 128);
         struct Group {
             u32x4 w[2], x[1][4];
@@ -699,44 +729,54 @@ __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
         };
         // the next load's two entries and group; of this lane's entry its row of W2, its scales
         // and its token's row of h (an odd count: the last entry's weights times zeros)
-        int le = from / ng, lg = from - le * ng, left = to - from;
+        struct At {
+            int two, g, c;  // the entries, the group, the place among C
+            __device__ __forceinline__ bool next(int ng) {  // true: other entries
+                const int was = two;
+                g += ++c == C ? (WV - 1) * C + 1 : 1;
+                c = c == C ? 0 : c;
+                while (g >= ng) {
+                    g -= ng;
+                    ++two;
+                }
+                return two != was;
+            }
+        };
+        At l{w * C / ng, w * C % ng, 0}, m = l;  // of the next load, and of the next product
+        int left = steps;
         const uint8_t *row = nullptr, *scales = nullptr;
         uint32_t h_off = kFar;
         auto open = [&]() LLMINT8_MOE_INLINE {
-            const int mine = 2 * le + half, at = mine < entries ? mine : entries - 1;
+            const int mine = 2 * l.two + half, at = mine < entries ? mine : entries - 1;
             const int e = table[3 * at], first = table[3 * at + 1], count = mine < entries ? table[3 * at + 2] : 0;
             row = p.W2 + ((int64_t)e * p.H + n0 + (li & 7)) * ip + 16 * q;
             scales = p.s2 + (e * scale_rows + (n0 >> 7)) * isp;
-            h_off = (li & 7) < count ? (uint32_t)(pairs[first + (li & 7)] * p.I + 16 * q) * 2 : kFar;
+            h_off = (li & 7) < count ? (uint32_t)(pairs[first + (li & 7)] * ip + 16 * q) * 2 : kFar;
         };
         auto load = [&](Group& r) LLMINT8_MOE_INLINE {
-            const uint32_t far = left > 0 ? 0u : kFar;  // past the share: any weights times zeros
-            r.w[0] = *(const u32x4*)(row + lg * 128);
-            r.w[1] = *(const u32x4*)(row + lg * 128 + 64);
+            const uint8_t* from = row + l.g * 128;
+            r.w[0] = *(const u32x4*)from;
+            r.w[1] = *(const u32x4*)(from + 64);
+            const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, left > 0 ? h_bytes : 0);  // past the share: zeros
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = lg * 128 + at_step(i);
-                const uint32_t out = at + 16 * q < p.I ? far : kFar;  // past I: the next row's
-                r.x[0][i] = load16(rh, (h_off + (uint32_t)at * 2) | out);
-            }
-            r.s = load_scale(scales, lg);
+            for (int i = 0; i < 4; ++i) r.x[0][i] = load16(rh, h_off + 128 * (i >> 1) + 16 * (i & 1), l.g * 256);
+            r.s = load_scale(scales, l.g);
             __builtin_amdgcn_sched_barrier(0);  // as above
-            --left;
-            if (++lg == ng) {
-                lg = 0;
-                ++le;
-                if (le < twos) open();
+            if (--left > 0) {
+                if (l.next(ng)) open();
+            } else {  // from here on one line of weights
+                row = p.W2;
+                l.g = 0;
             }
         };
         v4f acc[1] = {};
-        int ce = le, cg = lg;  // the entries and group being multiplied
         // The results of an entry's rows with its own tokens; the even entry first, then the odd one:
         // a token may be in both.
-        auto flush = [&]() LLMINT8_MOE_INLINE {
+        auto flush = [&](int two) LLMINT8_MOE_INLINE {
             mfma_settle();
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const int at = 2 * ce + t;
+                const int at = 2 * two + t;
                 if (half == t && (q >> 1) == t && at < entries && (li & 7) < table[3 * at + 2]) {
                     const int pair = pairs[table[3 * at + 1] + (li & 7)];
                     const float pt = weights[pair];
@@ -752,16 +792,14 @@ __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
         open();
 #pragma unroll
         for (int d = 0; d < D; ++d) load(r[d]);
-        const int steps = to - from;
         for (int s = 0; s < steps; s += D) {  // whole rounds, as above
 #pragma unroll
             for (int d = 0; d < D; ++d) {
                 group_product<DT, 1>(r[d].w, scale_here(r[d].s), r[d].x, acc);
                 load(r[d]);
-                if (s + d < steps && (++cg == ng || s + d + 1 == steps)) {
-                    flush();
-                    cg = 0;
-                    ++ce;
+                if (s + d < steps) {
+                    const int two = m.two;
+                    if (m.next(ng) || s + d + 1 == steps) flush(two);
                 }
             }
         }
@@ -823,8 +861,8 @@ template <int DT, int MG>
 hipError_t launch_down(const Fp8MoeArgs& p, hipStream_t stream) {
     if constexpr (MG == 0) {
         const unsigned cols = (unsigned)(p.H / 8);
-        if (p.T <= 16) moe_down_light_kernel<DT, 16, 8><<<cols, 512, 0, stream>>>(p);
-        else moe_down_light_kernel<DT, 128, 8><<<cols, 512, 0, stream>>>(p);
+        if (p.T <= 16) moe_down_light_kernel<DT, 16, 8, 3, 2><<<cols, 512, 0, stream>>>(p);
+        else moe_down_light_kernel<DT, 128, 8, 3, 2><<<cols, 512, 0, stream>>>(p);
     } else {
         const unsigned cols = (unsigned)(p.H / 16);
         if constexpr (MG < 4) {

@@ -250,7 +250,7 @@ struct Fp8MoeArgs {
     int32_t* ids;    // T x k
     float* weights;  // T x k
     // workspace
-    uint16_t* h;     // (T k) x I
+    uint16_t* h;     // (T k) x pitch(I)
     int32_t* table;  // 1 + 3 T k: the entries of the second launch
     int32_t* pairs;  // T k: their pairs of token and choice
 };
