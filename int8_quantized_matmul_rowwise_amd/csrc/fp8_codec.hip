@@ -12,6 +12,9 @@
 //   p ^ (column / 8 % 16): the 8-byte writes of the 16 lanes of a row and the 16-byte reads of
 //   a column then spread over all banks.
 // Code rows are padded with zeros to a multiple of 128, a weight's scale rows to one of 4.
+// HBM-bound: 28672 x 8192 weights, both orders, 185 us = 5.1 TB/s; 2048 x 16384, ROWS and COLS,
+// 33.6 us = 4.0 TB/s (58 us with maxima passed between lanes through LDS one value at a time and
+// registers for two waves a SIMD: now two patterns to a dword, lane operands, at most 80 registers).
 #include "fp8_common.hpp"
 #include "launch.hpp"
 
@@ -32,13 +35,7 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* __restric
         const int64_t k = g * 128 + 8 * sl;
         u32x4 v = {0u, 0u, 0u, 0u};
         if (k < K) v = *(const u32x4*)(X + row * K + k);  // K is a multiple of 8
-        uint32_t m = max_pattern(v, 0u);
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) {
-            const uint32_t o = (uint32_t)__shfl_xor((int)m, off, kWave);
-            m = m > o ? m : o;
-        }
-        const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)m));
+        const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)row_max(max_pattern(magnitudes(v)))));
         *(u32x2*)(q + row * kp + k) = e4m3x8<DT>(v, e8m0_value(e));
         if (sl == 0) s[fp8_row_scale_at(row, g, M)] = (uint8_t)e;
     }
@@ -57,10 +54,11 @@ struct TileParams {
 
 // MODE 0: BLOCK, transposed codes; 1: BLOCK, both; 2: COLS; 3: COLS and ROWS
 template <int DT, int MODE>
-__global__ __launch_bounds__(256) void fp8_tile_kernel(TileParams p) {
+__global__ __launch_bounds__(256, 6) void fp8_tile_kernel(TileParams p) {
     constexpr bool BLOCK = MODE < 2;
     __shared__ __attribute__((aligned(16))) uint8_t tile[128 * 128];
-    __shared__ uint32_t red[4][128];
+    __shared__ u32x4 red[4][16];
+    __shared__ __attribute__((aligned(16))) uint8_t col_e[128], row_e[128];  // the scales' bytes
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int cc = tid & 15, rr = tid >> 4;  // columns 8 cc .. + 7, rows 8 rr .. + 7 of the tile
     const int64_t tc = blockIdx.x, tr = blockIdx.y;
@@ -82,38 +80,31 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(TileParams p) {
     }
     // ---- codes in order
     if constexpr (MODE == 3) {
+        uint32_t es[2] = {0u, 0u};
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            uint32_t m = max_pattern(v[u], 0u);
-#pragma unroll
-            for (int off = 8; off > 0; off >>= 1) {
-                const uint32_t o = (uint32_t)__shfl_xor((int)m, off, kWave);
-                m = m > o ? m : o;
-            }
-            const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)m));
+            const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)row_max(max_pattern(magnitudes(v[u])))));
+            es[u >> 2] |= e << (8 * (u & 3));
             const int64_t r = r0 + 8 * rr + u;
-            if (r < p.R) {
-                *(u32x2*)(p.q + r * cpitch + c) = e4m3x8<DT>(v[u], e8m0_value(e));
-                if (cc == 0) p.s[fp8_row_scale_at(r, tc, p.R)] = (uint8_t)e;
-            }
+            if (r < p.R) *(u32x2*)(p.q + r * cpitch + c) = e4m3x8<DT>(v[u], e8m0_value(e));
         }
+        if (cc == 0) *(u32x2*)(row_e + 8 * rr) = u32x2{es[0], es[1]};
     }
     // ---- the scales of the transposed codes: largest patterns of the tile or of its columns
     float sv[8];
+    u32x4 m = magnitudes(v[0]);  // of this thread's 8 columns over its 8 rows
+#pragma unroll
+    for (int u = 1; u < 8; ++u)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) m[d] = max_patterns(m[d], v[u][d] & 0x7fff7fffu);
     if constexpr (BLOCK) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) m = max_pattern(v[u], m);
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) {
-            const uint32_t o = (uint32_t)__shfl_xor((int)m, off, kWave);
-            m = m > o ? m : o;
-        }
-        if (lane == 0) red[w][0] = m;
+        const uint32_t t = max_patterns_rows(row_max(max_pattern(m)));
+        if (lane == 0) red[w][0][0] = t;
         __syncthreads();
+        uint32_t a = red[0][0][0];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = m > red[i][0] ? m : red[i][0];
-        const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)m));
+        for (int i = 1; i < 4; ++i) a = a > red[i][0][0] ? a : red[i][0][0];
+        const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)a));
 #pragma unroll
         for (int j = 0; j < 8; ++j) sv[j] = e8m0_value(e);
         if (tid == 0) {
@@ -127,34 +118,22 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(TileParams p) {
             }
         }
     } else {
-        uint32_t m[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m[j] = 0;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const uint32_t a = (v[u][j >> 1] >> (16 * (j & 1))) & 0x7fffu;
-                m[j] = m[j] > a ? m[j] : a;
-            }
-#pragma unroll
-            for (int off = 32; off >= 16; off >>= 1) {
-                const uint32_t o = (uint32_t)__shfl_xor((int)m[j], off, kWave);
-                m[j] = m[j] > o ? m[j] : o;
-            }
-            if (lane < 16) red[w][8 * cc + j] = m[j];
-        }
+        for (int d = 0; d < 4; ++d) m[d] = max_patterns_rows(m[d]);
+        if (lane < 16) red[w][cc] = m;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t o = red[i][8 * cc + j];
-                m[j] = m[j] > o ? m[j] : o;
-            }
-            const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)m[j]));
+            for (int d = 0; d < 4; ++d) m[d] = max_patterns(m[d], red[i][cc][d]);
+        uint32_t es[2] = {0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)(m[j >> 1] >> (16 * (j & 1)))));
+            es[j >> 2] |= e << (8 * (j & 3));
             sv[j] = e8m0_value(e);
-            if (rr == 0 && c + j < p.C) p.st[fp8_row_scale_at(c + j, tr, p.C)] = (uint8_t)e;
         }
+        if (rr == 0) *(u32x2*)(col_e + 8 * cc) = u32x2{es[0], es[1]};
     }
     if constexpr (MODE == 1) {
 #pragma unroll
@@ -173,6 +152,18 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(TileParams p) {
         *(u32x2*)(tile + (8 * cc + j) * 128 + ((rr ^ cc) << 3)) = e4m3x8<DT>(col, sv[j]);
     }
     __syncthreads();
+    if constexpr (!BLOCK) {
+        // 64 scales are 16 dwords of four 16 apart (those past the last are padding)
+        const int at = 64 * ((tid >> 4) & 1) + cc;
+        if (tid < 32 && c0 + at - cc < p.C)
+            *(uint32_t*)(p.st + fp8_row_scale_at(c0 + at, tr, p.C)) =
+                col_e[at] | (uint32_t)col_e[at + 16] << 8 | (uint32_t)col_e[at + 32] << 16 | (uint32_t)col_e[at + 48] << 24;
+        if constexpr (MODE == 3) {
+            if (tid >= 64 && tid < 96 && r0 + at - cc < p.R)
+                *(uint32_t*)(p.s + fp8_row_scale_at(r0 + at, tc, p.R)) =
+                    row_e[at] | (uint32_t)row_e[at + 16] << 8 | (uint32_t)row_e[at + 32] << 16 | (uint32_t)row_e[at + 48] << 24;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int col = 32 * i + (tid >> 3), piece = tid & 7;  // 16 bytes = row pieces 2 piece, 2 piece + 1

@@ -20,7 +20,7 @@ __host__ __device__ constexpr int64_t fp8_scale_pitch_of(int64_t n) { return rou
 // The scales of coded activations, one per row and group, as the product kernels take them: for
 // each group, for each 64 rows, a dword per row mod 16 that holds the bytes of the four rows
 // 16 apart -- the matrix instruction picks a byte of its scale operand, so one dword per lane
-// scales four pieces of 16 rows.  Bytes of rows past the last are not written.
+// scales four pieces of 16 rows.  What the bytes of rows past the last hold has no effect.
 __host__ __device__ constexpr int64_t fp8_row_scale_at(int64_t r, int64_t g, int64_t rows) {
     return (g * ceil_div(rows, 64) + (r >> 6)) * 64 + (r & 15) * 4 + ((r >> 4) & 3);
 }
@@ -38,17 +38,37 @@ __device__ __forceinline__ float e8m0_value(uint32_t b) {
     return __builtin_bit_cast(float, b ? b << 23 : 0x00400000u);
 }
 
-// Eight 16-bit values (one 16-byte piece): their magnitudes as patterns, whose unsigned order
-// is the order of the magnitudes (an infinity above the numbers, a NaN above that).
-__device__ __forceinline__ uint32_t max_pattern(const u32x4& v, uint32_t m) {
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        const uint32_t a = v[d] & 0x7fff7fffu;
-        const uint32_t lo = a & 0xffffu, hi = a >> 16;
-        m = m > lo ? m : lo;
-        m = m > hi ? m : hi;
-    }
+// Magnitudes are compared as 16-bit patterns, two to a dword: their unsigned order is the order of
+// the magnitudes (an infinity above the numbers, a NaN above that).
+__device__ __forceinline__ uint32_t max_patterns(uint32_t a, uint32_t b) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+__device__ __forceinline__ u32x4 magnitudes(const u32x4& v) { return v & 0x7fff7fffu; }
+__device__ __forceinline__ uint32_t max_pattern(const u32x4& m) {  // of eight magnitudes, one pattern
+    const uint32_t a = max_patterns(max_patterns(m[0], m[1]), max_patterns(m[2], m[3]));
+    return (a & 0xffffu) > a >> 16 ? a & 0xffffu : a >> 16;
+}
+// The largest of the 16 lanes of a row, in all of them: rotations as operands of the maximum.
+__device__ __forceinline__ uint32_t row_max(uint32_t m) {
+#define LLMINT8_ROR(N)                                                                          \
+    do {                                                                                        \
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x120 + N, 0xf, 0xf, false); \
+        m = m > o ? m : o;                                                                      \
+    } while (0)
+    LLMINT8_ROR(8);
+    LLMINT8_ROR(4);
+    LLMINT8_ROR(2);
+    LLMINT8_ROR(1);
+#undef LLMINT8_ROR
     return m;
+}
+// The larger patterns of lanes 16 apart, then 32 apart: of the four rows of a wave, in all of them.
+__device__ __forceinline__ uint32_t max_patterns_rows(uint32_t m) {
+    const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = max_patterns(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    return max_patterns(b[0], b[1]);
 }
 
 // Codes of two 16-bit values (a pattern pair) at the scale's value s, into half HI of `old`: the

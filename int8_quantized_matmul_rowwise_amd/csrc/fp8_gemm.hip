@@ -491,14 +491,12 @@ __global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, 
         asm volatile("" : "+v"(eb));
         eb = (int)((uint32_t)eb >> r.shift);
         if constexpr (FUSED) {
-            uint32_t m = 0;
+            u32x4 v = magnitudes(r.a[0]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = max_pattern(r.a[i], m);
+            for (int i = 1; i < 4; ++i)
 #pragma unroll
-            for (int off = 16; off <= 32; off <<= 1) {
-                const uint32_t o = (uint32_t)__shfl_xor((int)m, off, kWave);
-                m = m > o ? m : o;
-            }
+                for (int d = 0; d < 4; ++d) v[d] = max_patterns(v[d], r.a[i][d] & 0x7fff7fffu);
+            const uint32_t m = max_patterns_rows(max_pattern(v));
             ea = (int)e8m0_of(to_f32<DT>((uint16_t)m));
             const float s = e8m0_value((uint32_t)ea);
             u32x2 c[4];
