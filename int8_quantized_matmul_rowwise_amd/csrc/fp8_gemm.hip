@@ -80,7 +80,9 @@ __device__ __forceinline__ bool last_part(int32_t* counter, int parts, int* flag
         if (done == parts) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
-    const bool last = *flag != 0;
+    // (one answer for the wave: a branch on a lane's value would make the compiler take all that the
+    // code before it places -- resources, offsets -- for lanes' values, and loop over them)
+    const bool last = __builtin_amdgcn_readfirstlane(*flag) != 0;
     __syncthreads();  // before the word is used again
     return last;
 }
@@ -132,15 +134,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
     const int my_tiles = local < x_cnt ? (x_cnt - local + on_xcd - 1) / on_xcd : 0;
     if (my_tiles == 0) return;  // the same for every wave
     // SPLIT: one tile (T workgroups), its stages from k0
-    const int part = SPLIT ? (x_start + local) / T1 : 0, k0 = SPLIT ? part * tp.part : 0;
+    // (a quotient comes from the vector unit: read back, or every load that it places would loop over lanes)
+    const int part = SPLIT ? __builtin_amdgcn_readfirstlane((x_start + local) / T1) : 0, k0 = SPLIT ? part * tp.part : 0;
     const int all = (int)(p.pitch / BK), nk = SPLIT ? (all - k0 < tp.part ? all - k0 : tp.part) : all;
     auto tile_origin = [&](int i, int64_t& m0, int64_t& n0) LLMINT8_FP8_INLINE {
         const int t = SPLIT ? (x_start + local) - part * T1 : x_start + local + i * on_xcd;
         const int in_group = kGroupM * tp.tiles_n;
         const int first_m = (t / in_group) * kGroupM;
         const int gm = tp.tiles_m - first_m < kGroupM ? tp.tiles_m - first_m : kGroupM;
-        m0 = (int64_t)(first_m + (t % in_group) % gm) * BM;
-        n0 = (int64_t)((t % in_group) / gm) * BN;
+        m0 = (int64_t)__builtin_amdgcn_readfirstlane(first_m + (t % in_group) % gm) * BM;
+        n0 = (int64_t)__builtin_amdgcn_readfirstlane((t % in_group) / gm) * BN;
     };
 
     // ---- operand loads: rows past M or N lie past the resources and read zero, as do all of
@@ -155,10 +158,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
         ra = buffer_rsrc(p.A + m0 * p.pitch, rows_a * p.pitch);
         rb = buffer_rsrc(p.B + n0 * p.pitch, rows_b * p.pitch);
     };
-    __amdgpu_buffer_rsrc_t ra0, rb0, ra1, rb1, ra2, rb2;
+    __amdgpu_buffer_rsrc_t ra0, rb0, ra1, rb1, ra2, rb2;  // (SPLIT: one tile, the first pair)
     tile_rsrc(0, ra0, rb0);
-    tile_rsrc(1, ra1, rb1);
-    tile_rsrc(2, ra2, rb2);
+    if constexpr (!SPLIT) {
+        tile_rsrc(1, ra1, rb1);
+        tile_rsrc(2, ra2, rb2);
+    }
     uint32_t off[4];  // of both operands: row 8 (4 wu + j) + lane / 8, its chunk lane % 8
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -167,9 +172,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
     }
     auto slot_a = [&](int s) LLMINT8_FP8_INLINE { return smem + s * kSlotA; };
     auto slot_b = [&](int s) LLMINT8_FP8_INLINE { return smem + 2 * kSlotA + s * kSlotB; };
-    auto issue = [&](__amdgpu_buffer_rsrc_t rs, uint8_t* slot, int k, int j) LLMINT8_FP8_INLINE {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(slot + (4 * wu + j) * 1024), 16, (int)off[j], (k0 + k) * BK, 0, 0);
+    // `left`: the tiles from the current one on, so that a load d tiles ahead has one if d < left; a
+    // load without one lies past its resource (which, empty, takes no scalar offset: the check
+    // subtracts that)
+    int left = my_tiles;
+    auto issue = [&](int d, __amdgpu_buffer_rsrc_t r0, __amdgpu_buffer_rsrc_t r1, __amdgpu_buffer_rsrc_t r2, uint8_t* slot, int k,
+                     int j) LLMINT8_FP8_INLINE {
+        const __amdgpu_buffer_rsrc_t rs = SPLIT ? r0 : pick(d, r0, r1, r2);
+        const uint32_t far = SPLIT && d ? 0x80000000u : 0u;
+        const int at = __builtin_amdgcn_readfirstlane(d < left ? (k0 + k) * BK : 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(slot + (4 * wu + j) * 1024), 16, (int)(off[j] | far), at, 0, 0);
     };
+    auto issue_a = [&](int d, uint8_t* slot, int k, int j) LLMINT8_FP8_INLINE { issue(d, ra0, ra1, ra2, slot, k, j); };
+    auto issue_b = [&](int d, uint8_t* slot, int k, int j) LLMINT8_FP8_INLINE { issue(d, rb0, rb1, rb2, slot, k, j); };
 
     // ---- the scales of a stage: offsets and bytes of this tile's and the next tile's, held as
     // scalars (past the last tile: none, the loads return zeros)
@@ -188,20 +203,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
         b_n = ROWB ? (int)round_up(rows_b, 64) : (int)ceil_div(rows_b, 128);
     };
     scale_range(0, a_at0, a_n0, b_at0, b_n0);
-    scale_range(1, a_at1, a_n1, b_at1, b_n1);
+    if constexpr (!SPLIT) scale_range(1, a_at1, a_n1, b_at1, b_n1);
     auto load_scales = [&](int next, int kt, int& sm, int (&sn)[NS]) LLMINT8_FP8_INLINE {
-        const int k = k0 + kt;
+        int k = kt, a_at = a_at0, a_n = a_n0, b_at = b_at0, b_n = b_n0;
+        if constexpr (SPLIT) {
+            k = __builtin_amdgcn_readfirstlane(k0 + (next ? 0 : kt));  // past the part: any scales, unused
+        } else {
+            a_at = pick(next, a_at0, a_at1);
+            a_n = pick(next, a_n0, a_n1);
+            b_at = pick(next, b_at0, b_at1);
+            b_n = pick(next, b_n0, b_n1);
+        }
         int li = lane & 15;  // opaque: the offsets are computed here, not held in registers
         asm volatile("" : "+v"(li));
-        const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(p.sa + (int64_t)k * ta + pick(next, a_at0, a_at1), pick(next, a_n0, a_n1));
+        const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(p.sa + (int64_t)k * ta + a_at, a_n);
         sm = (int)__builtin_amdgcn_raw_buffer_load_b32(ra, (uint32_t)(64 * wm + 4 * li), 0, 0);
         if constexpr (ROWB) {
-            const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.sb + (int64_t)k * tb + pick(next, b_at0, b_at1), pick(next, b_n0, b_n1));
+            const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.sb + (int64_t)k * tb + b_at, b_n);
 #pragma unroll
             for (int f = 0; f < NS; ++f)
                 sn[f] = (int)__builtin_amdgcn_raw_buffer_load_b32(rb, (uint32_t)(16 * NF * wn + 64 * f + 4 * li), 0, 0);
         } else {
-            const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.sb + pick(next, b_at0, b_at1) * p.spitch, pick(next, b_n0, b_n1) * p.spitch);
+            const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.sb + b_at * p.spitch, b_n * p.spitch);
             sn[0] = (int)__builtin_amdgcn_raw_buffer_load_b8(rb, (uint32_t)(((16 * NF * wn) >> 7) * (int)p.spitch + k), 0, 0);
         }
     };
@@ -223,7 +246,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
         // both operands' loads are two stages ahead: stage k2 of the tile d ahead
         const int d = __builtin_amdgcn_readfirstlane(kt + 2 < nk ? 0 : (kt + 2 < 2 * nk ? 1 : 2));
         const int k2 = kt + 2 - d * nk;
-        const __amdgpu_buffer_rsrc_t rs_a = pick(d, ra0, ra1, ra2), rs_b = pick(d, rb0, rb1, rb2);
         uint8_t* to_b = slot_b(sb == 0 ? 2 : sb - 1);
         const uint8_t* An = slot_a(sa ^ 1) + wm * (16 * MF * BK);
         const uint8_t* Bc = slot_b(sb) + wn * (16 * NF * BK);
@@ -244,7 +266,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
         for (int f = 0; f < kPhases; ++f) {
 #pragma unroll
             for (int l = 0; l < 4; ++l)
-                if (l * kPhases / 4 == f) issue(rs_b, to_b, k2, l);
+                if (l * kPhases / 4 == f) issue_b(d, to_b, k2, l);
             w[f + 2] = read(Bc, f + 2);
             mfma_row(f);
             __builtin_amdgcn_sched_barrier(0);
@@ -254,14 +276,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
         fm[P ^ 1][0] = read(An, 0);
         fm[P ^ 1][1] = read(An, 1);
 #pragma unroll
-        for (int l = 0; l < 2; ++l) issue(rs_a, slot_a(sa), k2, l);
+        for (int l = 0; l < 2; ++l) issue_a(d, slot_a(sa), k2, l);
         mfma_row(NF - 2);
         __builtin_amdgcn_sched_barrier(0);
         fm[P ^ 1][2] = read(An, 2);
         fm[P ^ 1][3] = read(An, 3);
         fn[1] = read(Bn, 1);
 #pragma unroll
-        for (int l = 2; l < 4; ++l) issue(rs_a, slot_a(sa), k2, l);
+        for (int l = 2; l < 4; ++l) issue_a(d, slot_a(sa), k2, l);
         mfma_row(NF - 1);
         __builtin_amdgcn_sched_barrier(0);
         sm = nsm;
@@ -303,14 +325,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
     // ---- prologue: stages 0 and 1 of both operands, the first scales
     load_scales(0, 0, sm, sn);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) issue(ra0, slot_a(0), 0, j);
+    for (int j = 0; j < 4; ++j) issue_a(0, slot_a(0), 0, j);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) issue(rb0, slot_b(0), 0, j);
+    for (int j = 0; j < 4; ++j) issue_b(0, slot_b(0), 0, j);
     const int d1 = nk > 1 ? 0 : 1, k1 = 1 - d1;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) issue(pick(d1, rb0, rb1, rb1), slot_b(1), k1, j);
+    for (int j = 0; j < 4; ++j) issue_b(d1, slot_b(1), k1, j);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) issue(pick(d1, ra0, ra1, ra1), slot_a(1), k1, j);
+    for (int j = 0; j < 4; ++j) issue_a(d1, slot_a(1), k1, j);
     LLMINT8_FP8_WAIT_BARRIER(8);
     auto first_reads = [&](int sa, int sb) LLMINT8_FP8_INLINE {
         fn[0] = read(slot_b(sb) + wn * (16 * NF * BK), 0);
@@ -342,6 +364,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
         }
         mfma_settle();
         if constexpr (SPLIT) {
+            constexpr int H = NF == 8 ? (ROWB ? 1 : 2) : 4;  // as the registers allow
             constexpr uint32_t kStep = 64 * kWaves * 16;  // bytes of one quad of every thread
             const int tile = x_start + local - part * T1;
             auto slot = [&](int i) LLMINT8_FP8_INLINE {
@@ -360,17 +383,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
             for (int i = 0; i < tp.split; ++i) {
                 const __amdgpu_buffer_rsrc_t rs = slot(i);
 #pragma unroll
-                for (int f = 0; f < NF; ++f) {
-                    v4f v[MF];
+                for (int f = 0; f < NF; f += H) {  // several loads under way
+                    v4f v[H][MF];
 #pragma unroll
-                    for (int j = 0; j < MF; ++j) v[j] = load_part(rs, 16 * tid, (f * MF + j) * kStep);
+                    for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int j = 0; j < MF; ++j) acc[f][j] += v[j];
+                        for (int j = 0; j < MF; ++j) v[h][j] = load_part(rs, 16 * tid, ((f + h) * MF + j) * kStep);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+#pragma unroll
+                        for (int j = 0; j < MF; ++j) acc[f + h][j] += v[h][j];
                 }
             }
         }
         output(ti, sb == 0 ? 2 : sb - 1);  // the slot of the last stage
-        if (ti + 1 < my_tiles) {
+        if (!SPLIT && ti + 1 < my_tiles) {
+            --left;
             ra0 = ra1;
             rb0 = rb1;
             ra1 = ra2;
@@ -600,6 +629,24 @@ int parts(int64_t groups, int64_t wanted, int64_t least) {
     return (int)ceil_div(groups, part);
 }
 
+// Parts of the sum of `tiles` (at most 512) tiles of 128 x 128, two of which fit a compute unit.
+// The estimate, in units of 10 ns, from measurements over 9 to 512 tiles and 4 to 128 groups: a group
+// takes 0.6 us where a workgroup has the unit to itself, else 0.9 us a pair; joining s parts takes
+// 2 us + 0.6 s us + 0.011 us a part and tile.  65 x 16384 x 4096 (32 tiles): 79.6 us unsplit, 47.9 in
+// 2 parts, 32.1 in 4, 29.3 in 8, 33.1 in 16; 512 x 4096 x 4096 (128 tiles): 21.2, 20.1 in 2, 25.4
+// in 4; 1000 x 4096 x 4096 (256 tiles): 22.8, 28.3 in 2.
+int parts128(int64_t tiles, int64_t groups) {
+    int64_t best = 60 * groups * (tiles > 256 ? 3 : 2) / 2, s = 1;
+    for (int64_t i = 2; i <= 16 && i <= groups && i * tiles <= 512; ++i) {
+        const int64_t cost = 60 * ceil_div(groups, i) * (tiles * i > 256 ? 3 : 2) / 2 + 200 + 60 * i + 11 * i * tiles / 10;
+        if (cost < best) {
+            best = cost;
+            s = i;
+        }
+    }
+    return parts(groups, s, 1);
+}
+
 }  // namespace
 
 Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb) {
@@ -615,18 +662,19 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb) {
         out = 256 * p.columns * p.pieces;
     } else {
         const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256), t128 = ceil_div(M, 128) * ceil_div(N, 128);
-        if (t256 < 256) {
+        // Tiles of 128 where all of them fit the card at once (two a compute unit): 2048 x 4096 x 4096
+        // 33.8 us, with tiles of 256 42.1; 333 x 4096 x 16384 38.3 and 44.0; past that tiles of 256:
+        // 2048 x 2064 x 7424 31.3 us, with tiles of 128 41.2; 1000 x 4096 x 16384 55.2 and 75.7.
+        // Between half and all of that with a long sum, tiles of 256 in parts: 2048 x 16384 x 4096 116 us
+        // in 2, with tiles of 128 136; 1000 x 8192 x 8192 (64 groups) 72.2 and 70.0.
+        if (t128 <= 512 && !(t128 > 256 && nk >= 96)) {
             p.kind = Fp8Plan::kTile128;
             out = 128 * 128;
             p.tiles = t128;
-            if (M > 128 && t256 <= 128 && nk >= 32) {
-                p.kind = Fp8Plan::kTile256;
-                out = 256 * 256;
-                p.tiles = t256;
-                p.split = parts(nk, 256 / t256, 8);
-            } else if (t128 <= 256) {
-                p.split = parts(nk, 512 / t128, 8);
-            }
+            p.split = parts128(t128, nk);
+        } else {
+            p.tiles = t256;
+            if (t256 <= 128) p.split = parts(nk, 256 / t256, 32);
         }
     }
     p.partial_bytes = p.split > 1 ? p.tiles * p.split * out * 4 : 0;

@@ -330,7 +330,7 @@ struct UpSetup {
     // same expert, whose workgroups do it), or of expert y.
     __device__ __forceinline__ int find(const Fp8MoeArgs& p, const int32_t* ids, int y, int by_pair, int& e) {
         const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-        e = by_pair ? ids[y] : y;
+        e = __builtin_amdgcn_readfirstlane(by_pair ? ids[y] : y);  // (from LDS it would count as a lane's value)
         int mine = -1;
         if (tid < 128 && tid < p.T)
             for (int j = 0; j < p.k; ++j)
@@ -340,7 +340,7 @@ struct UpSetup {
         const uint64_t have = __ballot(mine >= 0);
         if (w < 2 && lane == 0) part[w] = __popcll(have);
         __syncthreads();
-        const int count = dup ? 0 : part[0] + part[1];
+        const int count = __builtin_amdgcn_readfirstlane(dup ? 0 : part[0] + part[1]);
         if (mine >= 0) list[(w == 1 ? part[0] : 0) + __popcll(have & ((1ull << lane) - 1ull))] = mine;
         __syncthreads();
         return count;
@@ -524,11 +524,13 @@ __global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8
         int lt = 0, lg = w;  // the next load's tile and group
         auto load = [&](Group& r) LLMINT8_MOE_INLINE {
             const bool in = lt < my_tiles && lg < ng;  // else: one line of weights times zeros
-            const int t = in ? lt : 0, wg = in ? lg : 0;
+            // (read back: with the choices in LDS the compiler takes these for lanes' values)
+            const int t = __builtin_amdgcn_readfirstlane(in ? lt : 0), wg = __builtin_amdgcn_readfirstlane(in ? lg : 0);
+            const int x_bytes = __builtin_amdgcn_readfirstlane(in ? (int)(p.T * p.H * 2) : 0);
             const uint8_t* at = in ? W + 8 * t * hp + wg * 128 : p.W13;
             r.w[0] = *(const u32x4*)at;
             r.w[1] = *(const u32x4*)(at + 64);
-            load_row(buffer_rsrc(p.X, in ? p.T * p.H * 2 : 0), x_at, wg, lg == ng - 1, r.x[0]);
+            load_row(buffer_rsrc(p.X, x_bytes), x_at, wg, wg == ng - 1, r.x[0]);
             // (I is a multiple of 16: a tile's gate rows, and its up rows, lie in one block)
             const int64_t i0 = 8 * (int64_t)(tile0 + t);
             r.e = load_scale(rs, up_scale ? (uint32_t)(((p.I + i0) >> 7) * hsp) : (uint32_t)((i0 >> 7) * hsp), wg);
