@@ -253,16 +253,20 @@ int check_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
 }
 
 struct MoeLayout {
-    size_t h, table, pairs, total;
+    Fp8MoePlan plan;
+    size_t h, table, pairs, counters, partial, total;
 };
 
-MoeLayout moe_layout(int64_t T, int64_t I, int64_t k) {
+MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
     MoeLayout L;
+    L.plan = fp8_moe_plan(T, H, I, E, k);
     const size_t n = (size_t)T * (size_t)k;
     L.h = 0;
     L.table = align_up(n * (size_t)fp8_pitch(I) * 2);
     L.pairs = align_up(L.table + (1 + 3 * n) * 4);
-    L.total = align_up(L.pairs + n * 4);
+    L.counters = align_up(L.pairs + n * 4);
+    L.partial = align_up(L.counters + (L.plan.parts > 1 ? (size_t)L.plan.blocks * 4 : 0));
+    L.total = align_up(L.partial + (size_t)L.plan.partial_bytes);
     return L;
 }
 
@@ -270,7 +274,7 @@ MoeLayout moe_layout(int64_t T, int64_t I, int64_t k) {
 
 LLMINT8_API size_t fp8_moe_block_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
     if (check_moe(T, H, I, E, top_k)) return 0;
-    return moe_layout(T, I, top_k).total;
+    return moe_layout(T, H, I, E, top_k).total;
 }
 
 LLMINT8_API int fp8_moe_block(const void* X, int64_t T, int64_t H, int dtype, const float* logits, int64_t E,
@@ -287,7 +291,7 @@ LLMINT8_API int fp8_moe_block(const void* X, int64_t T, int64_t H, int dtype, co
     if (I > 0 && (!W13q || !aligned(W13q, 16) || !w13_scale || !aligned(w13_scale, 4) || !W2q || !aligned(W2q, 16) ||
                   !w2_scale || !aligned(w2_scale, 4)))
         return LLMINT8_EINVAL;
-    const MoeLayout L = moe_layout(T, I, top_k);
+    const MoeLayout L = moe_layout(T, H, I, E, top_k);
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < L.total) return LLMINT8_EWORKSPACE;
     const size_t e = (size_t)E, pairs = (size_t)T * (size_t)top_k;
     const Range r[] = {{Y, (size_t)T * (size_t)H * 2},
@@ -305,6 +309,6 @@ LLMINT8_API int fp8_moe_block(const void* X, int64_t T, int64_t H, int dtype, co
     uint8_t* ws = (uint8_t*)workspace;
     const Fp8MoeArgs a{(const uint16_t*)X, T, H, logits, E, (int)top_k, renormalize != 0, W13q, w13_scale, W2q, w2_scale,
                        I, (uint16_t*)Y, topk_ids, topk_weights, (uint16_t*)(ws + L.h), (int32_t*)(ws + L.table),
-                       (int32_t*)(ws + L.pairs)};
-    return hip_status(stage("fp8_moe", [&] { return launch_fp8_moe(dtype, a, (hipStream_t)stream); }));
+                       (int32_t*)(ws + L.pairs), (int32_t*)(ws + L.counters), (float*)(ws + L.partial)};
+    return hip_status(stage("fp8_moe", [&] { return launch_fp8_moe(dtype, a, L.plan, (hipStream_t)stream); }));
 }

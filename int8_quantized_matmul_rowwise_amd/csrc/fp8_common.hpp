@@ -96,4 +96,35 @@ __device__ __forceinline__ u32x2 e4m3x8(const u32x4& v, float s) {
 // needs, which the compiler (ROCm 7.2) has been seen to leave out across a branch.
 __device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)bytes, 0x00020000);
+}
+
+// ---- sums split over workgroups
+constexpr int kCoherent = 16;  // cache policy: coherent across the XCDs, past their L2s
+
+// A workgroup's share of a sum is in memory (stores of every wave issued): true for the one that
+// finds all `parts` in, which leaves the counter at zero.  flag: a word of LDS.
+__device__ __forceinline__ bool last_part(int32_t* counter, int parts, int* flag) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const int done = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
+        *flag = done == parts;
+        if (done == parts) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    // (one answer for the wave: a branch on a lane's value would make the compiler take all that the
+    // code before it places -- resources, offsets -- for lanes' values, and loop over them)
+    const bool last = __builtin_amdgcn_readfirstlane(*flag) != 0;
+    __syncthreads();  // before the word is used again
+    return last;
+}
+__device__ __forceinline__ v4f load_part(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t at) {
+    return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off, at, kCoherent));
+}
+__device__ __forceinline__ void store_part(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t at, const v4f& v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, off, at, kCoherent);
+}
+
 }  // namespace llmint8

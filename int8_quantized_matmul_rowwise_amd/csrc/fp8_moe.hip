@@ -26,6 +26,8 @@
 // are 8 gate and the same 8 up columns in the first launch, and 8 columns of two experts in the
 // second, whose tokens are the two halves of its columns (the products of one expert's rows with
 // the other's tokens are not used).  Otherwise 16 columns and MG pieces of tokens.
+#include <cmath>
+
 #include "fp8_common.hpp"
 #include "launch.hpp"
 
@@ -42,9 +44,6 @@ constexpr int kLightMean = 6;
 
 #define LLMINT8_MOE_INLINE __attribute__((always_inline))
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)bytes, 0x00020000);
-}
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t off, int at = 0) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, at, 0));
 }
@@ -347,15 +346,15 @@ struct UpSetup {
     }
 };
 
-// ---- gate, up and SwiGLU: a workgroup takes `span` tiles of 16 columns of I of one expert (16
-// gate rows and 16 up rows each), its waves split the groups of H.  A wave's groups, tile after
-// tile, run through D sets of registers, so that the next tile's weights are on their way while
-// a tile's sums meet.  Workgroup 0 writes the table.
+// ---- gate, up and SwiGLU: a workgroup takes `span` (at most its waves) tiles of 16 columns of I of
+// one expert (16 gate rows and 16 up rows each).  Their groups of H, tile after tile, are split
+// evenly over the waves and run through D sets of registers; what a wave has of a tile (it meets at
+// most two) goes to LDS, and the waves meet once, after the last.  Workgroup 0 writes the table.
 template <int DT, int MG>
-__global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(Fp8MoeArgs p, int spans, int span, int by_pair, int chunk) {
+__global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(Fp8MoeArgs p, int spans, int span, int by_pair, int chunk, int n_zero) {
     constexpr int WV = kUpWaves, D = 2;
     union Shared {
-        v4f red[WV][2 * MG][64];
+        v4f red[WV][2][2 * MG][64];  // of a wave's first tile and of its second
         struct {
             uint32_t mask[kMaxExperts][4];
             int first[kMaxExperts];
@@ -368,6 +367,7 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
     const int k = p.k;
     const int32_t* ids = setup.template route<WV>(p);
     if (blockIdx.x == 0) {
+        for (int i = tid; i < n_zero; i += blockDim.x) p.counters[i] = 0;
         build_table(ids, (int)p.T, (int)p.E, k, chunk, p.table, p.pairs, sh.t.mask, sh.t.first);
         return;
     }
@@ -380,8 +380,7 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
     const int64_t hp = fp8_pitch(p.H), hsp = fp8_scale_pitch_of(p.H);
     const int tiles = (int)(p.I / 16), ng = (int)(hp / 128);
     const int my_tiles = tiles - tile0 < span ? tiles - tile0 : span;
-    const int gw = (ng + WV - 1) / WV;  // groups of a wave (its last may lie past H: zeros)
-    const int steps = my_tiles * gw;
+    const int all = my_tiles * ng, from = all * w / WV, to = all * (w + 1) / WV;
     const uint8_t* W = p.W13 + (int64_t)e * 2 * p.I * hp;
     const uint8_t* S = p.s13 + (int64_t)e * ceil_div(2 * p.I, 128) * hsp;
     const int64_t ip = fp8_pitch(p.I);
@@ -398,9 +397,9 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
             const int i = c0 + 16 * j + li;
             x_at[j].set(i < count ? (uint32_t)((list[i] / k) * p.H) * 2 : kFar, (int)p.H, ng, q);
         }
-        int lt = 0, lg = w;  // the next load's tile and group
+        int lt = from / ng, lg = from - lt * ng, left = to - from;  // the next load's tile and group
         auto load = [&](Group& r) LLMINT8_MOE_INLINE {
-            const bool in = lt < my_tiles && lg < ng;
+            const bool in = left > 0;  // past the share: zeros
             const int64_t i0 = 16 * (int64_t)(in ? tile0 + lt : tile0);
             const int wg = in ? lg : 0, bytes = in ? 16 * (int)hp : 0;
             const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(W + i0 * hp, bytes), ru = buffer_rsrc(W + (p.I + i0) * hp, bytes);
@@ -415,71 +414,68 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
             // the scales of the 16 rows (I is a multiple of 16: one block of rows each)
             r.eg = load_scale(S + (i0 >> 7) * hsp, wg);
             r.eu = load_scale(S + ((p.I + i0) >> 7) * hsp, wg);
-            lg += WV;
-            if (lg >= gw * WV) {
-                lg = w;
+            --left;
+            if (++lg == ng) {
+                lg = 0;
                 ++lt;
             }
             __builtin_amdgcn_sched_barrier(0);  // the sets are issued, and so waited for, one after the other
         };
         v4f ag[MG] = {}, au[MG] = {};
-        int tile = tile0, done = 0;
-        // after a tile's last group: the waves' sums meet, SwiGLU, h
-        auto finish = [&]() LLMINT8_MOE_INLINE {
-            mfma_settle();
-#pragma unroll
-            for (int j = 0; j < MG; ++j) {
-                sh.red[w][j][lane] = ag[j];
-                sh.red[w][MG + j][lane] = au[j];
-                ag[j] = au[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-            }
-            __syncthreads();
-            // an output a thread: the waves' sums in their order
-            const float* red = (const float*)sh.red;
-            for (int o = tid; o < 256 * MG; o += 64 * WV) {
-                float a[WV], b[WV];
-#pragma unroll
-                for (int i = 0; i < WV; ++i) {
-                    a[i] = red[i * (512 * MG) + o];
-                    b[i] = red[i * (512 * MG) + 256 * MG + o];
-                }
-                float gate = a[0], up = b[0];
-#pragma unroll
-                for (int i = 1; i < WV; ++i) {
-                    gate += a[i];
-                    up += b[i];
-                }
-                const int l = (o >> 2) & 63, i = c0 + 16 * (o >> 8) + (l & 15);
-                if (i < count) p.h[(int64_t)list[i] * ip + 16 * tile + 4 * (l >> 4) + (o & 3)] = swiglu<DT>(gate, up);
-            }
-            if (tile == tiles - 1) pad_rows(p, list, c0, count < c0 + 16 * MG ? count : c0 + 16 * MG, ip);
-            __syncthreads();
-            ++tile;
-        };
+        int slot = 0, cg = lg;  // of the tile and group being multiplied
         Group r[D];
 #pragma unroll
         for (int d = 0; d < D; ++d) load(r[d]);
         // (whole rounds of D steps: a way out between them would make the compiler wait, at the top,
         // for every set instead of the first; steps past the last multiply zeros)
+        const int steps = to - from;
         for (int s = 0; s < steps; s += D) {
 #pragma unroll
             for (int d = 0; d < D; ++d) {
                 group_product<DT, MG>(r[d].g, scale_here(r[d].eg), r[d].x, ag);
                 group_product<DT, MG>(r[d].u, scale_here(r[d].eu), r[d].x, au);
                 load(r[d]);
-                if (s + d < steps && ++done == gw) {
-                    done = 0;
-                    finish();
+                if (s + d < steps && (++cg == ng || s + d + 1 == steps)) {
+                    mfma_settle();
+#pragma unroll
+                    for (int j = 0; j < MG; ++j) {
+                        sh.red[w][slot][j][lane] = ag[j];
+                        sh.red[w][slot][MG + j][lane] = au[j];
+                        ag[j] = au[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                    }
+                    slot = 1;
+                    cg = 0;
                 }
             }
         }
+        __syncthreads();
+        // an output a thread at a time: its tile's sums in the order of the waves, SwiGLU, h
+        const float* red = (const float*)sh.red;
+        for (int t = 0; t < my_tiles; ++t) {
+            for (int o = tid; o < 256 * MG; o += 64 * WV) {
+                float gate = 0.0f, up = 0.0f;
+#pragma unroll
+                for (int i = 0; i < WV; ++i) {
+                    const int a = all * i / WV, b = all * (i + 1) / WV, first = a / ng;
+                    if (a < b && first <= t && t <= (b - 1) / ng) {
+                        const float* at = red + (2 * i + (t - first)) * (512 * MG) + o;
+                        gate += at[0];
+                        up += at[256 * MG];
+                    }
+                }
+                const int l = (o >> 2) & 63, i = c0 + 16 * (o >> 8) + (l & 15);
+                if (i < count) p.h[(int64_t)list[i] * ip + 16 * (tile0 + t) + 4 * (l >> 4) + (o & 3)] = swiglu<DT>(gate, up);
+            }
+        }
+        if (tile0 + my_tiles == tiles) pad_rows(p, list, c0, count < c0 + 16 * MG ? count : c0 + 16 * MG, ip);
+        __syncthreads();
     }
 }
 
 // ---- the same in the light form: 8 columns of I a tile, rows 0 .. 7 of the instruction gate and
 // 8 .. 15 up.
 template <int DT, bool ROUTE>
-__global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8MoeArgs p, int spans, int span, int by_pair, int chunk) {
+__global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8MoeArgs p, int spans, int span, int by_pair, int chunk, int n_zero) {
     constexpr int WV = kLightUpWaves, D = 2;
     union Shared {
         v4f red[WV][64];
@@ -494,6 +490,7 @@ __global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8
     const int li = lane & 15, q = lane >> 4;
     const int32_t* ids = setup.template route<WV>(p);
     if (blockIdx.x == 0) {
+        for (int i = tid; i < n_zero; i += blockDim.x) p.counters[i] = 0;
         build_table(ids, (int)p.T, (int)p.E, p.k, chunk, p.table, p.pairs, sh.t.mask, sh.t.first);
         return;
     }
@@ -581,6 +578,36 @@ __global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8
     }
 }
 
+// The end of the second launch: a block of 4 Q columns of every token, the waves' sums in their
+// order; with several parts (grid.y) theirs go through memory, and the last adds them up in their
+// order.
+template <int DT, int Q, int MAXT, int WV>
+__device__ __forceinline__ void put_tokens(const Fp8MoeArgs& p, const v4f (&ysum)[WV][MAXT][Q]) {
+    __shared__ int flag;
+    const int n = (int)p.T * Q, parts = gridDim.y;
+    auto store = [&](int i, const v4f& y) LLMINT8_MOE_INLINE {
+        u32x2 o;
+        o[0] = (uint32_t)from_f32<DT>(y[0]) | ((uint32_t)from_f32<DT>(y[1]) << 16);
+        o[1] = (uint32_t)from_f32<DT>(y[2]) | ((uint32_t)from_f32<DT>(y[3]) << 16);
+        *(u32x2*)(p.Y + (int64_t)(i / Q) * p.H + (int64_t)blockIdx.x * (4 * Q) + 4 * (i % Q)) = o;
+    };
+    const __amdgpu_buffer_rsrc_t rp = buffer_rsrc(p.partial + (int64_t)blockIdx.x * parts * n * 4, (int64_t)parts * n * 16);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += 64 * WV) {
+        v4f y = ysum[0][i / Q][i % Q];
+#pragma unroll
+        for (int v = 1; v < WV; ++v) y += ysum[v][i / Q][i % Q];
+        if (parts == 1) store(i, y);
+        else store_part(rp, 16 * i, 16 * n * blockIdx.y, y);
+    }
+    if (parts == 1 || !last_part(p.counters + blockIdx.x, parts, &flag)) return;
+    for (int i = threadIdx.x; i < n; i += 64 * WV) {
+        v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int v = 0; v < parts; ++v) y += load_part(rp, 16 * i, 16 * n * v);
+        store(i, y);
+    }
+}
+
 // ---- down and the weighted sum: a workgroup takes 16 columns of H of all entries.  Their groups
 // of I, entry after entry, are split evenly over the waves and run through D sets of registers;
 // a wave ends an entry (or its share of it) by adding p times its sums to its own rows of token
@@ -605,7 +632,8 @@ __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
     }
     for (int i = tid; i < WV * T * 4; i += 64 * WV) ysum[i / (4 * T)][(i >> 2) % T][i & 3] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     __syncthreads();
-    const int total = entries * ng, from = (int)((int64_t)total * w / WV), to = (int)((int64_t)total * (w + 1) / WV);
+    const int total = entries * ng, shares = WV * (int)gridDim.y, share = (int)blockIdx.y * WV + w;
+    const int from = (int)((int64_t)total * share / shares), to = (int)((int64_t)total * (share + 1) / shares);
     if (from < to) {
         const uint32_t w_off = (uint32_t)(li * ip + 16 * q);
         const int64_t h_bytes = (int64_t)n * ip * 2;
@@ -684,16 +712,7 @@ __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
             }
         }
     }
-    __syncthreads();
-    for (int i = tid; i < T * 4; i += 64 * WV) {
-        v4f y = ysum[0][i >> 2][i & 3];
-#pragma unroll
-        for (int v = 1; v < WV; ++v) y += ysum[v][i >> 2][i & 3];
-        u32x2 o;
-        o[0] = (uint32_t)from_f32<DT>(y[0]) | ((uint32_t)from_f32<DT>(y[1]) << 16);
-        o[1] = (uint32_t)from_f32<DT>(y[2]) | ((uint32_t)from_f32<DT>(y[3]) << 16);
-        *(u32x2*)(p.Y + (int64_t)(i >> 2) * p.H + n0 + 4 * (i & 3)) = o;
-    }
+    put_tokens<DT, 4, MAXT, WV>(p, ysum);
 }
 
 // ---- the same in the light form: 8 columns of H, two entries (of up to 8 tokens) at a time, the
@@ -718,9 +737,10 @@ __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
     }
     for (int i = tid; i < WV * T * 2; i += 64 * WV) ysum[i / (2 * T)][(i >> 1) % T][i & 1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     __syncthreads();
-    // the steps (groups of I, two entries after two entries) go round the waves C at a time, so that
-    // what the workgroup reads at a time lies together
-    const int total = twos * ng, round = WV * C, own = total - total / round * round - w * C;
+    // this part's steps (groups of I, two entries after two entries) go round the waves C at a time,
+    // so that what the workgroup reads at a time lies together
+    const int begin = (int)((int64_t)twos * ng * blockIdx.y / gridDim.y), end = (int)((int64_t)twos * ng * (blockIdx.y + 1) / gridDim.y);
+    const int total = end - begin, round = WV * C, own = total - total / round * round - w * C;
     const int steps = total / round * C + (own < 0 ? 0 : (own < C ? own : C));
     if (steps > 0) {
         const int64_t h_bytes = (int64_t)n * ip * 2;
@@ -744,7 +764,7 @@ __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
                 return two != was;
             }
         };
-        At l{w * C / ng, w * C % ng, 0}, m = l;  // of the next load, and of the next product
+        At l{(begin + w * C) / ng, (begin + w * C) % ng, 0}, m = l;  // of the next load, and of the next product
         int left = steps;
         const uint8_t *row = nullptr, *scales = nullptr;
         uint32_t h_off = kFar;
@@ -806,16 +826,7 @@ __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
             }
         }
     }
-    __syncthreads();
-    for (int i = tid; i < T * 2; i += 64 * WV) {
-        v4f y = ysum[0][i >> 1][i & 1];
-#pragma unroll
-        for (int v = 1; v < WV; ++v) y += ysum[v][i >> 1][i & 1];
-        u32x2 o;
-        o[0] = (uint32_t)from_f32<DT>(y[0]) | ((uint32_t)from_f32<DT>(y[1]) << 16);
-        o[1] = (uint32_t)from_f32<DT>(y[2]) | ((uint32_t)from_f32<DT>(y[3]) << 16);
-        *(u32x2*)(p.Y + (int64_t)(i >> 1) * p.H + n0 + 4 * (i & 1)) = o;
-    }
+    put_tokens<DT, 2, MAXT, WV>(p, ysum);
 }
 
 // The first launch's grid: workgroup 0 (the table), then `rows` (pairs or experts) of `spans` spans
@@ -841,71 +852,101 @@ UpGrid up_grid(const Fp8MoeArgs& p, int columns, int64_t enough, int64_t longest
 
 // MG: pieces of 16 tokens multiplied at once; 0: the light form
 template <int DT, int MG>
-hipError_t launch_up(const Fp8MoeArgs& p, int chunk, hipStream_t stream) {
+hipError_t launch_up(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream) {
+    const int chunk = plan.chunk, n_zero = plan.parts > 1 ? (int)plan.blocks : 0;
     if constexpr (MG == 0) {
         const UpGrid g = up_grid(p, 8, 1024, 3);
         constexpr int kThreads = 64 * kLightUpWaves;
         if (p.T <= kRouteTokens) {
-            moe_up_light_kernel<DT, true><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk);
+            moe_up_light_kernel<DT, true><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk, n_zero);
         } else {
             moe_route_kernel<<<(unsigned)p.T, 64, 0, stream>>>(p);
-            moe_up_light_kernel<DT, false><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk);
+            moe_up_light_kernel<DT, false><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk, n_zero);
         }
     } else {
         const UpGrid g = up_grid(p, 16, 1024, 8);
         moe_route_kernel<<<(unsigned)p.T, 64, 0, stream>>>(p);
-        moe_up_kernel<DT, MG><<<(unsigned)g.grid, 64 * kUpWaves, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk);
+        moe_up_kernel<DT, MG><<<(unsigned)g.grid, 64 * kUpWaves, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk, n_zero);
     }
     return hipGetLastError();
 }
 
 template <int DT, int MG>
-hipError_t launch_down(const Fp8MoeArgs& p, hipStream_t stream) {
+hipError_t launch_down(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream) {
+    const dim3 grid((unsigned)plan.blocks, (unsigned)plan.parts);
     if constexpr (MG == 0) {
-        const unsigned cols = (unsigned)(p.H / 8);
-        if (p.T <= 16) moe_down_light_kernel<DT, 16, 8, 3, 2><<<cols, 512, 0, stream>>>(p);
-        else moe_down_light_kernel<DT, 128, 8, 3, 2><<<cols, 512, 0, stream>>>(p);
+        if (p.T <= 16) moe_down_light_kernel<DT, 16, 8, 3, 2><<<grid, 512, 0, stream>>>(p);
+        else moe_down_light_kernel<DT, 128, 8, 3, 2><<<grid, 512, 0, stream>>>(p);
     } else {
-        const unsigned cols = (unsigned)(p.H / 16);
         if constexpr (MG < 4) {
             if (p.T <= 64) {
-                moe_down_kernel<DT, MG, 64, 16><<<cols, 1024, 0, stream>>>(p);
+                moe_down_kernel<DT, MG, 64, 16><<<grid, 1024, 0, stream>>>(p);
                 return hipGetLastError();
             }
         }
-        moe_down_kernel<DT, MG, 128, 8><<<cols, 512, 0, stream>>>(p);
+        moe_down_kernel<DT, MG, 128, 8><<<grid, 512, 0, stream>>>(p);
     }
     return hipGetLastError();
 }
 
 template <int DT>
-hipError_t moe_launch(const Fp8MoeArgs& p, hipStream_t stream) {
-    // pieces by the tokens that an expert has on average (one that has more is read once per 16 MG
-    // of them); with few, the light forms where the others would leave compute units idle: 16
-    // tokens, 60 experts of 2064 x 1424, top 4: up 74 us light, 83 not, down 51 and 50; 8 tokens, 8
-    // experts of 4096 x 14336, top 2: up 192 light, 171 not, down 103 and 94; 1 token, 64 experts of
-    // 2048 x 768, top 8: up 9.5 and 12.7, down 7.4 and 10.6
-    const int64_t mean16 = 16 * p.T * p.k / p.E;
-    const int mg = mean16 <= 12 * 16 || p.T <= 16 ? 1 : (mean16 <= 28 * 16 || p.T <= 32 ? 2 : 4);
-    const bool few = p.T <= 8 || mean16 <= kLightMean * 16;
-    const int64_t rows = p.T * p.k < p.E ? p.T * p.k : p.E;
-    const bool light_up = few && (p.I / 16) * rows <= 4096, light_down = few && p.H / 16 < 256;
-    const int chunk = light_down ? 8 : 16 * mg;  // tokens of an entry
-    hipError_t e = light_up    ? launch_up<DT, 0>(p, chunk, stream)
-                   : mg == 1   ? launch_up<DT, 1>(p, chunk, stream)
-                   : mg == 2   ? launch_up<DT, 2>(p, chunk, stream)
-                               : launch_up<DT, 4>(p, chunk, stream);
+hipError_t moe_launch(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream) {
+    const int up = plan.light_up ? 0 : plan.pieces, down = plan.light_down ? 0 : plan.pieces;
+    const hipError_t e = up == 0   ? launch_up<DT, 0>(p, plan, stream)
+                         : up == 1 ? launch_up<DT, 1>(p, plan, stream)
+                         : up == 2 ? launch_up<DT, 2>(p, plan, stream)
+                                   : launch_up<DT, 4>(p, plan, stream);
     if (e != hipSuccess) return e;
-    return light_down ? launch_down<DT, 0>(p, stream)
-           : mg == 1  ? launch_down<DT, 1>(p, stream)
-           : mg == 2  ? launch_down<DT, 2>(p, stream)
-                      : launch_down<DT, 4>(p, stream);
+    return down == 0   ? launch_down<DT, 0>(p, plan, stream)
+           : down == 1 ? launch_down<DT, 1>(p, plan, stream)
+           : down == 2 ? launch_down<DT, 2>(p, plan, stream)
+                       : launch_down<DT, 4>(p, plan, stream);
+}
+
+// Parts of the second launch's sum.  A compute unit reads about 20 bytes a nanosecond whether it
+// holds one workgroup or two, so a few workgroups past a multiple of 256 cost as many rounds as
+// a full one; parts even that out, for about 3 us of joining and 1.5 us a round of setting up.  37
+// tokens, 60 experts, top 4: 2064 x 1424 (258 blocks) 77.6 us in one part, 62.8 in 2, 56.9 in 4, 62.7
+// in 8; 2048 x 1408 (256 blocks) 39.9, 42.6, 46.2, 56.2.
+int down_parts(int64_t blocks, int64_t steps) {
+    const int64_t work = steps * 11;  // 10 ns: of one block's steps of 16 rows of 128 bytes
+    int64_t best = 0;
+    int s = 1;
+    for (int64_t i = 1; i <= 8; ++i) {
+        const int64_t rounds = ceil_div(blocks * i, 256), cost = rounds * work / i + 150 * rounds + (i > 1 ? 300 : 0);
+        if (i == 1 || cost < best) {
+            best = cost;
+            s = (int)i;
+        }
+    }
+    return s;
 }
 
 }  // namespace
 
-hipError_t launch_fp8_moe(int dt, const Fp8MoeArgs& p, hipStream_t stream) {
-    return dt == F16 ? moe_launch<F16>(p, stream) : moe_launch<BF16>(p, stream);
+Fp8MoePlan fp8_moe_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
+    Fp8MoePlan plan;
+    // pieces by the tokens that an expert has on average (one that has more is read once per 16 MG
+    // of them); with few, the light forms where the others would leave compute units idle: 16
+    // tokens, 64 experts of 2048 x 768, top 4: up 37.3 us light, 39.4 not, down 18.0 and 29.6; 8 tokens, 8
+    // experts of 4096 x 14336, top 2: up 193 light, 169 not, down 101 and 91; 1 token, 64 experts of
+    // 2048 x 768, top 8: up 8.9 and 11.6, down 6.8 and 9.5
+    const int64_t mean16 = 16 * T * k / E;
+    plan.pieces = mean16 <= 12 * 16 || T <= 16 ? 1 : (mean16 <= 28 * 16 || T <= 32 ? 2 : 4);
+    const bool few = T <= 8 || mean16 <= kLightMean * 16;
+    const int64_t rows = T * k < E ? T * k : E;  // the experts met, at most
+    plan.light_up = few && (I / 16) * rows <= 4096;
+    plan.light_down = few && H / 16 < 256;
+    plan.chunk = plan.light_down ? 8 : 16 * plan.pieces;
+    plan.blocks = H / (plan.light_down ? 8 : 16);
+    const int64_t met = k == E ? rows : (int64_t)((double)E * -expm1((double)T * log1p(-(double)k / (double)E))) + 1;  // of even choices
+    plan.parts = down_parts(plan.blocks, (plan.light_down ? ceil_div(met, 2) : met) * ceil_div(I, 128));
+    plan.partial_bytes = plan.parts > 1 ? T * H * plan.parts * 4 : 0;
+    return plan;
+}
+
+hipError_t launch_fp8_moe(int dt, const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream) {
+    return dt == F16 ? moe_launch<F16>(p, plan, stream) : moe_launch<BF16>(p, plan, stream);
 }
 
 }  // namespace llmint8

@@ -235,6 +235,15 @@ struct Fp8GemmArgs {
 };
 hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& p, const Fp8Plan& plan, hipStream_t stream);
 
+struct Fp8MoePlan {
+    int pieces;  // of 16 tokens multiplied at once: 1, 2 or 4
+    bool light_up, light_down;
+    int chunk;   // tokens of an entry of the second launch
+    int parts;   // of its sum
+    int64_t blocks, partial_bytes;  // its blocks of columns; parts > 1: the partial sums' bytes
+};
+Fp8MoePlan fp8_moe_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k);
+
 struct Fp8MoeArgs {
     const uint16_t* X;
     int64_t T, H;
@@ -253,7 +262,9 @@ struct Fp8MoeArgs {
     uint16_t* h;     // (T k) x pitch(I)
     int32_t* table;  // 1 + 3 T k: the entries of the second launch
     int32_t* pairs;  // T k: their pairs of token and choice
+    int32_t* counters;  // parts > 1: one a block of columns
+    float* partial;
 };
-hipError_t launch_fp8_moe(int dt, const Fp8MoeArgs& p, hipStream_t stream);
+hipError_t launch_fp8_moe(int dt, const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream);
 
 }  // namespace llmint8
