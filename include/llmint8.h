@@ -58,8 +58,8 @@
  *                            stats_copy, stats_sync, stats_copy_cols, group_colmax,
  *                            quantize_weight_groups, group_xpass, gemm_group,
  *                            gemm_group_small, fill_zero, block_quantize, block_dequantize,
- *                            scratch_symbol, fp8_weight, fp8_rows, fp8_gemm, fp8_cols_dy,
- *                            fp8_cols_x, fp8_gemm_dx, fp8_gemm_dw, fp8_moe).
+ *                            scratch_symbol, fp8_weight, fp8_rows, fp8_gemm, fp8_cols,
+ *                            fp8_gemm_dx, fp8_gemm_dw, fp8_moe).
  */
 #ifndef LLMINT8_H
 #define LLMINT8_H
@@ -351,7 +351,7 @@ int64_t fp8_scale_pitch(int64_t n);
  *   WqT       out, may be NULL with wT_scale: K rows of codes over N, the same codes transposed,
  *             which the input gradient sums over.
  *   wT_scale  out: ceil(K/128) rows of scales over N.
- * K = 0 or N = 0 is a no-op.
+ * K = 0 or N = 0 is a no-op.  K and N are at most 2^22 (LLMINT8_ERANGE).
  */
 int fp8_quantize_weight_block(const void* W, int64_t K, int64_t N, int dtype, uint8_t* Wq, uint8_t* w_scale,
                               uint8_t* WqT, uint8_t* wT_scale, void* stream);

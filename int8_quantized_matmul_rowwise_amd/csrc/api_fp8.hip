@@ -50,7 +50,7 @@ LLMINT8_API int fp8_quantize_weight_block(const void* W, int64_t K, int64_t N, i
     if (rc) return rc;
     if (N == 0 || K == 0) return LLMINT8_OK;
     if ((WqT != nullptr) != (wT_scale != nullptr)) return LLMINT8_EINVAL;
-    if (WqT && N > kMaxSum) return LLMINT8_ERANGE;
+    if (N > kMaxSum) return LLMINT8_ERANGE;
     if (!W || !Wq || !w_scale || !aligned(W, 16) || !aligned(Wq, 16) || !aligned(w_scale, 4)) return LLMINT8_EINVAL;
     if (WqT && (!aligned(WqT, 16) || !aligned(wT_scale, 4))) return LLMINT8_EINVAL;
     const Range r[] = {{Wq, code_bytes(N, K)},
@@ -211,16 +211,12 @@ LLMINT8_API int fp8_matmul_block_backward(const void* dY, const void* X, int64_t
     float* partial = (float*)(ws + L.partial);
     hipError_t e = hipSuccess;
     if (sum_w)
-        e = stage("fp8_cols_dy", [&] {
-            return launch_fp8_cols(dtype, dY, M, N, ws + L.dyt, ws + L.s_dyt, sum_x ? ws + L.dyq : nullptr,
-                                   sum_x ? ws + L.s_dy : nullptr, counters, n_dx + n_dw, st);
+        e = stage("fp8_cols", [&] {
+            return launch_fp8_cols(dtype, dY, X, M, N, K, ws + L.dyt, ws + L.s_dyt, sum_x ? ws + L.dyq : nullptr,
+                                   sum_x ? ws + L.s_dy : nullptr, ws + L.xt, ws + L.s_xt, counters, n_dx + n_dw, st);
         });
     else if (sum_x)
         e = stage("fp8_rows", [&] { return launch_fp8_rows(dtype, dY, M, N, ws + L.dyq, ws + L.s_dy, counters, n_dx, st); });
-    if (e == hipSuccess && sum_w)
-        e = stage("fp8_cols_x", [&] {
-            return launch_fp8_cols(dtype, X, M, K, ws + L.xt, ws + L.s_xt, nullptr, nullptr, nullptr, 0, st);
-        });
     if (e == hipSuccess && out_x)
         e = sum_x ? stage("fp8_gemm_dx", [&] {
                         const Fp8GemmArgs a{ws + L.dyq, WqT, M, K, fp8_pitch(N), ws + L.s_dy, wT_scale, fp8_scale_pitch_of(N), (uint16_t*)dX,

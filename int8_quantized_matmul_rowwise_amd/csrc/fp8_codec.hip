@@ -12,9 +12,10 @@
 //   p ^ (column / 8 % 16): the 8-byte writes of the 16 lanes of a row and the 16-byte reads of
 //   a column then spread over all banks.
 // Code rows are padded with zeros to a multiple of 128, a weight's scale rows to one of 4.
-// HBM-bound: 28672 x 8192 weights, both orders, 185 us = 5.1 TB/s; 2048 x 16384, ROWS and COLS,
-// 33.6 us = 4.0 TB/s (58 us with maxima passed between lanes through LDS one value at a time and
-// registers for two waves a SIMD: now two patterns to a dword, lane operands, at most 80 registers).
+// HBM-bound: 28672 x 8192 weights, both orders, 184 us = 5.1 TB/s; 2048 x 16384 (ROWS and COLS) and
+// 2048 x 4096 (COLS) in one launch 36 us = 4.2 TB/s (two launches 43 us; 67 us with maxima passed
+// between lanes through LDS one value at a time and registers for two waves a SIMD: now two
+// patterns to a dword, lane operands, at most 80 registers).
 #include "fp8_common.hpp"
 #include "launch.hpp"
 
@@ -48,38 +49,36 @@ struct TileParams {
     uint8_t* s;   // their scales: BLOCK ceil(R/128) x sp(C), ROWS fp8_row_scale_at
     uint8_t* qt;  // codes transposed: C x pitch(R)
     uint8_t* st;  // their scales: BLOCK ceil(C/128) x sp(R), COLS fp8_row_scale_at
-    int32_t* zero;
-    int64_t n_zero;
 };
 
-// MODE 0: BLOCK, transposed codes; 1: BLOCK, both; 2: COLS; 3: COLS and ROWS
+// One tile.  MODE 0: BLOCK, transposed codes; 1: BLOCK, both; 2: COLS, with ROWS where q is given
+struct TileShared {
+    __attribute__((aligned(16))) uint8_t tile[128 * 128];
+    u32x4 red[4][16];
+    __attribute__((aligned(16))) uint8_t col_e[128], row_e[128];  // the scales' bytes
+};
+
 template <int DT, int MODE>
-__global__ __launch_bounds__(256, 6) void fp8_tile_kernel(TileParams p) {
+__device__ __forceinline__ void code_tile(const TileParams& p, int64_t tc, int64_t tr, TileShared& sh) {
     constexpr bool BLOCK = MODE < 2;
-    __shared__ __attribute__((aligned(16))) uint8_t tile[128 * 128];
-    __shared__ u32x4 red[4][16];
-    __shared__ __attribute__((aligned(16))) uint8_t col_e[128], row_e[128];  // the scales' bytes
+    uint8_t *const tile = sh.tile, *const col_e = sh.col_e, *const row_e = sh.row_e;
+    auto& red = sh.red;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int cc = tid & 15, rr = tid >> 4;  // columns 8 cc .. + 7, rows 8 rr .. + 7 of the tile
-    const int64_t tc = blockIdx.x, tr = blockIdx.y;
-    if constexpr (!BLOCK) {
-        const int64_t id = (tr * gridDim.x + tc) * 256 + tid;
-        for (int64_t i = id; i < p.n_zero; i += (int64_t)gridDim.x * gridDim.y * 256) p.zero[i] = 0;
-    }
     const int64_t c0 = tc * 128, r0 = tr * 128;
     const int64_t cpitch = fp8_pitch(p.C), rpitch = fp8_pitch(p.R);
     const int64_t csp = fp8_scale_pitch_of(p.C), rsp = fp8_scale_pitch_of(p.R);
     const bool last_c = c0 + 128 >= p.C, last_r = r0 + 128 >= p.R;
     const int64_t c = c0 + 8 * cc;
+    // rows past R and columns past C read zero
+    const int64_t rows = p.R - r0 < 128 ? p.R - r0 : 128;
+    const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(p.A + r0 * p.C, rows * p.C * 2);
+    const uint32_t row_bytes = (uint32_t)p.C * 2, at = c < p.C ? 8 * rr * row_bytes + (uint32_t)c * 2 : 0x80000000u;
     u32x4 v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const int64_t r = r0 + 8 * rr + u;
-        v[u] = u32x4{0u, 0u, 0u, 0u};
-        if (r < p.R && c < p.C) v[u] = *(const u32x4*)(p.A + r * p.C + c);  // C is a multiple of 8
-    }
+    for (int u = 0; u < 8; ++u) v[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, at + u * row_bytes, 0, 0));
     // ---- codes in order
-    if constexpr (MODE == 3) {
+    if (MODE == 2 && p.q) {  // ROWS
         uint32_t es[2] = {0u, 0u};
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -158,7 +157,7 @@ __global__ __launch_bounds__(256, 6) void fp8_tile_kernel(TileParams p) {
         if (tid < 32 && c0 + at - cc < p.C)
             *(uint32_t*)(p.st + fp8_row_scale_at(c0 + at, tr, p.C)) =
                 col_e[at] | (uint32_t)col_e[at + 16] << 8 | (uint32_t)col_e[at + 32] << 16 | (uint32_t)col_e[at + 48] << 24;
-        if constexpr (MODE == 3) {
+        if (p.q) {
             if (tid >= 64 && tid < 96 && r0 + at - cc < p.R)
                 *(uint32_t*)(p.s + fp8_row_scale_at(r0 + at, tc, p.R)) =
                     row_e[at] | (uint32_t)row_e[at + 16] << 8 | (uint32_t)row_e[at + 32] << 16 | (uint32_t)row_e[at + 48] << 24;
@@ -174,6 +173,25 @@ __global__ __launch_bounds__(256, 6) void fp8_tile_kernel(TileParams p) {
     }
 }
 
+template <int DT, int MODE>
+__global__ __launch_bounds__(256, 6) void fp8_tile_kernel(TileParams p) {
+    __shared__ TileShared sh;
+    code_tile<DT, MODE>(p, blockIdx.x, blockIdx.y, sh);
+}
+
+// Both operands of the weight gradient in one launch: the tiles of `a`, then those of `b`.  Zeroes
+// the counters of the products that follow.
+template <int DT>
+__global__ __launch_bounds__(256, 6) void fp8_cols_kernel(TileParams a, TileParams b, int tiles_a, int32_t* zero, int64_t n_zero) {
+    __shared__ TileShared sh;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n_zero; i += (int64_t)gridDim.x * 256) zero[i] = 0;
+    const bool first = (int)blockIdx.x < tiles_a;
+    const TileParams p{first ? a.A : b.A,  first ? a.R : b.R,   first ? a.C : b.C,  first ? a.q : b.q,
+                       first ? a.s : b.s, first ? a.qt : b.qt, first ? a.st : b.st};
+    const int t = first ? blockIdx.x : blockIdx.x - tiles_a, across = (int)ceil_div(p.C, 128), down = __builtin_amdgcn_readfirstlane(t / across);
+    code_tile<DT, 2>(p, t - down * across, down, sh);
+}
+
 template <int MODE>
 hipError_t tile_launch(int dt, const TileParams& p, hipStream_t stream) {
     const dim3 g((unsigned)ceil_div(p.C, 128), (unsigned)ceil_div(p.R, 128));
@@ -187,7 +205,7 @@ hipError_t tile_launch(int dt, const TileParams& p, hipStream_t stream) {
 hipError_t launch_fp8_weight(int dt, const void* W, int64_t K, int64_t N, uint8_t* Wq, uint8_t* s_w, uint8_t* WqT,
                              uint8_t* s_wT, hipStream_t stream) {
     if (K == 0 || N == 0) return hipSuccess;
-    const TileParams p{(const uint16_t*)W, K, N, WqT, s_wT, Wq, s_w, nullptr, 0};
+    const TileParams p{(const uint16_t*)W, K, N, WqT, s_wT, Wq, s_w};
     return WqT ? tile_launch<1>(dt, p, stream) : tile_launch<0>(dt, p, stream);
 }
 
@@ -201,11 +219,16 @@ hipError_t launch_fp8_rows(int dt, const void* X, int64_t M, int64_t K, uint8_t*
     return hipGetLastError();
 }
 
-hipError_t launch_fp8_cols(int dt, const void* A, int64_t R, int64_t C, uint8_t* qt, uint8_t* st, uint8_t* q, uint8_t* s,
-                           int32_t* zero, int64_t n_zero, hipStream_t stream) {
-    if (R == 0 || C == 0) return hipSuccess;
-    const TileParams p{(const uint16_t*)A, R, C, q, s, qt, st, zero, n_zero};
-    return q ? tile_launch<3>(dt, p, stream) : tile_launch<2>(dt, p, stream);
+hipError_t launch_fp8_cols(int dt, const void* A, const void* B, int64_t R, int64_t CA, int64_t CB, uint8_t* at, uint8_t* s_at,
+                           uint8_t* a, uint8_t* s_a, uint8_t* bt, uint8_t* s_bt, int32_t* zero, int64_t n_zero,
+                           hipStream_t stream) {
+    if (R == 0 || CA == 0 || CB == 0) return hipSuccess;
+    const TileParams pa{(const uint16_t*)A, R, CA, a, s_a, at, s_at}, pb{(const uint16_t*)B, R, CB, nullptr, nullptr, bt, s_bt};
+    const int64_t rows = ceil_div(R, 128), ta = rows * ceil_div(CA, 128), tb = rows * ceil_div(CB, 128);
+    const unsigned grid = (unsigned)(ta + tb);
+    if (dt == F16) fp8_cols_kernel<F16><<<grid, 256, 0, stream>>>(pa, pb, (int)ta, zero, n_zero);
+    else fp8_cols_kernel<BF16><<<grid, 256, 0, stream>>>(pa, pb, (int)ta, zero, n_zero);
+    return hipGetLastError();
 }
 
 }  // namespace llmint8

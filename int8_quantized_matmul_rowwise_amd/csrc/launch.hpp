@@ -202,11 +202,12 @@ hipError_t launch_fp8_weight(int dt, const void* W, int64_t K, int64_t N, uint8_
 // (also zeroes zero[0, n_zero): the counters of the products' split sums)
 hipError_t launch_fp8_rows(int dt, const void* X, int64_t M, int64_t K, uint8_t* q, uint8_t* s, int32_t* zero,
                            int64_t n_zero, hipStream_t stream);
-// qt C x pitch(R): the codes of A (R x C) transposed, with a scale st per column of A and group
-// of 128 rows (at fp8_row_scale_at); q, s (both or neither): launch_fp8_rows of the same matrix
-// (and zeroes zero[0, n_zero) as above)
-hipError_t launch_fp8_cols(int dt, const void* A, int64_t R, int64_t C, uint8_t* qt, uint8_t* st, uint8_t* q, uint8_t* s,
-                           int32_t* zero, int64_t n_zero, hipStream_t stream);
+// at CA x pitch(R): the codes of A (R x CA) transposed, with a scale s_at per column of A and group
+// of 128 rows (at fp8_row_scale_at); a, s_a (both or neither): launch_fp8_rows of the same matrix;
+// bt, s_bt: those of B (R x CB) transposed (zeroes zero[0, n_zero) as above)
+hipError_t launch_fp8_cols(int dt, const void* A, const void* B, int64_t R, int64_t CA, int64_t CB, uint8_t* at, uint8_t* s_at,
+                           uint8_t* a, uint8_t* s_a, uint8_t* bt, uint8_t* s_bt, int32_t* zero, int64_t n_zero,
+                           hipStream_t stream);
 
 // How a product of M x N outputs over nk groups runs.
 struct Fp8Plan {

@@ -42,6 +42,7 @@ def moe(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=2), lm.EINVAL), (dict(K=-16), lm.EINVAL), (dict(K=24), lm.EINVAL), (dict(N=12), lm.EINVAL),
     (dict(K=(1 << 22) + 16), lm.ERANGE), (dict(N=(1 << 22) + 8), lm.ERANGE), (dict(W=None), lm.EINVAL),
+    (dict(N=(1 << 22) + 8, WqT=None, sT=None), lm.ERANGE),
     (dict(W=A + 8), lm.EINVAL), (dict(Wq=None), lm.EINVAL), (dict(Wq=B + 4), lm.EINVAL), (dict(s=None), lm.EINVAL),
     (dict(s=C + 2), lm.EINVAL), (dict(WqT=None), lm.EINVAL), (dict(sT=None), lm.EINVAL), (dict(WqT=D + 8), lm.EINVAL),
     (dict(Wq=A), lm.EINVAL), (dict(WqT=B + 128), lm.EINVAL), (dict(s=B), lm.EINVAL), (dict(sT=C), lm.EINVAL),
@@ -111,9 +112,9 @@ def _calls():
         "matmul": (lambda: mm(M=300, K=1024, N=520), ["fp8_rows", "fp8_gemm"]),
         "matmul_fused": (lambda: mm(M=2, K=1024, N=520, ws=None, wsb=0), ["fp8_gemm"]),
         "matmul_k0": (lambda: mm(K=0), ["fill_zero"]),
-        "backward": (lambda: back(M=300, K=1024, N=520), ["fp8_cols_dy", "fp8_cols_x", "fp8_gemm_dx", "fp8_gemm_dw"]),
+        "backward": (lambda: back(M=300, K=1024, N=520), ["fp8_cols", "fp8_gemm_dx", "fp8_gemm_dw"]),
         "backward_dx": (lambda: back(M=300, dW=None), ["fp8_rows", "fp8_gemm_dx"]),
-        "backward_dw": (lambda: back(M=300, dX=None), ["fp8_cols_dy", "fp8_cols_x", "fp8_gemm_dw"]),
+        "backward_dw": (lambda: back(M=300, dX=None), ["fp8_cols", "fp8_gemm_dw"]),
         "backward_no_tokens": (lambda: back(M=0, ws=None), ["fill_zero"]),
         "backward_n0": (lambda: back(N=0, ws=None, dY=None), ["fill_zero"]),
         "moe": (lambda: moe(), ["fp8_moe"]),
