@@ -7,10 +7,10 @@
 //   [g; u] = W13hat_e x (2I values), h = RN_T(silu(g) u), y = RN_T(sum_j p_j W2hat_e h).
 //
 // Bound by the bytes of the experts met, each read once (once per 16 MG tokens of one expert).  Two
-// launches: gate, up and SwiGLU (h goes to the workspace), then down and the weighted sum; a third
-// one before them chooses the experts where every workgroup of the first doing it for itself would
-// cost more than a launch (more than kRouteTokens tokens, or many workgroups).
-//
+// launches: gate, up and SwiGLU (h goes to the workspace), then down and the weighted sum.  The
+// experts are chosen by every workgroup of the first for itself, or, with more tokens or choices than
+// kRouteTokens and kRouteChoices, by a launch before it: 4 tokens, top 8: 25.8 us and 3.5 + 25.0; 8
+// tokens, top 8: 53.5 and 4.2 + 46.8.
 // The products run on 16-bit matrix instructions (16x16x32): a code is exact in either 16-bit
 // type, so nothing is lost against the coded weight, and the activations keep their 16 bits --
 // few tokens leave the matrix units idle anyway.  Weights are the row side (16 rows), an expert's
@@ -39,7 +39,7 @@ constexpr int kMaxTokens = 128;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 16;
 constexpr int kUpWaves = 8, kLightUpWaves = 4;
-constexpr int kRouteTokens = kLightUpWaves;  // one a wave
+constexpr int kRouteTokens = 8, kRouteChoices = 32;
 constexpr int kLightMean = 6;
 
 #define LLMINT8_MOE_INLINE __attribute__((always_inline))
@@ -91,11 +91,11 @@ __device__ __forceinline__ float wave_reduce(float v, float none, F&& f) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
-// The experts and weights of one token, by one wave; lane j < k returns choice j.  A lane holds C
+// The experts and (weigh) weights of one token, by one wave; lane j < k returns choice j.  A lane holds C
 // neighbouring experts, so that among equal values the lowest lane, and in it the first expert,
 // is the lowest index.
 template <int C>
-__device__ __forceinline__ void route_lanes(const float* __restrict__ l, int E, int k, int renormalize, int& id, float& p) {
+__device__ __forceinline__ void route_lanes(const float* __restrict__ l, int E, int k, int renormalize, bool weigh, int& id, float& p) {
     const float kNone = -__builtin_inff();
     const int lane = threadIdx.x & 63;
     float v[C], all[C];
@@ -104,9 +104,8 @@ __device__ __forceinline__ void route_lanes(const float* __restrict__ l, int E, 
         v[i] = C * lane + i < E ? usable_logit(l[C * lane + i]) : kNone;
         all[i] = v[i];
     }
-    float top = 0.0f, chosen = 0.0f;
+    float mine = kNone;  // lane j: choice j's logit
     id = -1;
-    p = 0.0f;
     for (int j = 0; j < k; ++j) {
         float best = v[0];
 #pragma unroll
@@ -124,35 +123,35 @@ __device__ __forceinline__ void route_lanes(const float* __restrict__ l, int E, 
             taken = taken || it;
         }
         at = C * from + __builtin_amdgcn_readlane(at, from);
-        if (j == 0) top = most;
-        const float x = expf(most - top);
-        chosen += x;
         if (lane == j) {
             id = at;
-            p = x;
+            mine = most;
         }
     }
-    float z = chosen;
+    if (!weigh) return;
+    const float top = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, mine)));
+    p = id >= 0 ? expf(mine - top) : 0.0f;
+    float own = p;
     if (!renormalize) {
-        float own = 0.0f;
+        own = 0.0f;
 #pragma unroll
-        for (int i = 0; i < C; ++i) own += expf(all[i] - top);
-        z = wave_reduce(own, 0.0f, [](float a, float b) { return a + b; });
+        for (int i = 0; i < C; ++i) own += all[i] > kNone ? expf(all[i] - top) : 0.0f;
     }
+    const float z = wave_reduce(own, 0.0f, [](float a, float b) { return a + b; });
     if (id >= 0) p /= z;
 }
 
-__device__ __forceinline__ void route_token(const float* __restrict__ l, int E, int k, int renormalize, int& id, float& p) {
-    if (E <= 64) route_lanes<1>(l, E, k, renormalize, id, p);
-    else if (E <= 256) route_lanes<4>(l, E, k, renormalize, id, p);
-    else route_lanes<16>(l, E, k, renormalize, id, p);
+__device__ __forceinline__ void route_token(const float* __restrict__ l, int E, int k, int renormalize, bool weigh, int& id, float& p) {
+    if (E <= 64) route_lanes<1>(l, E, k, renormalize, weigh, id, p);
+    else if (E <= 256) route_lanes<4>(l, E, k, renormalize, weigh, id, p);
+    else route_lanes<16>(l, E, k, renormalize, weigh, id, p);
 }
 
 __global__ __launch_bounds__(64) void moe_route_kernel(Fp8MoeArgs p) {
     const int t = blockIdx.x, lane = threadIdx.x;
     int id;
     float w;
-    route_token(p.logits + (int64_t)t * p.E, (int)p.E, p.k, p.renormalize, id, w);
+    route_token(p.logits + (int64_t)t * p.E, (int)p.E, p.k, p.renormalize, true, id, w);
     if (lane < p.k) {
         p.ids[t * p.k + lane] = id;
         p.weights[t * p.k + lane] = w;
@@ -300,7 +299,7 @@ __device__ __forceinline__ void pad_rows(const Fp8MoeArgs& p, const int* list, i
 // workgroup 0 writes them down) and its expert's tokens
 template <bool ROUTE>
 struct UpSetup {
-    int32_t own[ROUTE ? kRouteTokens * kMaxTopK : 1];
+    int32_t own[ROUTE ? kRouteChoices : 1];
     int list[kMaxTokens];  // the expert's tokens, ascending, as token * top_k + choice
     int part[2], dup;
 
@@ -311,8 +310,8 @@ struct UpSetup {
             const int lane = threadIdx.x & 63;
             for (int t = threadIdx.x >> 6; t < p.T; t += WV) {
                 int id;
-                float wt;
-                route_token(p.logits + t * p.E, (int)p.E, p.k, p.renormalize, id, wt);
+                float wt = 0.0f;
+                route_token(p.logits + t * p.E, (int)p.E, p.k, p.renormalize, blockIdx.x == 0, id, wt);
                 if (lane < p.k) {
                     own[t * p.k + lane] = id;
                     if (blockIdx.x == 0) {
@@ -325,16 +324,17 @@ struct UpSetup {
         __syncthreads();
         return ROUTE ? own : p.ids;
     }
-    // The tokens of this workgroup's expert: of pair y (by_pair; none if an earlier pair has the
-    // same expert, whose workgroups do it), or of expert y.
-    __device__ __forceinline__ int find(const Fp8MoeArgs& p, const int32_t* ids, int y, int by_pair, int& e) {
+    // This workgroup's expert, of pair y (by_pair; negative: none chosen) or expert y, and its
+    // tokens (none if an earlier pair has the same expert, whose workgroups do it).
+    __device__ __forceinline__ int expert(const int32_t* ids, int y, int by_pair) {
+        return __builtin_amdgcn_readfirstlane(by_pair ? ids[y] : y);  // (from LDS it would count as a lane's value)
+    }
+    __device__ __forceinline__ int find(const Fp8MoeArgs& p, const int32_t* ids, int y, int by_pair, int e) {
         const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-        e = __builtin_amdgcn_readfirstlane(by_pair ? ids[y] : y);  // (from LDS it would count as a lane's value)
         int mine = -1;
         if (tid < 128 && tid < p.T)
             for (int j = 0; j < p.k; ++j)
                 if (ids[tid * p.k + j] == e) mine = tid * p.k + j;
-        if (e < 0) mine = -1;
         if (by_pair && mine >= 0 && mine < y) dup = 1;
         const uint64_t have = __ballot(mine >= 0);
         if (w < 2 && lane == 0) part[w] = __popcll(have);
@@ -372,9 +372,10 @@ __global__ __launch_bounds__(64 * kUpWaves, MG == 1 ? 4 : 2) void moe_up_kernel(
         return;
     }
     const int y = (int)(blockIdx.x - 1) / spans, tile0 = (int)(blockIdx.x - 1) % spans * span;
-    int e;
+    const int e = setup.expert(ids, y, by_pair);
+    if (e < 0) return;  // the same in every thread, as below
     const int count = setup.find(p, ids, y, by_pair, e);
-    if (count == 0) return;  // the same in every thread
+    if (count == 0) return;
     const int* list = setup.list;
 
     const int64_t hp = fp8_pitch(p.H), hsp = fp8_scale_pitch_of(p.H);
@@ -495,9 +496,8 @@ __global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8
         return;
     }
     const int y = (int)(blockIdx.x - 1) / spans, tile0 = (int)(blockIdx.x - 1) % spans * span;
-    int e;
-    const int count = setup.find(p, ids, y, by_pair, e);
-    if (count == 0) return;  // the same in every thread
+    const int e = setup.expert(ids, y, by_pair);
+    if (e < 0) return;  // the same in every thread, as below
 
     const int64_t hp = fp8_pitch(p.H), hsp = fp8_scale_pitch_of(p.H);
     const int tiles = (int)(p.I / 8), ng = (int)(hp / 128);
@@ -515,29 +515,54 @@ __global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8
         u32x4 w[2], x[1][4];
         Scale e;
     };
+    RowAt x_at;
+    struct At {
+        int t, g;  // the next load's tile and group
+    };
+    At at{0, w};
+    auto next = [&]() LLMINT8_MOE_INLINE {
+        at.g += WV;
+        if (at.g >= gw * WV) {
+            at.g = w;
+            ++at.t;
+        }
+        __builtin_amdgcn_sched_barrier(0);  // as above
+    };
+    // (read back: with the choices in LDS the compiler takes these for lanes' values)
+    auto load_w = [&](Group& r) LLMINT8_MOE_INLINE {
+        const bool in = at.t < my_tiles && at.g < ng;  // else: one line of weights times zeros
+        const int t = __builtin_amdgcn_readfirstlane(in ? at.t : 0), g = __builtin_amdgcn_readfirstlane(in ? at.g : 0);
+        const uint8_t* from = in ? W + 8 * t * hp + g * 128 : p.W13;
+        r.w[0] = *(const u32x4*)from;
+        r.w[1] = *(const u32x4*)(from + 64);
+        // (I is a multiple of 16: a tile's gate rows, and its up rows, lie in one block)
+        const int64_t i0 = 8 * (int64_t)(tile0 + t);
+        r.e = load_scale(rs, up_scale ? (uint32_t)(((p.I + i0) >> 7) * hsp) : (uint32_t)((i0 >> 7) * hsp), g);
+    };
+    auto load_x = [&](Group& r) LLMINT8_MOE_INLINE {
+        const bool in = at.t < my_tiles && at.g < ng;
+        const int g = __builtin_amdgcn_readfirstlane(in ? at.g : 0);
+        const int bytes = __builtin_amdgcn_readfirstlane(in ? (int)(p.T * p.H * 2) : 0);
+        load_row(buffer_rsrc(p.X, bytes), x_at, g, g == ng - 1, r.x[0]);
+    };
+    // the first weights are on their way while the expert's tokens are looked up
+    Group r[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        load_w(r[d]);
+        next();
+    }
+    const int count = setup.find(p, ids, y, by_pair, e);
+    if (count == 0) return;
     for (int c0 = 0; c0 < count; c0 += 16) {
-        RowAt x_at;
         x_at.set(c0 + li < count ? (uint32_t)((setup.list[c0 + li] / p.k) * p.H) * 2 : kFar, (int)p.H, ng, q);
-        int lt = 0, lg = w;  // the next load's tile and group
-        auto load = [&](Group& r) LLMINT8_MOE_INLINE {
-            const bool in = lt < my_tiles && lg < ng;  // else: one line of weights times zeros
-            // (read back: with the choices in LDS the compiler takes these for lanes' values)
-            const int t = __builtin_amdgcn_readfirstlane(in ? lt : 0), wg = __builtin_amdgcn_readfirstlane(in ? lg : 0);
-            const int x_bytes = __builtin_amdgcn_readfirstlane(in ? (int)(p.T * p.H * 2) : 0);
-            const uint8_t* at = in ? W + 8 * t * hp + wg * 128 : p.W13;
-            r.w[0] = *(const u32x4*)at;
-            r.w[1] = *(const u32x4*)(at + 64);
-            load_row(buffer_rsrc(p.X, x_bytes), x_at, wg, wg == ng - 1, r.x[0]);
-            // (I is a multiple of 16: a tile's gate rows, and its up rows, lie in one block)
-            const int64_t i0 = 8 * (int64_t)(tile0 + t);
-            r.e = load_scale(rs, up_scale ? (uint32_t)(((p.I + i0) >> 7) * hsp) : (uint32_t)((i0 >> 7) * hsp), wg);
-            lg += WV;
-            if (lg >= gw * WV) {
-                lg = w;
-                ++lt;
-            }
-            __builtin_amdgcn_sched_barrier(0);  // as above
-        };
+        at = At{0, w};
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (c0 > 0) load_w(r[d]);
+            load_x(r[d]);
+            next();
+        }
         v4f acc[1] = {};
         int tile = tile0, done = 0;
         auto finish = [&]() LLMINT8_MOE_INLINE {
@@ -561,14 +586,13 @@ __global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8
             __syncthreads();
             ++tile;
         };
-        Group r[D];
-#pragma unroll
-        for (int d = 0; d < D; ++d) load(r[d]);
         for (int s = 0; s < steps; s += D) {  // whole rounds, as above
 #pragma unroll
             for (int d = 0; d < D; ++d) {
                 group_product<DT, 1>(r[d].w, scale_here(r[d].e), r[d].x, acc);
-                load(r[d]);
+                load_w(r[d]);
+                load_x(r[d]);
+                next();
                 if (s + d < steps && ++done == gw) {
                     done = 0;
                     finish();
@@ -834,6 +858,8 @@ __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
 // once per span, as long as about `enough` workgroups are left: 4 tokens, 64 experts of 2048 x 768,
 // top 8: 25.5 us with spans of 3, 32.6 with single tiles; longer ones gain nothing (8 tokens, 128
 // such experts: 48.3 us with spans of 3, 47.3 with 6, 59.6 with 1; 16 tokens, top 4: 38.6, 44.9, 47.2).
+// The heavy form, 37 tokens, 60 experts of 2064 x 1424, top 4: 78 us with 1024 workgroups left, 89 with
+// 512 and with 2048; 64 tokens, 160 experts of 5120 x 1536, top 6: 451, 451 and 456.
 struct UpGrid {
     int by_pair, spans, span;
     int64_t grid;
@@ -857,7 +883,7 @@ hipError_t launch_up(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t st
     if constexpr (MG == 0) {
         const UpGrid g = up_grid(p, 8, 1024, 3);
         constexpr int kThreads = 64 * kLightUpWaves;
-        if (p.T <= kRouteTokens) {
+        if (p.T <= kRouteTokens && p.T * p.k <= kRouteChoices) {
             moe_up_light_kernel<DT, true><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk, n_zero);
         } else {
             moe_route_kernel<<<(unsigned)p.T, 64, 0, stream>>>(p);
