@@ -87,7 +87,8 @@ Fp8Layout fp8_layout(int64_t M, int64_t K, int64_t N) {
 const char* plan_name(const Fp8Plan& p) {
     switch (p.kind) {
         case Fp8Plan::kTile256: return p.split > 1 ? "fp8_tile256_split" : "fp8_tile256";
-        case Fp8Plan::kTile128: return p.split > 1 ? "fp8_tile128_split" : "fp8_tile128";
+        case Fp8Plan::kTile128: return "fp8_tile128";
+        case Fp8Plan::kSingle: return p.split > 1 ? "fp8_single_split" : "fp8_single";
         case Fp8Plan::kSmall: return p.split > 1 ? "fp8_small_split" : "fp8_small";
         default: return "fp8_small_fused";
     }

@@ -74,6 +74,34 @@ __device__ __forceinline__ v4f mfma_fp8(const v8i& n, const v8i& m, const v4f& c
     return c;
 }
 
+// A wave's 64 x 16 NF results from row m0, column n0 on, through its staging area `ys` in LDS, 16
+// rows m at a time: row r's 16-byte piece c sits at piece c ^ r (mod the pieces of a row).
+template <int DT, int NF>
+__device__ __forceinline__ void store_tile(const Fp8GemmArgs& p, const v4f (&acc)[NF][MF], uint8_t* ys, int64_t m0, int64_t n0) {
+    int lane = threadIdx.x & 63;  // opaque: nothing derived from it here is held through the stages
+    asm volatile("" : "+v"(lane));
+    const int li = lane & 15, q = lane >> 4;
+    constexpr int kPieces = 2 * NF;
+#pragma unroll
+    for (int j = 0; j < MF; ++j) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            u32x2 v;
+            v[0] = (uint32_t)from_f32<DT>(acc[f][j][0]) | ((uint32_t)from_f32<DT>(acc[f][j][1]) << 16);
+            v[1] = (uint32_t)from_f32<DT>(acc[f][j][2]) | ((uint32_t)from_f32<DT>(acc[f][j][3]) << 16);
+            const int c = (2 * f + (q >> 1)) ^ (li & (kPieces - 1));
+            *(u32x2*)(ys + (li * kPieces + c) * 16 + 8 * (q & 1)) = v;
+        }
+#pragma unroll
+        for (int it = 0; it < 16 * kPieces / 64; ++it) {
+            const int row = it * (64 / kPieces) + lane / kPieces, ch = lane % kPieces;
+            const u32x4 v = *(const u32x4*)(ys + (row * kPieces + (ch ^ (row & (kPieces - 1)))) * 16);
+            const int64_t m = m0 + 16 * j + row, n = n0 + 8 * ch;
+            if (m < p.M && n < p.N) *(u32x4*)(p.Y + m * p.N + n) = v;
+        }
+    }
+}
+
 // ROWB: B has a scale per row (else per 128 rows, one for a wave's columns).  SPLIT: few tiles; a
 // workgroup takes one part of one tile's stages, dumps its sums, and the last of the tile's parts
 // to end adds them up in their order and writes the output.
@@ -261,37 +289,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
         for (int f = 0; f < NS; ++f) sn[f] = nsn[f];
     };
 
-    // ---- output of tile ti, through the B slot its last stage freed, 16 rows m of a wave at a
-    // time: row r's 16-byte piece c sits at piece c ^ r (mod the pieces of a row)
-    auto output = [&](int ti, int sb) LLMINT8_FP8_INLINE {
-        int lane = tid & 63;  // opaque: nothing derived from it here is held through the stages
-        asm volatile("" : "+v"(lane));
-        const int li = lane & 15, q = lane >> 4;
-        int64_t m0, n0;
-        tile_origin(ti, m0, n0);
-        constexpr int kPieces = 2 * NF;
-        uint8_t* ys = slot_b(sb) + wu * (16 * 16 * kPieces);
-        const int64_t wm0 = m0 + 64 * wm, wn0 = n0 + 16 * NF * wn;
-#pragma unroll
-        for (int j = 0; j < MF; ++j) {
-#pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                u32x2 v;
-                v[0] = (uint32_t)from_f32<DT>(acc[f][j][0]) | ((uint32_t)from_f32<DT>(acc[f][j][1]) << 16);
-                v[1] = (uint32_t)from_f32<DT>(acc[f][j][2]) | ((uint32_t)from_f32<DT>(acc[f][j][3]) << 16);
-                const int c = (2 * f + (q >> 1)) ^ (li & (kPieces - 1));
-                *(u32x2*)(ys + (li * kPieces + c) * 16 + 8 * (q & 1)) = v;
-            }
-#pragma unroll
-            for (int it = 0; it < 16 * kPieces / 64; ++it) {
-                const int row = it * (64 / kPieces) + lane / kPieces, ch = lane % kPieces;
-                const u32x4 v = *(const u32x4*)(ys + (row * kPieces + (ch ^ (row & (kPieces - 1)))) * 16);
-                const int64_t m = wm0 + 16 * j + row, n = wn0 + 8 * ch;
-                if (m < p.M && n < p.N) *(u32x4*)(p.Y + m * p.N + n) = v;
-            }
-        }
-    };
-
     // ---- prologue: stages 0 and 1 of both operands, the first scales
     load_scales(0, 0, sm, sn);
 #pragma unroll
@@ -334,7 +331,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
         }
         mfma_settle();
         if constexpr (SPLIT) {
-            constexpr int H = NF == 8 ? (ROWB ? 1 : 2) : 4;  // as the registers allow
+            constexpr int H = ROWB ? 1 : 2;  // as the registers allow
             constexpr uint32_t kStep = 64 * kWaves * 16;  // bytes of one quad of every thread
             const int tile = x_start + local - part * T1;
             auto slot = [&](int i) LLMINT8_FP8_INLINE {
@@ -367,7 +364,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
                 }
             }
         }
-        output(ti, sb == 0 ? 2 : sb - 1);  // the slot of the last stage
+        int64_t m0, n0;
+        tile_origin(ti, m0, n0);  // out through the slot of the last stage
+        store_tile<DT, NF>(p, acc, slot_b(sb == 0 ? 2 : sb - 1) + wu * (16 * 32 * NF), m0 + 64 * wm, n0 + 16 * NF * wn);
         if (!SPLIT && ti + 1 < my_tiles) {
             --left;
             ra0 = ra1;
@@ -393,15 +392,244 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tiled_kernel(TiledParams 
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
+// ---- at most one tile (or part of one) a compute unit: there a stage of the kernel above takes what
+// a load from memory takes, divided by the two stages that it looks ahead.  Here a workgroup of four
+// waves has the unit's LDS to itself and looks four stages ahead (4 slots of A, 5 of B); its tile of
+// 128 x 128, its stage and its layout are the same.  Scales must not be waited for out of turn (loads
+// return in order), so they come for four stages at a time, a round ahead: lane quarter q loads a
+// row operand's dword of the round's stage q, which lane swaps then give to all quarters; a block
+// operand's dword holds the four stages' bytes (a part's first stage is a multiple of 4).
+template <int DT, bool ROWB>
+__global__ __launch_bounds__(256, 1) void fp8_single_kernel(TiledParams tp) {
+    constexpr int WM = 2, WN = 2, NF = 4, D = 4;
+    constexpr int BM = 16 * MF * WM, BN = 16 * NF * WN;
+    constexpr int kSlotA = BM * BK, kSlotB = BN * BK;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[D * kSlotA + (D + 1) * kSlotB];
+    const Fp8GemmArgs& p = tp.a;
+    const int tid = threadIdx.x, lane = tid & 63, wu = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wu % WM, wn = wu / WM;
+    const int li = lane & 15, q = lane >> 4;
+
+    // ---- this workgroup's tile and part: runs of tiles to an XCD, part after part, as above
+    const int T1 = tp.tiles_m * tp.tiles_n, T = T1 * tp.split;
+    const int xcd = blockIdx.x % kXcds, per = T / kXcds, rem = T % kXcds;
+    const int id = xcd * per + (xcd < rem ? xcd : rem) + blockIdx.x / kXcds;
+    const int part = __builtin_amdgcn_readfirstlane(id / T1), tile = id - part * T1;
+    const int in_group = kGroupM * tp.tiles_n, first_m = tile / in_group * kGroupM;
+    const int gm = tp.tiles_m - first_m < kGroupM ? tp.tiles_m - first_m : kGroupM;
+    const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(first_m + tile % in_group % gm) * BM;
+    const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(tile % in_group / gm) * BN;
+    const int all = (int)(p.pitch / BK), k0 = part * tp.part, nk = all - k0 < tp.part ? all - k0 : tp.part;
+    const int64_t rows_a = p.M - m0 < BM ? p.M - m0 : BM, rows_b = p.N - n0 < BN ? p.N - n0 : BN;
+
+    // ---- operand loads; those past the part lie past the resources
+    const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(p.A + m0 * p.pitch, rows_a * p.pitch);
+    const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.B + n0 * p.pitch, rows_b * p.pitch);
+    uint32_t off[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = 8 * (4 * wu + j) + lane / 8;
+        off[j] = (uint32_t)(r * p.pitch + (((lane & 7) ^ swz(r)) << 4));
+    }
+    auto slot_a = [&](int s) LLMINT8_FP8_INLINE { return smem + s * kSlotA; };
+    auto slot_b = [&](int s) LLMINT8_FP8_INLINE { return smem + D * kSlotA + s * kSlotB; };
+    auto issue = [&](__amdgpu_buffer_rsrc_t rs, uint8_t* slot, int k, int j) LLMINT8_FP8_INLINE {
+        const uint32_t far = k < nk ? 0u : 0x80000000u;
+        const int at = __builtin_amdgcn_readfirstlane(k < nk ? (k0 + k) * BK : 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(slot + (4 * wu + j) * 1024), 16, (int)(off[j] | far), at, 0, 0);
+    };
+
+    // ---- scales of the stages k .. k + 3
+    const int64_t ta = round_up(p.M, 64), tb = round_up(p.N, 64);
+    struct Scales {
+        int a, b;  // as loaded
+    };
+    auto row_scales = [&](const uint8_t* scales, int64_t t, int64_t r0, int64_t rows, int at, int k) LLMINT8_FP8_INLINE {
+        const int g = __builtin_amdgcn_readfirstlane(k0 + k), n = all - g < 4 ? all - g : 4;
+        const int64_t bytes = n > 0 ? (n - 1) * t + round_up(rows, 64) : 0;
+        const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(scales + g * t + r0, bytes);
+        return (int)__builtin_amdgcn_raw_buffer_load_b32(rs, (uint32_t)(q * (int)t + at + 4 * li), 0, 0);
+    };
+    auto load_scales = [&](int k) LLMINT8_FP8_INLINE {
+        Scales r;
+        r.a = row_scales(p.sa, ta, m0, rows_a, 64 * wm, k);
+        if constexpr (ROWB) {
+            r.b = row_scales(p.sb, tb, n0, rows_b, 64 * wn, k);
+        } else {
+            const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(p.sb + (n0 >> 7) * p.spitch, p.spitch);
+            r.b = (int)__builtin_amdgcn_raw_buffer_load_b32(rs, (uint32_t)(k0 + k), 0, 0);  // past the row: zeros
+        }
+        return r;
+    };
+    auto spread = [&](int v, int (&s)[D]) LLMINT8_FP8_INLINE {  // quarter q's to all, for each q
+        const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+        s[0] = lo[0];
+        s[1] = lo[1];
+        s[2] = hi[0];
+        s[3] = hi[1];
+    };
+
+    const int rd = li * BK + (((2 * q) ^ swz(li)) << 4);
+    auto read = [&](const uint8_t* slot, int f) LLMINT8_FP8_INLINE {
+        const v4i lo = *(const v4i*)(slot + f * 16 * BK + rd), hi = *(const v4i*)(slot + f * 16 * BK + (rd ^ 16));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    v4f acc[NF][MF] = {};
+    v8i fm[2][MF], fn[2];
+    int sm[D], sn[D];
+    Scales ahead;
+    auto take_scales = [&]() LLMINT8_FP8_INLINE {
+        spread(ahead.a, sm);
+        if constexpr (ROWB) spread(ahead.b, sn);
+        else sn[0] = ahead.b;
+    };
+
+    // Stage k, B in slot sb; P = k % 4, the slot of A; TAIL: past the last whole round, where no scales
+    // are loaded.  The barrier leaves the loads after the next stage's in flight: B's and A's of two
+    // stages and B's of a third, and this round's scales if they are among them.
+    auto stage = [&](auto ptag, auto tail, int sb, int k) LLMINT8_FP8_INLINE {
+        constexpr int P = decltype(ptag)::value;
+        constexpr bool TAIL = decltype(tail)::value;
+        uint8_t* to_b = slot_b(sb == 0 ? D : sb - 1);
+        const uint8_t* An = slot_a((P + 1) % D) + wm * (16 * MF * BK);
+        const uint8_t* Bc = slot_b(sb) + wn * (16 * NF * BK);
+        const uint8_t* Bn = slot_b(sb == D ? 0 : sb + 1) + wn * (16 * NF * BK);
+        v8i w[NF];
+        w[0] = fn[0];
+        w[1] = fn[1];
+        auto mfma_row = [&](int f) LLMINT8_FP8_INLINE {
+#pragma unroll
+            for (int j = 0; j < MF; ++j)
+                acc[f][j] = mfma_fp8(w[f], fm[P & 1][j], acc[f][j], sn[ROWB ? P : 0], ROWB ? f : P, sm[P], j);
+        };
+        if constexpr (P == 0 && !TAIL) {
+            ahead = load_scales(k + D);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int f = 0; f < NF - 2; ++f) {
+#pragma unroll
+            for (int l = 2 * f; l < 2 * f + 2; ++l) issue(rb, to_b, k + D, l);
+            w[f + 2] = read(Bc, f + 2);
+            mfma_row(f);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (P == 3 || TAIL) LLMINT8_FP8_WAIT_BARRIER(20);
+        else LLMINT8_FP8_WAIT_BARRIER(22);
+        fn[0] = read(Bn, 0);
+        fm[(P & 1) ^ 1][0] = read(An, 0);
+        fm[(P & 1) ^ 1][1] = read(An, 1);
+#pragma unroll
+        for (int l = 0; l < 2; ++l) issue(ra, slot_a(P), k + D, l);
+        mfma_row(NF - 2);
+        __builtin_amdgcn_sched_barrier(0);
+        fm[(P & 1) ^ 1][2] = read(An, 2);
+        fm[(P & 1) ^ 1][3] = read(An, 3);
+        fn[1] = read(Bn, 1);
+#pragma unroll
+        for (int l = 2; l < 4; ++l) issue(ra, slot_a(P), k + D, l);
+        mfma_row(NF - 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (P == 3) take_scales();
+    };
+
+    // ---- the first four stages; the first one's are there when all but the other three's are
+    ahead = load_scales(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < D; ++k) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) issue(rb, slot_b(k), k, j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) issue(ra, slot_a(k), k, j);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    LLMINT8_FP8_WAIT_BARRIER(24);
+    take_scales();
+    fn[0] = read(slot_b(0) + wn * (16 * NF * BK), 0);
+#pragma unroll
+    for (int j = 0; j < MF; ++j) fm[0][j] = read(slot_a(0) + wm * (16 * MF * BK), j);
+    fn[1] = read(slot_b(0) + wn * (16 * NF * BK), 1);
+    int k = 0, sb = 0;
+    auto advance = [&]() LLMINT8_FP8_INLINE {
+        ++k;
+        sb = sb == D ? 0 : sb + 1;
+    };
+    while (k + D <= nk) {
+        stage(std::integral_constant<int, 0>{}, std::false_type{}, sb, k);
+        advance();
+        stage(std::integral_constant<int, 1>{}, std::false_type{}, sb, k);
+        advance();
+        stage(std::integral_constant<int, 2>{}, std::false_type{}, sb, k);
+        advance();
+        stage(std::integral_constant<int, 3>{}, std::false_type{}, sb, k);
+        advance();
+    }
+    const int rest = nk - k;
+    if (rest > 0) {
+        stage(std::integral_constant<int, 0>{}, std::true_type{}, sb, k);
+        advance();
+    }
+    if (rest > 1) {
+        stage(std::integral_constant<int, 1>{}, std::true_type{}, sb, k);
+        advance();
+    }
+    if (rest > 2) {
+        stage(std::integral_constant<int, 2>{}, std::true_type{}, sb, k);
+        advance();
+    }
+    mfma_settle();
+    uint8_t* last = slot_b(sb == 0 ? D : sb - 1);  // the slot of the last stage, which no load is bound for
+    if (tp.split > 1) {
+        constexpr uint32_t kStep = 256 * 16;  // bytes of one quad of every thread
+        auto slot = [&](int i) LLMINT8_FP8_INLINE {
+            return buffer_rsrc(p.partial + ((int64_t)tile * tp.split + i) * (BM * BN), (int64_t)BM * BN * 4);
+        };
+        const __amdgpu_buffer_rsrc_t own = slot(part);
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int j = 0; j < MF; ++j) store_part(own, 16 * tid, (f * MF + j) * kStep, acc[f][j]);
+        if (!last_part(p.counters + tile, tp.split, (int*)last)) return;  // (which waited for all loads)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int j = 0; j < MF; ++j) acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < tp.split; ++i) {
+            const __amdgpu_buffer_rsrc_t rs = slot(i);
+            v4f v[NF][MF];
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int j = 0; j < MF; ++j) v[f][j] = load_part(rs, 16 * tid, (f * MF + j) * kStep);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int j = 0; j < MF; ++j) acc[f][j] += v[f][j];
+        }
+    }
+    store_tile<DT, NF>(p, acc, last + wu * (16 * 32 * NF), m0 + 64 * wm, n0 + 16 * NF * wn);
+    // no load into this workgroup's LDS may outlive it
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// the stages of one of `split` parts: whole rounds of scales
+int single_part(int64_t groups, int64_t split) { return (int)(split > 1 ? round_up(ceil_div(groups, split), 4) : groups); }
+
 template <int DT, int WM, int WN, int NF, bool ROWB>
 hipError_t tiled_launch(const Fp8GemmArgs& a, int split, hipStream_t stream) {
     constexpr int BM = 16 * MF * WM, BN = 16 * NF * WN;
     const int nk = (int)(a.pitch / BK);
     TiledParams p{a, (int)ceil_div(a.M, BM), (int)ceil_div(a.N, BN), split, (int)ceil_div(nk, split)};
     const int64_t T = (int64_t)p.tiles_m * p.tiles_n;
-    if (split > 1) {
-        fp8_tiled_kernel<DT, WM, WN, NF, ROWB, true><<<(unsigned)(T * split), 64 * WM * WN, 0, stream>>>(p);
-        return hipGetLastError();
+    if constexpr (NF == 8) {  // (tiles of 128 in parts run in fp8_single_kernel)
+        if (split > 1) {
+            fp8_tiled_kernel<DT, WM, WN, NF, ROWB, true><<<(unsigned)(T * split), 64 * WM * WN, 0, stream>>>(p);
+            return hipGetLastError();
+        }
     }
     int dev = 0, cus = 0;
     hipError_t e = hipGetDevice(&dev);
@@ -417,6 +645,15 @@ hipError_t tiled(int dt, const Fp8GemmArgs& a, int split, hipStream_t stream) {
     if (a.spitch == 0)
         return dt == F16 ? tiled_launch<F16, WM, WN, NF, true>(a, split, stream) : tiled_launch<BF16, WM, WN, NF, true>(a, split, stream);
     return dt == F16 ? tiled_launch<F16, WM, WN, NF, false>(a, split, stream) : tiled_launch<BF16, WM, WN, NF, false>(a, split, stream);
+}
+
+template <int DT>
+hipError_t single(const Fp8GemmArgs& a, int split, hipStream_t stream) {
+    const TiledParams p{a, (int)ceil_div(a.M, 128), (int)ceil_div(a.N, 128), split, single_part(a.pitch / BK, split)};
+    const unsigned grid = (unsigned)((int64_t)p.tiles_m * p.tiles_n * split);
+    if (a.spitch == 0) fp8_single_kernel<DT, true><<<grid, 256, 0, stream>>>(p);
+    else fp8_single_kernel<DT, false><<<grid, 256, 0, stream>>>(p);
+    return hipGetLastError();
 }
 
 // ---- few rows (M <= 64): the product is bound by B's bytes, each read once straight into
@@ -599,22 +836,21 @@ int parts(int64_t groups, int64_t wanted, int64_t least) {
     return (int)ceil_div(groups, part);
 }
 
-// Parts of the sum of `tiles` (at most 512) tiles of 128 x 128, two of which fit a compute unit.
-// The estimate, in units of 10 ns, from measurements over 9 to 512 tiles and 4 to 128 groups: a group
-// takes 0.6 us where a workgroup has the unit to itself, else 0.9 us a pair; joining s parts takes
-// 2 us + 0.6 s us + 0.011 us a part and tile.  65 x 16384 x 4096 (32 tiles): 79.6 us unsplit, 47.9 in
-// 2 parts, 32.1 in 4, 29.3 in 8, 33.1 in 16; 512 x 4096 x 4096 (128 tiles): 21.2, 20.1 in 2, 25.4
-// in 4; 1000 x 4096 x 4096 (256 tiles): 22.8, 28.3 in 2.
-int parts128(int64_t tiles, int64_t groups) {
-    int64_t best = 60 * groups * (tiles > 256 ? 3 : 2) / 2, s = 1;
-    for (int64_t i = 2; i <= 16 && i <= groups && i * tiles <= 512; ++i) {
-        const int64_t cost = 60 * ceil_div(groups, i) * (tiles * i > 256 ? 3 : 2) / 2 + 200 + 60 * i + 11 * i * tiles / 10;
-        if (cost < best) {
-            best = cost;
-            s = i;
-        }
-    }
-    return parts(groups, s, 1);
+// Parts of the sum of `tiles` (at most 256) tiles of 128 x 128, one workgroup a compute unit.  The
+// estimate, in units of 0.1 ns, from measurements over 5 to 256 tiles and 3 to 128 groups: a group
+// takes 0.42 us, up to 0.54 us as more workgroups share the memory; joining s parts takes 2 us + 1 us
+// a part + 11 ns a part and tile.  65 x 16384 x 4096 (32 tiles): 57.1 us unsplit, 37.3 in 2 parts,
+// 27.3 in 4, 27.0 in 8; 200 x 8192 x 8192 (128 tiles): 35.7, 30.9 in 2; 512 x 4096 x 4096 (128
+// tiles): 16.7, 19.1 in 2.
+int single_parts(int64_t tiles, int64_t groups) {
+    auto cost = [&](int64_t i) {
+        const int64_t wgs = tiles * i;
+        return single_part(groups, i) * (4200 + 1200 * wgs / 256) + (i > 1 ? 20000 + 10000 * i + 110 * wgs : 0);
+    };
+    int64_t s = 1;
+    for (int64_t i = 2; i * tiles <= 256 && i <= groups / 4; ++i)
+        if (cost(i) < cost(s)) s = i;
+    return (int)ceil_div(groups, single_part(groups, s));
 }
 
 }  // namespace
@@ -622,7 +858,10 @@ int parts128(int64_t tiles, int64_t groups) {
 Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb) {
     Fp8Plan p{Fp8Plan::kTile256, 0, 0, 1, 0, 0};
     int64_t out = 256 * 256;
-    if (M <= 64 && !rowb) {
+    // Few rows straight from memory; past 32 rows only while B is small, as there the tiles, whose rows
+    // are shared, catch up: 64 x 16384 x 4096 38.1 us, in a tile's kernel 25.9, 48 x 8192 x 8192 24.0 and
+    // 22.7; 64 x 4096 x 4096 11.4 and 13.7, 32 x 16384 x 4096 24.3 and 25.7.
+    if (!rowb && (M <= 32 || (M <= 64 && N * nk <= (int64_t)1 << 17))) {
         const bool fused = x16 && M <= 4 && N * nk <= (int64_t)1 << 17;
         p.kind = fused ? Fp8Plan::kFused : Fp8Plan::kSmall;
         p.pieces = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
@@ -636,12 +875,14 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb) {
         // 33.8 us, with tiles of 256 42.1; 333 x 4096 x 16384 38.3 and 44.0; past that tiles of 256:
         // 2048 x 2064 x 7424 31.3 us, with tiles of 128 41.2; 1000 x 4096 x 16384 55.2 and 75.7.
         // Between half and all of that with a long sum, tiles of 256 in parts: 2048 x 16384 x 4096 116 us
-        // in 2, with tiles of 128 136; 1000 x 8192 x 8192 (64 groups) 72.2 and 70.0.
+        // in 2, with tiles of 128 136; 1000 x 8192 x 8192 (64 groups) 72.2 and 70.0.  One tile a unit:
+        // the kernel that looks further ahead: 512 x 8192 x 8192 (256 tiles) 41.2 us, else 51.3; 200 x
+        // 784 x 632 (10 tiles) 6.7 and 7.5.
         if (t128 <= 512 && !(t128 > 256 && nk >= 96)) {
-            p.kind = Fp8Plan::kTile128;
+            p.kind = t128 <= 256 ? Fp8Plan::kSingle : Fp8Plan::kTile128;
             out = 128 * 128;
             p.tiles = t128;
-            p.split = parts128(t128, nk);
+            if (t128 <= 256) p.split = single_parts(t128, nk);
         } else {
             p.tiles = t256;
             if (t256 <= 128) p.split = parts(nk, 256 / t256, 32);
@@ -655,6 +896,7 @@ hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& a, const Fp8Plan& plan, hi
     if (a.M == 0 || a.N == 0) return hipSuccess;
     if (plan.kind == Fp8Plan::kTile256) return tiled<4, 2, 8>(dt, a, plan.split, stream);
     if (plan.kind == Fp8Plan::kTile128) return tiled<2, 2, 4>(dt, a, plan.split, stream);
+    if (plan.kind == Fp8Plan::kSingle) return dt == F16 ? single<F16>(a, plan.split, stream) : single<BF16>(a, plan.split, stream);
     return dt == F16 ? small<F16>(a, plan, stream) : small<BF16>(a, plan, stream);
 }
 

@@ -17,9 +17,9 @@
 // tokens the column side, 16 to a piece; a group of 128 takes four instructions, whose order of
 // the terms is free as long as both operands agree.  bf16 takes the scale in the conversion (an
 // exact shift of the exponent); fp16 could not hold it, so there each group's sum is added with its
-// scale.  Sums are fp32; the waves of a workgroup split them and meet in LDS in a fixed order, and
-// every token has a column of its own, so neither the order of atomics nor a token's neighbours
-// change its bits.
+// scale.  Sums are fp32; waves and workgroups split them and meet in a fixed order, so a result's
+// bits follow from the inputs alone (where the splits lie depends on the sizes and on the experts
+// that the tokens meet together).
 //
 // Two forms of both launches.  Where experts have few tokens (a mean of kLightMean at most) the
 // work is cut finer, so that small layers fill the compute units: the 16 rows of an instruction

@@ -211,7 +211,7 @@ hipError_t launch_fp8_cols(int dt, const void* A, const void* B, int64_t R, int6
 
 // How a product of M x N outputs over nk groups runs.
 struct Fp8Plan {
-    enum Kind { kTile256, kTile128, kSmall, kFused } kind;
+    enum Kind { kTile256, kTile128, kSingle, kSmall, kFused } kind;
     int pieces;   // kSmall: pieces of 16 rows m (1, 2 or 4); kFused: 1
     int columns;  // kSmall, kFused: pieces of 16 columns of a workgroup
     int split;    // parts of the sum, each a workgroup's; their partial sums go through memory
