@@ -21,11 +21,16 @@
 // bits follow from the inputs alone (where the splits lie depends on the sizes and on the experts
 // that the tokens meet together).
 //
-// Two forms of both launches.  Where experts have few tokens (a mean of kLightMean at most) the
+// Three forms of both launches.  Where experts have few tokens (a mean of kLightMean at most) the
 // work is cut finer, so that small layers fill the compute units: the 16 rows of an instruction
 // are 8 gate and the same 8 up columns in the first launch, and 8 columns of two experts in the
 // second, whose tokens are the two halves of its columns (the products of one expert's rows with
-// the other's tokens are not used).  Otherwise 16 columns and MG pieces of tokens.
+// the other's tokens are not used).  Otherwise 16 columns and MG pieces of tokens, and in large
+// layers with several pieces 128 columns that share the tokens' values in LDS.
+//
+// Read at: 8 tokens, 8 experts of 4096 x 14336, top 2: 165 and 91 us, 5.4 TB/s; 37 tokens, 60 experts of
+// 2064 x 1424, top 4: 78 and 57 us, 3.6 TB/s; one token, 64 experts of 2048 x 768, top 8: 10 and 6.8 us
+// (2.2 TB/s: the two launches' latencies).
 #include <cmath>
 
 #include "fp8_common.hpp"
@@ -48,6 +53,7 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t off,
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, at, 0));
 }
 constexpr uint32_t kFar = 0x80000000u;  // an offset past every resource: reads zero
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // A step's instructions bound these kernels before its bytes do, so what a step computes is kept
 // short: the group's place rides in the scalar offset, a step without a group has empty resources
@@ -853,6 +859,295 @@ __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
     put_tokens<DT, 2, MAXT, WV>(p, ysum);
 }
 
+// ---- many tokens an expert (16 MG at a time) in a large layer: there the tokens' values, which every wave of the
+// kernels above reads for itself, are most of what a compute unit reads (12 TB/s from the L2s in all).
+// Here the eight waves of a workgroup take a tile of 16 columns each, and share the tokens: a group's
+// values come straight into LDS (16-byte chunk c of token t at chunk c ^ t, so that 16 tokens' reads
+// of one chunk meet all banks), two groups ahead in three slots.  The waves meet once per group;
+// each has whole sums, so nothing is joined.
+template <int MG>
+struct Tokens {
+    static constexpr int kLoads = MG / 2;  // of a wave: 4 tokens each
+    static constexpr int kSlot = 16 * MG * 256;
+    uint32_t off[kLoads], past[kLoads];  // this lane's chunks in the first group; kFar: none in the last
+
+    // row: of token t its offset, or kFar; n: values of a row (past them the last group reads zeros)
+    template <class F>
+    __device__ __forceinline__ void set(F&& row, int n, int ng) {
+        const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int t = 4 * (kLoads * w + j) + lane / 16, c = (lane ^ t) & 15;
+            off[j] = row(t) + 16 * c;
+            past[j] = 128 * (ng - 1) + 8 * c < n ? 0u : kFar;
+        }
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint8_t* slot, int g, int ng) const {
+        const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int at = __builtin_amdgcn_readfirstlane(g < ng ? 256 * g : 0);
+        const uint32_t far = g < ng ? 0u : kFar, tail = g == ng - 1 ? kFar : 0u;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const uint32_t o = off[j] | far | (tail & past[j]);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(slot + (kLoads * w + j) * 1024), 16, (int)o, at, 0, 0);
+        }
+    }
+    static __device__ __forceinline__ void read(const uint8_t* slot, u32x4 (&x)[MG][4]) {
+        const int li = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
+#pragma unroll
+        for (int j = 0; j < MG; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[j][i] = *(const u32x4*)(slot + (16 * j + li) * 256 + (((8 * (i >> 1) + 2 * q + (i & 1)) ^ li) << 4));
+    }
+};
+
+// wait for this wave's LDS reads and all but the N newest loads, then the bare barrier
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <int DT, int MG>
+__global__ __launch_bounds__(512, 2) void moe_up_many_kernel(Fp8MoeArgs p, int spans, int chunk, int n_zero) {
+    constexpr int D = 2, S = 3, kWeightLoads = 6;  // (of a step: vector loads all, as the waits count them)
+    struct Shared {  // (one variable: with several the compiler waits for all loads at each read)
+        union {
+            __attribute__((aligned(1024))) uint8_t x[S][Tokens<MG>::kSlot];
+            struct {
+                uint32_t mask[kMaxExperts][4];
+                int first[kMaxExperts];
+            } t;
+        };
+        UpSetup<false> setup;
+    };
+    __shared__ Shared sh;
+    auto& setup = sh.setup;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, q = lane >> 4;
+    const int32_t* ids = setup.template route<8>(p);
+    if (blockIdx.x == 0) {
+        for (int i = tid; i < n_zero; i += blockDim.x) p.counters[i] = 0;
+        build_table(ids, (int)p.T, (int)p.E, p.k, chunk, p.table, p.pairs, sh.t.mask, sh.t.first);
+        return;
+    }
+    const int e = (int)(blockIdx.x - 1) / spans, span = (int)(blockIdx.x - 1) % spans;
+    const int count = setup.find(p, ids, e, 0, e);
+    if (count == 0) return;  // the same in every thread
+    const int* list = setup.list;
+    const int64_t hp = fp8_pitch(p.H), hsp = fp8_scale_pitch_of(p.H), ip = fp8_pitch(p.I);
+    const int tiles = (int)(p.I / 16), ng = (int)(hp / 128), tile = 8 * span + w;
+    const bool has = tile < tiles;
+    const int64_t i0 = 16 * (int64_t)(has ? tile : 0), s_bytes = ceil_div(2 * p.I, 128) * hsp;
+    const uint8_t* W = p.W13 + (int64_t)e * 2 * p.I * hp;
+    const uint8_t *Wg = W + i0 * hp, *Wu = W + (p.I + i0) * hp;
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(p.X, p.T * p.H * 2), rs = buffer_rsrc(p.s13 + (int64_t)e * s_bytes, s_bytes);
+    const uint32_t w_off = (uint32_t)(li * hp + 16 * q), sg = (uint32_t)((i0 >> 7) * hsp), su = (uint32_t)(((p.I + i0) >> 7) * hsp);
+    struct Group {
+        u32x4 g[2], u[2];
+        Scale eg, eu;
+    };
+    for (int c0 = 0; c0 < count; c0 += 16 * MG) {
+        Tokens<MG> tokens;
+        tokens.set([&](int t) { return c0 + t < count ? (uint32_t)((list[c0 + t] / p.k) * p.H) * 2 : kFar; }, (int)p.H, ng);
+        auto load_w = [&](Group& r, int g) LLMINT8_MOE_INLINE {
+            const bool in = g < ng && has;  // else zeros
+            const int at = in ? g : 0, bytes = in ? 16 * (int)hp : 0;
+            const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(Wg, bytes), ru = buffer_rsrc(Wu, bytes);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                r.g[h] = load16(rg, w_off + 64 * h, at * 128);
+                r.u[h] = load16(ru, w_off + 64 * h, at * 128);
+            }
+            r.eg = load_scale(rs, sg, at);
+            r.eu = load_scale(rs, su, at);
+            __builtin_amdgcn_sched_barrier(0);  // as above
+        };
+        auto load_x = [&](int g, int slot) LLMINT8_MOE_INLINE {
+            tokens.load(rx, sh.x[slot], g, ng);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        v4f ag[MG] = {}, au[MG] = {};
+        Group r[D];
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            load_x(d, d);
+            load_w(r[d], d);
+        }
+        int slot = 0;
+        for (int s = 0; s < ng; s += D) {  // whole rounds, as above
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                // the group's values are in, and every wave is done with the slot before it
+                wait_barrier<2 * kWeightLoads + Tokens<MG>::kLoads>();
+                load_x(s + d + 2, slot == 0 ? 2 : slot - 1);
+                u32x4 x[MG][4];
+                Tokens<MG>::read(sh.x[slot], x);
+                group_product<DT, MG>(r[d].g, scale_here(r[d].eg), x, ag);
+                group_product<DT, MG>(r[d].u, scale_here(r[d].eu), x, au);
+                load_w(r[d], s + d + 2);
+                slot = slot == 2 ? 0 : slot + 1;
+            }
+        }
+        mfma_settle();
+#pragma unroll
+        for (int j = 0; j < MG; ++j) {
+            const int i = c0 + 16 * j + li;
+            if (has && i < count) {
+                u32x2 o;
+                o[0] = (uint32_t)swiglu<DT>(ag[j][0], au[j][0]) | ((uint32_t)swiglu<DT>(ag[j][1], au[j][1]) << 16);
+                o[1] = (uint32_t)swiglu<DT>(ag[j][2], au[j][2]) | ((uint32_t)swiglu<DT>(ag[j][3], au[j][3]) << 16);
+                *(u32x2*)(p.h + (int64_t)list[i] * ip + i0 + 4 * q) = o;
+            }
+        }
+        if (span == spans - 1) pad_rows(p, list, c0, count < c0 + 16 * MG ? count : c0 + 16 * MG, ip);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load is bound for the slots any more
+        __syncthreads();
+    }
+}
+
+// The second launch: 128 columns of H, an entry after the other.
+template <int DT, int MG, int MAXT>
+__global__ __launch_bounds__(512, 2) void moe_down_many_kernel(Fp8MoeArgs p) {
+    constexpr int D = 2, S = 3, kWeightLoads = 3, MAXN = MAXT * kMaxTopK;
+    struct Shared {  // one variable, as above
+        __attribute__((aligned(1024))) uint8_t x[S][Tokens<MG>::kSlot];
+        v4f ysum[8][MAXT][4];  // a wave's 16 columns of every token
+        int32_t table[3 * MAXN / 8], pairs[MAXN];
+        float weights[MAXN];
+        int flag;
+    };
+    __shared__ Shared sh;
+    auto& xs = sh.x;
+    auto& ysum = sh.ysum;
+    auto& table = sh.table;
+    auto& pairs = sh.pairs;
+    auto& weights = sh.weights;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, q = lane >> 4;
+    const int T = (int)p.T, k = p.k, n = T * k;
+    const bool has = 128 * (int64_t)blockIdx.x + 16 * w < p.H;
+    const int64_t n0 = has ? 128 * (int64_t)blockIdx.x + 16 * w : 0;
+    const int64_t ip = fp8_pitch(p.I), isp = fp8_scale_pitch_of(p.I);
+    const int ng = (int)(ip / 128);
+    const int entries = __builtin_amdgcn_readfirstlane(p.table[0]);  // (at most E + n / (16 MG), and 12 E < n)
+    for (int i = tid; i < 3 * entries; i += 512) table[i] = p.table[1 + i];
+    for (int i = tid; i < n; i += 512) {
+        pairs[i] = p.pairs[i];
+        weights[i] = p.weights[i];
+    }
+    for (int i = tid; i < 8 * T * 4; i += 512) ysum[i / (4 * T)][(i >> 2) % T][i & 3] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    __syncthreads();
+    const int total = entries * ng, parts = gridDim.y, part = blockIdx.y;
+    const int from = (int)((int64_t)total * part / parts), to = (int)((int64_t)total * (part + 1) / parts);
+    if (from < to) {
+        const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, (int64_t)n * ip * 2);
+        const int64_t scale_rows = ceil_div(p.H, 128), e_scales = scale_rows * isp;
+        const uint32_t w_off = (uint32_t)(li * ip + 16 * q), s_row = (uint32_t)((n0 >> 7) * isp);
+        struct Group {
+            u32x4 w[2];
+            Scale s;
+        };
+        // the next load's entry and group, and that entry's expert and rows of h
+        int le = from / ng, lg = from - le * ng, expert = 0, left = to - from;
+        Tokens<MG> tokens;
+        auto open = [&]() LLMINT8_MOE_INLINE {
+            if (le >= entries) return;
+            expert = __builtin_amdgcn_readfirstlane(table[3 * le]);
+            const int first = table[3 * le + 1], count = table[3 * le + 2];
+            tokens.set([&](int t) { return t < count ? (uint32_t)(pairs[first + t] * ip) * 2 : kFar; }, (int)ip, ng);
+        };
+        auto load_x = [&](int slot) LLMINT8_MOE_INLINE {
+            tokens.load(rh, xs[slot], left > 0 ? lg : ng, ng);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto load_w = [&](Group& r) LLMINT8_MOE_INLINE {
+            const bool in = left > 0 && has;  // else zeros
+            const int g = in ? lg : 0;
+            const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(p.W2 + ((int64_t)expert * p.H + n0) * ip, in ? 16 * ip : 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) r.w[h] = load16(rw, w_off + 64 * h, g * 128);
+            r.s = load_scale(buffer_rsrc(p.s2 + expert * e_scales, e_scales), s_row, g);
+            __builtin_amdgcn_sched_barrier(0);
+            --left;
+            if (++lg == ng) {
+                lg = 0;
+                ++le;
+                open();
+            }
+        };
+        v4f acc[MG] = {};
+        int ce = le, cg = lg;  // the entry and group being multiplied
+        auto flush = [&]() LLMINT8_MOE_INLINE {
+            mfma_settle();
+            const int first = table[3 * ce + 1], count = table[3 * ce + 2];
+#pragma unroll
+            for (int j = 0; j < MG; ++j) {
+                const int i = 16 * j + li;
+                if (i < count) {
+                    const int pair = pairs[first + i];
+                    const float pt = weights[pair];
+                    v4f y = ysum[w][pair / k][q];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(pt, acc[j][r], y[r]);
+                    ysum[w][pair / k][q] = y;
+                }
+                acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+        };
+        Group r[D];
+        open();
+        // (the two parts of a load take the same place: load_w moves on)
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            load_x(d);
+            load_w(r[d]);
+        }
+        const int steps = to - from;
+        int slot = 0;
+        for (int s = 0; s < steps; s += D) {  // whole rounds, as above
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                wait_barrier<2 * kWeightLoads + Tokens<MG>::kLoads>();  // as above
+                load_x(slot == 0 ? 2 : slot - 1);
+                u32x4 x[MG][4];
+                Tokens<MG>::read(xs[slot], x);
+                group_product<DT, MG>(r[d].w, scale_here(r[d].s), x, acc);
+                load_w(r[d]);
+                slot = slot == 2 ? 0 : slot + 1;
+                if (s + d < steps && (++cg == ng || s + d + 1 == steps)) {
+                    flush();
+                    cg = 0;
+                    ++ce;
+                }
+            }
+        }
+    }
+    auto store = [&](int i, const v4f& y) LLMINT8_MOE_INLINE {
+        u32x2 o;
+        o[0] = (uint32_t)from_f32<DT>(y[0]) | ((uint32_t)from_f32<DT>(y[1]) << 16);
+        o[1] = (uint32_t)from_f32<DT>(y[2]) | ((uint32_t)from_f32<DT>(y[3]) << 16);
+        if (has) *(u32x2*)(p.Y + (int64_t)(i >> 2) * p.H + n0 + 4 * (i & 3)) = o;
+    };
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into this workgroup's LDS may outlive it
+    if (parts == 1) {
+        for (int i = lane; i < 4 * T; i += 64) store(i, ysum[w][i >> 2][i & 3]);
+        return;
+    }
+    // a part's sums, wave after wave; the last part to end adds them up in their order
+    const int64_t block_bytes = (int64_t)8 * 4 * T * 16;
+    const __amdgpu_buffer_rsrc_t rp = buffer_rsrc((const uint8_t*)p.partial + (int64_t)blockIdx.x * parts * block_bytes, parts * block_bytes);
+    const uint32_t own = (uint32_t)(w * 4 * T * 16);
+    for (int i = lane; i < 4 * T; i += 64) store_part(rp, own + 16 * i, (uint32_t)(part * block_bytes), ysum[w][i >> 2][i & 3]);
+    if (!last_part(p.counters + blockIdx.x, parts, &sh.flag)) return;
+    for (int i = lane; i < 4 * T; i += 64) {
+        v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int v = 0; v < parts; ++v) y += load_part(rp, own + 16 * i, (uint32_t)(v * block_bytes));
+        store(i, y);
+    }
+}
+
 // The first launch's grid: workgroup 0 (the table), then `rows` (pairs or experts) of `spans` spans
 // of `span` tiles.  A workgroup's setup (choosing the experts or reading them, the list) is paid
 // once per span, as long as about `enough` workgroups are left: 4 tokens, 64 experts of 2048 x 768,
@@ -877,7 +1172,7 @@ UpGrid up_grid(const Fp8MoeArgs& p, int columns, int64_t enough, int64_t longest
 }
 
 // MG: pieces of 16 tokens multiplied at once; 0: the light form
-template <int DT, int MG>
+template <int DT, int MG, bool MANY = false>
 hipError_t launch_up(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream) {
     const int chunk = plan.chunk, n_zero = plan.parts > 1 ? (int)plan.blocks : 0;
     if constexpr (MG == 0) {
@@ -890,43 +1185,50 @@ hipError_t launch_up(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t st
             moe_up_light_kernel<DT, false><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk, n_zero);
         }
     } else {
-        const UpGrid g = up_grid(p, 16, 1024, 8);
         moe_route_kernel<<<(unsigned)p.T, 64, 0, stream>>>(p);
-        moe_up_kernel<DT, MG><<<(unsigned)g.grid, 64 * kUpWaves, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk, n_zero);
+        if constexpr (MANY) {
+            const int spans = (int)ceil_div(p.I, 128);
+            moe_up_many_kernel<DT, MG><<<(unsigned)(1 + p.E * spans), 512, 0, stream>>>(p, spans, chunk, n_zero);
+        } else {
+            const UpGrid g = up_grid(p, 16, 1024, 8);
+            moe_up_kernel<DT, MG><<<(unsigned)g.grid, 64 * kUpWaves, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk, n_zero);
+        }
     }
     return hipGetLastError();
 }
 
-template <int DT, int MG>
+template <int DT, int MG, bool MANY = false>
 hipError_t launch_down(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream) {
     const dim3 grid((unsigned)plan.blocks, (unsigned)plan.parts);
     if constexpr (MG == 0) {
         if (p.T <= 16) moe_down_light_kernel<DT, 16, 8, 3, 2><<<grid, 512, 0, stream>>>(p);
         else moe_down_light_kernel<DT, 128, 8, 3, 2><<<grid, 512, 0, stream>>>(p);
     } else {
-        if constexpr (MG < 4) {
-            if (p.T <= 64) {
-                moe_down_kernel<DT, MG, 64, 16><<<grid, 1024, 0, stream>>>(p);
-                return hipGetLastError();
-            }
+        if constexpr (MANY) {
+            if (p.T <= 64) moe_down_many_kernel<DT, MG, 64><<<grid, 512, 0, stream>>>(p);
+            else moe_down_many_kernel<DT, MG, 128><<<grid, 512, 0, stream>>>(p);
+        } else {
+            if (p.T <= 64) moe_down_kernel<DT, MG, 64, 16><<<grid, 1024, 0, stream>>>(p);
+            else moe_down_kernel<DT, MG, 128, 8><<<grid, 512, 0, stream>>>(p);
         }
-        moe_down_kernel<DT, MG, 128, 8><<<grid, 512, 0, stream>>>(p);
     }
     return hipGetLastError();
 }
 
 template <int DT>
 hipError_t moe_launch(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream) {
-    const int up = plan.light_up ? 0 : plan.pieces, down = plan.light_down ? 0 : plan.pieces;
-    const hipError_t e = up == 0   ? launch_up<DT, 0>(p, plan, stream)
-                         : up == 1 ? launch_up<DT, 1>(p, plan, stream)
-                         : up == 2 ? launch_up<DT, 2>(p, plan, stream)
-                                   : launch_up<DT, 4>(p, plan, stream);
+    hipError_t e;
+    if (plan.many)
+        e = plan.pieces == 2 ? launch_up<DT, 2, true>(p, plan, stream) : launch_up<DT, 4, true>(p, plan, stream);
+    else
+        e = plan.light_up        ? launch_up<DT, 0>(p, plan, stream)
+            : plan.pieces == 1   ? launch_up<DT, 1>(p, plan, stream)
+                                 : launch_up<DT, 2>(p, plan, stream);
     if (e != hipSuccess) return e;
-    return down == 0   ? launch_down<DT, 0>(p, plan, stream)
-           : down == 1 ? launch_down<DT, 1>(p, plan, stream)
-           : down == 2 ? launch_down<DT, 2>(p, plan, stream)
-                       : launch_down<DT, 4>(p, plan, stream);
+    if (plan.many) return plan.pieces == 2 ? launch_down<DT, 2, true>(p, plan, stream) : launch_down<DT, 4, true>(p, plan, stream);
+    return plan.light_down     ? launch_down<DT, 0>(p, plan, stream)
+           : plan.pieces == 1  ? launch_down<DT, 1>(p, plan, stream)
+                               : launch_down<DT, 2>(p, plan, stream);
 }
 
 // Parts of the second launch's sum.  A compute unit reads about 20 bytes a nanosecond whether it
@@ -952,22 +1254,29 @@ int down_parts(int64_t blocks, int64_t steps) {
 
 Fp8MoePlan fp8_moe_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
     Fp8MoePlan plan;
-    // pieces by the tokens that an expert has on average (one that has more is read once per 16 MG
-    // of them); with few, the light forms where the others would leave compute units idle: 16
+    // Pieces by the tokens that an expert has on average (one that has more is read once per 16 MG
+    // of them).  With few, the light forms where the others would leave compute units idle: 16
     // tokens, 64 experts of 2048 x 768, top 4: up 37.3 us light, 39.4 not, down 18.0 and 29.6; 8 tokens, 8
     // experts of 4096 x 14336, top 2: up 193 light, 169 not, down 101 and 91; 1 token, 64 experts of
-    // 2048 x 768, top 8: up 8.9 and 11.6, down 6.8 and 9.5
+    // 2048 x 768, top 8: up 8.9 and 11.6, down 6.8 and 9.5.  With several pieces, the form that shares
+    // the tokens where its larger workgroups fill the card: 128 tokens, 8 experts of 4096 x 14336, top
+    // 2: 343 us, else 715; 64 tokens, 16 experts of 4096 x 2048 (8192 blocks of 128 x 128), top 4: 108 and
+    // 153; 44 tokens, 16 experts of 2752 x 448 (1408 blocks), top 6: 47.3 and 46.6; 64 tokens, 8 experts of
+    // 2048 x 1024 (1024 blocks), top 2: 43.2 and 36.3.
     const int64_t mean16 = 16 * T * k / E;
-    plan.pieces = mean16 <= 12 * 16 || T <= 16 ? 1 : (mean16 <= 28 * 16 || T <= 32 ? 2 : 4);
+    const int pieces = mean16 <= 12 * 16 || T <= 16 ? 1 : (mean16 <= 28 * 16 || T <= 32 ? 2 : 4);
+    plan.many = pieces > 1 && E * ceil_div(I, 128) * ceil_div(H, 128) >= 4096;
+    plan.pieces = plan.many || pieces < 2 ? pieces : 2;
     const bool few = T <= 8 || mean16 <= kLightMean * 16;
     const int64_t rows = T * k < E ? T * k : E;  // the experts met, at most
     plan.light_up = few && (I / 16) * rows <= 4096;
     plan.light_down = few && H / 16 < 256;
     plan.chunk = plan.light_down ? 8 : 16 * plan.pieces;
-    plan.blocks = H / (plan.light_down ? 8 : 16);
+    const int64_t columns = plan.light_down ? 8 : (plan.many ? 128 : 16);
+    plan.blocks = ceil_div(H, columns);
     const int64_t met = k == E ? rows : (int64_t)((double)E * -expm1((double)T * log1p(-(double)k / (double)E))) + 1;  // of even choices
-    plan.parts = down_parts(plan.blocks, (plan.light_down ? ceil_div(met, 2) : met) * ceil_div(I, 128));
-    plan.partial_bytes = plan.parts > 1 ? T * H * plan.parts * 4 : 0;
+    plan.parts = down_parts(plan.blocks, (plan.light_down ? ceil_div(met, 2) : met) * ceil_div(I, 128) * ceil_div(columns, 16));
+    plan.partial_bytes = plan.parts > 1 ? T * plan.blocks * columns * plan.parts * 4 : 0;
     return plan;
 }
 

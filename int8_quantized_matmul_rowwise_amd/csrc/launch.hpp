@@ -238,7 +238,7 @@ hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& p, const Fp8Plan& plan, hi
 
 struct Fp8MoePlan {
     int pieces;  // of 16 tokens multiplied at once: 1, 2 or 4
-    bool light_up, light_down;
+    bool light_up, light_down, many;
     int chunk;   // tokens of an entry of the second launch
     int parts;   // of its sum
     int64_t blocks, partial_bytes;  // its blocks of columns; parts > 1: the partial sums' bytes

@@ -399,6 +399,22 @@ def test_moe_masks_ties_and_odd_logits(T, dt):
     moe_check(torch.nan_to_num(X), one, w, 1, True)
 
 
+# many tokens an expert in a large layer: two and four pieces of 16 tokens, up to 64 tokens and more
+@pytest.mark.parametrize("T,H,I,E,k,dt", [(60, 4112, 2064, 8, 2, DTS[0]), (64, 4112, 2064, 8, 5, DTS[1]),
+                                          (128, 4112, 2064, 8, 2, DTS[0]), (128, 2064, 1040, 30, 6, DTS[1])])
+def test_moe_many_tokens(T, H, I, E, k, dt):
+    print(f"\n[case] moe many {dt} T={T} H={H} I={I} E={E} k={k}", flush=True)
+    g = gen(T + H + E)
+    X = randn(g, T, H).to(dt)
+    w = experts(g, E, H, I, dt)
+    l = 2 * randn(g, T, E)
+    moe_check(X, l, w, k, True)
+    l[:, E // 2] += 40  # every token on one expert
+    l[torch.rand(T, E, generator=g) < 0.3] = -math.inf
+    l[[1, T - 1]] = -math.inf  # rows of padding
+    moe_check(X, l, w, k, False)
+
+
 def test_moe_writes_its_outputs_alone():
     T, H, I, E, k = 7, 272, 144, 6, 2
     g = gen(12)
