@@ -249,6 +249,16 @@ int check_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
     return LLMINT8_OK;
 }
 
+const char* moe_plan_name(const Fp8MoePlan& p) {  // the form of the first launch, then of the second
+    if (p.many) return p.parts > 1 ? "fp8_moe_many_split" : "fp8_moe_many";
+    if (p.light_down) {
+        if (p.light_up) return p.parts > 1 ? "fp8_moe_light_split" : "fp8_moe_light";
+        return p.parts > 1 ? "fp8_moe_wide_light_split" : "fp8_moe_wide_light";
+    }
+    if (p.light_up) return p.parts > 1 ? "fp8_moe_light_wide_split" : "fp8_moe_light_wide";
+    return p.parts > 1 ? "fp8_moe_wide_split" : "fp8_moe_wide";
+}
+
 struct MoeLayout {
     Fp8MoePlan plan;
     size_t h, table, pairs, counters, partial, total;
@@ -302,7 +312,7 @@ LLMINT8_API int fp8_moe_block(const void* X, int64_t T, int64_t H, int dtype, co
                        {W2q, e * code_bytes(H, I)},
                        {w2_scale, e * scale_bytes(ceil_div(H, 128), I)}};
     if (clash(r, 4, 10)) return LLMINT8_EINVAL;
-    log_call("fp8_moe_block", T, H, I, dtype, NAN, "fp8_moe");
+    log_call("fp8_moe_block", T, H, I, dtype, NAN, moe_plan_name(L.plan));
     uint8_t* ws = (uint8_t*)workspace;
     const Fp8MoeArgs a{(const uint16_t*)X, T, H, logits, E, (int)top_k, renormalize != 0, W13q, w13_scale, W2q, w2_scale,
                        I, (uint16_t*)Y, topk_ids, topk_weights, (uint16_t*)(ws + L.h), (int32_t*)(ws + L.table),

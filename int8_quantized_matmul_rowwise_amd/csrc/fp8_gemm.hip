@@ -23,6 +23,10 @@
 // one byte for all of a wave's columns.
 // Persistent over the XCD's run of tiles, as the int8 product kernels: the next tile's first
 // loads are in flight during a tile's last stages and its output.
+// 4096 x 12288 x 36864: 1255 us, 2.95 PFLOP/s (the matrix units busy 75 % of the cycles at the 1.66 GHz
+// that the power leaves; a register-only loop of the instruction on random operands reaches 4.3);
+// 2048 x 4096 x 16384: 103 us, 2.67 PFLOP/s.  Weight gradient of that size: 118 us, 2.33 PFLOP/s: tiles of 16
+// stages, whose output (4 us, as all units write at once) the next tile does not hide.
 #include <type_traits>
 
 #include "fp8_common.hpp"
@@ -664,6 +668,8 @@ hipError_t single(const Fp8GemmArgs& a, int split, hipStream_t stream) {
 // launch and the round trip of a separate coding pass while there are few rows.
 // With few columns the groups are split over `split` workgroups too (grid.y, `part` groups each):
 // their sums go through memory and the last one adds them up in their order.
+// 16 x 8192 x 8192: 18.2 us, 3.7 TB/s; 1 x 4096 x 4096 (FUSED) 6.0 us, 2.8 TB/s, of which about 3 us are
+// the launch and the first load's way.
 template <int DT, int MG, int NF, int WV, bool FUSED, int U, int OCC>
 __global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, int split, int part) {
     static_assert(!FUSED || MG == 1, "one piece of rows");
@@ -862,12 +868,21 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb) {
     // are shared, catch up: 64 x 16384 x 4096 38.1 us, in a tile's kernel 25.9, 48 x 8192 x 8192 24.0 and
     // 22.7; 64 x 4096 x 4096 11.4 and 13.7, 32 x 16384 x 4096 24.3 and 25.7.
     if (!rowb && (M <= 32 || (M <= 64 && N * nk <= (int64_t)1 << 17))) {
-        const bool fused = x16 && M <= 4 && N * nk <= (int64_t)1 << 17;
+        // A coded in the kernel, or by a launch before it (every workgroup codes the rows that it
+        // multiplies): 1 x 4096 x 4096 6.7 and 7.9 us, 4 x 4096 x 8192 11.5 and 12.5, 4 x 8192 x 8192 18.9
+        // and 17.5; not where a long sum wants parts (1 x 16384 x 1024: 12.9 us, in parts 11.4).
+        const bool fused = x16 && M <= 4 && N * nk <= (int64_t)1 << 18 && (N >= 2048 || nk < 64);
         p.kind = fused ? Fp8Plan::kFused : Fp8Plan::kSmall;
         p.pieces = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
-        p.columns = fused || N < 8192 ? 1 : (p.pieces == 2 && N >= 12288 ? 4 : (p.pieces == 1 && N < 12288 ? 1 : 2));
+        // Pieces of 16 columns of a workgroup, while enough workgroups are left: 16 x 4096 x 4096 6.9 us with
+        // one, 7.7 with two, 16 x 8192 x 8192 18.4 and 19.4, 16 x 4096 x 8192 11.4 and 8.8, 16 x 4096 x
+        // 12288 16.1 and 15.0; 32 x 4096 x 8192 14.3, 10.4 and (four) 13.7, 32 x 4096 x 12288 20.6, 18.5, 15.2.
+        if (fused || N < 8192 || (p.pieces == 1 && N < 12288 && nk >= 64)) p.columns = 1;
+        else p.columns = p.pieces == 2 && N >= 12288 ? 4 : 2;
         p.tiles = ceil_div(N, 16 * p.columns);
-        if (!fused && p.tiles < 128) p.split = parts(nk, 256 / p.tiles, 8);
+        // Parts of the sum where columns alone leave units idle: 16 x 16384 x 1024 16.4 us, 8.9 in 4 parts;
+        // 64 x 4096 x 2048 11.3 and (2) 9.1; 16 x 4096 x 2048 5.8 and 5.9.
+        if (!fused && (p.tiles < 128 || (p.tiles == 128 && p.pieces > 1))) p.split = parts(nk, 256 / p.tiles, 8);
         out = 256 * p.columns * p.pieces;
     } else {
         const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256), t128 = ceil_div(M, 128) * ceil_div(N, 128);

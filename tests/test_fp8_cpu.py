@@ -137,6 +137,48 @@ def test_stages_and_their_failures(name, monkeypatch, capfd):
         assert run(st) == (lm.EHIP, want[: i + 1])
 
 
+@pytest.mark.parametrize("M,K,N,path", [
+    (1, 16, 8, "fp8_small_fused"), (4, 4096, 8192, "fp8_small_fused"), (5, 4096, 8192, "fp8_small"),
+    (1, 16384, 1024, "fp8_small_split"), (32, 4096, 4096, "fp8_small"), (33, 4096, 4096, "fp8_small"),
+    (33, 8192, 4096, "fp8_single_split"), (65, 128, 8, "fp8_single"), (100, 4240, 264, "fp8_single_split"),
+    (2048, 2048, 2048, "fp8_single"), (2048, 272, 2056, "fp8_tile128"), (4096, 4096, 2048, "fp8_tile128"),
+    (4104, 4096, 2048, "fp8_tile256"), (1200, 12304, 4104, "fp8_tile256_split"), (1200, 12160, 4104, "fp8_tile128"),
+])
+def test_routes(M, K, N, path, monkeypatch, capfd):
+    monkeypatch.setenv("LLMINT8_LOG", "1")
+    monkeypatch.setenv("LLMINT8_FAULT", "no_such_stage")
+    capfd.readouterr()
+    far = 1 << 44  # addresses that nothing reads
+    assert lm.lib().fp8_matmul_block(far, M, K, 0, 2 * far, 3 * far, N, 4 * far, 5 * far, 1 << 40, None) == lm.OK
+    assert re.findall(r"path=(\w+)", capfd.readouterr().err) == [path]
+    assert lm.fp8_matmul_block_workspace_bytes(M, K, N) < 1 << 30
+
+
+@pytest.mark.parametrize("T,H,I,E,k,path", [
+    (1, 2048, 768, 64, 8, "fp8_moe_light"), (3, 272, 1040, 600, 4, "fp8_moe_light_split"),
+    (8, 4096, 1024, 256, 8, "fp8_moe_light_wide"), (8, 4096, 14336, 8, 2, "fp8_moe_wide"),
+    (128, 144, 272, 16, 2, "fp8_moe_wide_split"), (2, 64, 4224, 520, 16, "fp8_moe_wide_light_split"),
+    (40, 144, 272, 9, 4, "fp8_moe_wide"), (60, 4112, 2064, 8, 2, "fp8_moe_many_split"),
+    (128, 2064, 1040, 30, 6, "fp8_moe_many_split"), (20, 32768, 2064, 1, 1, "fp8_moe_many"),
+])
+def test_moe_routes(T, H, I, E, k, path, monkeypatch, capfd):
+    monkeypatch.setenv("LLMINT8_LOG", "1")
+    monkeypatch.setenv("LLMINT8_FAULT", "no_such_stage")
+    capfd.readouterr()
+    far = 1 << 44  # addresses that nothing reads
+    assert lm.lib().fp8_moe_block(far, T, H, 0, 2 * far, E, k, 1, 3 * far, 4 * far, 5 * far, 6 * far, I, 7 * far,
+                                  8 * far, 9 * far, 10 * far, 1 << 40, None) == lm.OK
+    assert re.findall(r"path=(\w+)", capfd.readouterr().err) == [path]
+
+
+def test_moe_workspace_of_every_size():
+    for T in (0, 1, 2, 16, 17, 33, 128):
+        for E, k in ((1, 1), (2, 2), (8, 2), (16, 16), (1024, 16)):
+            for H, I in ((0, 16), (16, 0), (16, 16), (4112, 2064), (1 << 22, 16)):
+                n = lm.fp8_moe_block_workspace_bytes(T, H, I, E, k)
+                assert 0 <= n <= 16 * T * k * (I + 256) + 64 * T * (H + 256) + 64 * H + (1 << 20), (T, H, I, E, k)
+
+
 def test_binding_refuses_what_is_not_on_the_gpu():
     x = torch.zeros(4, 64, dtype=torch.float16)
     with pytest.raises(TypeError):

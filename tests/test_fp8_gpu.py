@@ -107,8 +107,13 @@ SHAPES = [(1, 16, 8), (1, 4096, 264), (3, 144, 1032), (16, 272, 520), (17, 1040,
           (100, 4240, 264), (300, 8208, 520), (260, 4240, 2056), (6, 1040, 16392), (4, 16400, 8200)]
 
 
+# the persistent tiled kernels: tiles of 128, of 256 (one and several a workgroup, odd and even counts
+# of groups), and tiles of 256 whose sums are split
+LARGE = [(2048, 272, 2056), (2400, 272, 4360), (4100, 144, 4360), (4100, 400, 4360), (1200, 12304, 4104)]
+
+
 @pytest.mark.parametrize("dt", DTS)
-@pytest.mark.parametrize("M,K,N", SHAPES)
+@pytest.mark.parametrize("M,K,N", SHAPES + LARGE)
 def test_matmul_exact_lattice(M, K, N, dt):
     print(f"\n[case] matmul lattice {dt} {M}x{K}x{N}", flush=True)
     g = gen(M + K + N)
@@ -237,8 +242,12 @@ def test_matmul_writes_its_output_alone(M, K, N):
 BACK = [(40, 264 * 16, 136), (2100, 272, 264), (300, 272, 4360), (24, 400, 6152), (1, 16, 8), (5, 144, 136), (128, 256, 128), (130, 272, 264), (333, 1040, 520), (64, 2064, 72), (700, 400, 1288)]
 
 
+# (as above; the last one's weight gradient splits tiles of 256, the one before splits tiles of 128)
+LARGE_BACK = [(200, 2064, 2056), (300, 4112, 4104), (5000, 144, 264), (12300, 2064, 2056)]
+
+
 @pytest.mark.parametrize("dt", DTS)
-@pytest.mark.parametrize("M,K,N", BACK)
+@pytest.mark.parametrize("M,K,N", BACK + LARGE_BACK)
 def test_backward_exact_lattice(M, K, N, dt):
     print(f"\n[case] backward lattice {dt} {M}x{K}x{N}", flush=True)
     g = gen(M + K + N)
@@ -401,7 +410,8 @@ def test_moe_masks_ties_and_odd_logits(T, dt):
 
 # many tokens an expert in a large layer: two and four pieces of 16 tokens, up to 64 tokens and more
 @pytest.mark.parametrize("T,H,I,E,k,dt", [(60, 4112, 2064, 8, 2, DTS[0]), (64, 4112, 2064, 8, 5, DTS[1]),
-                                          (128, 4112, 2064, 8, 2, DTS[0]), (128, 2064, 1040, 30, 6, DTS[1])])
+                                          (128, 4112, 2064, 8, 2, DTS[0]), (128, 2064, 1040, 30, 6, DTS[1]),
+                                          (20, 32768, 2064, 1, 1, DTS[1])])
 def test_moe_many_tokens(T, H, I, E, k, dt):
     print(f"\n[case] moe many {dt} T={T} H={H} I={I} E={E} k={k}", flush=True)
     g = gen(T + H + E)
