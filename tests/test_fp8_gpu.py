@@ -516,3 +516,69 @@ def test_on_another_stream():
     for o in outs:
         assert torch.equal(o, want)
     assert torch.cuda.current_stream() != side
+
+
+# ---- calls whose sums are split over workgroups: what the workspace held before, graphs that share
+# one, calls at the same time with one each
+
+def split_call(op, sizes):
+    """f(workspace) -> outputs, and the workspace's bytes"""
+    g = gen(sum(sizes))
+    dt = torch.bfloat16
+    if op == "moe":
+        T, H, I, E, k = sizes
+        X, l, w = randn(g, T, H).to(dt).cuda(), (2 * randn(g, T, E)).cuda(), experts(g, E, H, I, dt)
+        return (lambda ws: lm.fp8_moe_block(X, l, *w, top_k=k, workspace=ws)), lm.fp8_moe_block_workspace_bytes(T, H, I, E, k)
+    M, K, N = sizes
+    X, W = randn(g, M, K).to(dt).cuda(), randn(g, K, N).to(dt).cuda()
+    Wq, s, WqT, sT = lm.fp8_quantize_weight_block(W, transposed=True)
+    if op == "matmul":
+        return (lambda ws: (lm.fp8_matmul_block(X, Wq, s, workspace=ws),)), lm.fp8_matmul_block_workspace_bytes(M, K, N)
+    dY = randn(g, M, N).to(dt).cuda()
+    return (lambda ws: lm.fp8_matmul_block_backward(dY, X, WqT, sT, workspace=ws)), lm.fp8_matmul_block_backward_workspace_bytes(M, K, N)
+
+
+@pytest.mark.parametrize("op,sizes", [
+    ("matmul", (16, 4240, 264)), ("matmul", (100, 4240, 264)), ("matmul", (300, 8208, 520)), ("matmul", (1200, 12304, 4104)),
+    ("backward", (5000, 144, 264)), ("backward", (130, 272, 8200)), ("moe", (70, 272, 144, 64, 5)), ("moe", (128, 144, 272, 16, 2)),
+    ("moe", (2, 64, 4224, 520, 16)), ("moe", (60, 4112, 2064, 8, 2)),
+])
+def test_split_sums_and_their_workspaces(op, sizes):
+    print(f"\n[case] split {op} {sizes}", flush=True)
+    f, nb = split_call(op, sizes)
+    want = f(None)
+    ws, whole = framed((nb,), torch.uint8, 90)
+    for fill in (255, 0, 129):
+        ws.fill_(fill)
+        for a, b in zip(f(ws), want):
+            assert torch.equal(a, b), fill
+    assert frame_untouched(whole, nb, 90)
+    # two graphs with one workspace, replayed in turn
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = f(ws)
+        graphs.append((graph, out))
+    for r in range(3):
+        ws.fill_(255)
+        for graph, out in graphs:
+            for t in out:
+                t.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            for a, b in zip(out, want):
+                assert torch.equal(a, b), r
+    # two streams at once, a workspace each
+    sides = [(torch.cuda.Stream(), torch.full((nb,), 255, dtype=torch.uint8, device="cuda")) for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(6):
+        for side, own in sides:
+            with torch.cuda.stream(side):
+                outs.append(f(own))
+    torch.cuda.synchronize()
+    for out in outs:
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
