@@ -29,7 +29,7 @@
 // layers with several pieces 128 columns that share the tokens' values in LDS.
 //
 // Read at: 8 tokens, 8 experts of 4096 x 14336, top 2: 165 and 91 us, 5.4 TB/s; 37 tokens, 60 experts of
-// 2064 x 1424, top 4: 78 and 57 us, 3.6 TB/s; one token, 64 experts of 2048 x 768, top 8: 10 and 6.8 us
+// 2064 x 1424, top 4: 78 and 53 us, 3.7 TB/s; one token, 64 experts of 2048 x 768, top 8: 10 and 6.8 us
 // (2.2 TB/s: the two launches' latencies).
 #include <cmath>
 
@@ -608,29 +608,56 @@ __global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8
     }
 }
 
-// The end of the second launch: a block of 4 Q columns of every token, the waves' sums in their
-// order; with several parts (grid.y) theirs go through memory, and the last adds them up in their
-// order.
+// ---- the second launch's work: blocks of columns, each of `steps` steps, one block after the other
+// split evenly over the workgroups: each takes a run of steps, whole blocks and parts of its first
+// and last.  With as many workgroups as blocks a run is a block.
+struct Runs {
+    int64_t steps, total, groups;
+    int64_t from, to;  // this workgroup's
+
+    __device__ __forceinline__ void set(int64_t blocks, int64_t n) {
+        steps = n;
+        total = blocks * n;
+        groups = gridDim.x < total ? gridDim.x : total;  // (none without a step: the shares of a block are counted)
+        from = start(blockIdx.x);
+        to = start(blockIdx.x + 1);
+    }
+    __device__ __forceinline__ int64_t start(int64_t group) const {
+        if (group >= groups) return total;
+        return groups * steps == total ? group * steps : total * group / groups;
+    }
+    __device__ __forceinline__ int64_t owner(int64_t step) const { return ((step + 1) * groups - 1) / total; }
+};
+
+// The end of a run's share of a block of 4 Q columns: of every token the waves' sums in their order.
+// A block of several shares has those go through memory (`most` places a block), and the last one to
+// end adds them up in their order.
 template <int DT, int Q, int MAXT, int WV>
-__device__ __forceinline__ void put_tokens(const Fp8MoeArgs& p, const v4f (&ysum)[WV][MAXT][Q]) {
-    __shared__ int flag;
-    const int n = (int)p.T * Q, parts = gridDim.y;
+__device__ __forceinline__ void put_tokens(const Fp8MoeArgs& p, const v4f (&ysum)[WV][MAXT][Q], const Runs& runs, int block,
+                                           bool whole, int most, int* flag) {
+    const int n = (int)p.T * Q;
     auto store = [&](int i, const v4f& y) LLMINT8_MOE_INLINE {
         u32x2 o;
         o[0] = (uint32_t)from_f32<DT>(y[0]) | ((uint32_t)from_f32<DT>(y[1]) << 16);
         o[1] = (uint32_t)from_f32<DT>(y[2]) | ((uint32_t)from_f32<DT>(y[3]) << 16);
-        *(u32x2*)(p.Y + (int64_t)(i / Q) * p.H + (int64_t)blockIdx.x * (4 * Q) + 4 * (i % Q)) = o;
+        *(u32x2*)(p.Y + (int64_t)(i / Q) * p.H + (int64_t)block * (4 * Q) + 4 * (i % Q)) = o;
     };
-    const __amdgpu_buffer_rsrc_t rp = buffer_rsrc(p.partial + (int64_t)blockIdx.x * parts * n * 4, (int64_t)parts * n * 16);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += 64 * WV) {
+    auto sum = [&](int i) LLMINT8_MOE_INLINE {
         v4f y = ysum[0][i / Q][i % Q];
 #pragma unroll
         for (int v = 1; v < WV; ++v) y += ysum[v][i / Q][i % Q];
-        if (parts == 1) store(i, y);
-        else store_part(rp, 16 * i, 16 * n * blockIdx.y, y);
+        return y;
+    };
+    __syncthreads();
+    if (whole) {
+        for (int i = threadIdx.x; i < n; i += 64 * WV) store(i, sum(i));
+        return;
     }
-    if (parts == 1 || !last_part(p.counters + blockIdx.x, parts, &flag)) return;
+    const int first = (int)runs.owner(block * runs.steps), parts = (int)runs.owner(block * runs.steps + runs.steps - 1) - first + 1;
+    const __amdgpu_buffer_rsrc_t rp = buffer_rsrc(p.partial + (int64_t)block * most * n * 4, (int64_t)most * n * 16);
+    const int own = __builtin_amdgcn_readfirstlane(16 * n * ((int)blockIdx.x - first));
+    for (int i = threadIdx.x; i < n; i += 64 * WV) store_part(rp, 16 * i, own, sum(i));
+    if (!last_part(p.counters + block, parts, flag)) return;
     for (int i = threadIdx.x; i < n; i += 64 * WV) {
         v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int v = 0; v < parts; ++v) y += load_part(rp, 16 * i, 16 * n * v);
@@ -638,20 +665,20 @@ __device__ __forceinline__ void put_tokens(const Fp8MoeArgs& p, const v4f (&ysum
     }
 }
 
-// ---- down and the weighted sum: a workgroup takes 16 columns of H of all entries.  Their groups
-// of I, entry after entry, are split evenly over the waves and run through D sets of registers;
+// ---- down and the weighted sum: blocks of 16 columns of H, all entries.  A share's groups of I,
+// entry after entry, are split evenly over the waves and run through D sets of registers;
 // a wave ends an entry (or its share of it) by adding p times its sums to its own rows of token
 // sums in LDS.
 template <int DT, int MG, int MAXT, int WV>
-__global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
+__global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p, int blocks, int most) {
     constexpr int D = MG == 1 ? (WV == 8 ? 4 : 3) : 2, MAXN = MAXT * kMaxTopK;
     __shared__ v4f ysum[WV][MAXT][4];  // a wave's sums of 16 columns per token
     __shared__ int32_t table[3 * MAXN], pairs[MAXN];
     __shared__ float weights[MAXN];
+    __shared__ int flag;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, q = lane >> 4;
     const int T = (int)p.T, k = p.k, n = T * k;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int64_t ip = fp8_pitch(p.I), isp = fp8_scale_pitch_of(p.I);
     const int ng = (int)(ip / 128);
     const int entries = __builtin_amdgcn_readfirstlane(p.table[0]);
@@ -660,103 +687,112 @@ __global__ __launch_bounds__(64 * WV) void moe_down_kernel(Fp8MoeArgs p) {
         pairs[i] = p.pairs[i];
         weights[i] = p.weights[i];
     }
-    for (int i = tid; i < WV * T * 4; i += 64 * WV) ysum[i / (4 * T)][(i >> 2) % T][i & 3] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    __syncthreads();
-    const int total = entries * ng, shares = WV * (int)gridDim.y, share = (int)blockIdx.y * WV + w;
-    const int from = (int)((int64_t)total * share / shares), to = (int)((int64_t)total * (share + 1) / shares);
-    if (from < to) {
-        const uint32_t w_off = (uint32_t)(li * ip + 16 * q);
-        const int64_t h_bytes = (int64_t)n * ip * 2;
-        const int64_t scale_rows = ceil_div(p.H, 128);
-        struct Group {
-            u32x4 w[2], x[MG][4];
-            Scale s;
-        };
-        // the next load's entry and group, and that entry's expert and rows of h
-        int le = from / ng, lg = from - le * ng, expert = 0, left = to - from;
-        uint32_t h_off[MG];
-        auto open = [&]() LLMINT8_MOE_INLINE {
-            if (le >= entries) return;
-            expert = __builtin_amdgcn_readfirstlane(table[3 * le]);
-            const int first = table[3 * le + 1], count = table[3 * le + 2];
+    Runs runs;
+    runs.set(blocks, entries * ng > 0 ? entries * ng : 1);
+    for (int64_t at = runs.from; at < runs.to;) {
+        const int block = __builtin_amdgcn_readfirstlane((int)(at / runs.steps));
+        const int64_t ends = (block + 1) * runs.steps < runs.to ? (block + 1) * runs.steps : runs.to;
+        const int begin = __builtin_amdgcn_readfirstlane((int)(at - block * runs.steps)), end = __builtin_amdgcn_readfirstlane((int)(ends - block * runs.steps));
+        at = ends;
+        const int64_t n0 = 16 * (int64_t)block;
+        for (int i = tid; i < WV * T * 4; i += 64 * WV) ysum[i / (4 * T)][(i >> 2) % T][i & 3] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        __syncthreads();
+        const int from = begin + (int)((int64_t)(end - begin) * w / WV), to = begin + (int)((int64_t)(end - begin) * (w + 1) / WV);
+        if (from < to && entries * ng > 0) {
+            const uint32_t w_off = (uint32_t)(li * ip + 16 * q);
+            const int64_t h_bytes = (int64_t)n * ip * 2;
+            const int64_t scale_rows = ceil_div(p.H, 128);
+            struct Group {
+                u32x4 w[2], x[MG][4];
+                Scale s;
+            };
+            // the next load's entry and group, and that entry's expert and rows of h
+            int le = from / ng, lg = from - le * ng, expert = 0, left = to - from;
+            uint32_t h_off[MG];
+            auto open = [&]() LLMINT8_MOE_INLINE {
+                if (le >= entries) return;
+                expert = __builtin_amdgcn_readfirstlane(table[3 * le]);
+                const int first = table[3 * le + 1], count = table[3 * le + 2];
 #pragma unroll
-            for (int j = 0; j < MG; ++j) {
-                const int i = 16 * j + li;
-                h_off[j] = i < count ? (uint32_t)(pairs[first + i] * ip + 16 * q) * 2 : kFar;
-            }
-        };
-        auto load = [&](Group& r) LLMINT8_MOE_INLINE {
-            const bool in = left > 0;  // past the share: zeros
-            const int g = in ? lg : 0;  // (an empty resource takes no scalar offset: the check subtracts it)
-            const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(p.W2 + ((int64_t)expert * p.H + n0) * ip, in ? 16 * ip : 0);
-            const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, in ? h_bytes : 0);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) r.w[h] = load16(rw, w_off + 64 * h, g * 128);
-#pragma unroll
-            for (int j = 0; j < MG; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r.x[j][i] = load16(rh, h_off[j] + 128 * (i >> 1) + 16 * (i & 1), g * 256);
-            r.s = load_scale(p.s2 + (expert * scale_rows + (n0 >> 7)) * isp, lg);
-            __builtin_amdgcn_sched_barrier(0);  // as above
-            --left;
-            if (++lg == ng) {
-                lg = 0;
-                ++le;
-                open();
-            }
-        };
-        v4f acc[MG] = {};
-        int ce = le, cg = lg;  // the entry and group being multiplied
-        auto flush = [&]() LLMINT8_MOE_INLINE {
-            mfma_settle();
-            const int first = table[3 * ce + 1], count = table[3 * ce + 2];
-#pragma unroll
-            for (int j = 0; j < MG; ++j) {
-                const int i = 16 * j + li;
-                if (i < count) {
-                    const int pair = pairs[first + i];
-                    const float pt = weights[pair];
-                    v4f y = ysum[w][pair / k][q];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(pt, acc[j][r], y[r]);
-                    ysum[w][pair / k][q] = y;
+                for (int j = 0; j < MG; ++j) {
+                    const int i = 16 * j + li;
+                    h_off[j] = i < count ? (uint32_t)(pairs[first + i] * ip + 16 * q) * 2 : kFar;
                 }
-                acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-            }
-        };
-        Group r[D];
-        open();
+            };
+            auto load = [&](Group& r) LLMINT8_MOE_INLINE {
+                const bool in = left > 0;  // past the share: zeros
+                const int g = in ? lg : 0;  // (an empty resource takes no scalar offset: the check subtracts it)
+                const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(p.W2 + ((int64_t)expert * p.H + n0) * ip, in ? 16 * ip : 0);
+                const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, in ? h_bytes : 0);
 #pragma unroll
-        for (int d = 0; d < D; ++d) load(r[d]);
-        const int steps = to - from;
-        for (int s = 0; s < steps; s += D) {  // whole rounds, as above
+                for (int h = 0; h < 2; ++h) r.w[h] = load16(rw, w_off + 64 * h, g * 128);
 #pragma unroll
-            for (int d = 0; d < D; ++d) {
-                group_product<DT, MG>(r[d].w, scale_here(r[d].s), r[d].x, acc);
-                load(r[d]);
-                if (s + d < steps && (++cg == ng || s + d + 1 == steps)) {
-                    flush();
-                    cg = 0;
-                    ++ce;
+                for (int j = 0; j < MG; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r.x[j][i] = load16(rh, h_off[j] + 128 * (i >> 1) + 16 * (i & 1), g * 256);
+                r.s = load_scale(p.s2 + (expert * scale_rows + (n0 >> 7)) * isp, lg);
+                __builtin_amdgcn_sched_barrier(0);  // as above
+                --left;
+                if (++lg == ng) {
+                    lg = 0;
+                    ++le;
+                    open();
+                }
+            };
+            v4f acc[MG] = {};
+            int ce = le, cg = lg;  // the entry and group being multiplied
+            auto flush = [&]() LLMINT8_MOE_INLINE {
+                mfma_settle();
+                const int first = table[3 * ce + 1], count = table[3 * ce + 2];
+#pragma unroll
+                for (int j = 0; j < MG; ++j) {
+                    const int i = 16 * j + li;
+                    if (i < count) {
+                        const int pair = pairs[first + i];
+                        const float pt = weights[pair];
+                        v4f y = ysum[w][pair / k][q];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(pt, acc[j][r], y[r]);
+                        ysum[w][pair / k][q] = y;
+                    }
+                    acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                }
+            };
+            Group r[D];
+            open();
+#pragma unroll
+            for (int d = 0; d < D; ++d) load(r[d]);
+            const int steps = to - from;
+            for (int s = 0; s < steps; s += D) {  // whole rounds, as above
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    group_product<DT, MG>(r[d].w, scale_here(r[d].s), r[d].x, acc);
+                    load(r[d]);
+                    if (s + d < steps && (++cg == ng || s + d + 1 == steps)) {
+                        flush();
+                        cg = 0;
+                        ++ce;
+                    }
                 }
             }
         }
+        put_tokens<DT, 4, MAXT, WV>(p, ysum, runs, block, end - begin == runs.steps, most, &flag);
+        __syncthreads();  // before the sums are cleared
     }
-    put_tokens<DT, 4, MAXT, WV>(p, ysum);
 }
 
 // ---- the same in the light form: 8 columns of H, two entries (of up to 8 tokens) at a time, the
 // even one in rows and columns 0 .. 7 of the instruction, the odd one in 8 .. 15.
 template <int DT, int MAXT, int WV, int C, int D>
-__global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
+__global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p, int blocks, int most) {
     constexpr int MAXN = MAXT * kMaxTopK;
     __shared__ v4f ysum[WV][MAXT][2];  // a wave's sums of 8 columns per token
     __shared__ int32_t table[3 * MAXN], pairs[MAXN];
     __shared__ float weights[MAXN];
+    __shared__ int flag;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, q = lane >> 4, half = li >> 3;
     const int T = (int)p.T, k = p.k, n = T * k;
-    const int64_t n0 = (int64_t)blockIdx.x * 8;
     const int64_t ip = fp8_pitch(p.I), isp = fp8_scale_pitch_of(p.I);
     const int ng = (int)(ip / 128);
     const int entries = __builtin_amdgcn_readfirstlane(p.table[0]), twos = (entries + 1) / 2;
@@ -765,98 +801,107 @@ __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p) {
         pairs[i] = p.pairs[i];
         weights[i] = p.weights[i];
     }
-    for (int i = tid; i < WV * T * 2; i += 64 * WV) ysum[i / (2 * T)][(i >> 1) % T][i & 1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    __syncthreads();
-    // this part's steps (groups of I, two entries after two entries) go round the waves C at a time,
-    // so that what the workgroup reads at a time lies together
-    const int begin = (int)((int64_t)twos * ng * blockIdx.y / gridDim.y), end = (int)((int64_t)twos * ng * (blockIdx.y + 1) / gridDim.y);
-    const int total = end - begin, round = WV * C, own = total - total / round * round - w * C;
-    const int steps = total / round * C + (own < 0 ? 0 : (own < C ? own : C));
-    if (steps > 0) {
-        const int64_t h_bytes = (int64_t)n * ip * 2;
-        const int64_t scale_rows = ceil_div(p.H, 128);
-        struct Group {
-            u32x4 w[2], x[1][4];
-            Scale s;
-        };
-        // the next load's two entries and group; of this lane's entry its row of W2, its scales
-        // and its token's row of h (an odd count: the last entry's weights times zeros)
-        struct At {
-            int two, g, c;  // the entries, the group, the place among C
-            __device__ __forceinline__ bool next(int ng) {  // true: other entries
-                const int was = two;
-                g += ++c == C ? (WV - 1) * C + 1 : 1;
-                c = c == C ? 0 : c;
-                while (g >= ng) {
-                    g -= ng;
-                    ++two;
+    Runs runs;
+    runs.set(blocks, twos * ng > 0 ? twos * ng : 1);
+    for (int64_t run = runs.from; run < runs.to;) {
+        const int block = __builtin_amdgcn_readfirstlane((int)(run / runs.steps));
+        const int64_t ends = (block + 1) * runs.steps < runs.to ? (block + 1) * runs.steps : runs.to;
+        const int begin = __builtin_amdgcn_readfirstlane((int)(run - block * runs.steps)), end = __builtin_amdgcn_readfirstlane((int)(ends - block * runs.steps));
+        run = ends;
+        const int64_t n0 = 8 * (int64_t)block;
+        for (int i = tid; i < WV * T * 2; i += 64 * WV) ysum[i / (2 * T)][(i >> 1) % T][i & 1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        __syncthreads();
+        // this share's steps (groups of I, two entries after two entries) go round the waves C at a time,
+        // so that what the workgroup reads at a time lies together
+        const int total = end - begin, round = WV * C, own = total - total / round * round - w * C;
+        const int steps = total / round * C + (own < 0 ? 0 : (own < C ? own : C));
+        if (steps > 0 && twos * ng > 0) {
+            const int64_t h_bytes = (int64_t)n * ip * 2;
+            const int64_t scale_rows = ceil_div(p.H, 128);
+            struct Group {
+                u32x4 w[2], x[1][4];
+                Scale s;
+            };
+            // the next load's two entries and group; of this lane's entry its row of W2, its scales
+            // and its token's row of h (an odd count: the last entry's weights times zeros)
+            struct At {
+                int two, g, c;  // the entries, the group, the place among C
+                __device__ __forceinline__ bool next(int ng) {  // true: other entries
+                    const int was = two;
+                    g += ++c == C ? (WV - 1) * C + 1 : 1;
+                    c = c == C ? 0 : c;
+                    while (g >= ng) {
+                        g -= ng;
+                        ++two;
+                    }
+                    return two != was;
                 }
-                return two != was;
-            }
-        };
-        At l{(begin + w * C) / ng, (begin + w * C) % ng, 0}, m = l;  // of the next load, and of the next product
-        int left = steps;
-        const uint8_t *row = nullptr, *scales = nullptr;
-        uint32_t h_off = kFar;
-        auto open = [&]() LLMINT8_MOE_INLINE {
-            const int mine = 2 * l.two + half, at = mine < entries ? mine : entries - 1;
-            const int e = table[3 * at], first = table[3 * at + 1], count = mine < entries ? table[3 * at + 2] : 0;
-            row = p.W2 + ((int64_t)e * p.H + n0 + (li & 7)) * ip + 16 * q;
-            scales = p.s2 + (e * scale_rows + (n0 >> 7)) * isp;
-            h_off = (li & 7) < count ? (uint32_t)(pairs[first + (li & 7)] * ip + 16 * q) * 2 : kFar;
-        };
-        auto load = [&](Group& r) LLMINT8_MOE_INLINE {
-            const uint8_t* from = row + l.g * 128;
-            r.w[0] = *(const u32x4*)from;
-            r.w[1] = *(const u32x4*)(from + 64);
-            const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, left > 0 ? h_bytes : 0);  // past the share: zeros
+            };
+            At l{(begin + w * C) / ng, (begin + w * C) % ng, 0}, m = l;  // of the next load, and of the next product
+            int left = steps;
+            const uint8_t *row = nullptr, *scales = nullptr;
+            uint32_t h_off = kFar;
+            auto open = [&]() LLMINT8_MOE_INLINE {
+                const int mine = 2 * l.two + half, at = mine < entries ? mine : entries - 1;
+                const int e = table[3 * at], first = table[3 * at + 1], count = mine < entries ? table[3 * at + 2] : 0;
+                row = p.W2 + ((int64_t)e * p.H + n0 + (li & 7)) * ip + 16 * q;
+                scales = p.s2 + (e * scale_rows + (n0 >> 7)) * isp;
+                h_off = (li & 7) < count ? (uint32_t)(pairs[first + (li & 7)] * ip + 16 * q) * 2 : kFar;
+            };
+            auto load = [&](Group& r) LLMINT8_MOE_INLINE {
+                const uint8_t* from = row + l.g * 128;
+                r.w[0] = *(const u32x4*)from;
+                r.w[1] = *(const u32x4*)(from + 64);
+                const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(p.h, left > 0 ? h_bytes : 0);  // past the share: zeros
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r.x[0][i] = load16(rh, h_off + 128 * (i >> 1) + 16 * (i & 1), l.g * 256);
-            r.s = load_scale(scales, l.g);
-            __builtin_amdgcn_sched_barrier(0);  // as above
-            if (--left > 0) {
-                if (l.next(ng)) open();
-            } else {  // from here on one line of weights
-                row = p.W2;
-                l.g = 0;
-            }
-        };
-        v4f acc[1] = {};
-        // The results of an entry's rows with its own tokens; the even entry first, then the odd one:
-        // a token may be in both.
-        auto flush = [&](int two) LLMINT8_MOE_INLINE {
-            mfma_settle();
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int at = 2 * two + t;
-                if (half == t && (q >> 1) == t && at < entries && (li & 7) < table[3 * at + 2]) {
-                    const int pair = pairs[table[3 * at + 1] + (li & 7)];
-                    const float pt = weights[pair];
-                    v4f y = ysum[w][pair / k][q & 1];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(pt, acc[0][r], y[r]);
-                    ysum[w][pair / k][q & 1] = y;
+                for (int i = 0; i < 4; ++i) r.x[0][i] = load16(rh, h_off + 128 * (i >> 1) + 16 * (i & 1), l.g * 256);
+                r.s = load_scale(scales, l.g);
+                __builtin_amdgcn_sched_barrier(0);  // as above
+                if (--left > 0) {
+                    if (l.next(ng)) open();
+                } else {  // from here on one line of weights
+                    row = p.W2;
+                    l.g = 0;
                 }
-            }
-            acc[0] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        };
-        Group r[D];
-        open();
+            };
+            v4f acc[1] = {};
+            // The results of an entry's rows with its own tokens; the even entry first, then the odd one:
+            // a token may be in both.
+            auto flush = [&](int two) LLMINT8_MOE_INLINE {
+                mfma_settle();
 #pragma unroll
-        for (int d = 0; d < D; ++d) load(r[d]);
-        for (int s = 0; s < steps; s += D) {  // whole rounds, as above
+                for (int t = 0; t < 2; ++t) {
+                    const int at = 2 * two + t;
+                    if (half == t && (q >> 1) == t && at < entries && (li & 7) < table[3 * at + 2]) {
+                        const int pair = pairs[table[3 * at + 1] + (li & 7)];
+                        const float pt = weights[pair];
+                        v4f y = ysum[w][pair / k][q & 1];
 #pragma unroll
-            for (int d = 0; d < D; ++d) {
-                group_product<DT, 1>(r[d].w, scale_here(r[d].s), r[d].x, acc);
-                load(r[d]);
-                if (s + d < steps) {
-                    const int two = m.two;
-                    if (m.next(ng) || s + d + 1 == steps) flush(two);
+                        for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(pt, acc[0][r], y[r]);
+                        ysum[w][pair / k][q & 1] = y;
+                    }
+                }
+                acc[0] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            };
+            Group r[D];
+            open();
+#pragma unroll
+            for (int d = 0; d < D; ++d) load(r[d]);
+            for (int s = 0; s < steps; s += D) {  // whole rounds, as above
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    group_product<DT, 1>(r[d].w, scale_here(r[d].s), r[d].x, acc);
+                    load(r[d]);
+                    if (s + d < steps) {
+                        const int two = m.two;
+                        if (m.next(ng) || s + d + 1 == steps) flush(two);
+                    }
                 }
             }
         }
+        put_tokens<DT, 2, MAXT, WV>(p, ysum, runs, block, end - begin == runs.steps, most, &flag);
+        __syncthreads();  // before the sums are cleared
     }
-    put_tokens<DT, 2, MAXT, WV>(p, ysum);
 }
 
 // ---- many tokens an expert (16 MG at a time) in a large layer: there the tokens' values, which every wave of the
@@ -1199,18 +1244,17 @@ hipError_t launch_up(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t st
 
 template <int DT, int MG, bool MANY = false>
 hipError_t launch_down(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream) {
-    const dim3 grid((unsigned)plan.blocks, (unsigned)plan.parts);
+    const int blocks = (int)plan.blocks, most = plan.parts;
     if constexpr (MG == 0) {
-        if (p.T <= 16) moe_down_light_kernel<DT, 16, 8, 3, 2><<<grid, 512, 0, stream>>>(p);
-        else moe_down_light_kernel<DT, 128, 8, 3, 2><<<grid, 512, 0, stream>>>(p);
+        if (p.T <= 16) moe_down_light_kernel<DT, 16, 8, 3, 2><<<plan.groups, 512, 0, stream>>>(p, blocks, most);
+        else moe_down_light_kernel<DT, 128, 8, 3, 2><<<plan.groups, 512, 0, stream>>>(p, blocks, most);
+    } else if constexpr (MANY) {
+        const dim3 grid((unsigned)blocks, (unsigned)plan.parts);
+        if (p.T <= 64) moe_down_many_kernel<DT, MG, 64><<<grid, 512, 0, stream>>>(p);
+        else moe_down_many_kernel<DT, MG, 128><<<grid, 512, 0, stream>>>(p);
     } else {
-        if constexpr (MANY) {
-            if (p.T <= 64) moe_down_many_kernel<DT, MG, 64><<<grid, 512, 0, stream>>>(p);
-            else moe_down_many_kernel<DT, MG, 128><<<grid, 512, 0, stream>>>(p);
-        } else {
-            if (p.T <= 64) moe_down_kernel<DT, MG, 64, 16><<<grid, 1024, 0, stream>>>(p);
-            else moe_down_kernel<DT, MG, 128, 8><<<grid, 512, 0, stream>>>(p);
-        }
+        if (p.T <= 64) moe_down_kernel<DT, MG, 64, 16><<<plan.groups, 1024, 0, stream>>>(p, blocks, most);
+        else moe_down_kernel<DT, MG, 128, 8><<<plan.groups, 512, 0, stream>>>(p, blocks, most);
     }
     return hipGetLastError();
 }
@@ -1231,23 +1275,18 @@ hipError_t moe_launch(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t s
                                : launch_down<DT, 2>(p, plan, stream);
 }
 
-// Parts of the second launch's sum.  A compute unit reads about 20 bytes a nanosecond whether it
-// holds one workgroup or two, so a few workgroups past a multiple of 256 cost as many rounds as
-// a full one; parts even that out, for about 3 us of joining and 1.5 us a round of setting up.  37
-// tokens, 60 experts, top 4: 2064 x 1424 (258 blocks) 77.6 us in one part, 62.8 in 2, 56.9 in 4, 62.7
-// in 8; 2048 x 1408 (256 blocks) 39.9, 42.6, 46.2, 56.2.
-int down_parts(int64_t blocks, int64_t steps) {
-    const int64_t work = steps * 11;  // 10 ns: of one block's steps of 16 rows of 128 bytes
-    int64_t best = 0;
-    int s = 1;
-    for (int64_t i = 1; i <= 8; ++i) {
-        const int64_t rounds = ceil_div(blocks * i, 256), cost = rounds * work / i + 150 * rounds + (i > 1 ? 300 : 0);
-        if (i == 1 || cost < best) {
-            best = cost;
-            s = (int)i;
-        }
-    }
-    return s;
+// Workgroups of the second launch (light or wide).  A compute unit reads about 20 bytes a nanosecond
+// whether it holds one of them or two, so a few blocks past a multiple of 256 would cost a whole round:
+// there 256 workgroups share the blocks' steps evenly; and half as many blocks or fewer are taken in
+// parts.  The estimate, in 10 ns, has 3 us for joining and 1.5 us for setting up a run.  37 tokens, 60
+// experts, top 4: 2064 x 1424 (258 blocks) 78.1 us a block each, shared by 256 53.2, by 512 54.5; 8 tokens,
+// 64 experts of 1024 x 768, top 4 (128 blocks) 11.9 and 11.1; 4 tokens, 64 of 2048 x 768 (256) 12.8.
+unsigned down_groups(int64_t blocks, int64_t steps) {
+    const int64_t work = steps * 11;  // of one block's steps of 16 rows of 128 bytes
+    const int64_t plain = ceil_div(blocks, 256) * (work + 150);
+    if (blocks > 256) return (unsigned)(blocks * work / 256 + 700 < plain ? 256 : blocks);
+    const int64_t parts = blocks > 0 ? 256 / blocks : 1;
+    return (unsigned)(parts > 1 && work / parts + 600 < plain ? blocks * parts : blocks);
 }
 
 }  // namespace
@@ -1275,7 +1314,15 @@ Fp8MoePlan fp8_moe_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
     const int64_t columns = plan.light_down ? 8 : (plan.many ? 128 : 16);
     plan.blocks = ceil_div(H, columns);
     const int64_t met = k == E ? rows : (int64_t)((double)E * -expm1((double)T * log1p(-(double)k / (double)E))) + 1;  // of even choices
-    plan.parts = down_parts(plan.blocks, (plan.light_down ? ceil_div(met, 2) : met) * ceil_div(I, 128) * ceil_div(columns, 16));
+    if (plan.many) {
+        // 128 columns a block and 8 parts of each: 64 tokens, 16 experts of 4096 x 2048 (32 blocks) 39.3 us, in
+        // 4 parts 48.8, in 16 52.6; 100 tokens, 64 experts of 2048 x 768 54.2, 74.2, 59.1; one a unit is enough
+        plan.parts = plan.blocks >= 256 ? 1 : 8;
+        plan.groups = 0;
+    } else {
+        plan.groups = down_groups(plan.blocks, (plan.light_down ? ceil_div(met, 2) : met) * ceil_div(I, 128));
+        plan.parts = plan.groups == plan.blocks ? 1 : (int)(plan.groups / (plan.blocks > 0 ? plan.blocks : 1)) + 2;
+    }
     plan.partial_bytes = plan.parts > 1 ? T * plan.blocks * columns * plan.parts * 4 : 0;
     return plan;
 }

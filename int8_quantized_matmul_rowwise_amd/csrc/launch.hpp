@@ -240,8 +240,10 @@ struct Fp8MoePlan {
     int pieces;  // of 16 tokens multiplied at once: 1, 2 or 4
     bool light_up, light_down, many;
     int chunk;   // tokens of an entry of the second launch
-    int parts;   // of its sum
-    int64_t blocks, partial_bytes;  // its blocks of columns; parts > 1: the partial sums' bytes
+    int64_t blocks;  // of its columns
+    unsigned groups;  // its workgroups, but with `many`: one a block and part
+    int parts;   // of a block's sum, at most
+    int64_t partial_bytes;  // parts > 1: of the partial sums
 };
 Fp8MoePlan fp8_moe_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k);
 
