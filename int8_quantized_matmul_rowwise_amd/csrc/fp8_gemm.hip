@@ -492,7 +492,7 @@ __global__ __launch_bounds__(256, 1) void fp8_single_kernel(TiledParams tp) {
 
     // Stage k, B in slot sb; P = k % 4, the slot of A; TAIL: past the last whole round, where no scales
     // are loaded.  The barrier leaves the loads after the next stage's in flight: B's and A's of two
-    // stages and B's of a third, and this round's scales if they are among them.
+    // stages and B's of a third, and the four stages' scales if they are among them.
     auto stage = [&](auto ptag, auto tail, int sb, int k) LLMINT8_FP8_INLINE {
         constexpr int P = decltype(ptag)::value;
         constexpr bool TAIL = decltype(tail)::value;
