@@ -250,13 +250,11 @@ int check_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
 }
 
 const char* moe_plan_name(const Fp8MoePlan& p) {  // the form of the first launch, then of the second
-    if (p.many) return p.parts > 1 ? "fp8_moe_many_split" : "fp8_moe_many";
-    if (p.light_down) {
-        if (p.light_up) return p.parts > 1 ? "fp8_moe_light_split" : "fp8_moe_light";
-        return p.parts > 1 ? "fp8_moe_wide_light_split" : "fp8_moe_wide_light";
-    }
-    if (p.light_up) return p.parts > 1 ? "fp8_moe_light_wide_split" : "fp8_moe_light_wide";
-    return p.parts > 1 ? "fp8_moe_wide_split" : "fp8_moe_wide";
+    static const char* const names[3][3][2] = {
+        {{"fp8_moe_light", "fp8_moe_light_split"}, {"fp8_moe_light_wide", "fp8_moe_light_wide_split"}, {"fp8_moe_light_many", "fp8_moe_light_many_split"}},
+        {{"fp8_moe_wide_light", "fp8_moe_wide_light_split"}, {"fp8_moe_wide", "fp8_moe_wide_split"}, {"fp8_moe_wide_many", "fp8_moe_wide_many_split"}},
+        {{"fp8_moe_many_light", "fp8_moe_many_light_split"}, {"fp8_moe_many_wide", "fp8_moe_many_wide_split"}, {"fp8_moe_many", "fp8_moe_many_split"}}};
+    return names[p.up][p.down][p.parts > 1];
 }
 
 struct MoeLayout {

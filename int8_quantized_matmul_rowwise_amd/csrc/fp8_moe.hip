@@ -21,12 +21,12 @@
 // bits follow from the inputs alone (where the splits lie depends on the sizes and on the experts
 // that the tokens meet together).
 //
-// Three forms of both launches.  Where experts have few tokens (a mean of kLightMean at most) the
-// work is cut finer, so that small layers fill the compute units: the 16 rows of an instruction
-// are 8 gate and the same 8 up columns in the first launch, and 8 columns of two experts in the
-// second, whose tokens are the two halves of its columns (the products of one expert's rows with
-// the other's tokens are not used).  Otherwise 16 columns and MG pieces of tokens, and in large
-// layers with several pieces 128 columns that share the tokens' values in LDS.
+// Three forms of both launches.  Light: the work is cut finer, so that small layers fill the compute
+// units: the 16 rows of an instruction are 8 gate and the same 8 up columns in the first launch, and
+// 8 columns of two experts in the second, whose tokens are the two halves of its columns (the
+// products of one expert's rows with the other's tokens are not used).  Wide: 16 columns and MG
+// pieces of tokens, the waves splitting the groups.  Many: 128 columns, a tile of 16 to a wave, which
+// share the tokens' values in LDS.
 //
 // Read at: 8 tokens, 8 experts of 4096 x 14336, top 2: 165 and 91 us, 5.4 TB/s; 37 tokens, 60 experts of
 // 2064 x 1424, top 4: 78 and 53 us, 3.7 TB/s; one token, 64 experts of 2048 x 768, top 8: 10 and 6.8 us
@@ -45,7 +45,6 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 16;
 constexpr int kUpWaves = 8, kLightUpWaves = 4;
 constexpr int kRouteTokens = 8, kRouteChoices = 32;
-constexpr int kLightMean = 6;
 
 #define LLMINT8_MOE_INLINE __attribute__((always_inline))
 
@@ -993,12 +992,16 @@ __global__ __launch_bounds__(512, 2) void moe_up_many_kernel(Fp8MoeArgs p, int s
         u32x4 g[2], u[2];
         Scale eg, eu;
     };
+    // Workgroups start at different groups: rows of 4096 bytes have a group's lines in the same few
+    // memory channels.
+    const int g0 = __builtin_amdgcn_readfirstlane((int)((blockIdx.x - 1) * 5 % ng));
+    auto group_at = [&](int s) LLMINT8_MOE_INLINE { return s >= ng ? ng : (s + g0 >= ng ? s + g0 - ng : s + g0); };
     for (int c0 = 0; c0 < count; c0 += 16 * MG) {
         Tokens<MG> tokens;
         tokens.set([&](int t) { return c0 + t < count ? (uint32_t)((list[c0 + t] / p.k) * p.H) * 2 : kFar; }, (int)p.H, ng);
-        auto load_w = [&](Group& r, int g) LLMINT8_MOE_INLINE {
-            const bool in = g < ng && has;  // else zeros
-            const int at = in ? g : 0, bytes = in ? 16 * (int)hp : 0;
+        auto load_w = [&](Group& r, int s) LLMINT8_MOE_INLINE {
+            const bool in = s < ng && has;  // else zeros
+            const int at = in ? group_at(s) : 0, bytes = in ? 16 * (int)hp : 0;
             const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(Wg, bytes), ru = buffer_rsrc(Wu, bytes);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -1009,8 +1012,8 @@ __global__ __launch_bounds__(512, 2) void moe_up_many_kernel(Fp8MoeArgs p, int s
             r.eu = load_scale(rs, su, at);
             __builtin_amdgcn_sched_barrier(0);  // as above
         };
-        auto load_x = [&](int g, int slot) LLMINT8_MOE_INLINE {
-            tokens.load(rx, sh.x[slot], g, ng);
+        auto load_x = [&](int s, int slot) LLMINT8_MOE_INLINE {
+            tokens.load(rx, sh.x[slot], group_at(s), ng);
             __builtin_amdgcn_sched_barrier(0);
         };
         v4f ag[MG] = {}, au[MG] = {};
@@ -1076,7 +1079,7 @@ __global__ __launch_bounds__(512, 2) void moe_down_many_kernel(Fp8MoeArgs p) {
     const int64_t n0 = has ? 128 * (int64_t)blockIdx.x + 16 * w : 0;
     const int64_t ip = fp8_pitch(p.I), isp = fp8_scale_pitch_of(p.I);
     const int ng = (int)(ip / 128);
-    const int entries = __builtin_amdgcn_readfirstlane(p.table[0]);  // (at most E + n / (16 MG), and 12 E < n)
+    const int entries = __builtin_amdgcn_readfirstlane(p.table[0]);  // (at most E + n / (16 MG), which the plan holds to MAXN / 8)
     for (int i = tid; i < 3 * entries; i += 512) table[i] = p.table[1 + i];
     for (int i = tid; i < n; i += 512) {
         pairs[i] = p.pairs[i];
@@ -1261,18 +1264,15 @@ hipError_t launch_down(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t 
 
 template <int DT>
 hipError_t moe_launch(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream) {
-    hipError_t e;
-    if (plan.many)
-        e = plan.pieces == 2 ? launch_up<DT, 2, true>(p, plan, stream) : launch_up<DT, 4, true>(p, plan, stream);
-    else
-        e = plan.light_up        ? launch_up<DT, 0>(p, plan, stream)
-            : plan.pieces == 1   ? launch_up<DT, 1>(p, plan, stream)
-                                 : launch_up<DT, 2>(p, plan, stream);
+    const hipError_t e = plan.up == Fp8MoePlan::kLight  ? launch_up<DT, 0>(p, plan, stream)
+                         : plan.up == Fp8MoePlan::kWide ? (plan.up_pieces == 1 ? launch_up<DT, 1>(p, plan, stream) : launch_up<DT, 2>(p, plan, stream))
+                         : plan.up_pieces == 2          ? launch_up<DT, 2, true>(p, plan, stream)
+                                                        : launch_up<DT, 4, true>(p, plan, stream);
     if (e != hipSuccess) return e;
-    if (plan.many) return plan.pieces == 2 ? launch_down<DT, 2, true>(p, plan, stream) : launch_down<DT, 4, true>(p, plan, stream);
-    return plan.light_down     ? launch_down<DT, 0>(p, plan, stream)
-           : plan.pieces == 1  ? launch_down<DT, 1>(p, plan, stream)
-                               : launch_down<DT, 2>(p, plan, stream);
+    return plan.down == Fp8MoePlan::kLight  ? launch_down<DT, 0>(p, plan, stream)
+           : plan.down == Fp8MoePlan::kWide ? (plan.down_pieces == 1 ? launch_down<DT, 1>(p, plan, stream) : launch_down<DT, 2>(p, plan, stream))
+           : plan.down_pieces == 2          ? launch_down<DT, 2, true>(p, plan, stream)
+                                            : launch_down<DT, 4, true>(p, plan, stream);
 }
 
 // Workgroups of the second launch (light or wide).  A compute unit reads about 20 bytes a nanosecond
@@ -1292,38 +1292,54 @@ unsigned down_groups(int64_t blocks, int64_t steps) {
 }  // namespace
 
 Fp8MoePlan fp8_moe_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
-    Fp8MoePlan plan;
-    // Pieces by the tokens that an expert has on average (one that has more is read once per 16 MG
-    // of them).  With few, the light forms where the others would leave compute units idle: 16
-    // tokens, 64 experts of 2048 x 768, top 4: up 37.3 us light, 39.4 not, down 18.0 and 29.6; 8 tokens, 8
-    // experts of 4096 x 14336, top 2: up 193 light, 169 not, down 101 and 91; 1 token, 64 experts of
-    // 2048 x 768, top 8: up 8.9 and 11.6, down 6.8 and 9.5.  With several pieces, the form that shares
-    // the tokens where its larger workgroups fill the card: 128 tokens, 8 experts of 4096 x 14336, top
-    // 2: 343 us, else 715; 64 tokens, 16 experts of 4096 x 2048 (8192 blocks of 128 x 128), top 4: 108 and
-    // 153; 44 tokens, 16 experts of 2752 x 448 (1408 blocks), top 6: 47.3 and 46.6; 64 tokens, 8 experts of
-    // 2048 x 1024 (1024 blocks), top 2: 43.2 and 36.3.
-    const int64_t mean16 = 16 * T * k / E;
-    const int pieces = mean16 <= 12 * 16 || T <= 16 ? 1 : (mean16 <= 28 * 16 || T <= 32 ? 2 : 4);
-    plan.many = pieces > 1 && E * ceil_div(I, 128) * ceil_div(H, 128) >= 4096;
-    plan.pieces = plan.many || pieces < 2 ? pieces : 2;
-    const bool few = T <= 8 || mean16 <= kLightMean * 16;
-    const int64_t rows = T * k < E ? T * k : E;  // the experts met, at most
-    plan.light_up = few && (I / 16) * rows <= 4096;
-    plan.light_down = few && H / 16 < 256;
-    plan.chunk = plan.light_down ? 8 : 16 * plan.pieces;
-    const int64_t columns = plan.light_down ? 8 : (plan.many ? 128 : 16);
-    plan.blocks = ceil_div(H, columns);
-    const int64_t met = k == E ? rows : (int64_t)((double)E * -expm1((double)T * log1p(-(double)k / (double)E))) + 1;  // of even choices
-    if (plan.many) {
-        // 128 columns a block and 8 parts of each: 64 tokens, 16 experts of 4096 x 2048 (32 blocks) 39.3 us, in
-        // 4 parts 48.8, in 16 52.6; 100 tokens, 64 experts of 2048 x 768 54.2, 74.2, 59.1; one a unit is enough
-        plan.parts = plan.blocks >= 256 ? 1 : 8;
-        plan.groups = 0;
-    } else {
-        plan.groups = down_groups(plan.blocks, (plan.light_down ? ceil_div(met, 2) : met) * ceil_div(I, 128));
-        plan.parts = plan.groups == plan.blocks ? 1 : (int)(plan.groups / (plan.blocks > 0 ? plan.blocks : 1)) + 2;
+    Fp8MoePlan plan{};
+    const int64_t n = T * k, mean16 = 16 * n / E;  // 16 times the tokens that an expert has on average
+    const int64_t some = k == E ? E : (int64_t)((double)E * -expm1((double)T * log1p(-(double)k / (double)E))) + 1;  // of even choices
+    const int64_t met = T == 0 ? 0 : (some < E ? some : E);
+    const int pieces = mean16 <= 28 * 16 || T <= 32 ? 2 : 4;
+    // The first launch, by estimates in 10 ns (from 45 layers of 4 to 256 experts, 1 to 128 tokens):
+    //   light: bytes at 3.1 TB/s, + 3 us; it chooses the experts itself where they are few (the others: + 3.5);
+    //   wide: bytes at 5.5 TB/s (with two pieces 3.2: every wave reads the tokens), + 15 us (12);
+    //   many: 11.3 ns a value of H for each 256 workgroups of 128 columns, + 3 us; it needs most experts
+    //     met, as workgroups without tokens leave the others unevenly on the card.
+    // 64 tokens, 32 experts of 2048 x 768, top 4: 33.6 light, 40.1 wide, 25.5 many; 4 tokens, 64 such, top 8:
+    // 25.9, 36.4, 40.8; 16 tokens, 64 of 4096 x 1408, top 6: 137, 124, 129; 64 tokens, 160 of 5120 x 1536, top
+    // 6: 496, 450, 413; 44 tokens, 16 of 2752 x 448, top 6: 27.6, 24.7, 28.4.
+    const int64_t bytes = met * 2 * I * fp8_pitch(H), wgs = met * ceil_div(I, 128);
+    const int64_t route = T <= kRouteTokens && n <= kRouteChoices ? 350 : 0;
+    plan.up_pieces = mean16 <= 14 * 16 || T <= 16 ? 1 : 2;
+    const int64_t light = bytes / 31000 + 300;
+    const int64_t wide = (plan.up_pieces == 1 ? bytes / 55000 + 1500 : bytes / 32000 + 1200) + route;
+    const int64_t many = ceil_div(wgs, 256) * H * 113 / 100 + 300 + route;
+    plan.up = Fp8MoePlan::kWide;
+    if (n >= E && many <= wide) {
+        plan.up = Fp8MoePlan::kMany;
+        plan.up_pieces = pieces;
     }
-    plan.partial_bytes = plan.parts > 1 ? T * plan.blocks * columns * plan.parts * 4 : 0;
+    if ((mean16 <= 8 * 16 || T <= 16) && light < (plan.up == Fp8MoePlan::kMany ? many : wide)) plan.up = Fp8MoePlan::kLight;
+    // The second launch.  Many: a few tokens an expert, enough columns for 8 parts of 128 to fill the card
+    // (parts: 64 tokens, 16 experts of 4096 x 2048, top 4: 39.3 us in 8, 48.8 in 4, 52.6 in 16), and at most as
+    // many entries as its table holds; 40 tokens, 32 experts of 2880 x 2880, top 6: 65 us, wide 96; 64
+    // tokens, 64 of 2048 x 1024 (16 blocks), top 6: 54.6 and 41.9.  Light where most experts have few tokens:
+    // 16 tokens, 64 of 2048 x 768, top 4: 18.1, wide 21.2; 64 tokens, 64 of 2048 x 1024, top 6: 49.6 and 41.9.
+    const int64_t entries = (E < n ? E : n) + n / (16 * pieces), blocks128 = ceil_div(H, 128);
+    if (mean16 >= 3 * 16 && T > 8 && blocks128 >= 20 && E * ceil_div(I, 128) * blocks128 >= 4096 && entries <= (T <= 64 ? 64 : 128) * kMaxTopK / 8) {
+        plan.down = Fp8MoePlan::kMany;
+        plan.down_pieces = pieces;
+        plan.chunk = 16 * pieces;
+        plan.blocks = blocks128;
+        plan.parts = blocks128 >= 256 ? 1 : 8;
+        plan.partial_bytes = plan.parts > 1 ? T * blocks128 * 128 * plan.parts * 4 : 0;
+        return plan;
+    }
+    plan.down = (T <= 8 || mean16 <= 3 * 16) && H / 16 < 256 ? Fp8MoePlan::kLight : Fp8MoePlan::kWide;
+    plan.down_pieces = mean16 <= 14 * 16 || T <= 16 ? 1 : 2;
+    const int64_t columns = plan.down == Fp8MoePlan::kLight ? 8 : 16;
+    plan.chunk = plan.down == Fp8MoePlan::kLight ? 8 : 16 * plan.down_pieces;
+    plan.blocks = H / columns;
+    plan.groups = down_groups(plan.blocks, (plan.down == Fp8MoePlan::kLight ? ceil_div(met, 2) : met) * ceil_div(I, 128));
+    plan.parts = plan.groups == plan.blocks ? 1 : (int)(plan.groups / (plan.blocks > 0 ? plan.blocks : 1)) + 2;
+    plan.partial_bytes = plan.parts > 1 ? T * H * plan.parts * 4 : 0;
     return plan;
 }
 

@@ -237,12 +237,12 @@ struct Fp8GemmArgs {
 hipError_t launch_fp8_gemm(int dt, const Fp8GemmArgs& p, const Fp8Plan& plan, hipStream_t stream);
 
 struct Fp8MoePlan {
-    int pieces;  // of 16 tokens multiplied at once: 1, 2 or 4
-    bool light_up, light_down, many;
-    int chunk;   // tokens of an entry of the second launch
-    int64_t blocks;  // of its columns
-    unsigned groups;  // its workgroups, but with `many`: one a block and part
-    int parts;   // of a block's sum, at most
+    enum Form { kLight, kWide, kMany } up, down;  // of the first launch and of the second
+    int up_pieces, down_pieces;  // of 16 tokens multiplied at once (kWide: 1 or 2, kMany: 2 or 4)
+    int chunk;        // tokens of an entry of the second launch
+    int64_t blocks;   // of its columns
+    unsigned groups;  // its workgroups; kMany: one a block and part
+    int parts;        // of a block's sum, at most
     int64_t partial_bytes;  // parts > 1: of the partial sums
 };
 Fp8MoePlan fp8_moe_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k);

@@ -359,7 +359,7 @@ MOE = [(1, 4352, 144, 8, 2), (12, 4112, 80, 9, 2), (3, 272, 1040, 600, 4), (70, 
        (50, 4128, 64, 6, 2), (20, 144, 80, 3, 2), (2, 64, 33 * 128, 520, 16), (128, 64, 48, 1024, 16),
        (1, 16, 16, 1, 1), (1, 256, 128, 8, 2), (1, 272, 144, 64, 8), (2, 528, 400, 12, 3), (4, 384, 272, 5, 5),
        (9, 256, 144, 70, 4), (17, 272, 208, 6, 2), (40, 144, 272, 9, 4), (64, 256, 128, 130, 8), (128, 128, 144, 4, 2),
-       (33, 128, 128, 3, 1), (5, 1040, 64, 20, 16)]
+       (33, 128, 128, 3, 1), (5, 1040, 64, 20, 16), (30, 528, 4112, 40, 1), (20, 2064, 4112, 8, 1)]
 
 
 @pytest.mark.parametrize("dt", DTS)
