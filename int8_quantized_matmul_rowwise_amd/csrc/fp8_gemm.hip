@@ -668,7 +668,7 @@ hipError_t single(const Fp8GemmArgs& a, int split, hipStream_t stream) {
 // launch and the round trip of a separate coding pass while there are few rows.
 // With few columns the groups are split over `split` workgroups too (grid.y, `part` groups each):
 // their sums go through memory and the last one adds them up in their order.
-// 16 x 8192 x 8192: 18.2 us, 3.7 TB/s; 1 x 4096 x 4096 (FUSED) 6.0 us, 2.8 TB/s, of which about 3 us are
+// 16 x 8192 x 8192: 14.8 us, 4.5 TB/s; 1 x 4096 x 4096 (FUSED) 5.7 us, 2.9 TB/s, of which about 3 us are
 // the launch and the first load's way.
 template <int DT, int MG, int NF, int WV, bool FUSED, int U, int OCC>
 __global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, int split, int part) {
@@ -686,28 +686,36 @@ __global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, 
     const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(p.sa, FUSED ? 0 : (int64_t)all * 64);
     uint32_t b_off[NF], a_off[MG];
 #pragma unroll
-    for (int f = 0; f < NF; ++f) b_off[f] = (uint32_t)((16 * f + li) * p.pitch + 32 * q);
+    for (int f = 0; f < NF; ++f) b_off[f] = (uint32_t)((16 * f + li) * p.pitch + 16 * q);
 #pragma unroll
-    for (int j = 0; j < MG; ++j) a_off[j] = (uint32_t)(FUSED ? (li * K + 32 * q) * 2 : (16 * j + li) * p.pitch + 32 * q);
+    for (int j = 0; j < MG; ++j) a_off[j] = (uint32_t)(FUSED ? (li * K + 16 * q) * 2 : (16 * j + li) * p.pitch + 16 * q);
 
+    // (lane quarter q holds bytes 16 q .. + 15 and 64 + 16 q .. + 15 of a group of either operand, so that
+    // a load takes half a line of a row)
     struct Group {
         u32x4 b[NF][2], a[NA];
         int eb, ea, shift;
     };
-    // group g (past the last: nothing in reach, zeros)
-    auto load = [&](int g, Group& r) LLMINT8_FP8_INLINE {
-        const bool in = g < nk;
+    // The groups go round from a different one in each workgroup: in rows of a power of two bytes a
+    // group's lines are in the same few memory channels (16 x 8192 x 28672: 53 us, 60 from the first;
+    // 4 x 16384 x 8192: 25.4 and 31.6).
+    const int turn = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 5 % (unsigned)(nk - g0)));
+    // the n-th group (past the last: nothing in reach, zeros)
+    auto load = [&](int n, Group& r) LLMINT8_FP8_INLINE {
+        const bool in = n < nk;
+        const int g = n + turn < nk ? n + turn : n + turn - (nk - g0);
         const uint32_t far = in ? 0u : 0x80000000u;  // past every resource
 #pragma unroll
         for (int f = 0; f < NF; ++f)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                r.b[f][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, (b_off[f] + (uint32_t)(g * BK + 16 * h)) | far, 0, 0));
+                r.b[f][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, (b_off[f] + (uint32_t)(g * BK + 64 * h)) | far, 0, 0));
         if constexpr (FUSED) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t k = (int64_t)g * BK + 32 * q + 8 * i;  // past K: the next row's, or nothing
-                const uint32_t off = (a_off[0] + (uint32_t)(g * BK + 8 * i) * 2) | (in && k < K && li < p.M ? 0u : 0x80000000u);
+                const int at = g * BK + 64 * (i >> 1) + 8 * (i & 1);
+                const int64_t k = at + 16 * q;  // past K: the next row's, or nothing
+                const uint32_t off = (a_off[0] + (uint32_t)at * 2) | (in && k < K && li < p.M ? 0u : 0x80000000u);
                 r.a[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, off, 0, 0));
             }
         } else {
@@ -715,7 +723,7 @@ __global__ __launch_bounds__(64 * WV, OCC) void fp8_small_kernel(Fp8GemmArgs p, 
             for (int j = 0; j < MG; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    r.a[2 * j + h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, (a_off[j] + (uint32_t)(g * BK + 16 * h)) | far, 0, 0));
+                    r.a[2 * j + h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, (a_off[j] + (uint32_t)(g * BK + 64 * h)) | far, 0, 0));
             r.ea = (int)__builtin_amdgcn_raw_buffer_load_b32(rs, (uint32_t)(g * 64 + 4 * li) | far, 0, 0);
         }
         // the dword that holds the byte (of a byte load the compiler widens the value at once, and
@@ -869,19 +877,18 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb) {
     // 22.7; 64 x 4096 x 4096 11.4 and 13.7, 32 x 16384 x 4096 24.3 and 25.7.
     if (!rowb && (M <= 32 || (M <= 64 && N * nk <= (int64_t)1 << 17))) {
         // A coded in the kernel, or by a launch before it (every workgroup codes the rows that it
-        // multiplies): 1 x 4096 x 4096 6.7 and 7.9 us, 4 x 4096 x 8192 11.5 and 12.5, 4 x 8192 x 8192 18.9
-        // and 17.5; not where a long sum wants parts (1 x 16384 x 1024: 12.9 us, in parts 11.4).
+        // multiplies): 1 x 4096 x 4096 5.7 and 7.1 us, 4 x 4096 x 8192 10.2 and 10.7, 4 x 8192 x 8192 18.5
+        // and 17.4; not where a long sum wants parts (1 x 16384 x 1024: 13.2 us, in parts 11.6).
         const bool fused = x16 && M <= 4 && N * nk <= (int64_t)1 << 18 && (N >= 2048 || nk < 64);
         p.kind = fused ? Fp8Plan::kFused : Fp8Plan::kSmall;
         p.pieces = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
-        // Pieces of 16 columns of a workgroup, while enough workgroups are left: 16 x 4096 x 4096 6.9 us with
-        // one, 7.7 with two, 16 x 8192 x 8192 18.4 and 19.4, 16 x 4096 x 8192 11.4 and 8.8, 16 x 4096 x
-        // 12288 16.1 and 15.0; 32 x 4096 x 8192 14.3, 10.4 and (four) 13.7, 32 x 4096 x 12288 20.6, 18.5, 15.2.
-        if (fused || N < 8192 || (p.pieces == 1 && N < 12288 && nk >= 64)) p.columns = 1;
-        else p.columns = p.pieces == 2 && N >= 12288 ? 4 : 2;
+        // Pieces of 16 columns of a workgroup, while 256 workgroups are left: 16 x 4096 x 4096 6.1 us with one,
+        // 7.7 with two, 16 x 8192 x 8192 18.4 and 14.8, 16 x 4096 x 16384 19.7 and 14.9; 32 x 4096 x 8192 14.0,
+        // 10.3 and (four) 13.7, 32 x 4096 x 12288 20.1, 18.3 and 15.2.
+        p.columns = fused || N < 8192 ? 1 : (p.pieces == 2 && N >= 12288 ? 4 : 2);
         p.tiles = ceil_div(N, 16 * p.columns);
-        // Parts of the sum where columns alone leave units idle: 16 x 16384 x 1024 16.4 us, 8.9 in 4 parts;
-        // 64 x 4096 x 2048 11.3 and (2) 9.1; 16 x 4096 x 2048 5.8 and 5.9.
+        // Parts of the sum where columns alone leave units idle: 16 x 16384 x 1024 16.5 us, 9.1 in 4 parts;
+        // 64 x 4096 x 2048 11.4 and (2) 9.1; 16 x 4096 x 2048 6.0 and 6.0.
         if (!fused && (p.tiles < 128 || (p.tiles == 128 && p.pieces > 1))) p.split = parts(nk, 256 / p.tiles, 8);
         out = 256 * p.columns * p.pieces;
     } else {
