@@ -29,7 +29,7 @@
 // share the tokens' values in LDS.
 //
 // Read at: 8 tokens, 8 experts of 4096 x 14336, top 2: 165 and 91 us, 5.4 TB/s; 37 tokens, 60 experts of
-// 2064 x 1424, top 4: 78 and 53 us, 3.7 TB/s; one token, 64 experts of 2048 x 768, top 8: 10 and 6.8 us
+// 2064 x 1424, top 4: 76 and 53 us, 3.8 TB/s; one token, 64 experts of 2048 x 768, top 8: 10 and 6.8 us
 // (2.2 TB/s: the two launches' latencies).
 #include <cmath>
 
@@ -993,7 +993,7 @@ __global__ __launch_bounds__(512, 2) void moe_up_many_kernel(Fp8MoeArgs p, int s
         Scale eg, eu;
     };
     // Workgroups start at different groups: rows of 4096 bytes have a group's lines in the same few
-    // memory channels.
+    // memory channels (64 tokens, 16 experts of 4096 x 2048, top 4: 53.7 us, from the first group 69).
     const int g0 = __builtin_amdgcn_readfirstlane((int)((blockIdx.x - 1) * 5 % ng));
     auto group_at = [&](int s) LLMINT8_MOE_INLINE { return s >= ng ? ng : (s + g0 >= ng ? s + g0 - ng : s + g0); };
     for (int c0 = 0; c0 < count; c0 += 16 * MG) {
