@@ -28,7 +28,7 @@
 // pieces of tokens, the waves splitting the groups.  Many: 128 columns, a tile of 16 to a wave, which
 // share the tokens' values in LDS.
 //
-// Read at: 8 tokens, 8 experts of 4096 x 14336, top 2: 165 and 91 us, 5.4 TB/s; 37 tokens, 60 experts of
+// Read at: 8 tokens, 8 experts of 4096 x 14336, top 2: 165 and 78 us, 5.4 TB/s; 37 tokens, 60 experts of
 // 2064 x 1424, top 4: 76 and 53 us, 3.8 TB/s; one token, 64 experts of 2048 x 768, top 8: 10 and 6.8 us
 // (2.2 TB/s: the two launches' latencies).
 #include <cmath>
@@ -1317,18 +1317,19 @@ Fp8MoePlan fp8_moe_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
         plan.up_pieces = pieces;
     }
     if ((mean16 <= 8 * 16 || T <= 16) && light < (plan.up == Fp8MoePlan::kMany ? many : wide)) plan.up = Fp8MoePlan::kLight;
-    // The second launch.  Many: a few tokens an expert, enough columns for 8 parts of 128 to fill the card
+    // The second launch.  Many: most experts met, columns of 128 enough for 8 parts of each to fill the card
     // (parts: 64 tokens, 16 experts of 4096 x 2048, top 4: 39.3 us in 8, 48.8 in 4, 52.6 in 16), and at most as
-    // many entries as its table holds; 40 tokens, 32 experts of 2880 x 2880, top 6: 65 us, wide 96; 64
-    // tokens, 64 of 2048 x 1024 (16 blocks), top 6: 54.6 and 41.9.  Light where most experts have few tokens:
-    // 16 tokens, 64 of 2048 x 768, top 4: 18.1, wide 21.2; 64 tokens, 64 of 2048 x 1024, top 6: 49.6 and 41.9.
+    // many entries as its table holds; 8 tokens, 8 of 4096 x 14336, top 2: 77.6 us, wide 91.0, light 104; 40
+    // tokens, 32 of 2880 x 2880, top 6: 65 and wide 96; 64 tokens, 64 of 2048 x 1024 (16 blocks), top 6: 54.6
+    // and wide 41.9.  Light where most experts have few tokens: 16 tokens, 64 of 2048 x 768, top 4: 18.1, wide
+    // 21.2; 64 tokens, 64 of 2048 x 1024, top 6: 49.6 and 41.9.
     const int64_t entries = (E < n ? E : n) + n / (16 * pieces), blocks128 = ceil_div(H, 128);
-    if (mean16 >= 3 * 16 && T > 8 && blocks128 >= 20 && E * ceil_div(I, 128) * blocks128 >= 4096 && entries <= (T <= 64 ? 64 : 128) * kMaxTopK / 8) {
+    if (n >= E && blocks128 >= 20 && E * ceil_div(I, 128) * blocks128 >= 4096 && entries <= (T <= 64 ? 64 : 128) * kMaxTopK / 8) {
         plan.down = Fp8MoePlan::kMany;
         plan.down_pieces = pieces;
         plan.chunk = 16 * pieces;
         plan.blocks = blocks128;
-        plan.parts = blocks128 >= 256 ? 1 : 8;
+        plan.parts = blocks128 >= 32 ? (int)(blocks128 <= 256 ? 256 / blocks128 : 1) : 8;
         plan.partial_bytes = plan.parts > 1 ? T * blocks128 * 128 * plan.parts * 4 : 0;
         return plan;
     }

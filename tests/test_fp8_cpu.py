@@ -157,7 +157,7 @@ def test_routes(M, K, N, path, monkeypatch, capfd):
 @pytest.mark.parametrize("T,H,I,E,k,path", [
     (1, 2048, 768, 64, 8, "fp8_moe_light"), (3, 272, 1040, 600, 4, "fp8_moe_light_split"),
     (1, 4352, 144, 8, 2, "fp8_moe_light_wide"), (70, 272, 144, 64, 5, "fp8_moe_light_wide_split"),
-    (8, 4096, 14336, 8, 2, "fp8_moe_wide"), (30, 528, 4112, 40, 1, "fp8_moe_wide_light_split"),
+    (8, 4096, 14336, 8, 2, "fp8_moe_wide_many_split"), (8, 2048, 768, 128, 8, "fp8_moe_wide_light"), (30, 528, 4112, 40, 1, "fp8_moe_wide_light_split"),
     (20, 2064, 4112, 8, 1, "fp8_moe_wide_light_split"), (50, 4128, 64, 6, 2, "fp8_moe_wide"),
     (128, 144, 272, 16, 2, "fp8_moe_many_wide_split"), (40, 144, 272, 9, 4, "fp8_moe_many_wide"),
     (128, 64, 48, 1024, 16, "fp8_moe_many_light_split"), (16, 2048, 768, 64, 4, "fp8_moe_many_light"),
