@@ -125,6 +125,20 @@ def test_matmul_exact_lattice(M, K, N, dt):
     assert torch.equal(Y.cpu(), want)
 
 
+@pytest.mark.parametrize("seed", range(16))
+def test_matmul_and_backward_sweep(seed):
+    g = gen(2000 + seed)
+    rnd = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    M, K, N, dt = rnd(1, 20 if seed % 2 else 700), 16 * rnd(1, 300), 8 * rnd(1, 400), DTS[seed // 2 % 2]
+    print(f"\n[case] matmul, backward sweep {dt} {M}x{K}x{N}", flush=True)
+    X, W, dY = lattice(g, M, K, dt=dt).cuda(), lattice(g, K, N, dt=dt).cuda(), lattice(g, M, N, dt=dt).cuda()
+    Wq, s, WqT, sT = lm.fp8_quantize_weight_block(W, transposed=True)
+    assert torch.equal(lm.fp8_matmul_block(X, Wq, s), (X.double() @ W.double()).float().to(dt))
+    dX, dW = lm.fp8_matmul_block_backward(dY, X, WqT, sT)
+    assert torch.equal(dX, (dY.double() @ W.double().t()).float().to(dt))
+    assert torch.equal(dW, (X.double().t() @ dY.double()).float().to(dt))
+
+
 # many tiles, several per workgroup, with few and many groups along K (the sums of the lattice are
 # exact in 64 bits on the GPU too)
 @pytest.mark.parametrize("dt", DTS)
@@ -423,6 +437,33 @@ def test_moe_many_tokens(T, H, I, E, k, dt):
     l[torch.rand(T, E, generator=g) < 0.3] = -math.inf
     l[[1, T - 1]] = -math.inf  # rows of padding
     moe_check(X, l, w, k, False)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_moe_sweep(seed):
+    g = gen(1000 + seed)
+    rnd = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    T, E = rnd(1, 128 if seed % 2 else 12), rnd(1, 40)
+    k, H, I, dt = rnd(1, min(E, 8)), 16 * rnd(1, 40), 16 * rnd(1, 30), DTS[seed % 2]
+    print(f"\n[case] moe sweep {dt} T={T} H={H} I={I} E={E} k={k}", flush=True)
+    l = 2 * randn(g, T, E)
+    l[torch.rand(T, E, generator=g) < 0.1 * (seed % 4)] = -math.inf
+    moe_check(randn(g, T, H).to(dt), l, experts(g, E, H, I, dt), k, bool(rnd(0, 1)))
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("T", [0, 1, 40, 128])
+def test_moe_without_inner_columns_or_tokens(T, dt):
+    """I = 0: the choices stand, the output is zero; T = 0: nothing."""
+    H, E, k = 48, 3, 2
+    g = gen(T)
+    X, l = randn(g, T, H).to(dt).cuda(), randn(g, T, E).cuda()
+    empty = [torch.empty(E, 0, 128, dtype=F8, device="cuda"), torch.empty(E, 0, 4, dtype=E8, device="cuda"),
+             torch.empty(E, H, 0, dtype=F8, device="cuda"), torch.empty(E, 1, 0, dtype=E8, device="cuda")]
+    Y = torch.full((T, H), 7.0, dtype=dt, device="cuda")
+    Y, ids, p = lm.fp8_moe_block(X, l, *empty, top_k=k, Y=Y)
+    assert Y.shape == (T, H) and not Y.any()
+    assert torch.equal(ids.long(), l.topk(k).indices) and torch.allclose(p, torch.softmax(l.topk(k).values, -1), atol=1e-6)
 
 
 def test_moe_writes_its_outputs_alone():
