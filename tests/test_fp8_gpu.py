@@ -623,3 +623,60 @@ def test_split_sums_and_their_workspaces(op, sizes):
     for out in outs:
         for a, b in zip(out, want):
             assert torch.equal(a, b)
+
+
+# ---- what the binding refuses
+
+def test_refusals_of_gpu_tensors():
+    W = torch.zeros(272, 264, dtype=torch.float16, device="cuda")
+    X, dY = torch.zeros(5, 272, dtype=torch.float16, device="cuda"), torch.zeros(5, 264, dtype=torch.float16, device="cuda")
+    Wq, s, WqT, sT = lm.fp8_quantize_weight_block(W, transposed=True)
+    T, H, I, E = 5, 272, 144, 4
+    w = experts(gen(1), E, H, I, torch.float16)
+    l = torch.zeros(T, E, device="cuda")
+    with pytest.raises(TypeError):
+        lm.fp8_quantize_weight_block(W.float())
+    with pytest.raises(TypeError):
+        lm.fp8_matmul_block(X.float(), Wq, s)
+    with pytest.raises(TypeError):
+        lm.fp8_matmul_block(X, Wq.view(torch.int8), s)
+    with pytest.raises(TypeError):
+        lm.fp8_matmul_block(X, Wq, s.cpu())
+    with pytest.raises(TypeError):
+        lm.fp8_matmul_block(X, Wq, s, Y=dY.bfloat16())
+    with pytest.raises(TypeError):
+        lm.fp8_moe_block(X, l.half(), *w, top_k=2)
+    with pytest.raises(TypeError):
+        lm.fp8_matmul_block(X, Wq, s, workspace=torch.zeros(1 << 20, device="cuda"))
+    with pytest.raises(ValueError):
+        lm.fp8_quantize_weight_block(W.t())
+    with pytest.raises(ValueError):
+        lm.fp8_matmul_block(X[:, ::2], Wq, s)
+    with pytest.raises(ValueError):
+        lm.fp8_matmul_block(X[0], Wq, s)
+    with pytest.raises(lm.LLMInt8Error):  # 264 features: no multiple of 16
+        lm.fp8_matmul_block(dY, Wq, s)
+    with pytest.raises(ValueError):
+        lm.fp8_matmul_block(X, Wq, s[:1])
+    with pytest.raises(ValueError):
+        lm.fp8_matmul_block(X, Wq, s, Y=X)
+    with pytest.raises(ValueError):
+        lm.fp8_matmul_block_backward(dY, X[:4], WqT, sT)
+    with pytest.raises(ValueError):
+        lm.fp8_matmul_block_backward(dY, X, Wq, sT)
+    with pytest.raises(ValueError):
+        lm.fp8_moe_block(X, l[:3], *w, top_k=2)
+    with pytest.raises(ValueError):
+        lm.fp8_moe_block(X, l, *w, top_k=5)
+    with pytest.raises(ValueError):
+        lm.fp8_moe_block(X, l, *w, top_k=0)
+    with pytest.raises(ValueError):
+        lm.fp8_moe_block(X, l, w[0][:3], *w[1:], top_k=2)
+    with pytest.raises(ValueError):
+        lm.fp8_moe_block(X, l, w[0].transpose(1, 2), *w[1:], top_k=2)
+    with pytest.raises(lm.LLMInt8Error):
+        lm.fp8_moe_block(X, l, *w, top_k=2, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(lm.LLMInt8Error):  # the output is an input
+        lm.fp8_matmul_block(torch.zeros(264, 272, dtype=torch.float16, device="cuda"), Wq, s,
+                            workspace=Wq.view(torch.uint8).view(-1))
+    torch.cuda.synchronize()
