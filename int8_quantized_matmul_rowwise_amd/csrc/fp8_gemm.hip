@@ -830,7 +830,12 @@ hipError_t small_launch(const Fp8GemmArgs& a, int split, hipStream_t stream) {
 
 template <int DT>
 hipError_t small(const Fp8GemmArgs& a, const Fp8Plan& plan, hipStream_t stream) {
-    if (plan.kind == Fp8Plan::kFused) return small_launch<DT, 1, 1, 8, true, 1, 4>(a, plan.split, stream);
+    if (plan.kind == Fp8Plan::kFused) {
+        if (plan.columns == 1) return small_launch<DT, 1, 1, 8, true, 1, 4>(a, plan.split, stream);
+        // fewer waves once there are many workgroups: 1 x 4096 x 8192 7.6 us with 8, 8.7 with 4, 1 x 4096 x
+        // 14336 14.3 and 12.1
+        return a.N < 12288 ? small_launch<DT, 1, 2, 8, true, 1, 4>(a, plan.split, stream) : small_launch<DT, 1, 2, 4, true, 1, 4>(a, plan.split, stream);
+    }
     switch (4 * plan.pieces + plan.columns) {
         case 4 + 1: return small_launch<DT, 1, 1, 4, false, 2, 4>(a, plan.split, stream);
         case 4 + 2: return small_launch<DT, 1, 2, 4, false, 1, 4>(a, plan.split, stream);
@@ -877,15 +882,16 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb) {
     // 22.7; 64 x 4096 x 4096 11.4 and 13.7, 32 x 16384 x 4096 24.3 and 25.7.
     if (!rowb && (M <= 32 || (M <= 64 && N * nk <= (int64_t)1 << 17))) {
         // A coded in the kernel, or by a launch before it (every workgroup codes the rows that it
-        // multiplies): 1 x 4096 x 4096 5.7 and 7.1 us, 4 x 4096 x 8192 10.2 and 10.7, 4 x 8192 x 8192 18.5
-        // and 17.4; not where a long sum wants parts (1 x 16384 x 1024: 13.2 us, in parts 11.6).
-        const bool fused = x16 && M <= 4 && N * nk <= (int64_t)1 << 18 && (N >= 2048 || nk < 64);
+        // multiplies): 1 x 4096 x 4096 5.7 and 7.1 us, 4 x 8192 x 8192 14.9 and 16.8, 4 x 8192 x 28672 49.0 and
+        // 48.4; not where a long sum wants parts (1 x 16384 x 1024: 13.2 us, in parts 11.6).
+        const bool fused = x16 && M <= 4 && N * nk <= (int64_t)1 << 19 && (N >= 2048 || nk < 64);
         p.kind = fused ? Fp8Plan::kFused : Fp8Plan::kSmall;
         p.pieces = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
         // Pieces of 16 columns of a workgroup, while 256 workgroups are left: 16 x 4096 x 4096 6.1 us with one,
         // 7.7 with two, 16 x 8192 x 8192 18.4 and 14.8, 16 x 4096 x 16384 19.7 and 14.9; 32 x 4096 x 8192 14.0,
-        // 10.3 and (four) 13.7, 32 x 4096 x 12288 20.1, 18.3 and 15.2.
-        p.columns = fused || N < 8192 ? 1 : (p.pieces == 2 && N >= 12288 ? 4 : 2);
+        // 10.3 and (four) 13.7, 32 x 4096 x 12288 20.1, 18.3 and 15.2; coded in the kernel, 1 x 4096 x 8192 9.3 and
+        // 7.6, 1 x 4096 x 4096 5.7 and 7.0.
+        p.columns = N < 8192 ? 1 : (p.pieces == 2 && N >= 12288 ? 4 : 2);
         p.tiles = ceil_div(N, 16 * p.columns);
         // Parts of the sum where columns alone leave units idle: 16 x 16384 x 1024 16.5 us, 9.1 in 4 parts;
         // 64 x 4096 x 2048 11.4 and (2) 9.1; 16 x 4096 x 2048 6.0 and 6.0.

@@ -138,7 +138,7 @@ def test_stages_and_their_failures(name, monkeypatch, capfd):
 
 
 @pytest.mark.parametrize("M,K,N,path", [
-    (1, 16, 8, "fp8_small_fused"), (4, 4096, 8192, "fp8_small_fused"), (5, 4096, 8192, "fp8_small"),
+    (1, 16, 8, "fp8_small_fused"), (4, 4096, 8192, "fp8_small_fused"), (4, 8192, 8192, "fp8_small_fused"), (4, 8192, 8200, "fp8_small"), (5, 4096, 8192, "fp8_small"),
     (1, 16384, 1024, "fp8_small_split"), (32, 4096, 4096, "fp8_small"), (33, 4096, 4096, "fp8_small"),
     (33, 8192, 4096, "fp8_single_split"), (65, 128, 8, "fp8_single"), (100, 4240, 264, "fp8_single_split"),
     (2048, 2048, 2048, "fp8_single"), (2048, 272, 2056, "fp8_tile128"), (4096, 4096, 2048, "fp8_tile128"),

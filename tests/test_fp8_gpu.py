@@ -107,9 +107,9 @@ SHAPES = [(1, 16, 8), (1, 4096, 264), (3, 144, 1032), (16, 272, 520), (17, 1040,
           (100, 4240, 264), (300, 8208, 520), (260, 4240, 2056), (6, 1040, 16392), (4, 16400, 8200)]
 
 
-# the persistent tiled kernels: tiles of 128, of 256 (one and several a workgroup, odd and even counts
+# two pieces of columns with A coded in the kernel; the persistent tiled kernels: tiles of 128, of 256 (one and several a workgroup, odd and even counts
 # of groups), and tiles of 256 whose sums are split
-LARGE = [(2048, 272, 2056), (2400, 272, 4360), (4100, 144, 4360), (4100, 400, 4360), (1200, 12304, 4104)]
+LARGE = [(1, 4112, 8200), (4, 1040, 12296), (3, 272, 16392), (2048, 272, 2056), (2400, 272, 4360), (4100, 144, 4360), (4100, 400, 4360), (1200, 12304, 4104)]
 
 
 @pytest.mark.parametrize("dt", DTS)
