@@ -53,6 +53,7 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t off,
 }
 constexpr uint32_t kFar = 0x80000000u;  // an offset past every resource: reads zero
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
+__device__ const u32x4 kZeroLine[8] = {};  // a group's weights where there are none
 
 // A step's instructions bound these kernels before its bytes do, so what a step computes is kept
 // short: the group's place rides in the scalar offset, a step without a group has empty resources
@@ -535,9 +536,9 @@ __global__ __launch_bounds__(64 * kLightUpWaves, 4) void moe_up_light_kernel(Fp8
     };
     // (read back: with the choices in LDS the compiler takes these for lanes' values)
     auto load_w = [&](Group& r) LLMINT8_MOE_INLINE {
-        const bool in = at.t < my_tiles && at.g < ng;  // else: one line of weights times zeros
+        const bool in = at.t < my_tiles && at.g < ng;  // else zeros (no line of weights: NaN times zero is NaN)
         const int t = __builtin_amdgcn_readfirstlane(in ? at.t : 0), g = __builtin_amdgcn_readfirstlane(in ? at.g : 0);
-        const uint8_t* from = in ? W + 8 * t * hp + g * 128 : p.W13;
+        const uint8_t* from = in ? W + 8 * t * hp + g * 128 : (const uint8_t*)kZeroLine;
         r.w[0] = *(const u32x4*)from;
         r.w[1] = *(const u32x4*)(from + 64);
         // (I is a multiple of 16: a tile's gate rows, and its up rows, lie in one block)

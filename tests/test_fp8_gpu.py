@@ -466,6 +466,55 @@ def test_moe_without_inner_columns_or_tokens(T, dt):
     assert torch.equal(ids.long(), l.topk(k).indices) and torch.allclose(p, torch.softmax(l.topk(k).values, -1), atol=1e-6)
 
 
+# each pair of forms; H of a number of groups that the light form's four waves do not share evenly
+NON_FINITE = [(1, 2064, 144, 64, 8), (3, 272, 1040, 60, 4), (12, 272, 144, 11, 4), (1, 4352, 144, 8, 2), (70, 272, 144, 64, 5),
+              (30, 528, 4112, 40, 1), (50, 4128, 64, 6, 2), (128, 144, 272, 16, 2), (40, 144, 272, 9, 4), (128, 144, 48, 700, 16),
+              (60, 4112, 2064, 8, 2)]
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("T,H,I,E,k", NON_FINITE)
+def test_moe_non_finite_values_stay_where_they_are(T, H, I, E, k, dt):
+    """NaN among an expert's weights or a token's values reaches the outputs whose sums it enters;
+    every other output keeps its bits."""
+    print(f"\n[case] moe non-finite {dt} T={T} H={H} I={I} E={E} k={k}", flush=True)
+    g = gen(T + H + I + E + k + 1)
+    X, l, w = randn(g, T, H).to(dt).cuda(), 2 * randn(g, T, E), experts(g, E, H, I, dt)
+    l[0::2, 0], l[1::2, 0] = -math.inf, 50.0  # the odd tokens alone meet expert 0
+    l = l.cuda()
+    Y, ids, p = lm.fp8_moe_block(X, l, *w, top_k=k)
+    meets = (ids == 0).any(1)
+    assert not meets[0::2].any() and meets[1::2].all() and torch.isfinite(Y.float()).all()
+
+    def run(X, w):
+        Y2, ids2, p2 = lm.fp8_moe_block(X, l, *w, top_k=k)
+        assert torch.equal(ids2, ids) and torch.equal(p2, p)
+        return Y2
+
+    def with_nan(q, at):
+        q = q.view(torch.uint8).clone()
+        q[at] = 0x7f
+        return q.view(F8)
+
+    # the first expert's first line of gate weights, and the end of its last up row
+    for at in ((0, 0, slice(0, 128)), (0, 2 * I - 1, slice(H - 16, H))):
+        Y2 = run(X, (with_nan(w[0], at),) + w[1:])
+        assert torch.equal(Y2[~meets], Y[~meets]), at
+        assert not torch.isfinite(Y2[meets].float()).any(), at
+    # a row of its down weights is an output column of its tokens
+    for row in (0, H - 1):
+        Y2 = run(X, w[:2] + (with_nan(w[2], (0, row, slice(0, 16))), w[3]))
+        keep = torch.ones_like(Y, dtype=torch.bool)
+        keep[meets, row] = False
+        assert torch.equal(Y2[keep], Y[keep]) and not torch.isfinite(Y2[~keep].float()).any(), row
+    # a token's own values
+    for t in {0, T - 1}:
+        X2 = X.clone()
+        X2[t, H - 1] = math.nan
+        Y2 = run(X2, w)
+        assert torch.equal(Y2[torch.arange(T) != t], Y[torch.arange(T) != t]) and not torch.isfinite(Y2[t].float()).any()
+
+
 def test_moe_writes_its_outputs_alone():
     T, H, I, E, k = 7, 272, 144, 6, 2
     g = gen(12)
