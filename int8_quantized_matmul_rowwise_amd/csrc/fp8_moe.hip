@@ -865,8 +865,9 @@ __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p, i
                 }
             };
             v4f acc[1] = {};
-            // The results of an entry's rows with its own tokens; the even entry first, then the odd one:
-            // a token may be in both.
+            // The results of an entry's rows with its own tokens; the even entry first, then the odd one: a
+            // token may be in both, on lanes of either half, whose sums are one word of LDS.  One lane takes
+            // part in one of the two at most, so without the fence the compiler might join them.
             auto flush = [&](int two) LLMINT8_MOE_INLINE {
                 mfma_settle();
 #pragma unroll
@@ -880,6 +881,8 @@ __global__ __launch_bounds__(64 * WV) void moe_down_light_kernel(Fp8MoeArgs p, i
                         for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(pt, acc[0][r], y[r]);
                         ysum[w][pair / k][q & 1] = y;
                     }
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
                 }
                 acc[0] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
             };

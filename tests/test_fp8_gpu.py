@@ -515,6 +515,18 @@ def test_moe_non_finite_values_stay_where_they_are(T, H, I, E, k, dt):
         assert torch.equal(Y2[torch.arange(T) != t], Y[torch.arange(T) != t]) and not torch.isfinite(Y2[t].float()).any()
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("T,H,I,E,k", [(8, 16, 128, 2, 2), (8, 272, 272, 16, 16), (7, 144, 2064, 5, 4), (16, 272, 128, 40, 6)])
+def test_moe_tokens_of_both_entries_at_once(T, H, I, E, k, dt):
+    """The light second launch takes two experts at a time: here their tokens are the same ones, so each
+    token's sum is added to from both, in the same step and in neighbouring ones."""
+    print(f"\n[case] moe both entries {dt} T={T} H={H} I={I} E={E} k={k}", flush=True)
+    g = gen(T * H + I + E)
+    l = randn(g, T, E)
+    l[:, k:] = -math.inf  # every token on the first k experts
+    moe_check(randn(g, T, H).to(dt), l, experts(g, E, H, I, dt), k, True)
+
+
 def test_moe_writes_its_outputs_alone():
     T, H, I, E, k = 7, 272, 144, 6, 2
     g = gen(12)
