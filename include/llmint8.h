@@ -402,6 +402,9 @@ int fp8_matmul_block_backward(const void* dY, const void* X, int64_t M, int64_t 
  *   all E;
  *   h_j = RN_T( silu(g) * u ),  [g; u] = W13hat[e_j] x,  y = RN_T( sum_j p_j W2hat[e_j] h_j ).
  * A token with fewer than top_k logits above -infinity gets that many experts; with none, y = 0.
+ * bf16: the weights' values are multiplied as bf16 numbers, which those of converted weights are at
+ * every scale; of codes made otherwise, what is no multiple of 2^-133 (possible at scales below 2^-124)
+ * is rounded to one.
  *   X         in : T x H, dtype (T <= 128, else LLMINT8_ERANGE; H and I multiples of 16).
  *   logits    in : T x E fp32 (E <= 1024, top_k <= 16, else LLMINT8_ERANGE).
  *   W13q, w13_scale  in : E times the conversion of an H x 2I weight, gate columns first.

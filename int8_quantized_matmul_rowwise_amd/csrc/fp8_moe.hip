@@ -15,9 +15,12 @@
 // type, so nothing is lost against the coded weight, and the activations keep their 16 bits --
 // few tokens leave the matrix units idle anyway.  Weights are the row side (16 rows), an expert's
 // tokens the column side, 16 to a piece; a group of 128 takes four instructions, whose order of
-// the terms is free as long as both operands agree.  bf16 takes the scale in the conversion (an
-// exact shift of the exponent); fp16 could not hold it, so there each group's sum is added with its
-// scale.  Sums are fp32; waves and workgroups split them and meet in a fixed order, so a result's
+// the terms is free as long as both operands agree.  bf16 takes the scale in the conversion: a
+// shift of the exponent, exact wherever the product is a multiple of bf16's smallest step 2^-133 (which
+// the instruction keeps).  Every product is at scales from 2^-124 on, as codes are multiples of 2^-9; at
+// the three below, a converted weight's are (what it was coded from was such a multiple, and four bits
+// of it are), and other codes would be rounded to that step.  fp16 could not hold the scale, so there
+// each group's sum is added with it.  Sums are fp32; waves and workgroups split them and meet in a fixed order, so a result's
 // bits follow from the inputs alone (where the splits lie depends on the sizes and on the experts
 // that the tokens meet together).
 //

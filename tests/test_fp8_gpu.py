@@ -527,6 +527,29 @@ def test_moe_tokens_of_both_entries_at_once(T, H, I, E, k, dt):
     moe_check(randn(g, T, H).to(dt), l, experts(g, E, H, I, dt), k, True)
 
 
+@pytest.mark.parametrize("T,H,I,E,k", [(2, 272, 144, 8, 2), (40, 144, 272, 9, 4), (50, 4128, 64, 6, 2), (60, 4112, 2064, 8, 2)])
+@pytest.mark.parametrize("which", [0, 2])
+def test_moe_smallest_scales(which, T, H, I, E, k):
+    """bf16, gate and up (0) or down (2) weights at the smallest scales: converted weights around bf16's
+    smallest numbers, and every small code at 2^-124, as exact as anywhere."""
+    print(f"\n[case] moe smallest scales {which} T={T} H={H} I={I} E={E} k={k}", flush=True)
+    g, dt = gen(T + H + I + which), torch.bfloat16
+    X, l, w = randn(g, T, H), 2 * randn(g, T, E), list(experts(g, E, H, I, dt))
+    shape = (H, 2 * I) if which == 0 else (I, H)
+    tiny = [lm.fp8_quantize_weight_block((randn(g, *shape) * 2.0 ** -127).to(dt).cuda()) for _ in range(E)]
+    w[which] = torch.stack([q.view(torch.uint8) for q, _ in tiny]).view(F8)
+    w[which + 1] = torch.stack([s.view(torch.uint8) for _, s in tiny]).view(E8)
+    assert not w[which + 1].view(torch.uint8).any()  # 2^-127, all of them
+    moe_check((X * (2.0 ** 122 if which == 0 else 1)).to(dt), l, w, k, True)
+    q = torch.randint(0, 16, w[which].shape, generator=g) + 128 * torch.randint(0, 2, w[which].shape, generator=g)
+    q[:, :, shape[0]:] = 0
+    w[which] = q.to(torch.uint8).cuda().view(F8)
+    s = w[which + 1].view(torch.uint8).clone()
+    s[:, :, :-(-shape[0] // 128)] = 127 - 124
+    w[which + 1] = s.view(E8)
+    moe_check((X * (2.0 ** 122 if which == 0 else 1)).to(dt), l, w, k, False)
+
+
 def test_moe_writes_its_outputs_alone():
     T, H, I, E, k = 7, 272, 144, 6, 2
     g = gen(12)
