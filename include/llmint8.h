@@ -405,7 +405,9 @@ int fp8_matmul_block_backward(const void* dY, const void* X, int64_t M, int64_t 
  * bf16: the weights' values are multiplied as bf16 numbers, which those of converted weights are at
  * every scale; of codes made otherwise, what is no multiple of 2^-133 (possible at scales below 2^-124)
  * is rounded to one.
- *   X         in : T x H, dtype (T <= 128, else LLMINT8_ERANGE; H and I multiples of 16).
+ *   X         in : T x H, dtype (T <= 128, H <= 2^22, else LLMINT8_ERANGE; H and I multiples of 16).
+ *   I            at most 2^21, and T top_k fp8_code_pitch(I) under 2^30 (the rows of h are addressed with
+ *                32 bits), else LLMINT8_ERANGE: I <= 2^21 up to 511 choices in all, 524160 at 128 x 16.
  *   logits    in : T x E fp32 (E <= 1024, top_k <= 16, else LLMINT8_ERANGE).
  *   W13q, w13_scale  in : E times the conversion of an H x 2I weight, gate columns first.
  *   W2q, w2_scale    in : E times the conversion of an I x H weight.

@@ -91,6 +91,22 @@ def test_moe_refuses(kw, code):
     assert moe(**kw) == code
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(I=1 << 21), lm.OK), (dict(I=(1 << 21) + 16), lm.ERANGE),
+    (dict(T=73, E=7, k=7, I=1 << 21), lm.OK), (dict(T=128, E=4, k=4, I=1 << 21), lm.ERANGE),
+    (dict(T=128, E=16, k=16, I=524160), lm.OK), (dict(T=128, E=16, k=16, I=524176), lm.ERANGE), (dict(T=64, E=16, k=16, I=524288), lm.OK),
+    (dict(H=1 << 22, I=16), lm.OK), (dict(H=(1 << 22) + 16, I=16), lm.ERANGE),
+])
+def test_moe_bounds_of_the_columns(kw, code, monkeypatch):
+    monkeypatch.setenv("LLMINT8_FAULT", "no_such_stage")  # a dry run
+    far = 1 << 44  # addresses that nothing reads
+    a = dict(X=far, l=2 * far, W13=3 * far, s13=4 * far, W2=5 * far, s2=6 * far, Y=7 * far, ids=8 * far, p=9 * far, ws=10 * far,
+             wsb=1 << 40)
+    assert moe(**{**a, **kw}) == code
+    n = lm.fp8_moe_block_workspace_bytes(kw.get("T", 3), kw.get("H", 64), kw["I"], kw.get("E", 4), kw.get("k", 2))
+    assert (n > 0) == (code == lm.OK)
+
+
 def test_sizes():
     for n in (0, 1, 16, 127, 128, 129, 512, 513, 4096, 12288):
         assert lm.lib().fp8_code_pitch(n) == lm.fp8_code_pitch(n) == ref.pitch(n)
