@@ -12,8 +12,6 @@ namespace llmint8 {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 
-constexpr int kFp8Block = 128;  // values of a group along each axis
-
 __host__ __device__ constexpr int64_t fp8_pitch(int64_t n) { return round_up(n, 128); }
 __host__ __device__ constexpr int64_t fp8_scale_pitch_of(int64_t n) { return round_up(ceil_div(n, 128), 4); }
 
