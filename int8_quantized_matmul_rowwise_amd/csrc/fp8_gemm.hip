@@ -880,7 +880,8 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb) {
     // Few rows straight from memory; past 32 rows only while B is small, as there the tiles, whose rows
     // are shared, catch up: 64 x 16384 x 4096 38.1 us, in a tile's kernel 25.9, 48 x 8192 x 8192 24.0 and
     // 22.7; 64 x 4096 x 4096 11.4 and 13.7, 32 x 16384 x 4096 24.3 and 25.7.
-    if (!rowb && (M <= 32 || (M <= 64 && N * nk <= (int64_t)1 << 17))) {
+    // (From 2^29 columns on their grid, of 8 threads a column, would pass the 2^32 threads of a launch.)
+    if (!rowb && N < (int64_t)1 << 29 && (M <= 32 || (M <= 64 && N * nk <= (int64_t)1 << 17))) {
         // A coded in the kernel, or by a launch before it (every workgroup codes the rows that it
         // multiplies): 1 x 4096 x 4096 5.7 and 7.1 us, 4 x 8192 x 8192 14.9 and 16.8, 4 x 8192 x 28672 49.0 and
         // 48.4; not where a long sum wants parts (1 x 16384 x 1024: 13.2 us, in parts 11.6).

@@ -170,6 +170,18 @@ def test_routes(M, K, N, path, monkeypatch, capfd):
     assert lm.fp8_matmul_block_workspace_bytes(M, K, N) < 1 << 30
 
 
+@pytest.mark.parametrize("M,N,path", [(1, (1 << 29) - 8, "fp8_small"), (32, (1 << 29) - 8, "fp8_small"), (1, 1 << 29, "fp8_tile256"),
+                                      (32, (1 << 31) - 8, "fp8_tile256")])
+def test_routes_of_very_many_columns(M, N, path, monkeypatch, capfd):
+    """The few-row kernels have a workgroup for some columns each: 2^32 threads would be too many for a launch."""
+    monkeypatch.setenv("LLMINT8_LOG", "1")
+    monkeypatch.setenv("LLMINT8_FAULT", "no_such_stage")
+    capfd.readouterr()
+    far = 1 << 50  # addresses that nothing reads
+    assert lm.lib().fp8_matmul_block(far, M, 16, 0, 2 * far, 3 * far, N, 4 * far, 5 * far, 1 << 40, None) == lm.OK
+    assert re.findall(r"path=(\w+)", capfd.readouterr().err) == [path]
+
+
 @pytest.mark.parametrize("T,H,I,E,k,path", [
     (1, 2048, 768, 64, 8, "fp8_moe_light"), (3, 272, 1040, 600, 4, "fp8_moe_light_split"),
     (1, 4352, 144, 8, 2, "fp8_moe_light_wide"), (70, 272, 144, 64, 5, "fp8_moe_light_wide_split"),

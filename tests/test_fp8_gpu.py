@@ -224,6 +224,34 @@ def test_matmul_empty():
     assert lm.fp8_matmul_block(torch.zeros(0, 64, dtype=torch.float16, device="cuda"), Wq, s).shape == (0, 8)
 
 
+def test_matmul_of_very_many_columns():
+    """2^29 + 136 columns (64 GiB of codes): more than a few-row kernel's grid can have.  Whole numbers, so
+    that pieces of the weight multiplied alone give the same bits."""
+    N, K = (1 << 29) + 136, 16
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GiB of free device memory")
+    print(f"\n[case] matmul very many columns {K}x{N}", flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    code = torch.arange(-3, 4, device="cuda").float().to(F8).view(torch.uint8)
+    Wq = torch.zeros(N, 128, dtype=torch.uint8, device="cuda")
+    step = 1 << 24
+    for a in range(0, N, step):
+        b = min(N, a + step)
+        Wq[a:b, :K] = code[torch.randint(0, 7, (b - a, K), generator=g, device="cuda")]
+    Wq, s = Wq.view(F8), torch.zeros(-(-N // 128), 4, dtype=torch.uint8, device="cuda")
+    s[:, 0] = torch.randint(125, 130, (s.shape[0],), generator=g, device="cuda")
+    s = s.view(E8)
+    X = torch.randint(-3, 4, (2, K), generator=g, device="cuda").half()
+    Y = lm.fp8_matmul_block(X, Wq, s)
+    for a in (0, step, N // 2 // 128 * 128, (1 << 29) - 128, N - N % 128 - (1 << 20)):
+        b = min(N, a + (1 << 20) + 8)
+        part = lm.fp8_matmul_block(X, Wq[a:b], s[a // 128: -(-b // 128)])
+        assert part.any() and torch.equal(Y[:, a:b], part), a
+    del Wq, s, Y, part
+    torch.cuda.empty_cache()
+
+
 def framed(shape, dt, fill=3.0):
     """(view, whole): a buffer of the shape between canaries."""
     n = math.prod(shape)
