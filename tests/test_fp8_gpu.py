@@ -369,6 +369,91 @@ def test_backward_writes_its_outputs_alone(M, K, N):
     assert torch.equal(a, dX) and torch.equal(b, dW)
 
 
+# ---- values that are not finite
+
+NOT_FINITE = [math.nan, math.inf, -math.inf]
+
+
+def is_nan_code(q):
+    return (q.view(torch.uint8) & 0x7f) == 0x7f
+
+
+def blocks_zeroed(W, at):
+    W = W.clone()
+    for k, n in at:
+        W[k // 128 * 128: k // 128 * 128 + 128, n // 128 * 128: n // 128 * 128 + 128] = 0
+    return W
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("v", NOT_FINITE)
+def test_quantize_weight_not_finite(v, dt):
+    """Its own code is NaN, its block's other values vanish beside it, no other block changes."""
+    K, N, at = 400, 264, [(5, 7), (391, 263)]
+    g = gen(21)
+    W = (randn(g, K, N) * 0.02).to(dt)
+    W2 = W.clone()
+    for k, n in at:
+        W2[k, n] = v
+    rest = lm.fp8_quantize_weight_block(blocks_zeroed(W, at).cuda(), transposed=True)
+    Wq, s, WqT, sT = lm.fp8_quantize_weight_block(W2.cuda(), transposed=True)
+    nan = torch.zeros(N, K, dtype=torch.bool, device="cuda")
+    for k, n in at:
+        nan[n, k] = True
+    assert torch.equal(is_nan_code(Wq)[:, :K], nan) and torch.equal(is_nan_code(WqT)[:, :N], nan.t())
+    assert not is_nan_code(Wq)[:, K:].any() and not is_nan_code(WqT)[:, N:].any()
+    for got, want, own in ((Wq, rest[0], nan), (WqT, rest[2], nan.t())):
+        keep = torch.ones(got.shape, dtype=torch.bool, device="cuda")
+        keep[:, :own.shape[1]] = ~own
+        assert torch.equal(got.float()[keep], want.float()[keep])
+    for got, want, blocks in ((s, rest[1], [(n, k) for k, n in at]), (sT, rest[3], at)):
+        keep = torch.ones(got.shape, dtype=torch.bool)
+        for r, c in blocks:
+            keep[r // 128, c // 128] = False
+        assert torch.equal(u8(got)[keep], u8(want)[keep])
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M", [2, 20, 100, 12000, 24000])
+def test_matmul_weights_not_finite(M, dt):
+    K, N, at = 400, 264, [(5, 7), (391, 263)]
+    print(f"\n[case] matmul weights not finite {dt} {M}x{K}x{N}", flush=True)
+    g = gen(22)
+    X, W = randn(g, M, K).to(dt).cuda(), (randn(g, K, N) * 0.02).to(dt)
+    W2 = W.clone()
+    for (k, n), v in zip(at, NOT_FINITE):
+        W2[k, n] = v
+    want = lm.fp8_matmul_block(X, *lm.fp8_quantize_weight_block(blocks_zeroed(W, at).cuda()))
+    Y = lm.fp8_matmul_block(X, *lm.fp8_quantize_weight_block(W2.cuda()))
+    cols = torch.zeros(N, dtype=torch.bool)
+    cols[[n for _, n in at]] = True
+    assert not torch.isfinite(Y[:, cols].float()).any() and torch.equal(Y[:, ~cols], want[:, ~cols])
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M,K,N", [(70, 400, 264), (300, 272, 4360), (5000, 144, 264), (4400, 4240, 1040)])
+def test_backward_not_finite(M, K, N, dt):
+    print(f"\n[case] backward not finite {dt} {M}x{K}x{N}", flush=True)
+    g = gen(23)
+    X, W, dY = randn(g, M, K).to(dt).cuda(), (randn(g, K, N) * 0.02).to(dt), randn(g, M, N).to(dt).cuda()
+    w = lm.fp8_quantize_weight_block(W.cuda(), transposed=True)[2:]
+    dX, dW = lm.fp8_matmul_block_backward(dY, X, *w)
+    for v in NOT_FINITE:
+        m, k, n = M - 1, K - 1, N - 1
+        Y2, X2, W2 = dY.clone(), X.clone(), W.clone()
+        Y2[m, n] = X2[0, k] = W2[0, n] = v
+        a, b = lm.fp8_matmul_block_backward(Y2, X, *w)
+        assert not torch.isfinite(a[m].float()).any() and torch.equal(a[:m], dX[:m]), v
+        assert not torch.isfinite(b[:, n].float()).any() and torch.equal(b[:, :n], dW[:, :n]), v
+        a, b = lm.fp8_matmul_block_backward(dY, X2, *w)
+        assert torch.equal(a, dX) and not torch.isfinite(b[k].float()).any() and torch.equal(b[:k], dW[:k]), v
+        w2 = lm.fp8_quantize_weight_block(W2.cuda(), transposed=True)[2:]
+        zeroed = lm.fp8_quantize_weight_block(blocks_zeroed(W, [(0, n)]).cuda(), transposed=True)[2:]
+        a, _ = lm.fp8_matmul_block_backward(dY, None, *w2, need_dw=False)
+        want, _ = lm.fp8_matmul_block_backward(dY, None, *zeroed, need_dw=False)
+        assert not torch.isfinite(a[:, 0].float()).any() and torch.equal(a[:, 1:], want[:, 1:]), v
+
+
 # ---- mixture of experts
 
 def experts(g, E, H, I, dt):
