@@ -20,9 +20,9 @@
 // the instruction keeps).  Every product is at scales from 2^-124 on, as codes are multiples of 2^-9; at
 // the three below, a converted weight's are (what it was coded from was such a multiple, and four bits
 // of it are), and other codes would be rounded to that step.  fp16 could not hold the scale, so there
-// each group's sum is added with it.  Sums are fp32; waves and workgroups split them and meet in a fixed order, so a result's
-// bits follow from the inputs alone (where the splits lie depends on the sizes and on the experts
-// that the tokens meet together).
+// each group's sum is added with it.  Sums are fp32; waves and workgroups split them and meet in a
+// fixed order, so a result's bits follow from the inputs alone (where the splits lie depends on the
+// sizes and on the experts that the tokens meet together).
 //
 // Three forms of both launches.  Light: the work is cut finer, so that small layers fill the compute
 // units: the 16 rows of an instruction are 8 gate and the same 8 up columns in the first launch, and
@@ -1208,8 +1208,9 @@ __global__ __launch_bounds__(512, 2) void moe_down_many_kernel(Fp8MoeArgs p) {
 // once per span, as long as about `enough` workgroups are left: 4 tokens, 64 experts of 2048 x 768,
 // top 8: 25.5 us with spans of 3, 32.6 with single tiles; longer ones gain nothing (8 tokens, 128
 // such experts: 48.3 us with spans of 3, 47.3 with 6, 59.6 with 1; 16 tokens, top 4: 38.6, 44.9, 47.2).
-// The heavy form, 37 tokens, 60 experts of 2064 x 1424, top 4: 78 us with 1024 workgroups left, 89 with
-// 512 and with 2048; 64 tokens, 160 experts of 5120 x 1536, top 6: 451, 451 and 456.
+// The wide form, 37 tokens, 60 experts of 2064 x 1424, top 4 (where the form for many tokens runs now): 78
+// us with 1024 workgroups left, 89 with 512 and with 2048; 64 tokens, 160 experts of 5120 x 1536, top 6:
+// 451, 451 and 456.
 struct UpGrid {
     int by_pair, spans, span;
     int64_t grid;
@@ -1324,12 +1325,20 @@ Fp8MoePlan fp8_moe_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
         plan.up_pieces = pieces;
     }
     if ((mean16 <= 8 * 16 || T <= 16) && light < (plan.up == Fp8MoePlan::kMany ? many : wide)) plan.up = Fp8MoePlan::kLight;
-    // The second launch.  Many: most experts met, columns of 128 enough for 8 parts of each to fill the card
-    // (parts: 64 tokens, 16 experts of 4096 x 2048, top 4: 39.3 us in 8, 48.8 in 4, 52.6 in 16), and at most as
-    // many entries as its table holds; 8 tokens, 8 of 4096 x 14336, top 2: 77.6 us, wide 91.0, light 104; 40
-    // tokens, 32 of 2880 x 2880, top 6: 65 and wide 96; 64 tokens, 64 of 2048 x 1024 (16 blocks), top 6: 54.6
-    // and wide 41.9.  Light where most experts have few tokens: 16 tokens, 64 of 2048 x 768, top 4: 18.1, wide
-    // 21.2; 64 tokens, 64 of 2048 x 1024, top 6: 49.6 and 41.9.
+    // The second launch.  Many: most experts met, at least 20 blocks of 128 columns (8 parts of each are 160
+    // workgroups), and at most as many entries as its table holds.  Parts: 64 tokens, 16 experts of 4096 x
+    // 2048, top 4: 39.3 us in 8, 48.8 in 4, 52.6 in 16.  8 tokens, 8 of 4096 x 14336, top 2: 77.6 us, wide 91.0,
+    // light 104; 40 tokens, 32 of 2880 x 2880, top 6: 65 and wide 96.  Whole calls with this form and with the
+    // better of the others, by blocks: 64 tokens, 64 experts, I = 1024, top 6: 16 blocks 108.7 us and 96.3, 18
+    // 114.4 and 119.5, 19 117.3 and 127.9, 20 122.6 and 133.2; 32 tokens, 16, 2048, top 4: 16 blocks 65.0 and
+    // 60.2, 19 68.0 and 75.5, 20 70.4 and 77.4.  By experts, groups and blocks multiplied: 2048 (16 tokens, 8 of 4096 x
+    // 1024, top 2) 39.5 and 41.3, 2560 55.2 and 56.0, 3520 58.9 and 62.3, 4096 60.5 and 64.4, 8192 90.5 and 94.8: below
+    // the border too it gains a little.
+    // Light where most experts have few tokens: 16 tokens, 64 of 2048 x 768, top 4: 18.1, wide 21.2; 64 tokens,
+    // 64 of 2048 x 1024, top 6: 49.6 and 41.9; and while wide blocks are under one a compute unit, from where on
+    // either may be ahead by up to 5 %.  Whole calls: one token, top 8 of 64, I = 1024: H = 3584 29.0 and 30.3, 4096
+    // 30.1 and 31.1; one token, top 6 of 64, 5120 x 1536: 54.8 and 57.8; 4 tokens, top 8 of 128, 4096 x 1408: 133.2
+    // and 131.5; 8 tokens, top 4 of 32, 4096 x 1024: 75.8 and 74.9; 16 tokens, top 2 of 128, 4096 x 1024: 93.6 and 91.0.
     const int64_t entries = (E < n ? E : n) + n / (16 * pieces), blocks128 = ceil_div(H, 128);
     if (n >= E && blocks128 >= 20 && E * ceil_div(I, 128) * blocks128 >= 4096 && entries <= (T <= 64 ? 64 : 128) * kMaxTopK / 8) {
         plan.down = Fp8MoePlan::kMany;
