@@ -18,6 +18,8 @@ float8_e8m0fnu): a product, its gradient, and a mixture-of-experts layer for few
     Wq, s_w, WqT, s_wT = fp8_quantize_weight_block(W, transposed=True)
     dX, dW = fp8_matmul_block_backward(dY, X, WqT, s_wT)
     Y, ids, p = fp8_moe_block(X, logits, W13q, s_w13, W2q, s_w2, top_k=8)
+
+No call is recorded for autograd: outputs do not require a gradient, whatever the inputs do.
 """
 from __future__ import annotations
 
@@ -571,7 +573,10 @@ def fp8_matmul_block_workspace_bytes(M: int, K: int, N: int) -> int:
 
 def fp8_matmul_block(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, Y: Optional[torch.Tensor] = None,
                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Y = X W (M x N) of X (M x K, fp16/bf16), coded per row in groups of 128, with a converted weight."""
+    """Y = X W (M x N) of X (M x K, fp16/bf16), coded per row in groups of 128, with a converted weight.
+
+    Like every call here it is not recorded for autograd: Y does not require a gradient, whatever X does.  A
+    training step calls fp8_matmul_block_backward itself, or both from a torch.autograd.Function."""
     if _fp8_arg(X, "X", _T16).dim() != 2:
         raise ValueError("X must be 2-D")
     M, K = X.shape

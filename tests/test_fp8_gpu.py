@@ -352,6 +352,38 @@ def test_backward_one_of_the_two_and_empty_sums():
     assert e.shape == (0, K) and z.shape == (K, N) and not z.any()
 
 
+def test_product_and_gradient_under_autograd():
+    """The calls are not recorded; a torch.autograd.Function of the two is, and its gradients are those of
+    the product (exact here: whole numbers)."""
+    M, K, N, dt = 40, 272, 136, torch.bfloat16
+    g = gen(15)
+    X, W, dY = (lattice(g, *sh, dt=dt).cuda() for sh in ((M, K), (K, N), (M, N)))
+
+    class Product(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, X, W):
+            Wq, s, WqT, sT = lm.fp8_quantize_weight_block(W, transposed=True)
+            ctx.save_for_backward(X, WqT, sT)
+            return lm.fp8_matmul_block(X, Wq, s)
+
+        @staticmethod
+        def backward(ctx, dY):
+            X, WqT, sT = ctx.saved_tensors
+            return lm.fp8_matmul_block_backward(dY.contiguous(), X, WqT, sT, need_dx=ctx.needs_input_grad[0],
+                                                need_dw=ctx.needs_input_grad[1])
+
+    X.requires_grad_()
+    W.requires_grad_()
+    Y = Product.apply(X, W)
+    Y.backward(dY)
+    x, w, dy = X.detach().double(), W.detach().double(), dY.double()
+    assert torch.equal(Y, (x @ w).float().to(dt))
+    assert torch.equal(X.grad, (dy @ w.t()).float().to(dt)) and torch.equal(W.grad, (x.t() @ dy).float().to(dt))
+    Wq, s = lm.fp8_quantize_weight_block(W)
+    plain = lm.fp8_matmul_block(X, Wq, s)
+    assert not plain.requires_grad and torch.equal(plain, Y)
+
+
 @pytest.mark.parametrize("M,K,N", [(3, 144, 72), (200, 400, 264)])
 def test_backward_writes_its_outputs_alone(M, K, N):
     g = gen(11)
