@@ -252,6 +252,49 @@ def test_matmul_of_very_many_columns():
     torch.cuda.empty_cache()
 
 
+def trits(seed, *shape, dt=torch.float16):
+    """-1, 0, 1 at random, on the GPU: sums of up to 2^24 products are exact in fp32."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randint(-1, 2, shape, generator=g, device="cuda", dtype=torch.int8).to(dt)
+
+
+# the longest sum, in each kernel; (2056 x 2056: tiles of 256 in parts, against rows of it alone)
+@pytest.mark.parametrize("M,N", [(1, 8), (3, 2056), (20, 136), (64, 72), (130, 136), (300, 264), (2056, 2056)])
+def test_matmul_longest_sum(M, N):
+    K, dt = 1 << 22, torch.bfloat16
+    print(f"\n[case] matmul longest sum {M}x{K}x{N}", flush=True)
+    X, W = trits(M, M, K, dt=dt), trits(M + N, K, N, dt=dt)
+    Wq, s = lm.fp8_quantize_weight_block(W)
+    Y = lm.fp8_matmul_block(X, Wq, s)
+    if M > 2000:
+        want = torch.cat([lm.fp8_matmul_block(X[a: a + 128], Wq, s) for a in range(0, M, 128)])
+    else:
+        want = sum(X[:, a: a + (1 << 18)].double() @ W[a: a + (1 << 18)].double() for a in range(0, K, 1 << 18)).float().to(dt)
+    assert Y.any() and torch.equal(Y, want)
+    del X, W, Wq, s, Y, want
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M,K,N", [(1 << 22, 144, 136), (1 << 22, 16, 8), (40, 1 << 22, 72), (40, 144, 1 << 22)])
+def test_longest_sides_of_product_and_gradient(M, K, N):
+    print(f"\n[case] longest side {M}x{K}x{N}", flush=True)
+    dt = torch.float16
+    X, W, dY = trits(1, M, K, dt=dt), trits(2, K, N, dt=dt), trits(3, M, N, dt=dt)
+    Wq, s, WqT, sT = lm.fp8_quantize_weight_block(W, transposed=True)
+    step = 1 << 18
+
+    def product(a, b):  # the sum in pieces
+        return sum(a[:, i: i + step].double() @ b[i: i + step].double() for i in range(0, a.shape[1], step)).float().to(dt)
+
+    assert torch.equal(lm.fp8_matmul_block(X, Wq, s), product(X, W))
+    dX, dW = lm.fp8_matmul_block_backward(dY, X, WqT, sT)
+    assert torch.equal(dX, product(dY, W.t().contiguous()))
+    assert torch.equal(dW, product(X.t().contiguous(), dY))
+    del X, W, dY, Wq, s, WqT, sT, dX, dW
+    torch.cuda.empty_cache()
+
+
 def framed(shape, dt, fill=3.0):
     """(view, whole): a buffer of the shape between canaries."""
     n = math.prod(shape)
