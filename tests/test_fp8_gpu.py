@@ -738,6 +738,67 @@ def test_moe_smallest_scales(which, T, H, I, E, k):
     moe_check((X * (2.0 ** 122 if which == 0 else 1)).to(dt), l, w, k, False)
 
 
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 1 << 22, 16, 1, 1), (2, 1 << 22, 16, 5, 2), (20, 1 << 22, 16, 2, 1), (1, 16, 1 << 21, 8, 2),
+                                       (70, 48, 1 << 21, 3, 2), (128, 16, 1 << 20, 2, 2), (12, 16, 1 << 20, 9, 2)])
+@pytest.mark.parametrize("dt", DTS)
+def test_moe_longest_sides(dt, T, H, I, E, k):
+    """The longest rows, with values at 48 features and inner columns alone, both ends among them: a sum of
+    zeros is exact, so the reference and its bound are those of the 48."""
+    print(f"\n[case] moe longest sides {dt} T={T} H={H} I={I} E={E} k={k}", flush=True)
+    g = gen(T + H + I + E)
+
+    def some(n):
+        at = torch.cat([torch.arange(8), torch.randint(0, n, (32,), generator=g), n - 1 - torch.arange(8)])
+        return at.unique()
+
+    def codes(*shape):  # magnitudes 0.5 to 1.875
+        return (torch.randint(0x30, 0x40, shape, generator=g) + 128 * torch.randint(0, 2, shape, generator=g)).to(torch.uint8).cuda()
+
+    hs, cs = some(H), some(I)
+    x = randn(g, T, len(hs)).to(dt)
+    X = torch.zeros(T, H, dtype=dt)
+    X[:, hs] = x
+    rows = torch.cat([cs, I + cs])
+    c13, c2 = codes(E, len(rows), len(hs)), codes(E, H, len(cs))
+    W13 = torch.zeros(E, 2 * I, ref.pitch(H), dtype=torch.uint8, device="cuda")
+    W2 = torch.zeros(E, H, ref.pitch(I), dtype=torch.uint8, device="cuda")
+    for e in range(E):
+        W13[e, rows.cuda()[:, None], hs.cuda()] = c13[e]
+        W2[e][:, cs.cuda()] = c2[e]
+    s13 = torch.zeros(E, -(-2 * I // 128), ref.sp(H), dtype=torch.uint8)
+    s2 = torch.zeros(E, -(-H // 128), ref.sp(I), dtype=torch.uint8)
+    s13[:, :, : -(-H // 128)] = torch.randint(125, 128, (E, s13.shape[1], -(-H // 128)), generator=g, dtype=torch.uint8)
+    s2[:, :, : -(-I // 128)] = torch.randint(125, 128, (E, s2.shape[1], -(-I // 128)), generator=g, dtype=torch.uint8)
+    l = 2 * randn(g, T, E)
+    Y, ids, p = lm.fp8_moe_block(X.cuda(), l.cuda(), W13.view(F8), s13.cuda().view(E8), W2.view(F8), s2.cuda().view(E8), top_k=k)
+    v13 = torch.exp2(s13.double() - 127)[:, rows // 128][:, :, hs // 128] * c13.cpu().view(F8).float().double()
+    v2 = torch.exp2(s2.double() - 127)[:, torch.arange(H) // 128][:, :, cs // 128] * c2.cpu().view(F8).float().double()
+    y, err, rids, rp = _moe_of(x, l, v13, v2, k)
+    assert torch.equal(ids.cpu(), rids)
+    assert ((p.cpu().double() - rp).abs() <= 64 * 2.0 ** -24 * rp).all()
+    ref.assert_close(Y, y, err + y.abs() * 128 * 2.0 ** -24, "y")
+    del W13, W2, c13, c2, Y
+    torch.cuda.empty_cache()
+
+
+def _moe_of(x, l, v13, v2, k):
+    """fp8_ref.moe (renormalized), and its bound, for outputs of another width than the inputs."""
+    t, I = x.dtype, v2.shape[2]
+    ids, p = ref.route(l, k, True)
+    y = torch.zeros(x.shape[0], v2.shape[1], dtype=torch.float64)
+    err = torch.zeros_like(y)
+    for i, j in (ids >= 0).nonzero().tolist():
+        e, xi = int(ids[i, j]), x[i].double()
+        (g, u), (dg, du) = (v13[e] @ xi).split(I), (x.shape[1] * 2.0 ** -23 * (v13[e].abs() @ xi.abs())).split(I)
+        h = g * torch.sigmoid(g) * u
+        hr = h.to(torch.float32).to(t).double()
+        dh = 1.1 * dg * (u.abs() + du) + (g * torch.sigmoid(g)).abs() * du + 16 * 2.0 ** -23 * h.abs()
+        dh = dh + (hr - h).abs() + 2 * ref.U[t] * h.abs() + ref.TINY[t]
+        y[i] += p[i, j] * (v2[e] @ hr)
+        err[i] += p[i, j] * (v2[e].abs() @ dh + (I + 64) * 2.0 ** -23 * (v2[e].abs() @ (hr.abs() + dh)))
+    return y, err, ids, p
+
+
 def test_moe_writes_its_outputs_alone():
     T, H, I, E, k = 7, 272, 144, 6, 2
     g = gen(12)
