@@ -335,7 +335,8 @@ int int8_matmul_noalloc(const void* X, int64_t M, int64_t K, int dtype, const in
  *                                    multiple of 4, zero past the last group.
  * Non-finite values are outside the contract of the results, but not of the memory accesses:
  * one makes every output whose sum it enters not finite, the finite values of its group are
- * coded with its scale (as good as zero), and nothing else changes.
+ * coded with its scale (2^120 or 2^121: zero, but for bf16 values near the type's largest), and
+ * nothing else changes.
  *
  * Shapes and conventions as above (K a multiple of 16, N of 8), with a bound of 2^22 on M and
  * on the length of a sum in place of the int32 one (LLMINT8_ERANGE).
@@ -382,7 +383,7 @@ int fp8_matmul_block(const void* X, int64_t M, int64_t K, int dtype, const uint8
  *   dX  out, M x K, dtype, 16-byte aligned; NULL: not wanted (WqT and wT_scale may be NULL then).
  *   dW  out, K x N, dtype, 16-byte aligned; NULL: not wanted (X may be NULL then).
  *   workspace  fp8_matmul_block_backward_workspace_bytes(M, K, N, dX != NULL, dW != NULL) bytes,
- *              16-byte aligned.
+ *              16-byte aligned; free between calls, one for each call that may run at the same time.
  * An empty sum (N = 0 for dX, M = 0 for dW) gives zeros (no workspace needed).  M, K and N are at
  * most 2^22 (LLMINT8_ERANGE).
  */
@@ -415,7 +416,7 @@ int fp8_matmul_block_backward(const void* dY, const void* X, int64_t M, int64_t 
  *   topk_ids      out: T x top_k int32, the chosen experts, -1 where there is none.
  *   topk_weights  out: T x top_k fp32, p_j, 0 where there is none.
  *   workspace     fp8_moe_block_workspace_bytes(...) bytes (0 for invalid arguments), 16-byte
- *                 aligned.
+ *                 aligned; free between calls, one for each call that may run at the same time.
  * T = 0 or H = 0 is a no-op; I = 0 gives Y = 0.
  */
 size_t fp8_moe_block_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
