@@ -1231,17 +1231,18 @@ UpGrid up_grid(const Fp8MoeArgs& p, int columns, int64_t enough, int64_t longest
 template <int DT, int MG, bool MANY = false>
 hipError_t launch_up(const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream) {
     const int chunk = plan.chunk, n_zero = plan.parts > 1 ? (int)plan.blocks : 0;
+    const bool routes = MG == 0 && p.T <= kRouteTokens && p.T * p.k <= kRouteChoices;
+    if (!routes) {  // (what comes next reads the experts that this one writes)
+        moe_route_kernel<<<(unsigned)p.T, 64, 0, stream>>>(p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     if constexpr (MG == 0) {
         const UpGrid g = up_grid(p, 8, 1024, 3);
         constexpr int kThreads = 64 * kLightUpWaves;
-        if (p.T <= kRouteTokens && p.T * p.k <= kRouteChoices) {
-            moe_up_light_kernel<DT, true><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk, n_zero);
-        } else {
-            moe_route_kernel<<<(unsigned)p.T, 64, 0, stream>>>(p);
-            moe_up_light_kernel<DT, false><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk, n_zero);
-        }
+        if (routes) moe_up_light_kernel<DT, true><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk, n_zero);
+        else moe_up_light_kernel<DT, false><<<(unsigned)g.grid, kThreads, 0, stream>>>(p, g.spans, g.span, g.by_pair, chunk, n_zero);
     } else {
-        moe_route_kernel<<<(unsigned)p.T, 64, 0, stream>>>(p);
         if constexpr (MANY) {
             const int spans = (int)ceil_div(p.I, 128);
             moe_up_many_kernel<DT, MG><<<(unsigned)(1 + p.E * spans), 512, 0, stream>>>(p, spans, chunk, n_zero);
