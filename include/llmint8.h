@@ -59,7 +59,8 @@
  *                            quantize_weight_groups, group_xpass, gemm_group,
  *                            gemm_group_small, fill_zero, block_quantize, block_dequantize,
  *                            scratch_symbol, fp8_weight, fp8_rows, fp8_gemm, fp8_cols,
- *                            fp8_gemm_dx, fp8_gemm_dw, fp8_moe).
+ *                            fp8_gemm_dx, fp8_gemm_dw, fp8_moe, mxfp4_rows, mxfp4_columns,
+ *                            mxfp4_values, mxfp4_gemm, rmsnorm, rmsnorm_backward).
  */
 #ifndef LLMINT8_H
 #define LLMINT8_H
@@ -72,6 +73,9 @@ extern "C" {
 #endif
 
 enum llmint8_dtype { LLMINT8_F16 = 0, LLMINT8_BF16 = 1 };
+
+/* Codes that rmsnorm_forward makes of its output. */
+enum llmint8_codes { LLMINT8_CODES_NONE = 0, LLMINT8_CODES_FP8_BLOCK = 1, LLMINT8_CODES_MXFP4 = 2 };
 
 enum llmint8_status {
     LLMINT8_OK = 0,
@@ -424,6 +428,132 @@ int fp8_moe_block(const void* X, int64_t T, int64_t H, int dtype, const float* l
                   int renormalize, const uint8_t* W13q, const uint8_t* w13_scale, const uint8_t* W2q,
                   const uint8_t* w2_scale, int64_t I, void* Y, int32_t* topk_ids, float* topk_weights, void* workspace,
                   size_t workspace_bytes, void* stream);
+
+/*
+ * fp8_matmul_block on rows that are coded already (rmsnorm_forward with LLMINT8_CODES_FP8_BLOCK):
+ *   Xq       in : M rows of codes over K, 16-byte aligned.
+ *   x_scale  in : the rows' scales, ceil(K/128) times fp8_row_scale_pitch(M) bytes (M rounded up to a
+ *                 multiple of 64), 4-byte aligned: the byte of row m and group g is at
+ *                 g * fp8_row_scale_pitch(M) + (m/64) * 64 + (m%16) * 4 + (m/16)%4; what the bytes of
+ *                 rows past the last hold has no effect.
+ * Everything else as fp8_matmul_block, on its own workspace size; the result is bit for bit that of
+ * fp8_matmul_block on the values that were coded wherever both take the same kernel.
+ */
+int64_t fp8_row_scale_pitch(int64_t rows);
+size_t fp8_matmul_block_coded_workspace_bytes(int64_t M, int64_t K, int64_t N);
+int fp8_matmul_block_coded(const uint8_t* Xq, const uint8_t* x_scale, int64_t M, int64_t K, int dtype, const uint8_t* Wq,
+                           const uint8_t* w_scale, int64_t N, void* Y, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * Microscaled 4-bit floating point (e2m1 codes, a power-of-two scale per 32 values): the conversion,
+ * its inverse, and the product of two matrices of this format.
+ *
+ * The format.  A group of 32 consecutive values of a row (the sum's axis) with the largest magnitude a
+ * has the scale s = 2^e, the smallest power of two >= 2^-127 with a <= 7 s, kept as its e8m0 byte
+ * e + 127.  The code of x is the e2m1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) nearest to
+ * x / s, ties to even, magnitudes above 6 to 6; it stands for code * s.  A group with a value that is
+ * not finite has the byte 255 and stands for NaN as a whole; nothing else changes.
+ * Both operands of a product have the same layout:
+ *   codes   R rows of fp4_code_pitch(n) bytes: two codes to a byte, the first in the low half, n
+ *           rounded up to a multiple of 256 values, zero past n;
+ *   scales  ceil(R/32) rows of fp4_scale_pitch(n) bytes: tiles of 32 rows x 256 values, 256 bytes each;
+ *           the byte of row r and group g (of 32 values) is in row r/32 at
+ *           (g/8) * 256 + (g%4) * 64 + (r%16) * 4 + (g%8/4) * 2 + r%32/16;
+ *           zero past the last row and the last group.
+ * Codes of other origin may be used too: the products read the groups past n (whose codes have to be
+ * zero with a byte below 255) and no value of the rows past the last.
+ *
+ * Shapes and conventions as above (K a multiple of 16, N of 8), with M, K and N at most 2^22; calls
+ * with 2^24 or more tiles of 32 rows x 256 values to code, or of 128 x 128 outputs, are refused
+ * (LLMINT8_ERANGE).
+ */
+int64_t fp4_code_pitch(int64_t n);
+int64_t fp4_scale_pitch(int64_t n);
+
+/*
+ * Conversion of a matrix A (R x C, dtype, row-major):
+ *   columns = 0   groups along its rows (activations; a weight kept one row per output, N x K): R rows
+ *                 of codes over C; C a multiple of 16.
+ *   columns != 0  groups along its columns (a weight K x N): C rows of codes over R; R a multiple of
+ *                 16, C of 8.
+ *   q       out: the codes (16-byte aligned).
+ *   scale   out: the scales (4-byte aligned).
+ * R = 0 or C = 0 is a no-op.
+ */
+int mxfp4_quantize(const void* A, int64_t R, int64_t C, int dtype, int columns, uint8_t* q, uint8_t* scale, void* stream);
+
+/*
+ * The values that R rows of codes over n values (a multiple of 16) stand for, each rounded once:
+ *   A  out: R x n, dtype, row-major, 16-byte aligned.
+ */
+int mxfp4_dequantize(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t n, int dtype, void* A, void* stream);
+
+/*
+ * Y = X W on that format:
+ *   Y[m,n] = RN_T( sum over groups g of s_x[m,g] s_w[n,g] sum over k in g of Xq[m,k] Wq[n,k] ),
+ * X (16 bits) coded per row inside the call.  A group's sum of products is exact, the groups meet in
+ * fp32.
+ *   Wq, w_scale  in : N rows of codes over K, and their scales.
+ *   Y            out: M x N, dtype, 16-byte aligned.
+ *   workspace    mxfp4_matmul_workspace_bytes(M, K, N) bytes, 16-byte aligned; free between calls
+ *                (nothing in it has to survive, or to be zero), one for each call that may run at the
+ *                same time.
+ * M = 0 or N = 0 is a no-op; K = 0 gives Y = 0 (no workspace needed).  Outputs and workspace overlap
+ * nothing (LLMINT8_EINVAL).
+ *
+ * mxfp4_matmul_coded: the same of rows that are coded already (Xq, x_scale: M rows over K), as
+ * mxfp4_quantize and rmsnorm_forward make them.  The codes hold all that enters the sums, so X's rows
+ * coded once can serve several weights.
+ */
+size_t mxfp4_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N);
+int mxfp4_matmul(const void* X, int64_t M, int64_t K, int dtype, const uint8_t* Wq, const uint8_t* w_scale, int64_t N, void* Y,
+                 void* workspace, size_t workspace_bytes, void* stream);
+size_t mxfp4_matmul_coded_workspace_bytes(int64_t M, int64_t K, int64_t N);
+int mxfp4_matmul_coded(const uint8_t* Xq, const uint8_t* x_scale, int64_t M, int64_t K, int dtype, const uint8_t* Wq,
+                       const uint8_t* w_scale, int64_t N, void* Y, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, before a product: its output in 16 bits, as the
+ * codes of one of the formats above, or both.
+ *   h = RN_T(x + residual)  (x itself without a residual),
+ *   y = RN_T( h / sqrt(mean(h^2) + eps) * weight ),  the mean over a row's K values, in fp32,
+ * and the codes of y per row, in groups of 128 (e4m3) or 32 (e2m1) along K: bit for bit those which
+ * fp8_matmul_block and mxfp4_matmul make of y.
+ *   X, residual  in : M x K, dtype, 16-byte aligned; residual may be NULL.
+ *   weight       in : K, dtype, 16-byte aligned.
+ *   eps          positive and finite, else LLMINT8_EINVAL.
+ *   H        out: M x K, dtype, 16-byte aligned, h; NULL: not wanted (and it has to be NULL without a
+ *            residual).  H may be X or residual itself (in place); other overlaps are refused.
+ *   Y        out: M x K, dtype, 16-byte aligned, y; NULL: not wanted.
+ *   format   LLMINT8_CODES_NONE (Yq and y_scale NULL), LLMINT8_CODES_FP8_BLOCK or LLMINT8_CODES_MXFP4.
+ *   Yq       out: M rows of codes over K, 16-byte aligned.
+ *   y_scale  out: the rows' scales (4-byte aligned): ceil(K/128) times fp8_row_scale_pitch(M) bytes as
+ *            fp8_matmul_block_coded takes them, or ceil(M/32) rows of fp4_scale_pitch(K) bytes; zero
+ *            past the last row.
+ * A row of zeros gives zeros.  Squares are summed in fp32: a row whose sum of squares passes 2^128 gives
+ * zeros.  A row with a value that is not finite gives NaN or zeros in that row alone.  M and K are at
+ * most 2^22 (LLMINT8_ERANGE); K a multiple of 16.
+ */
+int rmsnorm_forward(const void* X, const void* residual, const void* weight, int64_t M, int64_t K, int dtype, float eps, void* H,
+                    void* Y, int format, uint8_t* Yq, uint8_t* y_scale, void* stream);
+
+/*
+ * Its gradient.  With r = 1 / sqrt(mean(h^2) + eps) and d = dy * weight:
+ *   dX = RN_T( r (d - h r^2 mean(d h)) + dh ),   dW = RN_T( sum over the rows of dy h r ).
+ * dX is the gradient of X and of residual alike.
+ *   dY   in : M x K, dtype, 16-byte aligned, the gradient of Y.
+ *   H    in : M x K, h of the forward call (X itself where there was no residual).
+ *   dH   in : M x K, the gradient that arrives at h by another way (the residual stream); may be NULL.
+ *   dX   out: M x K, dtype, 16-byte aligned.
+ *   dW   out: K, dtype, 16-byte aligned; NULL: not wanted.
+ *   workspace  rmsnorm_backward_workspace_bytes(M, K, dW != NULL) bytes, 16-byte aligned (none without
+ *              dW); free between calls, one for each call that may run at the same time.
+ * M = 0 gives dW = 0.  Sums run in a fixed order.  Outputs and workspace overlap nothing (LLMINT8_EINVAL).
+ */
+size_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t K, int need_dw);
+int rmsnorm_backward(const void* dY, const void* H, const void* weight, const void* dH, int64_t M, int64_t K, int dtype, float eps,
+                     void* dX, void* dW, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,16 @@ float8_e8m0fnu): a product, its gradient, and a mixture-of-experts layer for few
     dX, dW = fp8_matmul_block_backward(dY, X, WqT, s_wT)
     Y, ids, p = fp8_moe_block(X, logits, W13q, s_w13, W2q, s_w2, top_k=8)
 
+Microscaled 4-bit floating point (e2m1 codes, float8_e8m0fnu scales per 32 values), and the norm that
+feeds either product
+
+    Wq, s_w = mxfp4_quantize(W, columns=True)           # W: K x N
+    Y = mxfp4_matmul(X, Wq, s_w)
+    Xq, s_x, _, H = rmsnorm_quantize(X, weight, residual=R, format="mxfp4")
+    Y = mxfp4_matmul_coded(Xq, s_x, Wq, s_w, X.dtype)   # or format="fp8" and fp8_matmul_block_coded
+    Y, H = rmsnorm(X, weight, residual=R)
+    dX, dweight = rmsnorm_backward(dY, H, weight, dH=dH)
+
 No call is recorded for autograd: outputs do not require a gradient, whatever the inputs do.
 """
 from __future__ import annotations
@@ -86,6 +96,20 @@ _SIGNATURES = {
     "fp8_matmul_block": (_I, [_P, _I64, _I64, _I, _P, _P, _I64, _P, _P, _SZ, _P]),
     "fp8_matmul_block_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _I]),
     "fp8_matmul_block_backward": (_I, [_P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "fp8_row_scale_pitch": (_I64, [_I64]),
+    "fp8_matmul_block_coded_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "fp8_matmul_block_coded": (_I, [_P, _P, _I64, _I64, _I, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "fp4_code_pitch": (_I64, [_I64]),
+    "fp4_scale_pitch": (_I64, [_I64]),
+    "mxfp4_quantize": (_I, [_P, _I64, _I64, _I, _I, _P, _P, _P]),
+    "mxfp4_dequantize": (_I, [_P, _P, _I64, _I64, _I, _P, _P]),
+    "mxfp4_matmul_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "mxfp4_matmul": (_I, [_P, _I64, _I64, _I, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "mxfp4_matmul_coded_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "mxfp4_matmul_coded": (_I, [_P, _P, _I64, _I64, _I, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "rmsnorm_forward": (_I, [_P, _P, _P, _I64, _I64, _I, _F, _P, _P, _I, _P, _P, _P]),
+    "rmsnorm_backward_workspace_bytes": (_SZ, [_I64, _I64, _I]),
+    "rmsnorm_backward": (_I, [_P, _P, _P, _P, _I64, _I64, _I, _F, _P, _P, _P, _SZ, _P]),
     "fp8_moe_block_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
     "fp8_moe_block": (_I, [_P, _I64, _I64, _I, _P, _I64, _I64, _I, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
 }
@@ -704,6 +728,258 @@ def fp8_moe_block(X: torch.Tensor, logits: torch.Tensor, W13q: torch.Tensor, w13
     return Y, ids, p
 
 
+def fp8_row_scale_pitch(rows: int) -> int:
+    """Bytes of the scales of coded rows for a group of 128 values: rows rounded up to a multiple of 64."""
+    return -(-rows // 64) * 64
+
+
+def fp8_matmul_block_coded_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().fp8_matmul_block_coded_workspace_bytes(M, K, N))
+
+
+def fp8_matmul_block_coded(Xq: torch.Tensor, x_scale: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
+                           dtype: torch.dtype = torch.bfloat16, Y: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """fp8_matmul_block of rows that are coded already: Xq M x code_pitch(K) e4m3 and x_scale code_pitch(K) / 128
+    x fp8_row_scale_pitch(M) e8m0, as rmsnorm_quantize(format="fp8") gives them; Y is of `dtype`."""
+    return _coded_product("fp8_matmul_block_coded", Xq, x_scale, Wq, w_scale, dtype, Y, workspace, stream)
+
+
+# ---- microscaled 4-bit floating point
+
+_E2M1 = (torch.uint8, torch.float4_e2m1fn_x2)
+
+
+def fp4_code_pitch(n: int) -> int:
+    """Bytes of a row of e2m1 codes over n values: n rounded up to a multiple of 256, two to a byte."""
+    return -(-n // 256) * 128
+
+
+def fp4_scale_pitch(n: int) -> int:
+    """Bytes of the scales of 32 rows over n values: tiles of 256 bytes per 256 values."""
+    return -(-n // 256) * 256
+
+
+def mxfp4_quantize(X: torch.Tensor, columns: bool = False, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """X (R x C, fp16/bf16) -> (codes R x fp4_code_pitch(C) uint8, scales ceil(R/32) x fp4_scale_pitch(C) e8m0), in
+    groups of 32 along each row; with columns along each column (a weight K x N): codes C x fp4_code_pitch(R)."""
+    if _fp8_arg(X, "X", _T16).dim() != 2:
+        raise ValueError("X must be 2-D")
+    R, C = X.shape
+    dev = X.device
+    on = _fp8_on(dev, stream)
+    if on is not None:
+        with on:
+            return mxfp4_quantize(X, columns)
+    rows, n = (C, R) if columns else (R, C)
+    q = torch.empty((rows, fp4_code_pitch(n)), dtype=torch.uint8, device=dev)
+    s = torch.empty((-(-rows // 32), fp4_scale_pitch(n)), dtype=_E8M0[0], device=dev)
+    rc = lib().mxfp4_quantize(X.data_ptr(), R, C, _DT[X.dtype], int(columns), q.data_ptr(), s.data_ptr(),
+                              torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "mxfp4_quantize")
+    return q, s
+
+
+def mxfp4_dequantize(q: torch.Tensor, scale: torch.Tensor, n: int, dtype: torch.dtype = torch.bfloat16,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values (R x n, `dtype`) that R rows of e2m1 codes over n values stand for."""
+    if dtype not in _T16:
+        raise TypeError(f"dtype must be fp16 or bf16, got {dtype}")
+    if _fp8_arg(q, "q", _E2M1).dim() != 2 or q.shape[1] != fp4_code_pitch(n):
+        raise ValueError(f"q must be R x {fp4_code_pitch(n)} for n = {n}, got {tuple(q.shape)}")
+    R = q.shape[0]
+    dev = q.device
+    on = _fp8_on(dev, stream)
+    if on is not None:
+        with on:
+            return mxfp4_dequantize(q, scale, n, dtype, out)
+    _fp8_arg(scale, "scale", _E8M0, (-(-R // 32), fp4_scale_pitch(n)), dev)
+    if out is None:
+        out = torch.empty((R, n), dtype=dtype, device=dev)
+    else:
+        _fp8_arg(out, "out", (dtype,), (R, n), dev)
+    rc = lib().mxfp4_dequantize(q.data_ptr(), scale.data_ptr(), R, n, _DT[dtype], out.data_ptr(),
+                                torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "mxfp4_dequantize")
+    return out
+
+
+def mxfp4_matmul_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().mxfp4_matmul_workspace_bytes(M, K, N))
+
+
+def mxfp4_matmul(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, Y: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y = X W (M x N) of X (M x K, fp16/bf16), coded per row in groups of 32 inside the call, with a converted weight
+    (Wq N x fp4_code_pitch(K), w_scale ceil(N/32) x fp4_scale_pitch(K))."""
+    if _fp8_arg(X, "X", _T16).dim() != 2:
+        raise ValueError("X must be 2-D")
+    M, K = X.shape
+    dev = X.device
+    on = _fp8_on(dev, stream)
+    if on is not None:
+        with on:
+            return mxfp4_matmul(X, Wq, w_scale, Y, workspace)
+    if _fp8_arg(Wq, "Wq", _E2M1, device=dev).dim() != 2 or Wq.shape[1] != fp4_code_pitch(K):
+        raise ValueError(f"Wq must be N x {fp4_code_pitch(K)} for K = {K}, got {tuple(Wq.shape)}")
+    N = Wq.shape[0]
+    _fp8_arg(w_scale, "w_scale", _E8M0, (-(-N // 32), fp4_scale_pitch(K)), dev)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=X.dtype, device=dev)
+    else:
+        _fp8_arg(Y, "Y", (X.dtype,), (M, N), dev)
+    L = lib()
+    ws, at, size = _fp8_workspace(workspace, L.mxfp4_matmul_workspace_bytes(M, K, N), dev)
+    rc = L.mxfp4_matmul(X.data_ptr(), M, K, _DT[X.dtype], Wq.data_ptr(), w_scale.data_ptr(), N, Y.data_ptr(),
+                        at, size, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "mxfp4_matmul")
+    return Y
+
+
+def mxfp4_matmul_coded_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().mxfp4_matmul_coded_workspace_bytes(M, K, N))
+
+
+def mxfp4_matmul_coded(Xq: torch.Tensor, x_scale: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
+                       dtype: torch.dtype = torch.bfloat16, Y: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """mxfp4_matmul of rows that are coded already (Xq M x fp4_code_pitch(K), x_scale ceil(M/32) x fp4_scale_pitch(K), as
+    mxfp4_quantize and rmsnorm_quantize(format="mxfp4") give them); Y is of `dtype`."""
+    return _coded_product("mxfp4_matmul_coded", Xq, x_scale, Wq, w_scale, dtype, Y, workspace, stream)
+
+
+def _coded_product(name, Xq, x_scale, Wq, w_scale, dtype, Y, workspace, stream):
+    four = name == "mxfp4_matmul_coded"
+    codes = _E2M1 if four else _E4M3
+    if dtype not in _T16:
+        raise TypeError(f"dtype must be fp16 or bf16, got {dtype}")
+    if _fp8_arg(Xq, "Xq", codes).dim() != 2 or Xq.shape[1] % 128:
+        raise ValueError(f"Xq must be M rows of a multiple of 128 bytes, got {tuple(Xq.shape)}")
+    M, pitch = Xq.shape
+    dev = Xq.device
+    on = _fp8_on(dev, stream)
+    if on is not None:
+        with on:
+            return _coded_product(name, Xq, x_scale, Wq, w_scale, dtype, Y, workspace, None)
+    if _fp8_arg(Wq, "Wq", codes, device=dev).dim() != 2 or Wq.shape[1] != pitch:
+        raise ValueError(f"Wq must be N x {pitch} as Xq is, got {tuple(Wq.shape)}")
+    N = Wq.shape[0]
+    if four:
+        K = 2 * pitch  # the codes past the true one are zeros
+        _fp8_arg(x_scale, "x_scale", _E8M0, (-(-M // 32), fp4_scale_pitch(K)), dev)
+        _fp8_arg(w_scale, "w_scale", _E8M0, (-(-N // 32), fp4_scale_pitch(K)), dev)
+    else:
+        K = pitch
+        _fp8_arg(x_scale, "x_scale", _E8M0, (pitch // 128, fp8_row_scale_pitch(M)), dev)
+        _fp8_arg(w_scale, "w_scale", _E8M0, (-(-N // 128), fp8_scale_pitch(K)), dev)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=dtype, device=dev)
+    else:
+        _fp8_arg(Y, "Y", (dtype,), (M, N), dev)
+    L = lib()
+    ws, at, size = _fp8_workspace(workspace, getattr(L, name + "_workspace_bytes")(M, K, N), dev)
+    rc = getattr(L, name)(Xq.data_ptr(), x_scale.data_ptr(), M, K, _DT[dtype], Wq.data_ptr(), w_scale.data_ptr(), N,
+                          Y.data_ptr(), at, size, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, name)
+    return Y
+
+
+# ---- root-mean-square norm
+
+_FORMATS = {None: 0, "fp8": 1, "mxfp4": 2}
+
+
+def _norm(X, weight, residual, eps, format, keep, H, stream):
+    if _fp8_arg(X, "X", _T16).dim() != 2:
+        raise ValueError("X must be 2-D")
+    M, K = X.shape
+    dev, t = X.device, X.dtype
+    on = _fp8_on(dev, stream)
+    if on is not None:
+        with on:
+            return _norm(X, weight, residual, eps, format, keep, H, None)
+    _fp8_arg(weight, "weight", (t,), (K,), dev)
+    if residual is not None:
+        _fp8_arg(residual, "residual", (t,), (M, K), dev)
+        if H is None:
+            H = torch.empty((M, K), dtype=t, device=dev)
+        else:
+            _fp8_arg(H, "H", (t,), (M, K), dev)
+    elif H is not None:
+        raise ValueError("H is the sum with a residual: without one it would be X")
+    Y = torch.empty((M, K), dtype=t, device=dev) if keep else None
+    q = s = None
+    if format == "fp8":
+        q = torch.empty((M, fp8_code_pitch(K)), dtype=_E4M3[0], device=dev)
+        s = torch.empty((-(-K // 128), fp8_row_scale_pitch(M)), dtype=_E8M0[0], device=dev)
+    elif format == "mxfp4":
+        q = torch.empty((M, fp4_code_pitch(K)), dtype=torch.uint8, device=dev)
+        s = torch.empty((-(-M // 32), fp4_scale_pitch(K)), dtype=_E8M0[0], device=dev)
+    rc = lib().rmsnorm_forward(X.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), M, K, _DT[t], eps,
+                               None if H is None else H.data_ptr(), None if Y is None else Y.data_ptr(), _FORMATS[format],
+                               None if q is None else q.data_ptr(), None if s is None else s.data_ptr(),
+                               torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "rmsnorm_forward")
+    return q, s, Y, H
+
+
+def rmsnorm(X: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+            H: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(Y, H): H = X + residual (M x K, fp16/bf16; None without a residual) and its root-mean-square norm Y times
+    weight.  H may be given, also X or residual itself (in place)."""
+    _, _, Y, H = _norm(X, weight, residual, eps, None, True, H, stream)
+    return Y, H
+
+
+def rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     format: str = "fp8", keep: bool = False, H: Optional[torch.Tensor] = None, stream=None):
+    """(Yq, y_scale, Y, H): rmsnorm's Y as codes and scales, "fp8" for fp8_matmul_block_coded or "mxfp4" for
+    mxfp4_matmul_coded; Y in 16 bits too with keep (a weight gradient needs it), else None."""
+    if format not in ("fp8", "mxfp4"):
+        raise ValueError(f'format must be "fp8" or "mxfp4", got {format!r}')
+    return _norm(X, weight, residual, eps, format, keep, H, stream)
+
+
+def rmsnorm_backward_workspace_bytes(M: int, K: int, need_dw: bool = True) -> int:
+    return int(lib().rmsnorm_backward_workspace_bytes(M, K, int(need_dw)))
+
+
+def rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tensor, dH: Optional[torch.Tensor] = None,
+                     eps: float = 1e-6, need_dw: bool = True, dX: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(dX, dweight) of rmsnorm: H its sum (X where there was no residual), dH the gradient that arrives at H by
+    another way; dX is the gradient of X and of residual alike."""
+    if _fp8_arg(dY, "dY", _T16).dim() != 2:
+        raise ValueError("dY must be 2-D")
+    M, K = dY.shape
+    dev, t = dY.device, dY.dtype
+    on = _fp8_on(dev, stream)
+    if on is not None:
+        with on:
+            return rmsnorm_backward(dY, H, weight, dH, eps, need_dw, dX, workspace)
+    _fp8_arg(H, "H", (t,), (M, K), dev)
+    _fp8_arg(weight, "weight", (t,), (K,), dev)
+    if dH is not None:
+        _fp8_arg(dH, "dH", (t,), (M, K), dev)
+    if dX is None:
+        dX = torch.empty((M, K), dtype=t, device=dev)
+    else:
+        _fp8_arg(dX, "dX", (t,), (M, K), dev)
+    dW = torch.empty((K,), dtype=t, device=dev) if need_dw else None
+    L = lib()
+    ws, at, size = _fp8_workspace(workspace, L.rmsnorm_backward_workspace_bytes(M, K, int(need_dw)), dev)
+    rc = L.rmsnorm_backward(dY.data_ptr(), H.data_ptr(), weight.data_ptr(), None if dH is None else dH.data_ptr(), M, K, _DT[t], eps,
+                            dX.data_ptr(), None if dW is None else dW.data_ptr(), at, size, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "rmsnorm_backward")
+    return dX, dW
+
+
 __all__ = [
     "int8_quantize_weight", "int8_matmul", "int8_matmul_noalloc", "int8_matmul_stats", "int8_matmul_prepare", "int8_matmul_products", "int8_matmul_workspace_bytes",
     "int8_matmul_workspace_layout", "int8_matmul_accumulators", "workspace_views", "LLMInt8Error", "lib",
@@ -713,4 +989,8 @@ __all__ = [
     "fp8_code_pitch", "fp8_scale_pitch", "fp8_quantize_weight_block", "fp8_matmul_block",
     "fp8_matmul_block_workspace_bytes", "fp8_matmul_block_backward", "fp8_matmul_block_backward_workspace_bytes",
     "fp8_moe_block", "fp8_moe_block_workspace_bytes",
+    "fp8_row_scale_pitch", "fp8_matmul_block_coded", "fp8_matmul_block_coded_workspace_bytes",
+    "fp4_code_pitch", "fp4_scale_pitch", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_matmul", "mxfp4_matmul_workspace_bytes",
+    "mxfp4_matmul_coded", "mxfp4_matmul_coded_workspace_bytes", "rmsnorm", "rmsnorm_quantize", "rmsnorm_backward",
+    "rmsnorm_backward_workspace_bytes",
 ]

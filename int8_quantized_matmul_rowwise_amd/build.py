@@ -28,7 +28,8 @@ LIB = os.path.join(HERE, "libllmint8.so")
 PROBE_LIB = os.path.join(HERE, "libllmint8_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 SOURCES = ["api.hip", "xpass.hip", "weight.hip", "gemm.hip", "gemm_small.hip", "codec.hip", "gemm_group.hip",
-           "gemm_group_small.hip", "api_fp8.hip", "fp8_codec.hip", "fp8_gemm.hip", "fp8_moe.hip"]
+           "gemm_group_small.hip", "api_fp8.hip", "fp8_codec.hip", "fp8_gemm.hip", "fp8_moe.hip",
+           "api_mxfp4.hip", "mxfp4_codec.hip", "mxfp4_gemm.hip", "api_norm.hip", "rmsnorm.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -30,6 +30,19 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+struct Range {
+    const void* p;
+    size_t n;
+};
+
+// whether any of the outputs overlaps another range (outputs first, then inputs)
+bool clash(const Range* r, int outputs, int all) {
+    for (int i = 0; i < outputs; ++i)
+        for (int j = i + 1; j < all; ++j)
+            if (overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return true;
+    return false;
+}
+
 // ---- failure injection and logging (host layer only; both read the environment per call)
 //   LLMINT8_FAULT=<stage>  dry run: nothing is enqueued; every stage the call reaches before
 //                          the named one counts as done, the named one as failed, so the

@@ -26,19 +26,6 @@ int check_fp8_shape(int64_t M, int64_t K, int64_t N, int dtype) {
 size_t code_bytes(int64_t rows, int64_t sum) { return (size_t)rows * (size_t)fp8_pitch(sum); }
 size_t scale_bytes(int64_t rows, int64_t sum) { return (size_t)rows * (size_t)fp8_scale_pitch_of(sum); }
 
-struct Range {
-    const void* p;
-    size_t n;
-};
-
-// whether any of the outputs overlaps another range (outputs first, then inputs)
-bool clash(const Range* r, int outputs, int all) {
-    for (int i = 0; i < outputs; ++i)
-        for (int j = i + 1; j < all; ++j)
-            if (overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return true;
-    return false;
-}
-
 }  // namespace
 
 LLMINT8_API int64_t fp8_code_pitch(int64_t n) { return n < 0 ? 0 : fp8_pitch(n); }
@@ -72,13 +59,13 @@ struct Fp8Layout {
     size_t xq, s_x, counters, partial, total;
 };
 
-Fp8Layout fp8_layout(int64_t M, int64_t K, int64_t N) {
+Fp8Layout fp8_layout(int64_t M, int64_t K, int64_t N, bool coded) {
     Fp8Layout L;
-    L.plan = fp8_plan(M, N, ceil_div(K, 128), true, false);
-    const bool fused = L.plan.kind == Fp8Plan::kFused;
+    L.plan = fp8_plan(M, N, ceil_div(K, 128), !coded, false);
+    const bool codes = !coded && L.plan.kind != Fp8Plan::kFused;  // X's, in the workspace
     L.xq = 0;
-    L.s_x = align_up(fused ? 0 : code_bytes(M, K));
-    L.counters = align_up(L.s_x + (fused ? 0 : (size_t)fp8_row_scale_bytes(M, K)));
+    L.s_x = align_up(codes ? code_bytes(M, K) : 0);
+    L.counters = align_up(L.s_x + (codes ? (size_t)fp8_row_scale_bytes(M, K) : 0));
     L.partial = align_up(L.counters + (L.plan.split > 1 ? (size_t)L.plan.tiles * 4 : 0));
     L.total = align_up(L.partial + (size_t)L.plan.partial_bytes);
     return L;
@@ -94,49 +81,68 @@ const char* plan_name(const Fp8Plan& p) {
     }
 }
 
-}  // namespace
-
-LLMINT8_API size_t fp8_matmul_block_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-    if (check_fp8_shape(M, K, N, LLMINT8_F16) || M == 0 || N == 0 || K == 0) return 0;
-    return fp8_layout(M, K, N).total;
-}
-
-LLMINT8_API int fp8_matmul_block(const void* X, int64_t M, int64_t K, int dtype, const uint8_t* Wq,
-                                 const uint8_t* w_scale, int64_t N, void* Y, void* workspace, size_t workspace_bytes,
-                                 void* stream) {
+// X: 16 bits, or (coded) rows of codes with x_scale
+int product(const char* name, const void* X, const uint8_t* x_scale, bool coded, int64_t M, int64_t K, int dtype, const uint8_t* Wq,
+            const uint8_t* w_scale, int64_t N, void* Y, void* workspace, size_t workspace_bytes, void* stream) {
     int rc = check_fp8_shape(M, K, N, dtype);
     if (rc) return rc;
     if (M == 0 || N == 0) return LLMINT8_OK;
     if (!Y || !aligned(Y, 16)) return LLMINT8_EINVAL;
     hipStream_t st = (hipStream_t)stream;
     if (K == 0) {
-        log_call("fp8_matmul_block", M, K, N, dtype, NAN, "empty sum");
+        log_call(name, M, K, N, dtype, NAN, "empty sum");
         return hip_status(stage("fill_zero", [&] { return launch_fill_zero((float*)Y, M * N / 2, st); }));
     }
     if (!X || !aligned(X, 16) || !Wq || !aligned(Wq, 16) || !w_scale || !aligned(w_scale, 4)) return LLMINT8_EINVAL;
-    const Fp8Layout L = fp8_layout(M, K, N);
+    if (coded && (!x_scale || !aligned(x_scale, 4))) return LLMINT8_EINVAL;
+    const Fp8Layout L = fp8_layout(M, K, N, coded);
     if (L.total > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < L.total)) return LLMINT8_EWORKSPACE;
     const Range r[] = {{Y, (size_t)M * (size_t)N * 2},
                        {workspace, L.total},
-                       {X, (size_t)M * (size_t)K * 2},
+                       {X, coded ? code_bytes(M, K) : (size_t)M * (size_t)K * 2},
                        {Wq, code_bytes(N, K)},
-                       {w_scale, scale_bytes(ceil_div(N, 128), K)}};
-    if (clash(r, 2, 5)) return LLMINT8_EINVAL;
-    log_call("fp8_matmul_block", M, K, N, dtype, NAN, plan_name(L.plan));
+                       {w_scale, scale_bytes(ceil_div(N, 128), K)},
+                       {x_scale, coded ? (size_t)fp8_row_scale_bytes(M, K) : 0}};
+    if (clash(r, 2, 6)) return LLMINT8_EINVAL;
+    log_call(name, M, K, N, dtype, NAN, plan_name(L.plan));
     uint8_t* ws = (uint8_t*)workspace;
     int32_t* counters = L.plan.split > 1 ? (int32_t*)(ws + L.counters) : nullptr;
+    const int64_t n_counters = counters ? L.plan.tiles : 0;
     hipError_t e = hipSuccess;
-    if (L.plan.kind != Fp8Plan::kFused)
-        e = stage("fp8_rows", [&] {
-            return launch_fp8_rows(dtype, X, M, K, ws + L.xq, ws + L.s_x, counters, counters ? L.plan.tiles : 0, st);
-        });
+    if (coded) {
+        if (counters) e = stage("fill_zero", [&] { return launch_fill_zero((float*)counters, n_counters, st); });
+    } else if (L.plan.kind != Fp8Plan::kFused) {
+        e = stage("fp8_rows", [&] { return launch_fp8_rows(dtype, X, M, K, ws + L.xq, ws + L.s_x, counters, n_counters, st); });
+    }
     if (e == hipSuccess)
         e = stage("fp8_gemm", [&] {
-            const Fp8GemmArgs a{ws + L.xq, Wq, M, N, fp8_pitch(K), ws + L.s_x, w_scale, fp8_scale_pitch_of(K), (uint16_t*)Y,
-                                (const uint16_t*)X, K, counters, (float*)(ws + L.partial)};
+            const Fp8GemmArgs a{coded ? (const uint8_t*)X : ws + L.xq, Wq, M, N, fp8_pitch(K), coded ? x_scale : ws + L.s_x, w_scale,
+                                fp8_scale_pitch_of(K), (uint16_t*)Y, coded ? nullptr : (const uint16_t*)X, K, counters, (float*)(ws + L.partial)};
             return launch_fp8_gemm(dtype, a, L.plan, st);
         });
     return hip_status(e);
+}
+
+size_t product_workspace(int64_t M, int64_t K, int64_t N, bool coded) {
+    if (check_fp8_shape(M, K, N, LLMINT8_F16) || M == 0 || N == 0 || K == 0) return 0;
+    return fp8_layout(M, K, N, coded).total;
+}
+
+}  // namespace
+
+LLMINT8_API size_t fp8_matmul_block_workspace_bytes(int64_t M, int64_t K, int64_t N) { return product_workspace(M, K, N, false); }
+LLMINT8_API size_t fp8_matmul_block_coded_workspace_bytes(int64_t M, int64_t K, int64_t N) { return product_workspace(M, K, N, true); }
+
+LLMINT8_API int fp8_matmul_block(const void* X, int64_t M, int64_t K, int dtype, const uint8_t* Wq,
+                                 const uint8_t* w_scale, int64_t N, void* Y, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    return product("fp8_matmul_block", X, nullptr, false, M, K, dtype, Wq, w_scale, N, Y, workspace, workspace_bytes, stream);
+}
+
+LLMINT8_API int fp8_matmul_block_coded(const uint8_t* Xq, const uint8_t* x_scale, int64_t M, int64_t K, int dtype, const uint8_t* Wq,
+                                       const uint8_t* w_scale, int64_t N, void* Y, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+    return product("fp8_matmul_block_coded", Xq, x_scale, true, M, K, dtype, Wq, w_scale, N, Y, workspace, workspace_bytes, stream);
 }
 
 // ---- dX = dY W^T, dW = X^T dY

@@ -221,6 +221,14 @@ struct Fp8Plan {
 // x16: A is at hand in 16 bits (it may be coded in the product kernel); rowb: B has a scale per row
 Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t nk, bool x16, bool rowb);
 
+// parts of `groups` groups, at most `wanted`, such that none is empty and each has at least `least`
+inline int sum_parts(int64_t groups, int64_t wanted, int64_t least) {
+    const int64_t s = groups / least < wanted ? groups / least : wanted;
+    if (s < 2) return 1;
+    const int64_t part = (groups + s - 1) / s;
+    return (int)((groups + part - 1) / part);
+}
+
 struct Fp8GemmArgs {
     const uint8_t* A;  // M rows of codes
     const uint8_t* B;  // N rows of codes
@@ -269,5 +277,49 @@ struct Fp8MoeArgs {
     float* partial;
 };
 hipError_t launch_fp8_moe(int dt, const Fp8MoeArgs& p, const Fp8MoePlan& plan, hipStream_t stream);
+
+// ---- e2m1 codes with power-of-two scales per 32 values (the format: mxfp4_common.hpp)
+// q R x pitch(C) and s: X's rows coded (also zeroes zero[0, n_zero), as launch_fp8_rows)
+hipError_t launch_mxfp4_rows(int dt, const void* X, int64_t R, int64_t C, uint8_t* q, uint8_t* s, int32_t* zero, int64_t n_zero,
+                             hipStream_t stream);
+// q C x pitch(R) and s: the columns of A (R x C) coded
+hipError_t launch_mxfp4_columns(int dt, const void* A, int64_t R, int64_t C, uint8_t* q, uint8_t* s, hipStream_t stream);
+// A rows x n: the values that codes and scales stand for
+hipError_t launch_mxfp4_values(int dt, const uint8_t* q, const uint8_t* s, int64_t rows, int64_t n, void* A, hipStream_t stream);
+
+// A product of M x N outputs over nk lines of 256 values: the kinds of Fp8Plan, and its arguments (there
+// is no spitch: both operands have their scales in tiles).  x16: as fp8_plan
+using Mxfp4Plan = Fp8Plan;
+using Mxfp4GemmArgs = Fp8GemmArgs;
+Mxfp4Plan mxfp4_plan(int64_t M, int64_t N, int64_t nk, bool x16);
+hipError_t launch_mxfp4_gemm(int dt, const Mxfp4GemmArgs& p, const Mxfp4Plan& plan, hipStream_t stream);
+
+// ---- root-mean-square norm
+struct NormArgs {
+    const uint16_t *X, *R, *W;  // R: the residual, or NULL
+    int64_t M, K;
+    float eps;
+    uint16_t *H, *Y;  // the sum and the norm, each or NULL
+    int format;       // of the codes: enum llmint8_codes
+    uint8_t *q, *s;
+};
+hipError_t launch_rmsnorm(int dt, const NormArgs& p, hipStream_t stream);
+
+// How the gradient runs: rows split over `groups` workgroups, each with a row of partial sums of dW.
+struct NormBackwardPlan {
+    bool whole;  // a workgroup holds a whole row
+    int threads, vectors;  // whole: threads of a workgroup, pieces of 8 columns of a thread
+    int64_t groups;
+};
+NormBackwardPlan rmsnorm_backward_plan(int64_t M, int64_t K);
+struct NormBackwardArgs {
+    const uint16_t *dY, *H, *W, *dH;  // dH: the gradient that arrives at H, or NULL
+    int64_t M, K;
+    float eps;
+    uint16_t *dX, *dW;  // dW: or NULL
+    float* partial;     // groups x K, where dW is wanted
+    float* rows;        // !whole, where dW is wanted: M
+};
+hipError_t launch_rmsnorm_backward(int dt, const NormBackwardArgs& p, const NormBackwardPlan& plan, hipStream_t stream);
 
 }  // namespace llmint8

@@ -1,0 +1,423 @@
+// Root-mean-square norm with the residual's addition, its output in 16 bits and as codes, and its
+// gradient:
+//   h = RN_T(x + residual),  r = 1 / sqrt(mean(h^2) + eps),  y = RN_T(h r w),
+//   d = dy w,  dx = RN_T(r (d - h r^2 mean(d h)) + dh),  dw = RN_T(sum over rows of dy h r).
+// Sums in fp32.  The codes are those of y after its rounding, so that they are the ones which the
+// products make of y themselves.
+//
+// Both are bound by memory: a row is read once into registers (8 columns a piece and thread, a
+// workgroup a row), summed over lanes, then waves, and written.
+#include "../../include/llmint8.h"
+#include "launch.hpp"
+#include "mxfp4_common.hpp"
+
+namespace llmint8 {
+
+namespace {
+
+constexpr int kMaxVectors = 8;          // pieces of 8 columns a thread holds (whole rows)
+constexpr int64_t kMaxGrid = 1 << 20;   // workgroups of a launch: 2^32 threads are too many
+
+// The sum over the 64 lanes, in all of them, in a fixed order.
+__device__ __forceinline__ float wave_sum(float v) {
+#define LLMINT8_ROR(N) v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + N, 0xf, 0xf, false))
+    LLMINT8_ROR(8);
+    LLMINT8_ROR(4);
+    LLMINT8_ROR(2);
+    LLMINT8_ROR(1);
+#undef LLMINT8_ROR
+    const auto swapped = [](uint32_t x, bool far) {  // (a bit cast of a vector's element itself would take the first one)
+        const auto p = far ? __builtin_amdgcn_permlane32_swap(x, x, false, false) : __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        const uint32_t a = p[0], b = p[1];
+        return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+    };
+    v = swapped(__builtin_bit_cast(uint32_t, v), false);
+    return swapped(__builtin_bit_cast(uint32_t, v), true);
+}
+
+// N sums over the workgroup, in all of its threads; red: N x 16 words that the call before last may
+// have used.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float (*red)[16]) {
+    const int waves = blockDim.x >> 6, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+    if (waves == 1) return;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[i][w] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = red[i][0];
+        for (int j = 1; j < waves; ++j) v[i] += red[i][j];
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ float low(uint32_t v) { return to_f32<DT>((uint16_t)v); }
+template <int DT>
+__device__ __forceinline__ float high(uint32_t v) { return to_f32<DT>((uint16_t)(v >> 16)); }
+template <int DT>
+__device__ __forceinline__ uint32_t pack(float a, float b) { return (uint32_t)from_f32<DT>(a) | ((uint32_t)from_f32<DT>(b) << 16); }
+
+template <int DT>
+__device__ __forceinline__ u32x4 add(const u32x4& a, const u32x4& b) {
+    u32x4 o;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] = pack<DT>(low<DT>(a[d]) + low<DT>(b[d]), high<DT>(a[d]) + high<DT>(b[d]));
+    return o;
+}
+template <int DT>
+__device__ __forceinline__ float squares(const u32x4& h, float s) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const float a = low<DT>(h[d]), b = high<DT>(h[d]);
+        s = __builtin_fmaf(a, a, s);
+        s = __builtin_fmaf(b, b, s);
+    }
+    return s;
+}
+template <int DT>
+__device__ __forceinline__ u32x4 scaled(const u32x4& h, const u32x4& w, float r) {
+    u32x4 o;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] = pack<DT>(low<DT>(h[d]) * r * low<DT>(w[d]), high<DT>(h[d]) * r * high<DT>(w[d]));
+    return o;
+}
+
+// The workgroup's place in its XCD's run of rows: neighbours share the lines of the codes' scales.
+__device__ __forceinline__ int64_t in_runs(int64_t id, int64_t n) {
+    const int64_t xcd = id & 7, per = n >> 3, rem = n & 7;
+    return xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
+}
+
+// Eight neighbouring values y from column c of row `row` on, as codes and scales.
+template <int DT, int FORMAT>
+__device__ __forceinline__ void store_codes(const NormArgs& p, int64_t row, int64_t c, const u32x4& y) {
+    if constexpr (FORMAT == LLMINT8_CODES_FP8_BLOCK) {
+        const int64_t pitch = fp8_pitch(p.K);
+        const uint32_t e = e8m0_of(to_f32<DT>((uint16_t)row_max(max_pattern(magnitudes(y)))));
+        if (c >= pitch) return;
+        *(u32x2*)(p.q + row * pitch + c) = e4m3x8<DT>(y, e8m0_value(e));
+        if ((threadIdx.x & 15) == 0) p.s[fp8_row_scale_at(row, c >> 7, p.M)] = (uint8_t)e;
+    } else if constexpr (FORMAT == LLMINT8_CODES_MXFP4) {
+        const int64_t pitch = fp4_pitch(p.K);
+        const uint32_t e = fp4_scale_byte<DT>(quad_max(max_pattern(magnitudes(y))));
+        if (c >= 2 * pitch) return;
+        *(uint32_t*)(p.q + row * pitch + (c >> 1)) = e2m1x8<DT>(y, e8m0_value(e));
+        if ((threadIdx.x & 3) == 0) p.s[fp4_scale_at(row, c >> 5, fp4_scale_pitch_of(p.K))] = (uint8_t)e;
+    }
+}
+
+// The scales of the rows that fill the last tile of scales: zeros.
+template <int FORMAT>
+__device__ __forceinline__ void clear_scales(const NormArgs& p) {
+    constexpr bool four = FORMAT == LLMINT8_CODES_MXFP4;
+    const int64_t pad = round_up(p.M, four ? 32 : 64) - p.M, groups = four ? fp4_scale_pitch_of(p.K) / 32 : ceil_div(p.K, 128);
+    for (int64_t i = threadIdx.x; i < pad * groups; i += blockDim.x) {
+        const int64_t row = p.M + i / groups, g = i % groups;
+        p.s[four ? fp4_scale_at(row, g, fp4_scale_pitch_of(p.K)) : fp8_row_scale_at(row, g, p.M)] = 0;
+    }
+}
+
+// A workgroup a row, V pieces of 8 columns a thread.  (p.H may be p.X or p.R: each element is read
+// before it is written, by the same thread.)
+template <int DT, int V, int FORMAT>
+__global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs p) {
+    __shared__ float red[2][1][16];
+    const int T = blockDim.x, tid = threadIdx.x;
+    const float n = (float)p.K;
+    int turn = 0;
+    for (int64_t row = in_runs(blockIdx.x, gridDim.x); row < p.M; row += gridDim.x, turn ^= 1) {
+        u32x4 h[V], w[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int64_t c = ((int64_t)v * T + tid) * 8;
+            h[v] = w[v] = u32x4{0u, 0u, 0u, 0u};
+            if (c < p.K) {  // K is a multiple of 8
+                h[v] = *(const u32x4*)(p.X + row * p.K + c);
+                w[v] = *(const u32x4*)(p.W + c);
+            }
+        }
+        if (p.R) {
+            u32x4 b[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int64_t c = ((int64_t)v * T + tid) * 8;
+                b[v] = u32x4{0u, 0u, 0u, 0u};
+                if (c < p.K) b[v] = *(const u32x4*)(p.R + row * p.K + c);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int64_t c = ((int64_t)v * T + tid) * 8;
+                h[v] = add<DT>(h[v], b[v]);
+                if (p.H && c < p.K) *(u32x4*)(p.H + row * p.K + c) = h[v];
+            }
+        }
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[0] = squares<DT>(h[v], s[0]);
+        group_sum(s, red[turn]);
+        const float r = 1.0f / __builtin_sqrtf(s[0] / n + p.eps);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int64_t c = ((int64_t)v * T + tid) * 8;
+            const u32x4 y = scaled<DT>(h[v], w[v], r);
+            if (p.Y && c < p.K) *(u32x4*)(p.Y + row * p.K + c) = y;
+            store_codes<DT, FORMAT>(p, row, c, y);
+        }
+        if (FORMAT != LLMINT8_CODES_NONE && row == p.M - 1) clear_scales<FORMAT>(p);
+    }
+}
+
+// Rows longer than a workgroup's registers: read twice.
+template <int DT, int FORMAT>
+__global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs p) {
+    __shared__ float red[2][1][16];
+    const float n = (float)p.K;
+    int turn = 0;
+    for (int64_t row = in_runs(blockIdx.x, gridDim.x); row < p.M; row += gridDim.x, turn ^= 1) {
+        float s[1] = {0.0f};
+        for (int64_t c = 8 * threadIdx.x; c < p.K; c += 8192) {
+            u32x4 h = *(const u32x4*)(p.X + row * p.K + c);
+            if (p.R) {
+                h = add<DT>(h, *(const u32x4*)(p.R + row * p.K + c));
+                if (p.H) *(u32x4*)(p.H + row * p.K + c) = h;
+            }
+            s[0] = squares<DT>(h, s[0]);
+        }
+        group_sum(s, red[turn]);
+        const float r = 1.0f / __builtin_sqrtf(s[0] / n + p.eps);
+        for (int64_t base = 0; base < p.K; base += 8192) {
+            const int64_t c = base + 8 * threadIdx.x;
+            u32x4 y = {0u, 0u, 0u, 0u};
+            if (c < p.K) {
+                u32x4 h;  // (H may have taken the place of X or R)
+                if (p.R && p.H) h = *(const u32x4*)(p.H + row * p.K + c);
+                else h = *(const u32x4*)(p.X + row * p.K + c);
+                if (p.R && !p.H) h = add<DT>(h, *(const u32x4*)(p.R + row * p.K + c));
+                y = scaled<DT>(h, *(const u32x4*)(p.W + c), r);
+                if (p.Y) *(u32x4*)(p.Y + row * p.K + c) = y;
+            }
+            store_codes<DT, FORMAT>(p, row, c, y);
+        }
+        if (FORMAT != LLMINT8_CODES_NONE && row == p.M - 1) clear_scales<FORMAT>(p);
+    }
+}
+
+// ---- gradient
+
+// Pieces of a row of the gradient: sums over it, then dx and what the row adds to dw.
+template <int DT>
+__device__ __forceinline__ void row_sums(const u32x4& h, const u32x4& dy, const u32x4& w, float (&s)[2]) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const float a = low<DT>(h[d]), b = high<DT>(h[d]);
+        s[0] = __builtin_fmaf(a, a, s[0]);
+        s[0] = __builtin_fmaf(b, b, s[0]);
+        s[1] = __builtin_fmaf(low<DT>(dy[d]) * low<DT>(w[d]), a, s[1]);
+        s[1] = __builtin_fmaf(high<DT>(dy[d]) * high<DT>(w[d]), b, s[1]);
+    }
+}
+template <int DT>
+__device__ __forceinline__ u32x4 row_dx(const u32x4& h, const u32x4& dy, const u32x4& w, const u32x4& dh, float r, float m) {
+    u32x4 o;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const float a = r * (low<DT>(dy[d]) * low<DT>(w[d]) - low<DT>(h[d]) * m) + low<DT>(dh[d]);
+        const float b = r * (high<DT>(dy[d]) * high<DT>(w[d]) - high<DT>(h[d]) * m) + high<DT>(dh[d]);
+        o[d] = pack<DT>(a, b);
+    }
+    return o;
+}
+template <int DT>
+__device__ __forceinline__ void row_dw(const u32x4& h, const u32x4& dy, float r, float* acc) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        acc[2 * d] = __builtin_fmaf(low<DT>(dy[d]), low<DT>(h[d]) * r, acc[2 * d]);
+        acc[2 * d + 1] = __builtin_fmaf(high<DT>(dy[d]), high<DT>(h[d]) * r, acc[2 * d + 1]);
+    }
+}
+
+// A workgroup a row at a time, every gridDim.x-th one; dw's sums stay in registers over its rows.
+template <int DT, int V, bool DW>
+__global__ __launch_bounds__(1024) void rmsnorm_backward_kernel(NormBackwardArgs p) {
+    __shared__ float red[2][2][16];
+    const int T = blockDim.x, tid = threadIdx.x;
+    const float n = (float)p.K;
+    u32x4 w[V];
+    float acc[V][8] = {};
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int64_t c = ((int64_t)v * T + tid) * 8;
+        w[v] = u32x4{0u, 0u, 0u, 0u};
+        if (c < p.K) w[v] = *(const u32x4*)(p.W + c);
+    }
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
+        u32x4 h[V], dy[V], dh[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int64_t c = ((int64_t)v * T + tid) * 8;
+            h[v] = dy[v] = dh[v] = u32x4{0u, 0u, 0u, 0u};
+            if (c < p.K) {
+                h[v] = *(const u32x4*)(p.H + row * p.K + c);
+                dy[v] = *(const u32x4*)(p.dY + row * p.K + c);
+                if (p.dH) dh[v] = *(const u32x4*)(p.dH + row * p.K + c);
+            }
+        }
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) row_sums<DT>(h[v], dy[v], w[v], s);
+        group_sum(s, red[turn]);
+        const float r = 1.0f / __builtin_sqrtf(s[0] / n + p.eps), m = r * r * (s[1] / n);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int64_t c = ((int64_t)v * T + tid) * 8;
+            if (c < p.K) *(u32x4*)(p.dX + row * p.K + c) = row_dx<DT>(h[v], dy[v], w[v], dh[v], r, m);
+            if constexpr (DW) row_dw<DT>(h[v], dy[v], r, acc[v]);
+        }
+    }
+    if constexpr (DW) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int64_t c = ((int64_t)v * T + tid) * 8;
+            if (c >= p.K) continue;
+            float* to = p.partial + (int64_t)blockIdx.x * p.K + c;
+            *(v4f*)to = v4f{acc[v][0], acc[v][1], acc[v][2], acc[v][3]};
+            *(v4f*)(to + 4) = v4f{acc[v][4], acc[v][5], acc[v][6], acc[v][7]};
+        }
+    }
+}
+
+// Rows longer than a workgroup's registers: read twice; r of each row is kept for dw.
+template <int DT>
+__global__ __launch_bounds__(1024) void rmsnorm_backward_long_kernel(NormBackwardArgs p) {
+    __shared__ float red[2][2][16];
+    const float n = (float)p.K;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
+        float s[2] = {0.0f, 0.0f};
+        for (int64_t c = 8 * threadIdx.x; c < p.K; c += 8192)
+            row_sums<DT>(*(const u32x4*)(p.H + row * p.K + c), *(const u32x4*)(p.dY + row * p.K + c), *(const u32x4*)(p.W + c), s);
+        group_sum(s, red[turn]);
+        const float r = 1.0f / __builtin_sqrtf(s[0] / n + p.eps), m = r * r * (s[1] / n);
+        if (threadIdx.x == 0 && p.rows) p.rows[row] = r;
+        for (int64_t c = 8 * threadIdx.x; c < p.K; c += 8192) {
+            const u32x4 none = {0u, 0u, 0u, 0u};
+            const u32x4 dh = p.dH ? *(const u32x4*)(p.dH + row * p.K + c) : none;
+            *(u32x4*)(p.dX + row * p.K + c) =
+                row_dx<DT>(*(const u32x4*)(p.H + row * p.K + c), *(const u32x4*)(p.dY + row * p.K + c), *(const u32x4*)(p.W + c), dh, r, m);
+        }
+    }
+}
+// dw's sums over every gridDim.y-th row: 2048 columns a workgroup.
+template <int DT>
+__global__ __launch_bounds__(256) void rmsnorm_dw_long_kernel(NormBackwardArgs p) {
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (c >= p.K) return;
+    float acc[8] = {};
+    for (int64_t row = blockIdx.y; row < p.M; row += gridDim.y)
+        row_dw<DT>(*(const u32x4*)(p.H + row * p.K + c), *(const u32x4*)(p.dY + row * p.K + c), p.rows[row], acc);
+    float* to = p.partial + (int64_t)blockIdx.y * p.K + c;
+    *(v4f*)to = v4f{acc[0], acc[1], acc[2], acc[3]};
+    *(v4f*)(to + 4) = v4f{acc[4], acc[5], acc[6], acc[7]};
+}
+
+// dw from the partial sums (groups x K): a workgroup 64 columns, 16 runs of rows side by side, then
+// joined in their order.
+template <int DT>
+__global__ __launch_bounds__(256) void rmsnorm_dw_join_kernel(const float* __restrict__ partial, int64_t groups, int64_t K, uint16_t* __restrict__ dW) {
+    __shared__ v4f sums[16][16];
+    const int cc = threadIdx.x & 15, rr = threadIdx.x >> 4;
+    const int64_t c = (int64_t)blockIdx.x * 64 + 4 * cc, run = ceil_div(groups, 16);
+    v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < K) {
+        const int64_t end = (rr + 1) * run < groups ? (rr + 1) * run : groups;
+        for (int64_t g = rr * run; g < end; ++g) s += *(const v4f*)(partial + g * K + c);
+    }
+    sums[rr][cc] = s;
+    __syncthreads();
+    if (rr == 0 && c < K) {
+        for (int i = 1; i < 16; ++i) s += sums[i][cc];
+        *(u32x2*)(dW + c) = u32x2{pack<DT>(s[0], s[1]), pack<DT>(s[2], s[3])};
+    }
+}
+
+template <int DT, int FORMAT>
+void norm_launch(const NormArgs& p, hipStream_t stream) {
+    const unsigned grid = (unsigned)(p.M < kMaxGrid ? p.M : kMaxGrid);
+    // the columns that a row's codes cover: the codes' padding is written by the threads past K
+    const int64_t pieces = ceil_div(FORMAT == LLMINT8_CODES_NONE ? p.K : round_up(p.K, FORMAT == LLMINT8_CODES_MXFP4 ? 256 : 128), 8);
+    auto threads = [&](int v) { return (unsigned)round_up(ceil_div(pieces, v), 64); };
+    if (pieces <= 1024) rmsnorm_kernel<DT, 1, FORMAT><<<grid, threads(1), 0, stream>>>(p);
+    else if (pieces <= 2048) rmsnorm_kernel<DT, 2, FORMAT><<<grid, threads(2), 0, stream>>>(p);
+    else if (pieces <= 4096) rmsnorm_kernel<DT, 4, FORMAT><<<grid, threads(4), 0, stream>>>(p);
+    else if (pieces <= 1024 * kMaxVectors) rmsnorm_kernel<DT, kMaxVectors, FORMAT><<<grid, threads(kMaxVectors), 0, stream>>>(p);
+    else rmsnorm_long_kernel<DT, FORMAT><<<grid, 1024, 0, stream>>>(p);
+}
+
+template <int DT>
+void norm_launch(const NormArgs& p, hipStream_t stream) {
+    if (p.format == LLMINT8_CODES_NONE) norm_launch<DT, LLMINT8_CODES_NONE>(p, stream);
+    else if (p.format == LLMINT8_CODES_FP8_BLOCK) norm_launch<DT, LLMINT8_CODES_FP8_BLOCK>(p, stream);
+    else norm_launch<DT, LLMINT8_CODES_MXFP4>(p, stream);
+}
+
+template <int DT, bool DW>
+void backward_launch(const NormBackwardArgs& p, const NormBackwardPlan& plan, hipStream_t stream) {
+    const unsigned grid = (unsigned)plan.groups, threads = (unsigned)plan.threads;
+    if (plan.vectors == 1) rmsnorm_backward_kernel<DT, 1, DW><<<grid, threads, 0, stream>>>(p);
+    else if (plan.vectors == 2) rmsnorm_backward_kernel<DT, 2, DW><<<grid, threads, 0, stream>>>(p);
+    else rmsnorm_backward_kernel<DT, 4, DW><<<grid, threads, 0, stream>>>(p);
+}
+
+template <int DT>
+hipError_t backward_launch(const NormBackwardArgs& p, const NormBackwardPlan& plan, hipStream_t stream) {
+    if (!plan.whole) {
+        rmsnorm_backward_long_kernel<DT><<<(unsigned)(p.M < kMaxGrid ? p.M : kMaxGrid), 1024, 0, stream>>>(p);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess || !p.dW) return e;
+        rmsnorm_dw_long_kernel<DT><<<dim3((unsigned)ceil_div(p.K, 2048), (unsigned)plan.groups), 256, 0, stream>>>(p);
+    } else if (p.dW) {
+        backward_launch<DT, true>(p, plan, stream);
+    } else {
+        backward_launch<DT, false>(p, plan, stream);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !p.dW) return e;
+    rmsnorm_dw_join_kernel<DT><<<(unsigned)ceil_div(p.K, 64), 256, 0, stream>>>(p.partial, plan.groups, p.K, p.dW);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(int dt, const NormArgs& p, hipStream_t stream) {
+    if (p.M == 0 || p.K == 0) return hipSuccess;
+    if (dt == F16) norm_launch<F16>(p, stream);
+    else norm_launch<BF16>(p, stream);
+    return hipGetLastError();
+}
+
+NormBackwardPlan rmsnorm_backward_plan(int64_t M, int64_t K) {
+    const int64_t pieces = ceil_div(K, 8);
+    NormBackwardPlan p{pieces <= 4096, 0, 0, 0};
+    if (!p.whole) {
+        p.groups = M < 64 ? M : 64;
+        return p;
+    }
+    p.vectors = pieces <= 512 ? 1 : (pieces <= 2048 ? 2 : 4);
+    p.threads = (int)round_up(ceil_div(pieces, p.vectors), 64);
+    const int64_t most = 256 * (p.threads <= 512 ? 2 : 1);
+    p.groups = M < most ? M : most;
+    return p;
+}
+
+hipError_t launch_rmsnorm_backward(int dt, const NormBackwardArgs& p, const NormBackwardPlan& plan, hipStream_t stream) {
+    if (p.M == 0 || p.K == 0) return hipSuccess;
+    return dt == F16 ? backward_launch<F16>(p, plan, stream) : backward_launch<BF16>(p, plan, stream);
+}
+
+}  // namespace llmint8
