@@ -49,7 +49,7 @@ LLMINT8_API int rmsnorm_forward(const void* X, const void* residual, const void*
     if (clash(r, 4, 7)) return LLMINT8_EINVAL;
     log_call("rmsnorm_forward", M, K, 0, dtype, NAN, four ? "rmsnorm_mxfp4" : (codes ? "rmsnorm_fp8_block" : "rmsnorm"));
     return hip_status(stage("rmsnorm", [&] {
-        const NormArgs a{(const uint16_t*)X, (const uint16_t*)residual, (const uint16_t*)weight, M, K, eps, (uint16_t*)H, (uint16_t*)Y, format, Yq, y_scale};
+        const NormArgs a{(const uint16_t*)X, (const uint16_t*)residual, (const uint16_t*)weight, M, K, 1.0 / (double)K, eps, (uint16_t*)H, (uint16_t*)Y, format, Yq, y_scale};
         return launch_rmsnorm(dtype, a, (hipStream_t)stream);
     }));
 }
@@ -98,7 +98,7 @@ LLMINT8_API int rmsnorm_backward(const void* dY, const void* H, const void* weig
     log_call("rmsnorm_backward", M, K, 0, dtype, NAN, L.plan.whole ? "rmsnorm_backward" : "rmsnorm_backward_long");
     return hip_status(stage("rmsnorm_backward", [&] {
         uint8_t* ws = (uint8_t*)workspace;
-        const NormBackwardArgs a{(const uint16_t*)dY, (const uint16_t*)H, (const uint16_t*)weight, (const uint16_t*)dH, M, K, eps, (uint16_t*)dX,
+        const NormBackwardArgs a{(const uint16_t*)dY, (const uint16_t*)H, (const uint16_t*)weight, (const uint16_t*)dH, M, K, 1.0 / (double)K, eps, (uint16_t*)dX,
                                  (uint16_t*)dW, (float*)ws, dW && !L.plan.whole ? (float*)(ws + L.rows) : nullptr};
         return launch_rmsnorm_backward(dtype, a, L.plan, st);
     }));

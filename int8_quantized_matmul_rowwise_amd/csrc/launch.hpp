@@ -298,6 +298,7 @@ hipError_t launch_mxfp4_gemm(int dt, const Mxfp4GemmArgs& p, const Mxfp4Plan& pl
 struct NormArgs {
     const uint16_t *X, *R, *W;  // R: the residual, or NULL
     int64_t M, K;
+    double inv_k;  // 1 / K
     float eps;
     uint16_t *H, *Y;  // the sum and the norm, each or NULL
     int format;       // of the codes: enum llmint8_codes
@@ -315,6 +316,7 @@ NormBackwardPlan rmsnorm_backward_plan(int64_t M, int64_t K);
 struct NormBackwardArgs {
     const uint16_t *dY, *H, *W, *dH;  // dH: the gradient that arrives at H, or NULL
     int64_t M, K;
+    double inv_k;  // 1 / K
     float eps;
     uint16_t *dX, *dW;  // dW: or NULL
     float* partial;     // groups x K, where dW is wanted

@@ -79,12 +79,22 @@ __device__ __forceinline__ float squares(const u32x4& h, float s) {
     }
     return s;
 }
+// h w r: the product of two 16-bit values is exact in fp32, so y has one rounding before its own.
 template <int DT>
 __device__ __forceinline__ u32x4 scaled(const u32x4& h, const u32x4& w, float r) {
     u32x4 o;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) o[d] = pack<DT>(low<DT>(h[d]) * r * low<DT>(w[d]), high<DT>(h[d]) * r * high<DT>(w[d]));
+    for (int d = 0; d < 4; ++d) o[d] = pack<DT>(low<DT>(h[d]) * low<DT>(w[d]) * r, high<DT>(h[d]) * high<DT>(w[d]) * r);
     return o;
+}
+
+// 1 / sqrt(sum / n + eps), rounded once to fp32: the hardware's estimate in 64 bits and one step of
+// Newton's on it (codes of y flip where y is next to a border, so r is not left with three roundings).
+__device__ __forceinline__ float inverse_root(float sum, double inv_n, float eps) {
+    const double v = __builtin_fma((double)sum, inv_n, (double)eps);
+    const double y = __builtin_amdgcn_rsq(v);
+    const double z = y * __builtin_fma(-0.5 * v * y, y, 1.5);
+    return sum < __builtin_inff() ? (float)z : (sum == sum ? 0.0f : __builtin_nanf(""));
 }
 
 // The workgroup's place in its XCD's run of rows: neighbours share the lines of the codes' scales.
@@ -128,7 +138,6 @@ template <int DT, int V, int FORMAT>
 __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs p) {
     __shared__ float red[2][1][16];
     const int T = blockDim.x, tid = threadIdx.x;
-    const float n = (float)p.K;
     int turn = 0;
     for (int64_t row = in_runs(blockIdx.x, gridDim.x); row < p.M; row += gridDim.x, turn ^= 1) {
         u32x4 h[V], w[V];
@@ -160,7 +169,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs p) {
 #pragma unroll
         for (int v = 0; v < V; ++v) s[0] = squares<DT>(h[v], s[0]);
         group_sum(s, red[turn]);
-        const float r = 1.0f / __builtin_sqrtf(s[0] / n + p.eps);
+        const float r = inverse_root(s[0], p.inv_k, p.eps);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int64_t c = ((int64_t)v * T + tid) * 8;
@@ -176,7 +185,6 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs p) {
 template <int DT, int FORMAT>
 __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs p) {
     __shared__ float red[2][1][16];
-    const float n = (float)p.K;
     int turn = 0;
     for (int64_t row = in_runs(blockIdx.x, gridDim.x); row < p.M; row += gridDim.x, turn ^= 1) {
         float s[1] = {0.0f};
@@ -189,7 +197,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs p) {
             s[0] = squares<DT>(h, s[0]);
         }
         group_sum(s, red[turn]);
-        const float r = 1.0f / __builtin_sqrtf(s[0] / n + p.eps);
+        const float r = inverse_root(s[0], p.inv_k, p.eps);
         for (int64_t base = 0; base < p.K; base += 8192) {
             const int64_t c = base + 8 * threadIdx.x;
             u32x4 y = {0u, 0u, 0u, 0u};
@@ -246,7 +254,6 @@ template <int DT, int V, bool DW>
 __global__ __launch_bounds__(1024) void rmsnorm_backward_kernel(NormBackwardArgs p) {
     __shared__ float red[2][2][16];
     const int T = blockDim.x, tid = threadIdx.x;
-    const float n = (float)p.K;
     u32x4 w[V];
     float acc[V][8] = {};
 #pragma unroll
@@ -272,7 +279,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_kernel(NormBackwardArgs
 #pragma unroll
         for (int v = 0; v < V; ++v) row_sums<DT>(h[v], dy[v], w[v], s);
         group_sum(s, red[turn]);
-        const float r = 1.0f / __builtin_sqrtf(s[0] / n + p.eps), m = r * r * (s[1] / n);
+        const float r = inverse_root(s[0], p.inv_k, p.eps), m = r * r * (float)(s[1] * p.inv_k);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int64_t c = ((int64_t)v * T + tid) * 8;
@@ -296,14 +303,13 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_kernel(NormBackwardArgs
 template <int DT>
 __global__ __launch_bounds__(1024) void rmsnorm_backward_long_kernel(NormBackwardArgs p) {
     __shared__ float red[2][2][16];
-    const float n = (float)p.K;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
         float s[2] = {0.0f, 0.0f};
         for (int64_t c = 8 * threadIdx.x; c < p.K; c += 8192)
             row_sums<DT>(*(const u32x4*)(p.H + row * p.K + c), *(const u32x4*)(p.dY + row * p.K + c), *(const u32x4*)(p.W + c), s);
         group_sum(s, red[turn]);
-        const float r = 1.0f / __builtin_sqrtf(s[0] / n + p.eps), m = r * r * (s[1] / n);
+        const float r = inverse_root(s[0], p.inv_k, p.eps), m = r * r * (float)(s[1] * p.inv_k);
         if (threadIdx.x == 0 && p.rows) p.rows[row] = r;
         for (int64_t c = 8 * threadIdx.x; c < p.K; c += 8192) {
             const u32x4 none = {0u, 0u, 0u, 0u};

@@ -247,6 +247,8 @@ __device__ __forceinline__ void tiled_product(const TiledParams& tp) {
 
     v4f acc[NF][MF];
     v8i fm[2][MF], fn[2];      // m pieces of the stage and of the next, the next stage's first n pieces
+    constexpr int R = 2 * NF, LA = 4;  // kFp4: pieces of half a line along n, read LA ahead
+    v4i hm[2][MF], hn[LA];             // and by halves: m pieces of either half, the next n pieces
     int sm[NA], sn[NS], nsm[NA], nsn[NS];  // scales of the stage and of the next
 
     // Stage kt of a tile, in slots sa, sb; P = kt % 2.
@@ -263,16 +265,8 @@ __device__ __forceinline__ void tiled_product(const TiledParams& tp) {
         w[0] = fn[0];
         w[1] = fn[1];
         auto mfma_row = [&](int f) LLMINT8_FP8_INLINE {
-            if constexpr (FOUR) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < MF; ++j)
-                        acc[f][j] = mfma_fp4(half_of(w[f], h), half_of(fm[P][j], h), acc[f][j], sn[f / 2], 2 * h + f % 2, sm[j / 2], 2 * h + j % 2);
-            } else {
-#pragma unroll
-                for (int j = 0; j < MF; ++j) acc[f][j] = mfma_fp8(w[f], fm[P][j], acc[f][j], sn[ROWB ? f / 4 : 0], ROWB ? f % 4 : 0, sm[0], j);
-            }
+            for (int j = 0; j < MF; ++j) acc[f][j] = mfma_fp8(w[f], fm[P][j], acc[f][j], sn[ROWB ? f / 4 : 0], ROWB ? f % 4 : 0, sm[0], j);
         };
         // the next stage's scales (before B's loads, which the barrier leaves in flight)
         const int next = __builtin_amdgcn_readfirstlane(kt + 1 < nk ? 0 : 1);
@@ -309,6 +303,47 @@ __device__ __forceinline__ void tiled_product(const TiledParams& tp) {
         for (int f = 0; f < NS; ++f) sn[f] = nsn[f];
     };
 
+    // The same by halves of a line (kFp4): the instruction takes half a line in half the time, so n pieces
+    // are read LA = 4 ahead, and m pieces of one half while the other is multiplied, which takes half
+    // the registers.
+    auto half = [&](const uint8_t* slot, int f, int h) LLMINT8_FP8_INLINE { return *(const v4i*)(slot + f * 16 * BK + (h ? rd ^ 64 : rd)); };
+    auto stage_by_halves = [&](int sa, int sb, int kt) LLMINT8_FP8_INLINE {
+        const int d = __builtin_amdgcn_readfirstlane(kt + 2 < nk ? 0 : (kt + 2 < 2 * nk ? 1 : 2));
+        const int k2 = kt + 2 - d * nk;
+        uint8_t* to_b = slot_b(sb == 0 ? 2 : sb - 1);
+        const uint8_t *Ac = slot_a(sa) + wm * (16 * MF * BK), *An = slot_a(sa ^ 1) + wm * (16 * MF * BK);
+        const uint8_t *Bc = slot_b(sb) + wn * (16 * NF * BK), *Bn = slot_b(sb == 2 ? 0 : sb + 1) + wn * (16 * NF * BK);
+        v4i w[R];
+#pragma unroll
+        for (int r = 0; r < LA; ++r) w[r] = hn[r];
+        const int next = __builtin_amdgcn_readfirstlane(kt + 1 < nk ? 0 : 1);
+        load_scales(next, next ? 0 : kt + 1, nsm, nsn);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (r < R - LA) {
+#pragma unroll
+                for (int l = 0; l < 4; ++l)
+                    if (l * (R - LA) / 4 == r) issue_b(d, to_b, k2, l);
+                w[r + LA] = half(Bc, (r + LA) % NF, (r + LA) / NF);
+                if (r < MF) hm[1][r] = half(Ac, r, 1);
+            } else {
+                if (r == R - LA) LLMINT8_FP8_WAIT_BARRIER(4);
+                hn[r - (R - LA)] = half(Bn, r - (R - LA), 0);
+                hm[0][r - (R - LA)] = half(An, r - (R - LA), 0);
+                issue_a(d, slot_a(sa), k2, r - (R - LA));
+            }
+            const int f = r % NF, h = r / NF;
+#pragma unroll
+            for (int j = 0; j < MF; ++j) acc[f][j] = mfma_fp4(w[r], hm[h][j], acc[f][j], sn[f / 2], 2 * h + f % 2, sm[j / 2], 2 * h + j % 2);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int j = 0; j < NA; ++j) sm[j] = nsm[j];
+#pragma unroll
+        for (int f = 0; f < NS; ++f) sn[f] = nsn[f];
+    };
+
     // ---- prologue: stages 0 and 1 of both operands, the first scales
     load_scales(0, 0, sm, sn);
 #pragma unroll
@@ -322,6 +357,15 @@ __device__ __forceinline__ void tiled_product(const TiledParams& tp) {
     for (int j = 0; j < 4; ++j) issue_a(d1, slot_a(1), k1, j);
     LLMINT8_FP8_WAIT_BARRIER(8);
     auto first_reads = [&](int sa, int sb) LLMINT8_FP8_INLINE {
+        if constexpr (FOUR) {
+            static_assert(LA == MF && LA <= NF, "one n piece and one m piece a step");
+#pragma unroll
+            for (int j = 0; j < LA; ++j) {
+                hn[j] = half(slot_b(sb) + wn * (16 * NF * BK), j, 0);
+                hm[0][j] = half(slot_a(sa) + wm * (16 * MF * BK), j, 0);
+            }
+            return;
+        }
         fn[0] = read(slot_b(sb) + wn * (16 * NF * BK), 0);
 #pragma unroll
         for (int j = 0; j < MF; ++j) fm[0][j] = read(slot_a(sa) + wm * (16 * MF * BK), j);
@@ -339,15 +383,23 @@ __device__ __forceinline__ void tiled_product(const TiledParams& tp) {
 #pragma unroll
             for (int j = 0; j < MF; ++j) acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         int kt = 0;
-        for (; kt + 2 <= nk; kt += 2) {
-            stage(std::integral_constant<int, 0>{}, sa, sb, kt);
-            advance();
-            stage(std::integral_constant<int, 1>{}, sa, sb, kt + 1);
-            advance();
+        if constexpr (FOUR) {
+            for (; kt < nk; ++kt) {
+                stage_by_halves(sa, sb, kt);
+                advance();
+            }
         }
-        if (kt < nk) {
-            stage(std::integral_constant<int, 0>{}, sa, sb, kt);
-            advance();
+        if constexpr (!FOUR) {
+            for (; kt + 2 <= nk; kt += 2) {
+                stage(std::integral_constant<int, 0>{}, sa, sb, kt);
+                advance();
+                stage(std::integral_constant<int, 1>{}, sa, sb, kt + 1);
+                advance();
+            }
+            if (kt < nk) {
+                stage(std::integral_constant<int, 0>{}, sa, sb, kt);
+                advance();
+            }
         }
         mfma_settle();
         if constexpr (SPLIT) {
@@ -399,7 +451,7 @@ __device__ __forceinline__ void tiled_product(const TiledParams& tp) {
             b_at0 = b_at1;
             b_n0 = b_n1;
             scale_range(ti + 2, a_at1, a_n1, b_at1, b_n1);
-            if (nk & 1) {
+            if (!FOUR && (nk & 1)) {
 #pragma unroll
                 for (int j = 0; j < MF; ++j) fm[0][j] = fm[1][j];
             }
