@@ -308,8 +308,10 @@ hipError_t launch_rmsnorm(int dt, const NormArgs& p, hipStream_t stream);
 
 // How the gradient runs: rows split over `groups` workgroups, each with a row of partial sums of dW.
 struct NormBackwardPlan {
-    bool whole;  // a workgroup holds a whole row
-    int threads, vectors;  // whole: threads of a workgroup, pieces of 8 columns of a thread
+    bool whole;    // a workgroup holds whole rows
+    int vectors, row_threads;  // whole: pieces of 8 columns of a thread, threads of a row
+    bool ahead;    // whole: the next row's loads under way
+    int threads;   // whole: of a workgroup
     int64_t groups;
 };
 NormBackwardPlan rmsnorm_backward_plan(int64_t M, int64_t K);

@@ -20,9 +20,9 @@ template <int DT>
 __global__ __launch_bounds__(256) void mxfp4_rows_kernel(const uint16_t* __restrict__ X, int64_t R, int64_t C, uint8_t* __restrict__ q,
                                                          uint8_t* __restrict__ s, int32_t* __restrict__ zero, int64_t n_zero) {
     __shared__ __attribute__((aligned(16))) uint8_t scales[256];
-    const int64_t tiles = ceil_div(C, 256), id = blockIdx.x;
-    for (int64_t i = id * 256 + threadIdx.x; i < n_zero; i += (int64_t)gridDim.x * 256) zero[i] = 0;
-    const int64_t tr = id / tiles, tc = id - tr * tiles;
+    const uint32_t tiles = (uint32_t)ceil_div(C, 256), id = blockIdx.x;
+    for (int64_t i = (int64_t)id * 256 + threadIdx.x; i < n_zero; i += (int64_t)gridDim.x * 256) zero[i] = 0;
+    const int64_t tr = id / tiles, tc = id % tiles;
     const int sub = threadIdx.x >> 5, sl = threadIdx.x & 31;
     const int64_t c = tc * 256 + 8 * sl, pitch = fp4_pitch(C);
     u32x4 v[4];
@@ -40,7 +40,7 @@ __global__ __launch_bounds__(256) void mxfp4_rows_kernel(const uint16_t* __restr
         if ((sl & 3) == 0) scales[fp4_scale_at(8 * i + sub, sl >> 2, 256)] = (uint8_t)e;  // (rows past the last: zeros)
     }
     __syncthreads();
-    if (threadIdx.x < 64) ((uint32_t*)s)[id * 64 + threadIdx.x] = ((const uint32_t*)scales)[threadIdx.x];
+    if (threadIdx.x < 64) ((uint32_t*)s)[(int64_t)id * 64 + threadIdx.x] = ((const uint32_t*)scales)[threadIdx.x];
 }
 
 template <int DT>

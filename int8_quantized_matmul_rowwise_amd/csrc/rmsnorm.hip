@@ -15,7 +15,6 @@ namespace llmint8 {
 
 namespace {
 
-constexpr int kMaxVectors = 8;          // pieces of 8 columns a thread holds (whole rows)
 constexpr int64_t kMaxGrid = 1 << 20;   // workgroups of a launch: 2^32 threads are too many
 
 // The sum over the 64 lanes, in all of them, in a fixed order.
@@ -35,23 +34,26 @@ __device__ __forceinline__ float wave_sum(float v) {
     return swapped(__builtin_bit_cast(uint32_t, v), true);
 }
 
-// N sums over the workgroup, in all of its threads; red: N x 16 words that the call before last may
-// have used.
-template <int N>
-__device__ __forceinline__ void group_sum(float (&v)[N], float (*red)[16]) {
-    const int waves = blockDim.x >> 6, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+// N sums over T threads (whole waves), in all of them; red: words that the call before last may have
+// used.  Every wave of the workgroup calls it.
+template <int N, int T>
+__device__ __forceinline__ void group_sum(float (&v)[N], float (*red)[T / 64]) {
+    constexpr int W = T / 64;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-    if (waves == 1) return;
-    if (lane == 0) {
+    if constexpr (W > 1) {
+        const int lane = threadIdx.x & 63, w = (threadIdx.x % T) >> 6;
+        if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) red[i][w] = v[i];
-    }
-    __syncthreads();
+            for (int i = 0; i < N; ++i) red[i][w] = v[i];
+        }
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v[i] = red[i][0];
-        for (int j = 1; j < waves; ++j) v[i] += red[i][j];
+        for (int i = 0; i < N; ++i) {
+            v[i] = red[i][0];
+#pragma unroll
+            for (int j = 1; j < W; ++j) v[i] += red[i][j];
+        }
     }
 }
 
@@ -97,6 +99,14 @@ __device__ __forceinline__ float inverse_root(float sum, double inv_n, float eps
     return sum < __builtin_inff() ? (float)z : (sum == sum ? 0.0f : __builtin_nanf(""));
 }
 
+// Whether rows past the last fill the last tile of scales, and the workgroups that take rows.
+template <int FORMAT>
+__host__ __device__ __forceinline__ bool has_padding(const NormArgs& p) {
+    return FORMAT != LLMINT8_CODES_NONE && p.M % (FORMAT == LLMINT8_CODES_MXFP4 ? 32 : 64) != 0;
+}
+template <int FORMAT>
+__device__ __forceinline__ int64_t norm_groups(const NormArgs& p, int64_t grid) { return grid - (has_padding<FORMAT>(p) ? 1 : 0); }
+
 // The workgroup's place in its XCD's run of rows: neighbours share the lines of the codes' scales.
 __device__ __forceinline__ int64_t in_runs(int64_t id, int64_t n) {
     const int64_t xcd = id & 7, per = n >> 3, rem = n & 7;
@@ -121,25 +131,27 @@ __device__ __forceinline__ void store_codes(const NormArgs& p, int64_t row, int6
     }
 }
 
-// The scales of the rows that fill the last tile of scales: zeros.
+// The scales of the rows that fill the last tile of scales: zeros, written by a workgroup of their own
+// (the last one, where there are such rows), which adds nothing to the time of a row.
 template <int FORMAT>
 __device__ __forceinline__ void clear_scales(const NormArgs& p) {
     constexpr bool four = FORMAT == LLMINT8_CODES_MXFP4;
-    const int64_t pad = round_up(p.M, four ? 32 : 64) - p.M, groups = four ? fp4_scale_pitch_of(p.K) / 32 : ceil_div(p.K, 128);
-    for (int64_t i = threadIdx.x; i < pad * groups; i += blockDim.x) {
-        const int64_t row = p.M + i / groups, g = i % groups;
-        p.s[four ? fp4_scale_at(row, g, fp4_scale_pitch_of(p.K)) : fp8_row_scale_at(row, g, p.M)] = 0;
-    }
+    const int64_t end = round_up(p.M, four ? 32 : 64);
+    const int groups = (int)(four ? fp4_scale_pitch_of(p.K) / 32 : ceil_div(p.K, 128));
+    for (int g = threadIdx.x; g < groups; g += blockDim.x)
+        for (int64_t row = p.M; row < end; ++row) p.s[four ? fp4_scale_at(row, g, fp4_scale_pitch_of(p.K)) : fp8_row_scale_at(row, g, p.M)] = 0;
 }
 
 // A workgroup a row, V pieces of 8 columns a thread.  (p.H may be p.X or p.R: each element is read
 // before it is written, by the same thread.)
-template <int DT, int V, int FORMAT>
-__global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs p) {
-    __shared__ float red[2][1][16];
-    const int T = blockDim.x, tid = threadIdx.x;
+template <int DT, int V, int FORMAT, int T>
+__global__ __launch_bounds__(T, 4) void rmsnorm_kernel(NormArgs p) {
+    __shared__ float red[2][1][T / 64];
+    const int tid = threadIdx.x;
+    const int64_t groups = norm_groups<FORMAT>(p, gridDim.x);
+    if (FORMAT != LLMINT8_CODES_NONE && blockIdx.x >= groups) return clear_scales<FORMAT>(p);
     int turn = 0;
-    for (int64_t row = in_runs(blockIdx.x, gridDim.x); row < p.M; row += gridDim.x, turn ^= 1) {
+    for (int64_t row = in_runs(blockIdx.x, groups); row < p.M; row += groups, turn ^= 1) {
         u32x4 h[V], w[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -168,7 +180,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs p) {
         float s[1] = {0.0f};
 #pragma unroll
         for (int v = 0; v < V; ++v) s[0] = squares<DT>(h[v], s[0]);
-        group_sum(s, red[turn]);
+        group_sum<1, T>(s, red[turn]);
         const float r = inverse_root(s[0], p.inv_k, p.eps);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -177,16 +189,18 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs p) {
             if (p.Y && c < p.K) *(u32x4*)(p.Y + row * p.K + c) = y;
             store_codes<DT, FORMAT>(p, row, c, y);
         }
-        if (FORMAT != LLMINT8_CODES_NONE && row == p.M - 1) clear_scales<FORMAT>(p);
     }
 }
 
 // Rows longer than a workgroup's registers: read twice.
 template <int DT, int FORMAT>
 __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs p) {
-    __shared__ float red[2][1][16];
+    constexpr int T = 1024;
+    __shared__ float red[2][1][T / 64];
+    const int64_t groups = norm_groups<FORMAT>(p, gridDim.x);
+    if (FORMAT != LLMINT8_CODES_NONE && blockIdx.x >= groups) return clear_scales<FORMAT>(p);
     int turn = 0;
-    for (int64_t row = in_runs(blockIdx.x, gridDim.x); row < p.M; row += gridDim.x, turn ^= 1) {
+    for (int64_t row = in_runs(blockIdx.x, groups); row < p.M; row += groups, turn ^= 1) {
         float s[1] = {0.0f};
         for (int64_t c = 8 * threadIdx.x; c < p.K; c += 8192) {
             u32x4 h = *(const u32x4*)(p.X + row * p.K + c);
@@ -196,7 +210,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs p) {
             }
             s[0] = squares<DT>(h, s[0]);
         }
-        group_sum(s, red[turn]);
+        group_sum<1, T>(s, red[turn]);
         const float r = inverse_root(s[0], p.inv_k, p.eps);
         for (int64_t base = 0; base < p.K; base += 8192) {
             const int64_t c = base + 8 * threadIdx.x;
@@ -211,7 +225,6 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs p) {
             }
             store_codes<DT, FORMAT>(p, row, c, y);
         }
-        if (FORMAT != LLMINT8_CODES_NONE && row == p.M - 1) clear_scales<FORMAT>(p);
     }
 }
 
@@ -249,48 +262,84 @@ __device__ __forceinline__ void row_dw(const u32x4& h, const u32x4& dy, float r,
     }
 }
 
-// A workgroup a row at a time, every gridDim.x-th one; dw's sums stay in registers over its rows.
-template <int DT, int V, bool DW>
-__global__ __launch_bounds__(1024) void rmsnorm_backward_kernel(NormBackwardArgs p) {
-    __shared__ float red[2][2][16];
-    const int T = blockDim.x, tid = threadIdx.x;
+// T threads take a row at a time, and a workgroup blockDim.x / T rows side by side; with AHEAD the next
+// row's loads are under way while a row is summed.  dw's sums stay in registers over a thread's rows, and
+// those of the workgroup's rows meet in LDS at the end.
+template <int DT, int V, int T, bool DW, bool AHEAD>
+__global__ __launch_bounds__(AHEAD ? 512 : T, AHEAD ? 2 : 4) void rmsnorm_backward_kernel(NormBackwardArgs p) {
+    constexpr int kSide = AHEAD ? 512 / T : 1;  // rows side by side, at most
+    __shared__ float red[2][kSide][2][T / 64];
+    __shared__ v4f joined[DW && kSide > 1 ? 2 * V * T : 1];  // a row of dw's sums
+    const int tid = threadIdx.x % T, side = kSide > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / T) : 0, sides = kSide > 1 ? (int)blockDim.x / T : 1;
     u32x4 w[V];
     float acc[V][8] = {};
+    const u32x4 none = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int64_t c = ((int64_t)v * T + tid) * 8;
-        w[v] = u32x4{0u, 0u, 0u, 0u};
-        if (c < p.K) w[v] = *(const u32x4*)(p.W + c);
+        const int c = (v * T + tid) * 8;
+        w[v] = c < p.K ? *(const u32x4*)(p.W + c) : none;
     }
-    int turn = 0;
-    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
+    struct Row {
         u32x4 h[V], dy[V], dh[V];
+    };
+    auto load = [&](int64_t row, Row& x) __attribute__((always_inline)) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int64_t c = ((int64_t)v * T + tid) * 8;
-            h[v] = dy[v] = dh[v] = u32x4{0u, 0u, 0u, 0u};
-            if (c < p.K) {
-                h[v] = *(const u32x4*)(p.H + row * p.K + c);
-                dy[v] = *(const u32x4*)(p.dY + row * p.K + c);
-                if (p.dH) dh[v] = *(const u32x4*)(p.dH + row * p.K + c);
-            }
+            const int c = (v * T + tid) * 8;
+            const bool in = c < p.K && row < p.M;
+            const int64_t at = row * p.K + c;
+            x.h[v] = in ? *(const u32x4*)(p.H + at) : none;
+            x.dy[v] = in ? *(const u32x4*)(p.dY + at) : none;
+            x.dh[v] = in && p.dH ? *(const u32x4*)(p.dH + at) : none;
         }
+    };
+    const int64_t step = (int64_t)gridDim.x * sides;
+    int64_t row = (int64_t)blockIdx.x * sides + side;
+    Row x, next;
+    load(row, x);
+    int turn = 0;
+    for (int64_t first = (int64_t)blockIdx.x * sides; first < p.M; first += step, row += step, turn ^= 1) {  // (every side as often)
+        if (AHEAD) load(row + step, next);
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int v = 0; v < V; ++v) row_sums<DT>(h[v], dy[v], w[v], s);
-        group_sum(s, red[turn]);
+        for (int v = 0; v < V; ++v) row_sums<DT>(x.h[v], x.dy[v], w[v], s);
+        group_sum<2, T>(s, red[turn][side]);
         const float r = inverse_root(s[0], p.inv_k, p.eps), m = r * r * (float)(s[1] * p.inv_k);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int64_t c = ((int64_t)v * T + tid) * 8;
-            if (c < p.K) *(u32x4*)(p.dX + row * p.K + c) = row_dx<DT>(h[v], dy[v], w[v], dh[v], r, m);
-            if constexpr (DW) row_dw<DT>(h[v], dy[v], r, acc[v]);
+            const int c = (v * T + tid) * 8;
+            if (c < p.K && row < p.M) *(u32x4*)(p.dX + row * p.K + c) = row_dx<DT>(x.h[v], x.dy[v], w[v], x.dh[v], r, m);
+            if constexpr (DW) row_dw<DT>(x.h[v], x.dy[v], r, acc[v]);
         }
+        if (AHEAD) x = next;
+        else load(row + step, x);
     }
     if constexpr (DW) {
+        if constexpr (kSide > 1) {
+            for (int i = 1; i < sides; ++i) {  // the sides in their order, onto the first
+                __syncthreads();
+                if (side == i) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        joined[(2 * v) * T + tid] = v4f{acc[v][0], acc[v][1], acc[v][2], acc[v][3]};
+                        joined[(2 * v + 1) * T + tid] = v4f{acc[v][4], acc[v][5], acc[v][6], acc[v][7]};
+                    }
+                }
+                __syncthreads();
+                if (side == 0) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const v4f a = joined[(2 * v) * T + tid], b = joined[(2 * v + 1) * T + tid];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[v][e] += a[e], acc[v][4 + e] += b[e];
+                    }
+                }
+            }
+            if (side) return;
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int64_t c = ((int64_t)v * T + tid) * 8;
+            const int c = (v * T + tid) * 8;
             if (c >= p.K) continue;
             float* to = p.partial + (int64_t)blockIdx.x * p.K + c;
             *(v4f*)to = v4f{acc[v][0], acc[v][1], acc[v][2], acc[v][3]};
@@ -302,13 +351,14 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_kernel(NormBackwardArgs
 // Rows longer than a workgroup's registers: read twice; r of each row is kept for dw.
 template <int DT>
 __global__ __launch_bounds__(1024) void rmsnorm_backward_long_kernel(NormBackwardArgs p) {
-    __shared__ float red[2][2][16];
+    constexpr int T = 1024;
+    __shared__ float red[2][2][T / 64];
     int turn = 0;
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
         float s[2] = {0.0f, 0.0f};
         for (int64_t c = 8 * threadIdx.x; c < p.K; c += 8192)
             row_sums<DT>(*(const u32x4*)(p.H + row * p.K + c), *(const u32x4*)(p.dY + row * p.K + c), *(const u32x4*)(p.W + c), s);
-        group_sum(s, red[turn]);
+        group_sum<2, T>(s, red[turn]);
         const float r = inverse_root(s[0], p.inv_k, p.eps), m = r * r * (float)(s[1] * p.inv_k);
         if (threadIdx.x == 0 && p.rows) p.rows[row] = r;
         for (int64_t c = 8 * threadIdx.x; c < p.K; c += 8192) {
@@ -332,37 +382,58 @@ __global__ __launch_bounds__(256) void rmsnorm_dw_long_kernel(NormBackwardArgs p
     *(v4f*)(to + 4) = v4f{acc[4], acc[5], acc[6], acc[7]};
 }
 
-// dw from the partial sums (groups x K): a workgroup 64 columns, 16 runs of rows side by side, then
-// joined in their order.
+// dw from the partial sums (groups x K): a workgroup 32 columns, 32 runs of rows side by side, eight
+// loads of a thread under way, then joined in their order.
 template <int DT>
-__global__ __launch_bounds__(256) void rmsnorm_dw_join_kernel(const float* __restrict__ partial, int64_t groups, int64_t K, uint16_t* __restrict__ dW) {
-    __shared__ v4f sums[16][16];
-    const int cc = threadIdx.x & 15, rr = threadIdx.x >> 4;
-    const int64_t c = (int64_t)blockIdx.x * 64 + 4 * cc, run = ceil_div(groups, 16);
+__global__ __launch_bounds__(256) void rmsnorm_dw_join_kernel(const float* __restrict__ partial, int groups, int64_t K, uint16_t* __restrict__ dW) {
+    __shared__ v4f sums[32][8];
+    constexpr int U = 8;
+    const int cc = threadIdx.x & 7, rr = threadIdx.x >> 3;
+    const int64_t c = (int64_t)blockIdx.x * 32 + 4 * cc;
+    const int run = (int)ceil_div(groups, 32), first = rr * run, end = first + run < groups ? first + run : groups;
     v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c < K) {
-        const int64_t end = (rr + 1) * run < groups ? (rr + 1) * run : groups;
-        for (int64_t g = rr * run; g < end; ++g) s += *(const v4f*)(partial + g * K + c);
+        for (int g = first; g < end; g += U) {
+            v4f v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = *(const v4f*)(partial + (int64_t)(g + u < end ? g + u : g) * K + c);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (g + u < end) s += v[u];
+        }
     }
     sums[rr][cc] = s;
     __syncthreads();
     if (rr == 0 && c < K) {
-        for (int i = 1; i < 16; ++i) s += sums[i][cc];
+        for (int i = 1; i < 32; ++i) s += sums[i][cc];
         *(u32x2*)(dW + c) = u32x2{pack<DT>(s[0], s[1]), pack<DT>(s[2], s[3])};
     }
 }
 
+template <int DT, int V, int FORMAT>
+void norm_launch(const NormArgs& p, int64_t pieces, unsigned grid, hipStream_t stream) {
+    if (pieces <= 64 * V) rmsnorm_kernel<DT, V, FORMAT, 64><<<grid, 64, 0, stream>>>(p);
+    else if (pieces <= 128 * V) rmsnorm_kernel<DT, V, FORMAT, 128><<<grid, 128, 0, stream>>>(p);
+    else if (pieces <= 256 * V) rmsnorm_kernel<DT, V, FORMAT, 256><<<grid, 256, 0, stream>>>(p);
+    else if (pieces <= 512 * V) rmsnorm_kernel<DT, V, FORMAT, 512><<<grid, 512, 0, stream>>>(p);
+    else rmsnorm_kernel<DT, V, FORMAT, 1024><<<grid, 1024, 0, stream>>>(p);
+}
+
+// Pieces of 8 columns a thread: one while rows are few, since a row then takes its own latency (16 x
+// 8192 with codes 4.6 us with one, 4.8 with two, 5.5 with four); two or four once rows fill the card
+// several times over, so that a unit holds several workgroups (4096 x 8192, residual, to e2m1 53.1, 43.9
+// and 42.0 us, to e4m3 52.1, 45.8 and 45.4, to 16 bits 47.3, 50.2 and 51.5; 16384 x 1024 to e2m1 13.1, 11.0
+// and 14.8; 16384 x 256, residual, to e4m3 9.2, 11.1 and 17.6; 4096 x 16384 two 54.8, four 51.8).
 template <int DT, int FORMAT>
 void norm_launch(const NormArgs& p, hipStream_t stream) {
-    const unsigned grid = (unsigned)(p.M < kMaxGrid ? p.M : kMaxGrid);
+    const unsigned grid = (unsigned)(p.M < kMaxGrid ? p.M : kMaxGrid) + (has_padding<FORMAT>(p) ? 1 : 0);
     // the columns that a row's codes cover: the codes' padding is written by the threads past K
     const int64_t pieces = ceil_div(FORMAT == LLMINT8_CODES_NONE ? p.K : round_up(p.K, FORMAT == LLMINT8_CODES_MXFP4 ? 256 : 128), 8);
-    auto threads = [&](int v) { return (unsigned)round_up(ceil_div(pieces, v), 64); };
-    if (pieces <= 1024) rmsnorm_kernel<DT, 1, FORMAT><<<grid, threads(1), 0, stream>>>(p);
-    else if (pieces <= 2048) rmsnorm_kernel<DT, 2, FORMAT><<<grid, threads(2), 0, stream>>>(p);
-    else if (pieces <= 4096) rmsnorm_kernel<DT, 4, FORMAT><<<grid, threads(4), 0, stream>>>(p);
-    else if (pieces <= 1024 * kMaxVectors) rmsnorm_kernel<DT, kMaxVectors, FORMAT><<<grid, threads(kMaxVectors), 0, stream>>>(p);
-    else rmsnorm_long_kernel<DT, FORMAT><<<grid, 1024, 0, stream>>>(p);
+    const bool many = p.M >= 2048;
+    if (pieces > 4096) rmsnorm_long_kernel<DT, FORMAT><<<grid, 1024, 0, stream>>>(p);
+    else if (pieces > (many ? 1024 : 2048)) norm_launch<DT, 4, FORMAT>(p, pieces, grid, stream);
+    else if (pieces > (many ? 64 : 1024)) norm_launch<DT, 2, FORMAT>(p, pieces, grid, stream);
+    else norm_launch<DT, 1, FORMAT>(p, pieces, grid, stream);
 }
 
 template <int DT>
@@ -375,9 +446,20 @@ void norm_launch(const NormArgs& p, hipStream_t stream) {
 template <int DT, bool DW>
 void backward_launch(const NormBackwardArgs& p, const NormBackwardPlan& plan, hipStream_t stream) {
     const unsigned grid = (unsigned)plan.groups, threads = (unsigned)plan.threads;
-    if (plan.vectors == 1) rmsnorm_backward_kernel<DT, 1, DW><<<grid, threads, 0, stream>>>(p);
-    else if (plan.vectors == 2) rmsnorm_backward_kernel<DT, 2, DW><<<grid, threads, 0, stream>>>(p);
-    else rmsnorm_backward_kernel<DT, 4, DW><<<grid, threads, 0, stream>>>(p);
+#define LLMINT8_BACKWARD(V, T, AHEAD) \
+    if (plan.vectors == V && plan.row_threads == T && plan.ahead == AHEAD) rmsnorm_backward_kernel<DT, V, T, DW, AHEAD><<<grid, threads, 0, stream>>>(p)
+    LLMINT8_BACKWARD(1, 64, false);
+    LLMINT8_BACKWARD(1, 128, false);
+    LLMINT8_BACKWARD(1, 256, false);
+    LLMINT8_BACKWARD(1, 512, false);
+    LLMINT8_BACKWARD(1, 1024, false);
+    LLMINT8_BACKWARD(2, 1024, false);
+    LLMINT8_BACKWARD(1, 64, true);
+    LLMINT8_BACKWARD(2, 64, true);
+    LLMINT8_BACKWARD(4, 64, true);
+    LLMINT8_BACKWARD(4, 128, true);
+    LLMINT8_BACKWARD(4, 256, true);
+#undef LLMINT8_BACKWARD
 }
 
 template <int DT>
@@ -394,7 +476,7 @@ hipError_t backward_launch(const NormBackwardArgs& p, const NormBackwardPlan& pl
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.dW) return e;
-    rmsnorm_dw_join_kernel<DT><<<(unsigned)ceil_div(p.K, 64), 256, 0, stream>>>(p.partial, plan.groups, p.K, p.dW);
+    rmsnorm_dw_join_kernel<DT><<<(unsigned)ceil_div(p.K, 32), 256, 0, stream>>>(p.partial, (int)plan.groups, p.K, p.dW);
     return hipGetLastError();
 }
 
@@ -408,17 +490,23 @@ hipError_t launch_rmsnorm(int dt, const NormArgs& p, hipStream_t stream) {
 }
 
 NormBackwardPlan rmsnorm_backward_plan(int64_t M, int64_t K) {
-    const int64_t pieces = ceil_div(K, 8);
-    NormBackwardPlan p{pieces <= 4096, 0, 0, 0};
-    if (!p.whole) {
-        p.groups = M < 64 ? M : 64;
-        return p;
+    if (K > 16384) return {false, 0, 0, false, 0, M < 64 ? M : 64};
+    int columns = 512;
+    while (columns < K) columns *= 2;
+    // Few rows: a row over as many threads as it has pieces of 8 columns, and a workgroup a row, since
+    // a row takes its own latency (333 x 1040 4.1 us, else 5.6; 100 x 4096 4.6 and 5.2).  So, too, rows that
+    // with the next row ahead would not fit the registers (4096 x 16384 85 us, else 105).
+    if (columns > 8192 || M <= 512) {
+        const int V = columns > 8192 ? 2 : 1, T = columns / 8 / V;
+        return {true, V, T, false, T, M < 512 ? M : (columns > 8192 ? 256 : 512)};
     }
-    p.vectors = pieces <= 512 ? 1 : (pieces <= 2048 ? 2 : 4);
-    p.threads = (int)round_up(ceil_div(pieces, p.vectors), 64);
-    const int64_t most = 256 * (p.threads <= 512 ? 2 : 1);
-    p.groups = M < most ? M : most;
-    return p;
+    // Many rows: 512 threads a compute unit, a wave or several a row, the next row's loads under way
+    // (16384 x 1024 20.8 us, 43.7 with a workgroup of 128 threads a row and none ahead).
+    const int V = columns <= 2048 ? columns / 512 : 4, T = columns / 8 / V;
+    int64_t sides = 512 / T;
+    while (sides > 1 && M < 256 * sides) sides /= 2;
+    const int64_t groups = ceil_div(M, sides);
+    return {true, V, T, true, (int)(T * sides), groups < 256 ? groups : 256};
 }
 
 hipError_t launch_rmsnorm_backward(int dt, const NormBackwardArgs& p, const NormBackwardPlan& plan, hipStream_t stream) {
