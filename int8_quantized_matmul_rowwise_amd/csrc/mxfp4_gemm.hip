@@ -7,21 +7,295 @@
 // column side: a lane's four results are neighbours along n.  A group's products are whole multiples
 // of a quarter of its scales, at most 36, so their sum is exact; groups meet in fp32.
 #include "launch.hpp"
-#include "tile_gemm.hpp"
+#include "mxfp4_common.hpp"
 
 namespace llmint8 {
 
 namespace {
 
-#define LLMINT8_FP4_INLINE __attribute__((always_inline))
+constexpr int MF = 4;   // pieces of 16 rows m of a wave
+constexpr int BK = 128;  // bytes of a line
+constexpr int kXcds = 8;
+constexpr int kGroupM = 8;
 
-template <int DT, int WM, int WN, int NF, bool SPLIT>
-__global__ __launch_bounds__(64 * WM * WN, 2) void mxfp4_tiled_kernel(TiledParams tp) {
-    tiled_product<DT, WM, WN, NF, kFp4, SPLIT>(tp);
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+#define LLMINT8_FP4_INLINE __attribute__((always_inline))
+// wait for this wave's LDS reads and all but the N newest loads and stores, then the bare barrier
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
 }
-template <int DT>
-__global__ __launch_bounds__(256, 1) void mxfp4_single_kernel(TiledParams tp) {
-    single_product<DT, kFp4>(tp);
+
+// the instruction with bytes bn, bm of the scale dwords (constants after unrolling)
+__device__ __forceinline__ v4f mfma_fp4(const v4i& n, const v4i& m, const v4f& c, int sn, int bn, int sm, int bm) {
+    const v8i a = __builtin_shufflevector(n, n, 0, 1, 2, 3, -1, -1, -1, -1), b = __builtin_shufflevector(m, m, 0, 1, 2, 3, -1, -1, -1, -1);
+#define LLMINT8_MFMA(BN_, BM_) \
+    if (bn == BN_ && bm == BM_) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, BN_, sn, BM_, sm);
+#define LLMINT8_MFMA4(BN_) LLMINT8_MFMA(BN_, 0) LLMINT8_MFMA(BN_, 1) LLMINT8_MFMA(BN_, 2) LLMINT8_MFMA(BN_, 3)
+    LLMINT8_MFMA4(0) LLMINT8_MFMA4(1) LLMINT8_MFMA4(2) LLMINT8_MFMA4(3)
+#undef LLMINT8_MFMA4
+#undef LLMINT8_MFMA
+    return c;
+}
+
+// Where chunk c (16 bytes) of row r's line lies in LDS: at chunk c ^ swz(r), so that the 16 lanes of a
+// read meet the 64 banks once each (rows two apart at different chunks, odd rows in the other half).
+__host__ __device__ constexpr int swz(int r) { return (r >> 1) & 7; }
+
+struct TiledParams {
+    Mxfp4GemmArgs a;
+    int tiles_m, tiles_n;
+    int split, part;  // parts of the sum and the stages of one (split 1: all of them)
+};
+
+// A wave's 64 x 16 NF results from row m0, column n0 on, through its 2 KB of LDS `ys`: 16 rows m x 64
+// columns at a time, so that whole lines of 128 bytes leave (64 bytes of a row at a time, straight from
+// the registers, took 2048 x 4096 x 16384 from 64 to 94 us).  Row r's 16-byte piece c is at c ^ (r / 2).
+// Stores past the matrix lie past the resource.  Their offsets are all in the vector register: with one in a scalar register the compiler
+// (ROCm 7.2) takes a 16-byte store's data as read at once, and an instruction that overwrites it right
+// after the store has been seen to change what is stored.
+template <int DT, int NF>
+__device__ __forceinline__ void store_tile(const Mxfp4GemmArgs& p, const v4f (&acc)[NF][MF], uint8_t* ys, int64_t m0, int64_t n0) {
+    int lane = threadIdx.x & 63;  // opaque: nothing derived from it here is held through the stages
+    asm volatile("" : "+v"(lane));
+    const int li = lane & 15, q = lane >> 4, row = lane >> 3, ch = lane & 7;
+    const int64_t rows = p.M - m0 < 64 ? p.M - m0 : 64;
+    const __amdgpu_buffer_rsrc_t ry = buffer_rsrc(p.Y + (rows > 0 ? m0 * p.N : 0), rows > 0 ? rows * p.N * 2 : 0);
+#pragma unroll
+    for (int g = 0; g < NF; g += 4) {
+        const int64_t n = n0 + 16 * g + 8 * ch;
+        const uint32_t at = n < p.N ? (uint32_t)(row * p.N + n) * 2 : 0x80000000u;
+#pragma unroll
+        for (int j = 0; j < MF; ++j) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const v4f& a = acc[g + f][j];
+                u32x2 v;
+                v[0] = (uint32_t)from_f32<DT>(a[0]) | ((uint32_t)from_f32<DT>(a[1]) << 16);
+                v[1] = (uint32_t)from_f32<DT>(a[2]) | ((uint32_t)from_f32<DT>(a[3]) << 16);
+                *(u32x2*)(ys + li * 128 + (((2 * f + (q >> 1)) ^ (li >> 1)) << 4) + 8 * (q & 1)) = v;
+            }
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+                const int r = 8 * it + row;
+                const u32x4 v = *(const u32x4*)(ys + r * 128 + ((ch ^ (r >> 1)) << 4));
+                __builtin_amdgcn_raw_buffer_store_b128(v, ry, at + (uint32_t)((16 * j + 8 * it) * p.N) * 2, 0, 0);
+            }
+        }
+    }
+}
+
+// ---- tiles of BM x BN outputs, waves in WM x WN, each 64 rows m by 16 NF columns n.  A stage is a line
+// (256 values) of every row, loaded straight into LDS with its scales (one tile of scales an
+// instruction), D - 1 stages ahead: D sets of slots, and a set is loaded anew as soon as every wave has
+// read it.  The workgroup meets once a stage, LA steps before its end.  D = 2 where several waves a SIMD
+// cover for each other; with at most one tile (or part of one) a compute unit a workgroup of four waves
+// has the unit's LDS to itself, and D = 4.
+// A step is one n piece against the four m pieces, of half a line (128 values): n pieces are read LA
+// steps ahead, m pieces of a half while the other one is multiplied, the scales in the steps after the
+// barrier.
+// Persistent over the XCD's run of tiles: the next tile's first loads are under way during a tile's last
+// stage and its output.
+// SPLIT: few tiles; a workgroup takes one part of one tile's stages, dumps its sums, and the last of the
+// tile's parts (if there are several) to end adds them up in their order and writes the output.
+template <int DT, int WM, int WN, int NF, bool SPLIT, int D>
+__global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void mxfp4_tiled_kernel(TiledParams tp) {
+    constexpr int kWaves = WM * WN, R = 2 * NF, LA = 4;
+    constexpr int BM = 16 * MF * WM, BN = 16 * NF * WN;
+    constexpr int kSlotA = BM * BK, kSlotB = BN * BK, kSlotS = (BM + BN) / 32 * 256, kSet = kSlotA + kSlotB + kSlotS;
+    constexpr int NA = MF / 2, NS = NF / 2;  // scale dwords of a wave's rows and columns
+    constexpr int kLoads = 10;
+    static_assert(BM / 8 / kWaves == 4 && BN / 8 / kWaves == 4 && (BM + BN) / 32 / kWaves == 2 && BM == BN, "ten loads a wave and stage");
+    static_assert(LA == MF && LA <= NF, "one n piece and one m piece a step");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[D * kSet + kWaves * 2048];
+    const Mxfp4GemmArgs& p = tp.a;
+    const int tid = threadIdx.x, lane = tid & 63, wu = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wu % WM, wn = wu / WM;
+    const int li = lane & 15, q = lane >> 4;
+
+    // ---- this workgroup's tiles: a strided part of its XCD's contiguous run (ids congruent mod
+    // 8 share an XCD), in groups of kGroupM row tiles
+    const int T1 = tp.tiles_m * tp.tiles_n, T = SPLIT ? T1 * tp.split : T1;  // SPLIT: part after part
+    const int bid = blockIdx.x, nwg = gridDim.x;
+    const int xcd = bid % kXcds, local = bid / kXcds;
+    const int per = T / kXcds, rem = T % kXcds;
+    const int x_start = xcd * per + (xcd < rem ? xcd : rem), x_cnt = per + (xcd < rem ? 1 : 0);
+    const int on_xcd = (nwg - xcd + kXcds - 1) / kXcds;
+    const int my_tiles = local < x_cnt ? (x_cnt - local + on_xcd - 1) / on_xcd : 0;
+    if (my_tiles == 0) return;  // the same for every wave
+    // (a quotient comes from the vector unit: read back, or every load that it places would loop over lanes)
+    const int part = SPLIT ? __builtin_amdgcn_readfirstlane((x_start + local) / T1) : 0, k0 = SPLIT ? part * tp.part : 0;
+    const int all = (int)(p.pitch / BK), nk = SPLIT ? (all - k0 < tp.part ? all - k0 : tp.part) : all;
+    auto tile_origin = [&](int i, int64_t& m0, int64_t& n0) LLMINT8_FP4_INLINE {
+        const int t = SPLIT ? (x_start + local) - part * T1 : x_start + local + i * on_xcd;
+        const int in_group = kGroupM * tp.tiles_n;
+        const int first_m = (t / in_group) * kGroupM;
+        const int gm = tp.tiles_m - first_m < kGroupM ? tp.tiles_m - first_m : kGroupM;
+        m0 = (int64_t)__builtin_amdgcn_readfirstlane(first_m + (t % in_group) % gm) * BM;
+        n0 = (int64_t)__builtin_amdgcn_readfirstlane((t % in_group) / gm) * BN;
+    };
+
+    // ---- loads: a cursor over the stages of the tiles.  Rows past M or N lie past the resources and read
+    // zero, and so does everything past the last tile (into slots that no stage reads; an empty resource
+    // takes no scalar offset: the check subtracts that).
+    const int sp = all * 256;  // bytes of the scales of 32 rows
+    __amdgpu_buffer_rsrc_t ra, rb, rs;
+    int ahead_tile = 0, ahead_k = 0;
+    auto tile_rsrc = [&]() LLMINT8_FP4_INLINE {
+        int64_t m0 = 0, n0 = 0, rows_a = 0, rows_b = 0;
+        if (ahead_tile < my_tiles) {
+            tile_origin(ahead_tile, m0, n0);
+            rows_a = p.M - m0 < BM ? p.M - m0 : BM;
+            rows_b = p.N - n0 < BN ? p.N - n0 : BN;
+        }
+        ra = buffer_rsrc(p.A + m0 * p.pitch, rows_a * p.pitch);
+        rb = buffer_rsrc(p.B + n0 * p.pitch, rows_b * p.pitch);
+        // half of the waves load A's scales, half B's
+        rs = wu < kWaves / 2 ? buffer_rsrc(p.sa + (m0 >> 5) * sp, ceil_div(rows_a, 32) * sp) : buffer_rsrc(p.sb + (n0 >> 5) * sp, ceil_div(rows_b, 32) * sp);
+    };
+    uint32_t off[4];  // of both operands: row 8 (4 wu + j) + lane / 8, its chunk lane % 8
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = 8 * (4 * wu + j) + lane / 8;
+        off[j] = (uint32_t)(r * p.pitch + (((lane & 7) ^ swz(r)) << 4));
+    }
+    const uint32_t off_s = (uint32_t)(2 * (wu % (kWaves / 2)) * sp + 4 * lane);
+    auto issue = [&](uint8_t* set, int j) LLMINT8_FP4_INLINE {  // load j of the cursor's stage
+        const int k = ahead_tile < my_tiles ? k0 + ahead_k : 0;
+        if (j < 4) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(set + (4 * wu + j) * 1024), 16, (int)off[j], k * BK, 0, 0);
+        else if (j < 8) __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(set + kSlotA + (4 * wu + j - 4) * 1024), 16, (int)off[j - 4], k * BK, 0, 0);
+        else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(set + kSlotA + kSlotB + (2 * wu + j - 8) * 256), 4, (int)(off_s + (j - 8) * sp), k * 256, 0, 0);
+    };
+    auto next_tile = [&]() LLMINT8_FP4_INLINE {  // once the tile's stages are loaded
+        if (ahead_k == nk) {
+            ahead_k = 0;
+            ++ahead_tile;
+            tile_rsrc();
+        }
+    };
+
+    // ---- reads: piece f of a slot holds rows 16 f + li, chunk q of either half
+    const int rd = li * BK + ((q ^ swz(li)) << 4);
+    auto read_m = [&](const uint8_t* set, int j, int h) LLMINT8_FP4_INLINE { return *(const v4i*)(set + (wm * MF + j) * 16 * BK + (h ? rd ^ 64 : rd)); };
+    auto read_n = [&](const uint8_t* set, int f, int h) LLMINT8_FP4_INLINE { return *(const v4i*)(set + kSlotA + (wn * NF + f) * 16 * BK + (h ? rd ^ 64 : rd)); };
+    auto read_sm = [&](const uint8_t* set, int j) LLMINT8_FP4_INLINE { return *(const int*)(set + kSlotA + kSlotB + (wm * NA + j) * 256 + 4 * lane); };
+    auto read_sn = [&](const uint8_t* set, int f) LLMINT8_FP4_INLINE { return *(const int*)(set + kSlotA + kSlotB + (BM / 32 + wn * NS + f) * 256 + 4 * lane); };
+
+    v4f acc[NF][MF];
+    v4i hm[2][MF], hn[LA];             // m pieces of either half; the next LA n pieces
+    int sm[NA], sn[NS], nsm[NA], nsn[NS];  // scales of the stage and of the next
+
+    auto stage = [&](int cur) LLMINT8_FP4_INLINE {
+        uint8_t *set = smem + cur * kSet, *next = smem + (cur + 1 == D ? 0 : cur + 1) * kSet;
+        v4i w[R];
+#pragma unroll
+        for (int r = 0; r < LA; ++r) w[r] = hn[r];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (r < R - LA) {
+                w[r + LA] = read_n(set, (r + LA) % NF, (r + LA) / NF);
+                if (r < MF) hm[1][r] = read_m(set, r, 1);
+            } else {
+                const int i = r - (R - LA);
+                if (i == 0) wait_and_meet<(D - 2) * kLoads>();
+                hn[i] = read_n(next, i, 0);
+                hm[0][i] = read_m(next, i, 0);
+#pragma unroll
+                for (int s = i * (NA + NS) / LA; s < (i + 1) * (NA + NS) / LA; ++s) {
+                    if (s < NA) nsm[s] = read_sm(next, s);
+                    else nsn[s - NA] = read_sn(next, s - NA);
+                }
+#pragma unroll
+                for (int l = i * kLoads / LA; l < (i + 1) * kLoads / LA; ++l) issue(set, l);
+            }
+            const int f = r % NF, h = r / NF;
+#pragma unroll
+            for (int j = 0; j < MF; ++j) acc[f][j] = mfma_fp4(w[r], hm[h][j], acc[f][j], sn[f / 2], 2 * h + f % 2, sm[j / 2], 2 * h + j % 2);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        ++ahead_k;
+#pragma unroll
+        for (int j = 0; j < NA; ++j) sm[j] = nsm[j];
+#pragma unroll
+        for (int f = 0; f < NS; ++f) sn[f] = nsn[f];
+    };
+
+    // ---- the first D stages, the first reads
+    tile_rsrc();
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) issue(smem + d * kSet, j);
+        ++ahead_k;
+        next_tile();
+    }
+    wait_and_meet<(D - 1) * kLoads>();
+#pragma unroll
+    for (int j = 0; j < LA; ++j) {
+        hn[j] = read_n(smem, j, 0);
+        hm[0][j] = read_m(smem, j, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < NA; ++j) sm[j] = read_sm(smem, j);
+#pragma unroll
+    for (int f = 0; f < NS; ++f) sn[f] = read_sn(smem, f);
+    int cur = 0;
+    for (int ti = 0; ti < my_tiles; ++ti) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int j = 0; j < MF; ++j) acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int kt = 0; kt < nk;) {  // (the inner loop stays one block: a branch in it costs the registers)
+            const int end = nk - kt < nk - ahead_k ? nk : kt + nk - ahead_k;
+            for (; kt < end; ++kt) {
+                stage(cur);
+                cur = cur + 1 == D ? 0 : cur + 1;
+            }
+            next_tile();
+        }
+        mfma_settle();
+        if (SPLIT && tp.split > 1) {
+            constexpr int H = 2;  // as the registers allow
+            constexpr uint32_t kStep = 64 * kWaves * 16;  // bytes of one quad of every thread
+            const int tile = x_start + local - part * T1;
+            auto slot = [&](int i) LLMINT8_FP4_INLINE {
+                return buffer_rsrc(p.partial + ((int64_t)tile * tp.split + i) * (BM * BN), (int64_t)BM * BN * 4);
+            };
+            const __amdgpu_buffer_rsrc_t own = slot(part);
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int j = 0; j < MF; ++j) store_part(own, 16 * tid, (f * MF + j) * kStep, acc[f][j]);
+            if (!last_part(p.counters + tile, tp.split, (int*)(smem + D * kSet))) break;
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int j = 0; j < MF; ++j) acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < tp.split; ++i) {
+                const __amdgpu_buffer_rsrc_t rp = slot(i);
+#pragma unroll
+                for (int f = 0; f < NF; f += H) {  // several loads under way
+                    v4f v[H][MF];
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+#pragma unroll
+                        for (int j = 0; j < MF; ++j) v[h][j] = load_part(rp, 16 * tid, ((f + h) * MF + j) * kStep);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+#pragma unroll
+                        for (int j = 0; j < MF; ++j) acc[f + h][j] += v[h][j];
+                }
+            }
+        }
+        int64_t m0, n0;
+        tile_origin(ti, m0, n0);
+        store_tile<DT, NF>(p, acc, smem + D * kSet + wu * 2048, m0 + 64 * wm, n0 + 16 * NF * wn);
+    }
+    // no load into this workgroup's LDS may outlive it
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 template <int DT, int WM, int WN, int NF>
@@ -30,9 +304,9 @@ hipError_t tiled(const Mxfp4GemmArgs& a, int split, hipStream_t stream) {
     const int nk = (int)(a.pitch >> 7);
     const TiledParams p{a, (int)ceil_div(a.M, BM), (int)ceil_div(a.N, BN), split, (int)ceil_div(nk, split)};
     const int64_t T = (int64_t)p.tiles_m * p.tiles_n;
-    if constexpr (NF == 8) {  // (tiles of 128 in parts run in mxfp4_single_kernel)
+    if constexpr (NF == 8) {  // (tiles of 128 in parts: single)
         if (split > 1) {
-            mxfp4_tiled_kernel<DT, WM, WN, NF, true><<<(unsigned)(T * split), 64 * WM * WN, 0, stream>>>(p);
+            mxfp4_tiled_kernel<DT, WM, WN, NF, true, 2><<<(unsigned)(T * split), 64 * WM * WN, 0, stream>>>(p);
             return hipGetLastError();
         }
     }
@@ -41,14 +315,14 @@ hipError_t tiled(const Mxfp4GemmArgs& a, int split, hipStream_t stream) {
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
     if (e != hipSuccess) return e;
     const int64_t G = (int64_t)(cus > 0 ? cus : 1) * (8 / (WM * WN));
-    mxfp4_tiled_kernel<DT, WM, WN, NF, false><<<(unsigned)(T < G ? T : G), 64 * WM * WN, 0, stream>>>(p);
+    mxfp4_tiled_kernel<DT, WM, WN, NF, false, 2><<<(unsigned)(T < G ? T : G), 64 * WM * WN, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 template <int DT>
 hipError_t single(const Mxfp4GemmArgs& a, int split, hipStream_t stream) {
     const TiledParams p{a, (int)ceil_div(a.M, 128), (int)ceil_div(a.N, 128), split, (int)ceil_div(a.pitch >> 7, split)};
-    mxfp4_single_kernel<DT><<<(unsigned)((int64_t)p.tiles_m * p.tiles_n * split), 256, 0, stream>>>(p);
+    mxfp4_tiled_kernel<DT, 2, 2, 4, true, 4><<<(unsigned)((int64_t)p.tiles_m * p.tiles_n * split), 256, 0, stream>>>(p);
     return hipGetLastError();
 }
 
