@@ -827,7 +827,7 @@ def mxfp4_matmul(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, Y: Op
     N = Wq.shape[0]
     _fp8_arg(w_scale, "w_scale", _E8M0, (-(-N // 32), fp4_scale_pitch(K)), dev)
     if Y is None:
-        Y = torch.empty((M, N), dtype=X.dtype, device=dev)
+        Y = X.new_empty((M, N))
     else:
         _fp8_arg(Y, "Y", (X.dtype,), (M, N), dev)
     L = lib()
@@ -906,12 +906,12 @@ def _norm(X, weight, residual, eps, format, keep, H, stream):
     if residual is not None:
         _fp8_arg(residual, "residual", (t,), (M, K), dev)
         if H is None:
-            H = torch.empty((M, K), dtype=t, device=dev)
+            H = torch.empty_like(X)
         else:
             _fp8_arg(H, "H", (t,), (M, K), dev)
     elif H is not None:
         raise ValueError("H is the sum with a residual: without one it would be X")
-    Y = torch.empty((M, K), dtype=t, device=dev) if keep else None
+    Y = torch.empty_like(X) if keep else None
     q = s = None
     if format == "fp8":
         q = torch.empty((M, fp8_code_pitch(K)), dtype=_E4M3[0], device=dev)
@@ -967,10 +967,10 @@ def rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tensor, dH
     if dH is not None:
         _fp8_arg(dH, "dH", (t,), (M, K), dev)
     if dX is None:
-        dX = torch.empty((M, K), dtype=t, device=dev)
+        dX = torch.empty_like(dY)
     else:
         _fp8_arg(dX, "dX", (t,), (M, K), dev)
-    dW = torch.empty((K,), dtype=t, device=dev) if need_dw else None
+    dW = torch.empty_like(weight) if need_dw else None
     L = lib()
     ws, at, size = _fp8_workspace(workspace, L.rmsnorm_backward_workspace_bytes(M, K, int(need_dw)), dev)
     rc = L.rmsnorm_backward(dY.data_ptr(), H.data_ptr(), weight.data_ptr(), None if dH is None else dH.data_ptr(), M, K, _DT[t], eps,

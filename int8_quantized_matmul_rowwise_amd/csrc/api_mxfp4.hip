@@ -81,7 +81,7 @@ Mxfp4Layout mxfp4_layout(int64_t M, int64_t K, int64_t N, bool coded) {
 
 const char* plan_name(const Mxfp4Plan& p) {
     switch (p.kind) {
-        case Mxfp4Plan::kTile256: return p.split > 1 ? "mxfp4_tile256_split" : "mxfp4_tile256";
+        case Mxfp4Plan::kTile256: return "mxfp4_tile256";
         case Mxfp4Plan::kTile128: return "mxfp4_tile128";
         case Mxfp4Plan::kSingle: return p.split > 1 ? "mxfp4_single_split" : "mxfp4_single";
         case Mxfp4Plan::kSmall: return p.split > 1 ? "mxfp4_small_split" : "mxfp4_small";

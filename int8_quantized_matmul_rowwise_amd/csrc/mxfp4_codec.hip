@@ -25,13 +25,12 @@ __global__ __launch_bounds__(256) void mxfp4_rows_kernel(const uint16_t* __restr
     const int64_t tr = id / tiles, tc = id % tiles;
     const int sub = threadIdx.x >> 5, sl = threadIdx.x & 31;
     const int64_t c = tc * 256 + 8 * sl, pitch = fp4_pitch(C);
+    // rows past R and columns past C read zero
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(X + tr * 32 * C, (R - tr * 32 < 32 ? R - tr * 32 : 32) * C * 2);
+    const uint32_t row_bytes = (uint32_t)C * 2, at = c < C ? sub * row_bytes + (uint32_t)c * 2 : 0x80000000u;  // C is a multiple of 8
     u32x4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = tr * 32 + 8 * i + sub;
-        v[i] = u32x4{0u, 0u, 0u, 0u};
-        if (r < R && c < C) v[i] = *(const u32x4*)(X + r * C + c);  // C is a multiple of 8
-    }
+    for (int i = 0; i < 4; ++i) v[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, c < C ? at + 8 * i * row_bytes : at, 0, 0));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t r = tr * 32 + 8 * i + sub;

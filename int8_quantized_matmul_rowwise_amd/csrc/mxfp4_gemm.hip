@@ -23,6 +23,10 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 #define LLMINT8_FP4_INLINE __attribute__((always_inline))
 // wait for this wave's LDS reads and all but the N newest loads and stores, then the bare barrier
 template <int N>
+__device__ __forceinline__ void meet_once_read() {  // all but the N newest LDS reads
+    asm volatile("s_waitcnt lgkmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+template <int N>
 __device__ __forceinline__ void wait_and_meet() {
     __builtin_amdgcn_s_waitcnt(0xC07F);
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
@@ -95,11 +99,17 @@ __device__ __forceinline__ void store_tile(const Mxfp4GemmArgs& p, const v4f (&a
 // has the unit's LDS to itself, and D = 4.
 // A step is one n piece against the four m pieces, of half a line (128 values): n pieces are read LA
 // steps ahead, m pieces of a half while the other one is multiplied, the scales in the steps after the
-// barrier.
+// barrier.  (With whole lines a step the m pieces of two stages take 32 registers more and the kernel
+// spills: 2048 x 4096 x 16384 184 us.)  The loop is one block: a branch in it costs the registers too.
 // Persistent over the XCD's run of tiles: the next tile's first loads are under way during a tile's last
 // stage and its output.
 // SPLIT: few tiles; a workgroup takes one part of one tile's stages, dumps its sums, and the last of the
 // tile's parts (if there are several) to end adds them up in their order and writes the output.
+// 4096 x 12288 x 36864: 870 to 890 us, 4.2 PFLOP/s; 8192 x 8192 x 8192 244 us, 4.5; 2048 x 4096 x 16384 68 us,
+// 4.0.  The power sets the clock there (1.3 to 1.9 GHz): with codes that are all zero the first two take
+// 593 and 188 us.  A loop of the instruction alone, from registers, reaches 7.1 PFLOP/s on random codes and
+// 9.7 on zeros (32 x 32 x 64 6.4 and 9.8).  Of the 593 us, 470 are left without loads and LDS reads.
+// Loads of A and of the scales from the middle of a stage on: zeros 666 to 593, random 880 and 887.
 template <int DT, int WM, int WN, int NF, bool SPLIT, int D>
 __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void mxfp4_tiled_kernel(TiledParams tp) {
     constexpr int kWaves = WM * WN, R = 2 * NF, LA = 4;
@@ -107,6 +117,10 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void mxfp4_tiled_kern
     constexpr int kSlotA = BM * BK, kSlotB = BN * BK, kSlotS = (BM + BN) / 32 * 256, kSet = kSlotA + kSlotB + kSlotS;
     constexpr int NA = MF / 2, NS = NF / 2;  // scale dwords of a wave's rows and columns
     constexpr int kLoads = 10;
+    // Tiles of 256: the m pieces and the scales are all read by step QB, where the workgroup meets once more,
+    // and A and the scales are loaded from there on, B after the other barrier.
+    constexpr int kEarly = NF == 8 ? 6 : 0, QB = 6;
+    static_assert(!kEarly || (MF < QB && QB + 3 <= R - LA), "read before, loaded before the next barrier");
     static_assert(BM / 8 / kWaves == 4 && BN / 8 / kWaves == 4 && (BM + BN) / 32 / kWaves == 2 && BM == BN, "ten loads a wave and stage");
     static_assert(LA == MF && LA <= NF, "one n piece and one m piece a step");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[D * kSet + kWaves * 2048];
@@ -194,12 +208,18 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void mxfp4_tiled_kern
         for (int r = 0; r < LA; ++r) w[r] = hn[r];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            if (kEarly && r >= QB && r < QB + 3) {
+                if (r == QB) meet_once_read<QB - MF>();  // but the n pieces of the steps since the last m piece
+                constexpr int order[6] = {0, 1, 2, 3, 8, 9};
+                issue(set, order[2 * (r - QB)]);
+                issue(set, order[2 * (r - QB) + 1]);
+            }
             if (r < R - LA) {
                 w[r + LA] = read_n(set, (r + LA) % NF, (r + LA) / NF);
                 if (r < MF) hm[1][r] = read_m(set, r, 1);
             } else {
                 const int i = r - (R - LA);
-                if (i == 0) wait_and_meet<(D - 2) * kLoads>();
+                if (i == 0) wait_and_meet<(D - 2) * kLoads + kEarly>();
                 hn[i] = read_n(next, i, 0);
                 hm[0][i] = read_m(next, i, 0);
 #pragma unroll
@@ -208,7 +228,7 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void mxfp4_tiled_kern
                     else nsn[s - NA] = read_sn(next, s - NA);
                 }
 #pragma unroll
-                for (int l = i * kLoads / LA; l < (i + 1) * kLoads / LA; ++l) issue(set, l);
+                for (int l = kEarly ? 4 + i : i * kLoads / LA; l < (kEarly ? 5 + i : (i + 1) * kLoads / LA); ++l) issue(set, l);
             }
             const int f = r % NF, h = r / NF;
 #pragma unroll
@@ -299,17 +319,10 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void mxfp4_tiled_kern
 }
 
 template <int DT, int WM, int WN, int NF>
-hipError_t tiled(const Mxfp4GemmArgs& a, int split, hipStream_t stream) {
+hipError_t tiled(const Mxfp4GemmArgs& a, hipStream_t stream) {
     constexpr int BM = 16 * MF * WM, BN = 16 * NF * WN;
-    const int nk = (int)(a.pitch >> 7);
-    const TiledParams p{a, (int)ceil_div(a.M, BM), (int)ceil_div(a.N, BN), split, (int)ceil_div(nk, split)};
+    const TiledParams p{a, (int)ceil_div(a.M, BM), (int)ceil_div(a.N, BN), 1, (int)(a.pitch >> 7)};
     const int64_t T = (int64_t)p.tiles_m * p.tiles_n;
-    if constexpr (NF == 8) {  // (tiles of 128 in parts: single)
-        if (split > 1) {
-            mxfp4_tiled_kernel<DT, WM, WN, NF, true, 2><<<(unsigned)(T * split), 64 * WM * WN, 0, stream>>>(p);
-            return hipGetLastError();
-        }
-    }
     int dev = 0, cus = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
@@ -497,11 +510,16 @@ hipError_t small_launch(const Mxfp4GemmArgs& a, int split, hipStream_t stream) {
 
 template <int DT>
 hipError_t small(const Mxfp4GemmArgs& a, const Mxfp4Plan& plan, hipStream_t stream) {
-    if (plan.kind == Mxfp4Plan::kFused)
-        return plan.columns == 1 ? small_launch<DT, 1, 1, 8, true, 1, 4>(a, plan.split, stream) : small_launch<DT, 1, 2, 8, true, 1, 4>(a, plan.split, stream);
+    if (plan.kind == Mxfp4Plan::kFused) {
+        if (plan.columns == 1) return small_launch<DT, 1, 1, 8, true, 1, 4>(a, plan.split, stream);
+        // fewer waves once there are many workgroups: 1 x 8192 x 8192 9.4 us with 8, 10.5 with 4; 1 x 4096 x 14336 9.9
+        // and 9.3
+        return a.N < 12288 ? small_launch<DT, 1, 2, 8, true, 1, 4>(a, plan.split, stream) : small_launch<DT, 1, 2, 4, true, 1, 4>(a, plan.split, stream);
+    }
     switch (4 * plan.pieces + plan.columns) {
         case 4 + 1: return small_launch<DT, 1, 1, 4, false, 2, 4>(a, plan.split, stream);
-        case 4 + 2: return small_launch<DT, 1, 2, 4, false, 1, 4>(a, plan.split, stream);
+        case 4 + 2: return small_launch<DT, 1, 2, 8, false, 2, 2>(a, plan.split, stream);
+        case 4 + 4: return small_launch<DT, 1, 4, 8, false, 1, 2>(a, plan.split, stream);
         case 8 + 1: return small_launch<DT, 2, 1, 4, false, 1, 4>(a, plan.split, stream);
         case 8 + 2: return small_launch<DT, 2, 2, 8, false, 1, 2>(a, plan.split, stream);
         case 16 + 1: return small_launch<DT, 4, 1, 4, false, 1, 4>(a, plan.split, stream);
@@ -509,11 +527,15 @@ hipError_t small(const Mxfp4GemmArgs& a, const Mxfp4Plan& plan, hipStream_t stre
     }
 }
 
-// Parts of the sum of `tiles` (at most 256) tiles of 128 x 128, one workgroup a compute unit.
+// Parts of the sum of `tiles` (at most 256) tiles of 128 x 128, one workgroup a compute unit.  The
+// estimate, in units of 0.1 ns, from measurements over 32 to 256 tiles and 16 to 64 lines: a line takes
+// 0.44 us, up to 0.68 us as more workgroups share the memory; joining s parts takes 2 us + 1.6 us a
+// part + 20 ns a part and tile.  128 x 16384 x 4096 (32 tiles): 32.5 us unsplit, 28.0 in 2 parts, 20.3 in 4,
+// 29.6 in 8; 512 x 16384 x 4096 (128 tiles): 35.7, 34.1 in 2; 512 x 4096 x 4096 (128 tiles): 13.8, 20.4 in 2.
 int single_parts(int64_t tiles, int64_t lines) {
     auto cost = [&](int64_t i) {
         const int64_t wgs = tiles * i;
-        return ceil_div(lines, i) * (4200 + 1200 * wgs / 256) + (i > 1 ? 20000 + 10000 * i + 110 * wgs : 0);
+        return ceil_div(lines, i) * (4400 + 2400 * wgs / 256) + (i > 1 ? 20000 + 16000 * i + 200 * wgs : 0);
     };
     int64_t s = 1;
     for (int64_t i = 2; i * tiles <= 256 && i <= lines / 4; ++i)
@@ -525,26 +547,36 @@ int single_parts(int64_t tiles, int64_t lines) {
 
 Mxfp4Plan mxfp4_plan(int64_t M, int64_t N, int64_t nk, bool x16) {
     Mxfp4Plan p{Mxfp4Plan::kTile256, 0, 0, 1, 0, 0};
-    int64_t out = 256 * 256;
-    if (M <= 32 || (M <= 64 && N * nk <= (int64_t)1 << 17)) {
-        const bool fused = x16 && M <= 4 && N * nk <= (int64_t)1 << 19 && (N >= 2048 || nk < 32);
+    int64_t out = 0;  // of a workgroup whose sum is split
+    // Few rows straight from memory; past 32 rows while B is small, as there the tiles, whose rows are shared,
+    // catch up: 64 x 8192 x 8192 14.7 us, in a tile's kernel 18.9, 64 x 4096 x 16384 15.5 and 13.0, 48 x 16384 x 4096
+    // 19.0 and 19.5, 24 x 4096 x 16384 11.1 and 12.8.
+    if (M <= 32 || (M <= 64 && (N * nk <= (int64_t)1 << 17 || (N <= 8192 && N * nk <= (int64_t)1 << 18)))) {
+        // A coded in the kernel, or by a launch before it (every workgroup codes the rows that it multiplies;
+        // both launches together): 1 x 4096 x 4096 5.6 and 7.0 us, 4 x 8192 x 8192 10.5 and 11.3, 4 x 8192 x 28672
+        // 33.0 and 29.2, 8 x 4096 x 4096 6.5 and 7.3, 8 x 4096 x 14336 11.4 and 10.8, 16 x 2048 x 2048 5.0 and 6.4, 16 x
+        // 4096 x 4096 8.3 and 7.8; not where a long sum wants parts (4 x 16384 x 1024: 13.3 us, in parts 9.6).
+        const bool fused = x16 && M <= 16 && N * nk <= (int64_t)1 << (M <= 4 ? 19 : (M <= 8 ? 18 : 16)) && (N >= 2048 || nk < 32);
         p.kind = fused ? Mxfp4Plan::kFused : Mxfp4Plan::kSmall;
         p.pieces = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
-        p.columns = N < 8192 ? 1 : 2;
+        // Pieces of 16 columns of a workgroup: 16 x 4096 x 4096 4.8 us with one, 5.8 with two, 16 x 8192 x 8192 10.8,
+        // 9.0 and (four) 12.4, 16 x 8192 x 28672 33.6, 30.2 and 27.3; coded in the kernel, 1 x 4096 x 4096 5.6 with one,
+        // 6.5 with two, 1 x 8192 x 8192 12.2 and 9.4.
+        p.columns = N < 8192 ? 1 : (p.pieces == 1 && !fused && N >= 24576 ? 4 : 2);
         p.tiles = ceil_div(N, 16 * p.columns);
-        if (!fused && (p.tiles < 128 || (p.tiles == 128 && p.pieces > 1))) p.split = sum_parts(nk, 256 / p.tiles, 4);
+        // Parts of the sum where columns alone leave units idle (with the coding): 16 x 16384 x 1024 13.2 us, in 4
+        // parts 10.5; 64 x 8192 x 1024 15.4 and 11.5; 16 x 8192 x 1024 9.6 and 9.5.
+        if (!fused && (p.tiles < 128 || (p.tiles == 128 && p.pieces > 1))) p.split = sum_parts(nk, 256 / p.tiles, 8);
         out = 256 * p.columns * p.pieces;
-    } else {
-        const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256), t128 = ceil_div(M, 128) * ceil_div(N, 128);
-        if (t128 <= 512 && !(t128 > 256 && nk >= 48)) {
-            p.kind = t128 <= 256 ? Mxfp4Plan::kSingle : Mxfp4Plan::kTile128;
-            out = 128 * 128;
-            p.tiles = t128;
-            if (t128 <= 256) p.split = single_parts(t128, nk);
-        } else {
-            p.tiles = t256;
-            if (t256 <= 128) p.split = sum_parts(nk, 256 / t256, 16);
-        }
+    } else if (const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128); t128 <= 512) {
+        // Tiles of 128 where all of them fit the card at once (two a compute unit): 2048 x 4096 x 4096 23 us, with
+        // tiles of 256 29.7, 2048 x 16384 x 4096 71.4 and 95.6; past that 700 x 4096 x 16384 35.8 and 31.7, 2048 x 8192 x
+        // 8192 71.7 and 61.7.  One tile a unit: four sets of slots, and parts of the sum: 512 x 8192 x 8192 (256 tiles)
+        // 23.6 us, with two sets 26.5.
+        p.kind = t128 <= 256 ? Mxfp4Plan::kSingle : Mxfp4Plan::kTile128;
+        p.tiles = t128;
+        if (t128 <= 256) p.split = single_parts(t128, nk);
+        out = 128 * 128;
     }
     p.partial_bytes = p.split > 1 ? p.tiles * p.split * out * 4 : 0;
     return p;
@@ -552,8 +584,8 @@ Mxfp4Plan mxfp4_plan(int64_t M, int64_t N, int64_t nk, bool x16) {
 
 hipError_t launch_mxfp4_gemm(int dt, const Mxfp4GemmArgs& a, const Mxfp4Plan& plan, hipStream_t stream) {
     if (a.M == 0 || a.N == 0) return hipSuccess;
-    if (plan.kind == Mxfp4Plan::kTile256) return dt == F16 ? tiled<F16, 4, 2, 8>(a, plan.split, stream) : tiled<BF16, 4, 2, 8>(a, plan.split, stream);
-    if (plan.kind == Mxfp4Plan::kTile128) return dt == F16 ? tiled<F16, 2, 2, 4>(a, plan.split, stream) : tiled<BF16, 2, 2, 4>(a, plan.split, stream);
+    if (plan.kind == Mxfp4Plan::kTile256) return dt == F16 ? tiled<F16, 4, 2, 8>(a, stream) : tiled<BF16, 4, 2, 8>(a, stream);
+    if (plan.kind == Mxfp4Plan::kTile128) return dt == F16 ? tiled<F16, 2, 2, 4>(a, stream) : tiled<BF16, 2, 2, 4>(a, stream);
     if (plan.kind == Mxfp4Plan::kSingle) return dt == F16 ? single<F16>(a, plan.split, stream) : single<BF16>(a, plan.split, stream);
     return dt == F16 ? small<F16>(a, plan, stream) : small<BF16>(a, plan, stream);
 }

@@ -174,6 +174,26 @@ def test_stages_and_their_failures(name, monkeypatch, capfd):
         assert run(st) == (lm.EHIP, want[: i + 1])
 
 
+@pytest.mark.parametrize("M,K,N,path,coded", [
+    (1, 16, 8, "mxfp4_small_fused", "mxfp4_small"), (4, 8192, 16384, "mxfp4_small_fused", "mxfp4_small"), (4, 8192, 16392, "mxfp4_small", "mxfp4_small"),
+    (8, 8192, 8192, "mxfp4_small_fused", "mxfp4_small"), (9, 8192, 8192, "mxfp4_small", "mxfp4_small"), (16, 4096, 4096, "mxfp4_small_fused", "mxfp4_small"),
+    (17, 4096, 4096, "mxfp4_small", "mxfp4_small"), (16, 4096, 28672, "mxfp4_small", "mxfp4_small"), (1, 16384, 1024, "mxfp4_small_split", "mxfp4_small_split"),
+    (64, 8192, 8192, "mxfp4_small", "mxfp4_small"), (64, 4096, 16384, "mxfp4_single", "mxfp4_single"), (65, 256, 8, "mxfp4_single", "mxfp4_single"),
+    (128, 16384, 4096, "mxfp4_single_split", "mxfp4_single_split"), (2048, 4096, 4096, "mxfp4_tile128", "mxfp4_tile128"),
+    (2048, 16384, 4096, "mxfp4_tile128", "mxfp4_tile128"), (4096, 16384, 2056, "mxfp4_tile256", "mxfp4_tile256"),
+])
+def test_routes(M, K, N, path, coded, monkeypatch, capfd):
+    monkeypatch.setenv("LLMINT8_LOG", "1")
+    monkeypatch.setenv("LLMINT8_FAULT", "no_such_stage")
+    far = 1 << 44  # addresses that nothing reads
+    for name, call in ((path, lambda: mm(X=far, M=M, K=K, Wq=2 * far, s=3 * far, N=N, Y=4 * far, ws=5 * far, wsb=1 << 40)),
+                       (coded, lambda: mmc(X=far, xs=6 * far, M=M, K=K, Wq=2 * far, s=3 * far, N=N, Y=4 * far, ws=5 * far, wsb=1 << 40))):
+        capfd.readouterr()
+        assert call() == lm.OK
+        assert re.findall(r"path=(\w+)", capfd.readouterr().err) == [name]
+    assert lm.mxfp4_matmul_workspace_bytes(M, K, N) < 1 << 30
+
+
 def test_sizes():
     for n in (0, 1, 16, 255, 256, 257, 4096, 12288):
         assert lm.lib().fp4_code_pitch(n) == lm.fp4_code_pitch(n) == ref.code_pitch(n)
