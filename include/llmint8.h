@@ -531,9 +531,10 @@ int mxfp4_matmul_coded(const uint8_t* Xq, const uint8_t* x_scale, int64_t M, int
  *   y_scale  out: the rows' scales (4-byte aligned): ceil(K/128) times fp8_row_scale_pitch(M) bytes as
  *            fp8_matmul_block_coded takes them, or ceil(M/32) rows of fp4_scale_pitch(K) bytes; zero
  *            past the last row.
- * A row of zeros gives zeros.  Squares are summed in fp32: a row whose sum of squares passes 2^128 gives
- * zeros, and NaN where h * weight passes it too.  A row with a value that is not finite gives NaN or
- * zeros in that row alone.  M and K are at most 2^22 (LLMINT8_ERANGE); K a multiple of 16.
+ * A row of zeros gives zeros.  Squares are summed in fp32, and h * weight is an fp32 number: a row whose sum
+ * of squares passes 2^128 gives zeros, a value whose h * weight passes it is not finite.  A row with a
+ * value that is not finite gives NaN or zeros in that row alone.  M and K are at most 2^22
+ * (LLMINT8_ERANGE); K a multiple of 16.
  */
 int rmsnorm_forward(const void* X, const void* residual, const void* weight, int64_t M, int64_t K, int dtype, float eps, void* H,
                     void* Y, int format, uint8_t* Yq, uint8_t* y_scale, void* stream);

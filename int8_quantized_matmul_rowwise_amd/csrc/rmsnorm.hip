@@ -242,13 +242,14 @@ __device__ __forceinline__ void row_sums(const u32x4& h, const u32x4& dy, const 
         s[1] = __builtin_fmaf(high<DT>(dy[d]) * high<DT>(w[d]), b, s[1]);
     }
 }
+// m = r mean(d h).  (r^2 is not formed: in a row of zeros it passes fp32 with an eps below 2^-128.)
 template <int DT>
 __device__ __forceinline__ u32x4 row_dx(const u32x4& h, const u32x4& dy, const u32x4& w, const u32x4& dh, float r, float m) {
     u32x4 o;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-        const float a = r * (low<DT>(dy[d]) * low<DT>(w[d]) - low<DT>(h[d]) * m) + low<DT>(dh[d]);
-        const float b = r * (high<DT>(dy[d]) * high<DT>(w[d]) - high<DT>(h[d]) * m) + high<DT>(dh[d]);
+        const float a = r * (low<DT>(dy[d]) * low<DT>(w[d]) - low<DT>(h[d]) * r * m) + low<DT>(dh[d]);
+        const float b = r * (high<DT>(dy[d]) * high<DT>(w[d]) - high<DT>(h[d]) * r * m) + high<DT>(dh[d]);
         o[d] = pack<DT>(a, b);
     }
     return o;
@@ -304,7 +305,7 @@ __global__ __launch_bounds__(AHEAD ? 512 : T, AHEAD ? 2 : 4) void rmsnorm_backwa
 #pragma unroll
         for (int v = 0; v < V; ++v) row_sums<DT>(x.h[v], x.dy[v], w[v], s);
         group_sum<2, T>(s, red[turn][side]);
-        const float r = inverse_root(s[0], p.inv_k, p.eps), m = r * r * (float)(s[1] * p.inv_k);
+        const float r = inverse_root(s[0], p.inv_k, p.eps), m = r * (float)(s[1] * p.inv_k);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (v * T + tid) * 8;
@@ -359,7 +360,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_long_kernel(NormBackwar
         for (int64_t c = 8 * threadIdx.x; c < p.K; c += 8192)
             row_sums<DT>(*(const u32x4*)(p.H + row * p.K + c), *(const u32x4*)(p.dY + row * p.K + c), *(const u32x4*)(p.W + c), s);
         group_sum<2, T>(s, red[turn]);
-        const float r = inverse_root(s[0], p.inv_k, p.eps), m = r * r * (float)(s[1] * p.inv_k);
+        const float r = inverse_root(s[0], p.inv_k, p.eps), m = r * (float)(s[1] * p.inv_k);
         if (threadIdx.x == 0 && p.rows) p.rows[row] = r;
         for (int64_t c = 8 * threadIdx.x; c < p.K; c += 8192) {
             const u32x4 none = {0u, 0u, 0u, 0u};

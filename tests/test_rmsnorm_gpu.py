@@ -243,6 +243,20 @@ def test_backward(M, K, dt):
         assert torch.equal(again[0], dX) and torch.equal(again[1], dW)
 
 
+@pytest.mark.parametrize("M,K", [(3, 256), (3, 8208), (600, 1040), (3, 16400), (3, 32784)])
+def test_backward_of_zeros_with_the_smallest_eps(M, K):
+    """r = 2^64.. is an fp32 number, its square is not: a row of zeros has the gradient r d."""
+    dt, eps = torch.bfloat16, float(torch.tensor(2.0 ** -130))
+    H, _, w, g = inputs(M, K, dt)
+    H[0] = H[M - 1] = 0
+    dY = randn(g, M, K).to(dt)
+    dX, dW = lm.rmsnorm_backward(dY.cuda(), H.cuda(), w.cuda(), eps=eps)
+    x, xe, v, ve = ref.norm_backward(dY.double(), H.double(), w.double(), None, eps)
+    assert float(x[0].abs().max()) > 2.0 ** 64
+    ref.assert_close(dX, x, xe, "dX")
+    ref.assert_close(dW, v, ve, "dW")
+
+
 def test_backward_against_differences():
     """sum(dY * y) along a direction, from the reference's own norm in 64 bits; 16-bit gradients are off by
     half a step a value, which over K products of random sign stays far below the sum's size."""
