@@ -345,6 +345,9 @@ hipError_t single(const Mxfp4GemmArgs& a, int split, hipStream_t stream) {
 // the waves.  With FUSED (one piece of 16 rows), A is the 16-bit X itself: a lane codes its own groups.
 // With few columns the steps are split over `split` workgroups too (grid.y, `part` steps each):
 // their sums go through memory and the last one adds them up in their order.
+// Bound by memory, and at the smallest sizes by a launch and one round of loads: 16 x 8192 x 8192 9.2 us (36
+// MB, 3.9 TB/s), 16 x 8192 x 28672 27.3 (4.6), 1 x 4096 x 4096 with the coding 5.6 (8.9 MB), of which an empty kernel
+// takes about 2.
 template <int DT, int MG, int NF, int WV, bool FUSED, int U, int OCC>
 __global__ __launch_bounds__(64 * WV, OCC) void mxfp4_small_kernel(Mxfp4GemmArgs p, int split, int part) {
     static_assert(!FUSED || MG == 1, "one piece of rows");

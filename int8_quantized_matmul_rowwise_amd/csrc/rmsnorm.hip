@@ -6,7 +6,14 @@
 // products make of y themselves.
 //
 // Both are bound by memory: a row is read once into registers (8 columns a piece and thread, a
-// workgroup a row), summed over lanes, then waves, and written.
+// workgroup a row, up to 32768 columns and in the gradient 16384), summed over lanes, then waves, and
+// written.  With few rows a row's own latency is what is left: a load, two meetings, a store.
+// Norm: 1 x 4096 to 16 bits without a residual 1.8 us, 16 x 8192 to e2m1 codes 4.0; 4096 x 8192 with a residual to
+// e2m1 43.8 us (5.4 TB/s), to e4m3 45.5 (5.2), to 16 bits 47.4 (5.7); 2048 x 4096 to e4m3 11.3.
+// Gradient, with dw: 2048 x 4096 with dh 21 us, 8192 x 8192 with dh 106 (5.1 TB/s), 4096 x 16384 with dh 109 (4.9),
+// 333 x 1040 7.6 (two launches).  dw needs a sum over rows: each
+// workgroup keeps its own in registers over its rows, at most 512 rows of partial sums leave, and a second
+// launch joins them in their order (3.8 to 5 us); no atomics, so results do not change from run to run.
 #include "../../include/llmint8.h"
 #include "launch.hpp"
 #include "mxfp4_common.hpp"
