@@ -105,8 +105,8 @@ __device__ __forceinline__ void store_tile(const Mxfp4GemmArgs& p, const v4f (&a
 // stage and its output.
 // SPLIT: few tiles; a workgroup takes one part of one tile's stages, dumps its sums, and the last of the
 // tile's parts (if there are several) to end adds them up in their order and writes the output.
-// 4096 x 12288 x 36864: 870 to 890 us, 4.2 PFLOP/s; 8192 x 8192 x 8192 244 us, 4.5; 2048 x 4096 x 16384 68 us,
-// 4.0.  The power sets the clock there (1.3 to 1.9 GHz): with codes that are all zero the first two take
+// 4096 x 12288 x 36864: 870 to 890 us, 4.2 PFLOP/s (770 on another card); 8192 x 8192 x 8192 244 us, 4.5; 2048 x
+// 4096 x 16384 64 to 74 us, 3.7 to 4.3.  The power sets the clock there (1.3 to 1.9 GHz): with codes that are all zero the first two take
 // 593 and 188 us.  A loop of the instruction alone, from registers, reaches 7.1 PFLOP/s on random codes and
 // 9.7 on zeros (32 x 32 x 64 6.4 and 9.8).  Of the 593 us, 470 are left without loads and LDS reads.
 // Loads of A and of the scales from the middle of a stage on: zeros 666 to 593, random 880 and 887.
@@ -346,8 +346,8 @@ hipError_t single(const Mxfp4GemmArgs& a, int split, hipStream_t stream) {
 // With few columns the steps are split over `split` workgroups too (grid.y, `part` steps each):
 // their sums go through memory and the last one adds them up in their order.
 // Bound by memory, and at the smallest sizes by a launch and one round of loads: 16 x 8192 x 8192 9.2 us (36
-// MB, 3.9 TB/s), 16 x 8192 x 28672 27.3 (4.6), 1 x 4096 x 4096 with the coding 5.6 (8.9 MB), of which an empty kernel
-// takes about 2.
+// MB, 3.9 TB/s), 16 x 8192 x 28672 27.3 (4.6), 1 x 4096 x 4096 with the coding 5.6 (8.9 MB; the norm
+// of a single row, a launch with one round trip to memory, takes 1.8).
 template <int DT, int MG, int NF, int WV, bool FUSED, int U, int OCC>
 __global__ __launch_bounds__(64 * WV, OCC) void mxfp4_small_kernel(Mxfp4GemmArgs p, int split, int part) {
     static_assert(!FUSED || MG == 1, "one piece of rows");
