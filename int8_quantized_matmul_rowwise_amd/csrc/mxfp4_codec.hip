@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void mxfp4_rows_kernel(const uint16_t* __restr
     for (int i = 0; i < 4; ++i) {
         const int64_t r = tr * 32 + 8 * i + sub;
         const uint32_t e = fp4_scale_byte<DT>(quad_max(max_pattern(magnitudes(v[i]))));
-        if (r < R) *(uint32_t*)(q + r * pitch + (c >> 1)) = e2m1x8<DT>(v[i], e8m0_value(e));
+        if (r < R) *(uint32_t*)(q + r * pitch + (c >> 1)) = e2m1x8<DT>(v[i], fp4_code_scale(e));
         if ((sl & 3) == 0) scales[fp4_scale_at(8 * i + sub, sl >> 2, 256)] = (uint8_t)e;  // (rows past the last: zeros)
     }
     __syncthreads();
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256) void mxfp4_columns_kernel(const uint16_t* __re
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint32_t e = fp4_scale_byte<DT>((m[j >> 1] >> (16 * (j & 1))) & 0xffffu);
-        const float sv = e8m0_value(e);
+        const float sv = fp4_code_scale(e);
         const int col = 4 * cc + j;
         scales[fp4_scale_at(col, g, 256)] = (uint8_t)e;
         u32x4 code;

@@ -34,6 +34,11 @@ __device__ __forceinline__ uint32_t fp4_scale_byte(uint32_t pattern) {
     return pattern >= (DT == F16 ? 0x7c00u : 0x7f80u) ? 255u : (b > 0 ? (uint32_t)b : 0u);
 }
 
+// The value of the scale at which a group is coded.  With byte 255 (a finite number needs at most 253) that is
+// 2^127, where a zero still has the code zero, so that what pads a row stays zero: at NaN itself the
+// instruction codes a zero as something else.
+__device__ __forceinline__ float fp4_code_scale(uint32_t e) { return e8m0_value(e < 254u ? e : 254u); }
+
 // Codes of two 16-bit values (a pattern pair) at the scale's value s, into byte B of `old`: the
 // instruction divides by the power of two, rounds once and saturates.
 template <int DT, int B>

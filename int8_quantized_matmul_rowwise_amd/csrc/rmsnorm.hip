@@ -133,7 +133,7 @@ __device__ __forceinline__ void store_codes(const NormArgs& p, int64_t row, int6
         const int64_t pitch = fp4_pitch(p.K);
         const uint32_t e = fp4_scale_byte<DT>(quad_max(max_pattern(magnitudes(y))));
         if (c >= 2 * pitch) return;
-        *(uint32_t*)(p.q + row * pitch + (c >> 1)) = e2m1x8<DT>(y, e8m0_value(e));
+        *(uint32_t*)(p.q + row * pitch + (c >> 1)) = e2m1x8<DT>(y, fp4_code_scale(e));
         if ((threadIdx.x & 3) == 0) p.s[fp4_scale_at(row, c >> 5, fp4_scale_pitch_of(p.K))] = (uint8_t)e;
     }
 }

@@ -104,6 +104,29 @@ def test_quantize_not_finite(v, dt, columns):
 
 
 @pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("v", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("columns", [False, True])
+@pytest.mark.parametrize("n", [16, 48, 272, 528])
+def test_padding_of_groups_that_are_not_finite(n, columns, v, dt):
+    """Codes past n are zeros, in a last group of 16 values that is not finite too; scales past the last group and
+    row are zeros, and the other groups keep their codes."""
+    X = randn(gen(n), 40, n).to(dt)
+    Y = X.clone()
+    Y[3, n - 1] = Y[39, n - 16] = v
+    if columns:
+        X, Y = X.t().contiguous(), Y.t().contiguous()
+    q0, s0 = lm.mxfp4_quantize(X.cuda(), columns=columns)
+    q1, s1 = lm.mxfp4_quantize(Y.cuda(), columns=columns)
+    assert not q0[:, n // 2:].any() and not q1[:, n // 2:].any()
+    _, _, rs = ref.coded(Y.t() if columns else Y)
+    assert torch.equal(u8(s1), rs) and int((rs == 255).sum()) == 2
+    a, b = q0.cpu(), q1.cpu()
+    for r in (3, 39):
+        b[r, (n - 16) // 32 * 16:] = a[r, (n - 16) // 32 * 16:]
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt", DTS)
 def test_dequantize_every_code_and_scale(dt):
     n = 256
     q = torch.arange(256, dtype=torch.uint8)[:128].repeat(256, 1)
