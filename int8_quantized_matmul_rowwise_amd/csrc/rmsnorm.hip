@@ -192,7 +192,8 @@ __global__ __launch_bounds__(T, 4) void rmsnorm_kernel(NormArgs p) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int64_t c = ((int64_t)v * T + tid) * 8;
-            const u32x4 y = scaled<DT>(h[v], w[v], r);
+            // (past the row's end 0 in the place of r, which may be NaN: the codes' padding is zeros)
+            const u32x4 y = scaled<DT>(h[v], w[v], FORMAT == LLMINT8_CODES_NONE || c < p.K ? r : 0.0f);
             if (p.Y && c < p.K) *(u32x4*)(p.Y + row * p.K + c) = y;
             store_codes<DT, FORMAT>(p, row, c, y);
         }

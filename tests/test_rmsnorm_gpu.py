@@ -153,6 +153,31 @@ def test_rows_that_are_not_finite_stay_alone(K, dt):
         assert torch.equal(dX.cpu()[keep], lm.rmsnorm_backward(X.cuda(), X.cuda(), w, eps=EPS)[0].cpu()[keep])
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M,K", [(5, 16), (5, 144), (3, 272), (7, 1040), (2, 4112), (2, 8208), (2, 16400), (2, 32784), (2060, 272), (2060, 528),
+                                 (2060, 1040), (2060, 2064), (2060, 4112), (2060, 8208)])
+def test_padding_of_rows_that_are_not_finite(M, K, dt):
+    """Codes and scales past a row's last value are zeros whatever the row holds, and all of them are the codes of
+    Y: every kernel of the norm, at sizes whose rows do not fill the codes' lines."""
+    print(f"\n[case] rmsnorm padding {dt} {M}x{K}", flush=True)
+    X, _, w, _ = inputs(M, K, dt)
+    bad = {0: math.nan, M // 2: math.inf, M - 1: math.nan}
+    for r, v in bad.items():
+        X[r, K - 1 - 3 * r % K] = v
+    X, w = X.cuda(), w.cuda()
+    plain, _ = lm.rmsnorm(X, w, eps=EPS)
+    q, s, Y, _ = lm.rmsnorm_quantize(X, w, eps=EPS, format="mxfp4", keep=True)
+    q0, s0 = lm.mxfp4_quantize(plain)
+    assert torch.equal(u8(Y), u8(plain)) and torch.equal(u8(s), u8(s0)) and torch.equal(u8(q), u8(q0))
+    assert not q[:, K // 2:].any()
+    q, s, Y, _ = lm.rmsnorm_quantize(X, w, eps=EPS, format="fp8", keep=True)
+    assert torch.equal(u8(Y), u8(plain)) and not q.view(torch.uint8)[:, K:].any()
+    assert torch.isnan(q[0].float()[:K]).all() and torch.isnan(q[M - 1].float()[:K]).all()
+    codes, y = q.cpu().float().double(), plain.cpu()
+    codes[list(bad)], y[list(bad)] = 0, 0
+    assert torch.equal(codes, fp8_ref.coded_rows(y)[1])
+
+
 def test_norm_of_large_and_small_numbers():
     """Squares stay within fp32 up to a sum of 2^128; below eps a row is as good as divided by its root."""
     dt, K = torch.bfloat16, 256
