@@ -68,4 +68,14 @@ __host__ __device__ constexpr int64_t xqb_offset(int64_t r, int64_t k, int64_t n
     return ((r >> 4) * nsteps + (k >> 6)) * 1024 + (r & 15) * 64 + (k & 63);
 }
 
+// A 16-byte store at off + at (the lane's and a uniform part) of a buffer.  The whole offset is in the
+// vector register: with a scalar one the compiler (ROCm 7.2) leaves no wait state between the store and an
+// instruction that overwrites its data, and the store then takes the new values.  Opaque, or the sums of
+// all stores would be held in registers over the loop before them.
+template <int POLICY>
+__device__ __forceinline__ void store_wide(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t at, const u32x4& v) {
+    asm volatile("" : "+v"(off));
+    __builtin_amdgcn_raw_buffer_store_b128(v, rs, off + at, 0, POLICY);
+}
+
 }  // namespace llmint8

@@ -121,12 +121,8 @@ __device__ __forceinline__ bool last_part(int32_t* counter, int parts, int* flag
 __device__ __forceinline__ v4f load_part(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t at) {
     return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off, at, kCoherent));
 }
-// (The whole offset per lane: the compiler leaves no wait state between a wide store that has a scalar
-// offset and an instruction that overwrites its data, and the store then takes the new values.  Opaque, or the
-// sums of all stores would be held in registers over the main loop.)
 __device__ __forceinline__ void store_part(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t at, const v4f& v) {
-    asm volatile("" : "+v"(off));
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, off + at, 0, kCoherent);
+    store_wide<kCoherent>(rs, off, at, __builtin_bit_cast(u32x4, v));
 }
 
 }  // namespace llmint8

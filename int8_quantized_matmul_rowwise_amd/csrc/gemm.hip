@@ -579,8 +579,8 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_kernel(Params p) {
         };
         constexpr int kCoherent = 16;
         auto slot_rsrc = [&](int c) { return buffer_rsrc(sk_slot(c, t), (int64_t)BM * BN * 4); };
-        // lane part in the one VGPR offset, piece part in the scalar offset (a VGPR per
-        // piece would be hoisted over the main loop)
+        // lane part in the one VGPR offset; piece part, in the loads below, in the scalar offset
+        // (a VGPR per piece would be hoisted over the main loop; the stores need one: store_wide)
         const uint32_t lane_off = (uint32_t)tid * 16;
         auto piece = [&](int i, int j, int q) { return (uint32_t)(((i * NJ + j) * 4 + q) * (64 * kWaves) * 16); };
         {
@@ -592,10 +592,9 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_kernel(Params p) {
                     if (block_live(i, j))
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            __builtin_amdgcn_raw_buffer_store_b128(
-                                __builtin_bit_cast(u32x4, v4i{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                                                              acc[i][j][4 * q + 3]}),
-                                rs, lane_off, piece(i, j, q), kCoherent);
+                            store_wide<kCoherent>(rs, lane_off, piece(i, j, q),
+                                                  __builtin_bit_cast(u32x4, v4i{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                                                                acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]}));
         }
         // every wave's stores complete before the count
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

@@ -57,9 +57,8 @@ struct TiledParams {
 // A wave's 64 x 16 NF results from row m0, column n0 on, through its 2 KB of LDS `ys`: 16 rows m x 64
 // columns at a time, so that whole lines of 128 bytes leave (64 bytes of a row at a time, straight from
 // the registers, took 2048 x 4096 x 16384 from 64 to 94 us).  Row r's 16-byte piece c is at c ^ (r / 2).
-// Stores past the matrix lie past the resource.  Their offsets are all in the vector register: with one in a scalar register the compiler
-// (ROCm 7.2) takes a 16-byte store's data as read at once, and an instruction that overwrites it right
-// after the store has been seen to change what is stored.
+// Stores past the matrix lie past the resource.  Their offsets are all in the vector register (why: store_wide;
+// opaque as a whole by way of the lane).
 template <int DT, int NF>
 __device__ __forceinline__ void store_tile(const Mxfp4GemmArgs& p, const v4f (&acc)[NF][MF], uint8_t* ys, int64_t m0, int64_t n0) {
     int lane = threadIdx.x & 63;  // opaque: nothing derived from it here is held through the stages
