@@ -77,6 +77,37 @@ def test_norm_codes_are_those_of_its_output(M, K, dt, format):
     assert H is None and torch.equal(Y, lm.rmsnorm(X, w, eps=EPS)[0])
 
 
+# from 2048 rows on: two pieces of 8 columns a thread with one to eight waves a row, four with eight and sixteen
+MANY = [(2048, 528), (2051, 1024), (2049, 1040), (2080, 2064), (2050, 4112), (2049, 8192), (2050, 8208), (2048, 16400)]
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M,K", MANY)
+def test_norm_of_many_rows(M, K, dt):
+    print(f"\n[case] rmsnorm of many rows {dt} {M}x{K}", flush=True)
+    X, R, w, _ = inputs(M, K, dt)
+    h = summed(X, R)
+    X, R, w = X.cuda(), R.cuda(), w.cuda()
+    for res, sum_ in ((None, X.cpu()), (R, h)):
+        Y, H = lm.rmsnorm(X, w, residual=res, eps=EPS)
+        assert H is None if res is None else torch.equal(H.cpu(), sum_)
+        want, rel = ref.norm(sum_.double(), w.cpu().double(), EPS)
+        ref.assert_close(Y, want, rel * want.abs(), "Y")
+    assert not Y[1].any()
+    for keep in (False, True):
+        q, s, Y4, H = lm.rmsnorm_quantize(X, w, residual=R, eps=EPS, format="mxfp4", keep=keep)
+        q0, s0 = lm.mxfp4_quantize(Y)
+        assert torch.equal(q, q0) and torch.equal(u8(s), u8(s0)) and torch.equal(H.cpu(), h) and (Y4 is None or torch.equal(Y4, Y))
+        q, s, Y8, H = lm.rmsnorm_quantize(X, w, residual=R, eps=EPS, format="fp8", keep=keep)
+        assert torch.equal(H.cpu(), h) and (Y8 is None or torch.equal(Y8, Y))
+    _, rq, rs = fp8_ref.coded_rows(Y.cpu())
+    assert torch.equal(q.cpu().float().double(), rq)
+    m = torch.arange(M)
+    want = torch.zeros(-(-K // 128), lm.fp8_row_scale_pitch(M), dtype=torch.uint8)
+    want[:, m // 64 * 64 + m % 16 * 4 + m // 16 % 4] = rs[:, : want.shape[0]].t()
+    assert torch.equal(u8(s), want)
+
+
 @pytest.mark.parametrize("M,K,N", [(1, 144, 72), (5, 4096, 264), (20, 272, 136), (30, 8208, 72), (70, 400, 264), (300, 1040, 520), (2400, 272, 4360)])
 def test_fp8_product_of_coded_rows(M, K, N):
     """Past 4 rows the same kernels run on the same codes, so the bits are fp8_matmul_block's; up to 4 rows
