@@ -299,6 +299,51 @@ def test_backward(M, K, dt):
         assert torch.equal(again[0], dX) and torch.equal(again[1], dW)
 
 
+# a workgroup of sixteen waves a row; one, two and four waves a row with two, four and eight rows side by side
+BACK_DENSE = [(100, 1024), (100, 8192), (511, 8208), (600, 272), (513, 1024), (520, 1040), (520, 4096), (1030, 272), (1030, 1024), (1100, 1040),
+              (1030, 4096), (2050, 272), (2050, 1024), (2100, 1040), (2049, 2064), (5003, 16)]
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M,K", BACK_DENSE)
+def test_backward_of_dense_rows(M, K, dt):
+    """Every row and column enters dW."""
+    print(f"\n[case] rmsnorm backward, dense {dt} {M}x{K}", flush=True)
+    H, dH, w, g = inputs(M, K, dt)
+    H[1] = randn(g, K).to(dt)
+    dY = (randn(g, M, K) * 0.1).to(dt)
+    args = (dY.cuda(), H.cuda(), w.cuda())
+    for extra in (None, dH):
+        extra_ = None if extra is None else extra.cuda()
+        dX, dW = lm.rmsnorm_backward(*args, dH=extra_, eps=EPS)
+        x, xe, v, ve = ref.norm_backward(dY.double(), H.double(), w.double(), None if extra is None else extra.double(), EPS)
+        ref.assert_close(dX, x, xe, "dX")
+        ref.assert_close(dW, v, ve, "dW")
+        alone, none = lm.rmsnorm_backward(*args, dH=extra_, eps=EPS, need_dw=False)
+        assert none is None and torch.equal(alone, dX)
+        again = lm.rmsnorm_backward(*args, dH=extra_, eps=EPS)
+        assert torch.equal(again[0], dX) and torch.equal(again[1], dW)
+
+
+@pytest.mark.parametrize("M,K", [((1 << 19) + 40, 8208), ((1 << 21) + 3, 16)])
+def test_backward_past_32_bits_and_most_rows_zero(M, K):
+    """A row of zeros adds nothing to dW, without a rounding: the bound is that of the other rows alone."""
+    dt = torch.bfloat16
+    print(f"\n[case] rmsnorm backward, rows of zeros {M}x{K}", flush=True)
+    H, dY = torch.zeros(M, K, dtype=dt, device="cuda"), torch.zeros(M, K, dtype=dt, device="cuda")
+    rows = [0, 1, 2, 5, 255, 256, 2047, 2048, M // 2, M - 2, M - 1]
+    g = gen(K + 1)
+    h, dy, w = randn(g, len(rows), K).to(dt), randn(g, len(rows), K).to(dt), (1 + 0.2 * randn(g, K)).to(dt)
+    H[rows], dY[rows] = h.cuda(), dy.cuda()
+    dX, dW = lm.rmsnorm_backward(dY, H, w.cuda())
+    x, xe, v, ve = ref.norm_backward(dy.double(), h.double(), w.double(), None, 1e-6)
+    ref.assert_close(dX[rows], x, xe, "dX")
+    ref.assert_close(dW, v, ve, "dW")
+    assert int(dX.count_nonzero()) == int(dX[rows].count_nonzero())
+    del H, dY, dX
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("M,K", [(3, 256), (3, 8208), (600, 1040), (3, 16400), (3, 32784)])
 def test_backward_of_zeros_with_the_smallest_eps(M, K):
     """r = 2^64.. is an fp32 number, its square is not: a row of zeros has the gradient r d."""
