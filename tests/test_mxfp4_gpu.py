@@ -227,6 +227,26 @@ def test_matmul_exact_lattice(M, K, N, dt):
     assert torch.equal(lm.mxfp4_matmul_coded(Xq.view(torch.float4_e2m1fn_x2), sx.view(torch.uint8), Wq, s, dt), want)
 
 
+# few rows of wide weights: one or two pieces of 16 rows against one, two and four of 16 columns, several steps a wave,
+# and shares of them that are not equal
+WIDE = [(12, 4240, 4104), (17, 1040, 8200), (30, 4240, 8200), (32, 8208, 8456), (5, 4240, 24584), (16, 8208, 28680), (16, 272, 24576)]
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("M,K,N", WIDE)
+def test_matmul_few_rows_of_wide_weights(M, K, N, dt):
+    print(f"\n[case] mxfp4 wide {dt} {M}x{K}x{N}", flush=True)
+    g = gen(M + K + N)
+    X = lattice(g, M, K, dt=dt, spread=3).cuda()
+    W = lattice(g, N, K, dt=dt, spread=3).t().contiguous().cuda()
+    X[:, 32:64] *= 2
+    W[64:96] *= 4
+    Wq, s = lm.mxfp4_quantize(W, columns=True)
+    want = product(X, W)
+    assert torch.equal(lm.mxfp4_matmul(X, Wq, s), want)
+    assert torch.equal(lm.mxfp4_matmul_coded(*lm.mxfp4_quantize(X), Wq, s, dt), want)
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_matmul_sweep(seed):
     g = gen(3000 + seed)
