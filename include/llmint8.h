@@ -46,7 +46,8 @@
  *     127/s overflows fp32; bf16 only), are outside the contract.
  *   - Environment (read on every call, host side only):
  *       LLMINT8_LOG=1        prints each call's sizes, dtype, threshold, path (tiled or
- *                            small batch) and each launch ("stage") to stderr.
+ *                            small batch) and each launch ("stage") to stderr; of the
+ *                            mxfp4 products and the norm the kernel's form too ("plan").
  *       LLMINT8_FAULT=<stage> test switch, a dry run: nothing is enqueued; each stage the
  *                            call reaches before the named one is taken as done and the
  *                            named one as failed, so the call returns LLMINT8_EHIP and

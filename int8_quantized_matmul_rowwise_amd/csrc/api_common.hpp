@@ -63,13 +63,14 @@ bool log_on() {
 
 const char* dtype_name(int dt) { return dt == LLMINT8_F16 ? "fp16" : "bf16"; }
 
-// tau: NaN where the call takes no threshold
-void log_call(const char* fn, int64_t M, int64_t K, int64_t N, int dt, float tau, const char* path) {
-    if (!log_on()) return;
+// tau: NaN where the call takes no threshold.  Returns whether the log is on.
+bool log_call(const char* fn, int64_t M, int64_t K, int64_t N, int dt, float tau, const char* path) {
+    if (!log_on()) return false;
     char t[32] = "";
     if (!isnan(tau)) snprintf(t, sizeof t, " threshold=%g", (double)tau);
     fprintf(stderr, "[llmint8] %s M=%lld K=%lld N=%lld dtype=%s%s path=%s%s\n", fn, (long long)M, (long long)K,
             (long long)N, dtype_name(dt), t, path, fault_stage() ? " (dry run)" : "");
+    return true;
 }
 
 // Run one stage of a call: `launch` enqueues it and returns its HIP status.

@@ -111,7 +111,8 @@ int product(const char* name, const void* X, const uint8_t* x_scale, bool coded,
                        {Wq, code_bytes(N, K)},
                        {w_scale, scale_bytes(N, K)}};
     if (clash(r, 2, 6)) return LLMINT8_EINVAL;
-    log_call(name, M, K, N, dtype, NAN, plan_name(L.plan));
+    if (log_call(name, M, K, N, dtype, NAN, plan_name(L.plan)))
+        fprintf(stderr, "[llmint8]   plan pieces=%d columns=%d parts=%d\n", (int)L.plan.pieces, (int)L.plan.columns, (int)L.plan.split);
     uint8_t* ws = (uint8_t*)workspace;
     int32_t* counters = L.plan.split > 1 ? (int32_t*)(ws + L.counters) : nullptr;
     const int64_t n_counters = counters ? L.plan.tiles : 0;

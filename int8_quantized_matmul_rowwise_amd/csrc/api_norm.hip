@@ -47,10 +47,12 @@ LLMINT8_API int rmsnorm_forward(const void* X, const void* residual, const void*
                        {H == residual ? nullptr : residual, n},
                        {weight, (size_t)K * 2}};
     if (clash(r, 4, 7)) return LLMINT8_EINVAL;
-    log_call("rmsnorm_forward", M, K, 0, dtype, NAN, four ? "rmsnorm_mxfp4" : (codes ? "rmsnorm_fp8_block" : "rmsnorm"));
+    const NormPlan plan = rmsnorm_plan(M, K, format);
+    if (log_call("rmsnorm_forward", M, K, 0, dtype, NAN, four ? "rmsnorm_mxfp4" : (codes ? "rmsnorm_fp8_block" : "rmsnorm")))
+        fprintf(stderr, "[llmint8]   plan vectors=%d threads=%d\n", plan.vectors, plan.threads);
     return hip_status(stage("rmsnorm", [&] {
         const NormArgs a{(const uint16_t*)X, (const uint16_t*)residual, (const uint16_t*)weight, M, K, 1.0 / (double)K, eps, (uint16_t*)H, (uint16_t*)Y, format, Yq, y_scale};
-        return launch_rmsnorm(dtype, a, (hipStream_t)stream);
+        return launch_rmsnorm(dtype, a, plan, (hipStream_t)stream);
     }));
 }
 
@@ -95,7 +97,9 @@ LLMINT8_API int rmsnorm_backward(const void* dY, const void* H, const void* weig
     const size_t n = (size_t)M * (size_t)K * 2;
     const Range r[] = {{dX, n}, {dW, (size_t)K * 2}, {workspace, L.total}, {dY, n}, {H, n}, {weight, (size_t)K * 2}, {dH, n}};
     if (clash(r, 3, 7)) return LLMINT8_EINVAL;
-    log_call("rmsnorm_backward", M, K, 0, dtype, NAN, L.plan.whole ? "rmsnorm_backward" : "rmsnorm_backward_long");
+    if (log_call("rmsnorm_backward", M, K, 0, dtype, NAN, L.plan.whole ? "rmsnorm_backward" : "rmsnorm_backward_long"))
+        fprintf(stderr, "[llmint8]   plan vectors=%d threads=%d ahead=%d side=%d\n", L.plan.vectors, L.plan.row_threads, (int)L.plan.ahead,
+                L.plan.whole ? L.plan.threads / L.plan.row_threads : 0);
     return hip_status(stage("rmsnorm_backward", [&] {
         uint8_t* ws = (uint8_t*)workspace;
         const NormBackwardArgs a{(const uint16_t*)dY, (const uint16_t*)H, (const uint16_t*)weight, (const uint16_t*)dH, M, K, 1.0 / (double)K, eps, (uint16_t*)dX,

@@ -304,7 +304,12 @@ struct NormArgs {
     int format;       // of the codes: enum llmint8_codes
     uint8_t *q, *s;
 };
-hipError_t launch_rmsnorm(int dt, const NormArgs& p, hipStream_t stream);
+// Its kernel: pieces of 8 columns of a thread (0: rows longer than a workgroup's registers), threads of a row.
+struct NormPlan {
+    int vectors, threads;
+};
+NormPlan rmsnorm_plan(int64_t M, int64_t K, int format);
+hipError_t launch_rmsnorm(int dt, const NormArgs& p, const NormPlan& plan, hipStream_t stream);
 
 // How the gradient runs: rows split over `groups` workgroups, each with a row of partial sums of dW.
 struct NormBackwardPlan {

@@ -419,37 +419,35 @@ __global__ __launch_bounds__(256) void rmsnorm_dw_join_kernel(const float* __res
     }
 }
 
-template <int DT, int V, int FORMAT>
-void norm_launch(const NormArgs& p, int64_t pieces, unsigned grid, hipStream_t stream) {
-    if (pieces <= 64 * V) rmsnorm_kernel<DT, V, FORMAT, 64><<<grid, 64, 0, stream>>>(p);
-    else if (pieces <= 128 * V) rmsnorm_kernel<DT, V, FORMAT, 128><<<grid, 128, 0, stream>>>(p);
-    else if (pieces <= 256 * V) rmsnorm_kernel<DT, V, FORMAT, 256><<<grid, 256, 0, stream>>>(p);
-    else if (pieces <= 512 * V) rmsnorm_kernel<DT, V, FORMAT, 512><<<grid, 512, 0, stream>>>(p);
-    else rmsnorm_kernel<DT, V, FORMAT, 1024><<<grid, 1024, 0, stream>>>(p);
-}
-
-// Pieces of 8 columns a thread: one while rows are few, since a row then takes its own latency (16 x
-// 8192 with codes 4.6 us with one, 4.8 with two, 5.5 with four); two or four once rows fill the card
-// several times over, so that a unit holds several workgroups (4096 x 8192, residual, to e2m1 53.1, 43.9
-// and 42.0 us, to e4m3 52.1, 45.8 and 45.4, to 16 bits 47.3, 50.2 and 51.5; 16384 x 1024 to e2m1 13.1, 11.0
-// and 14.8; 16384 x 256, residual, to e4m3 9.2, 11.1 and 17.6; 4096 x 16384 two 54.8, four 51.8).
 template <int DT, int FORMAT>
-void norm_launch(const NormArgs& p, hipStream_t stream) {
-    const unsigned grid = (unsigned)(p.M < kMaxGrid ? p.M : kMaxGrid) + (has_padding<FORMAT>(p) ? 1 : 0);
-    // the columns that a row's codes cover: the codes' padding is written by the threads past K
-    const int64_t pieces = ceil_div(FORMAT == LLMINT8_CODES_NONE ? p.K : round_up(p.K, FORMAT == LLMINT8_CODES_MXFP4 ? 256 : 128), 8);
-    const bool many = p.M >= 2048;
-    if (pieces > 4096) rmsnorm_long_kernel<DT, FORMAT><<<grid, 1024, 0, stream>>>(p);
-    else if (pieces > (many ? 1024 : 2048)) norm_launch<DT, 4, FORMAT>(p, pieces, grid, stream);
-    else if (pieces > (many ? 64 : 1024)) norm_launch<DT, 2, FORMAT>(p, pieces, grid, stream);
-    else norm_launch<DT, 1, FORMAT>(p, pieces, grid, stream);
+hipError_t norm_launch(const NormArgs& p, const NormPlan& plan, hipStream_t stream) {
+    const unsigned grid = (unsigned)(p.M < kMaxGrid ? p.M : kMaxGrid) + (has_padding<FORMAT>(p) ? 1 : 0), threads = (unsigned)plan.threads;
+    switch (16 * plan.threads + plan.vectors) {
+#define LLMINT8_NORM(V, T) case 16 * T + V: rmsnorm_kernel<DT, V, FORMAT, T><<<grid, threads, 0, stream>>>(p); break
+        LLMINT8_NORM(1, 64);
+        LLMINT8_NORM(1, 128);
+        LLMINT8_NORM(1, 256);
+        LLMINT8_NORM(1, 512);
+        LLMINT8_NORM(1, 1024);
+        LLMINT8_NORM(2, 64);
+        LLMINT8_NORM(2, 128);
+        LLMINT8_NORM(2, 256);
+        LLMINT8_NORM(2, 512);
+        LLMINT8_NORM(2, 1024);
+        LLMINT8_NORM(4, 512);
+        LLMINT8_NORM(4, 1024);
+#undef LLMINT8_NORM
+        case 16 * 1024: rmsnorm_long_kernel<DT, FORMAT><<<grid, threads, 0, stream>>>(p); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
 }
 
 template <int DT>
-void norm_launch(const NormArgs& p, hipStream_t stream) {
-    if (p.format == LLMINT8_CODES_NONE) norm_launch<DT, LLMINT8_CODES_NONE>(p, stream);
-    else if (p.format == LLMINT8_CODES_FP8_BLOCK) norm_launch<DT, LLMINT8_CODES_FP8_BLOCK>(p, stream);
-    else norm_launch<DT, LLMINT8_CODES_MXFP4>(p, stream);
+hipError_t norm_launch(const NormArgs& p, const NormPlan& plan, hipStream_t stream) {
+    if (p.format == LLMINT8_CODES_NONE) return norm_launch<DT, LLMINT8_CODES_NONE>(p, plan, stream);
+    if (p.format == LLMINT8_CODES_FP8_BLOCK) return norm_launch<DT, LLMINT8_CODES_FP8_BLOCK>(p, plan, stream);
+    return norm_launch<DT, LLMINT8_CODES_MXFP4>(p, plan, stream);
 }
 
 template <int DT, bool DW>
@@ -491,11 +489,25 @@ hipError_t backward_launch(const NormBackwardArgs& p, const NormBackwardPlan& pl
 
 }  // namespace
 
-hipError_t launch_rmsnorm(int dt, const NormArgs& p, hipStream_t stream) {
+// Pieces of 8 columns a thread: one while rows are few, since a row then takes its own latency (16 x
+// 8192 with codes 4.6 us with one, 4.8 with two, 5.5 with four); two or four once rows fill the card
+// several times over, so that a unit holds several workgroups (4096 x 8192, residual, to e2m1 53.1, 43.9
+// and 42.0 us, to e4m3 52.1, 45.8 and 45.4, to 16 bits 47.3, 50.2 and 51.5; 16384 x 1024 to e2m1 13.1, 11.0
+// and 14.8; 16384 x 256, residual, to e4m3 9.2, 11.1 and 17.6; 4096 x 16384 two 54.8, four 51.8).
+NormPlan rmsnorm_plan(int64_t M, int64_t K, int format) {
+    // the columns that a row's codes cover: the codes' padding is written by the threads past K
+    const int64_t pieces = ceil_div(format == LLMINT8_CODES_NONE ? K : round_up(K, format == LLMINT8_CODES_MXFP4 ? 256 : 128), 8);
+    if (pieces > 4096) return {0, 1024};
+    const bool many = M >= 2048;
+    const int V = pieces > (many ? 1024 : 2048) ? 4 : (pieces > (many ? 64 : 1024) ? 2 : 1);
+    int T = 64;
+    while (T * V < pieces) T *= 2;
+    return {V, T};
+}
+
+hipError_t launch_rmsnorm(int dt, const NormArgs& p, const NormPlan& plan, hipStream_t stream) {
     if (p.M == 0 || p.K == 0) return hipSuccess;
-    if (dt == F16) norm_launch<F16>(p, stream);
-    else norm_launch<BF16>(p, stream);
-    return hipGetLastError();
+    return dt == F16 ? norm_launch<F16>(p, plan, stream) : norm_launch<BF16>(p, plan, stream);
 }
 
 NormBackwardPlan rmsnorm_backward_plan(int64_t M, int64_t K) {
