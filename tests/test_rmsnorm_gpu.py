@@ -142,6 +142,35 @@ def test_fp8_product_of_coded_rows(M, K, N):
         assert torch.equal(again, got)
 
 
+@pytest.mark.parametrize("M", [3, 20, 100, 300])
+def test_fp8_scales_of_rows_past_the_last_have_no_effect(M):
+    K, N, dt = 272, 136, torch.bfloat16
+    X, R, w, g = inputs(M, K, dt)
+    Wq, s_w = lm.fp8_quantize_weight_block((randn(g, K, N) * 0.02).to(dt).cuda())
+    q, s, _, _ = lm.rmsnorm_quantize(X.cuda(), w.cuda(), residual=R.cuda(), eps=EPS, format="fp8")
+    want = lm.fp8_matmul_block_coded(q, s, Wq, s_w, dt)
+    m = torch.arange(M, lm.fp8_row_scale_pitch(M))
+    s.view(torch.uint8)[:, (m // 64 * 64 + m % 16 * 4 + m // 16 % 4).cuda()] = 255
+    assert torch.isfinite(want).all() and torch.equal(lm.fp8_matmul_block_coded(q, s, Wq, s_w, dt), want)
+
+
+@pytest.mark.parametrize("M,K", [(5, 272), (2050, 1040), (2, 65552)])
+def test_the_same_tensor_twice(M, K):
+    """One tensor as X and residual, and H in its place; one as all of a gradient's inputs."""
+    X, _, w, _ = (t.cuda() if isinstance(t, torch.Tensor) else t for t in inputs(M, K, torch.bfloat16))
+    for format in (None, "fp8", "mxfp4"):
+        call = lambda x, r, h: (lm.rmsnorm(x, w, residual=r, eps=EPS, H=h) if format is None else
+                                lm.rmsnorm_quantize(x, w, residual=r, eps=EPS, format=format, keep=True, H=h))
+        want, x = call(X, X.clone(), None), X.clone()
+        for got in (call(X, X, None), call(x, x, x)):
+            for a, b in zip(got, want):
+                assert torch.equal(u8(a), u8(b))
+        assert torch.equal(x, want[-1])
+    want = lm.rmsnorm_backward(X, X.clone(), w, dH=X.clone(), eps=EPS)
+    for a, b in zip(lm.rmsnorm_backward(X, X, w, dH=X, eps=EPS), want):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("M,K", [(5, 272), (3, 16400), (2, 65552)])
 @pytest.mark.parametrize("format", ["fp8", "mxfp4", None])
 def test_norm_in_place(M, K, format):
