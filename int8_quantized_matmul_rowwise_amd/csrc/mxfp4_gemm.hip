@@ -345,8 +345,10 @@ hipError_t single(const Mxfp4GemmArgs& a, int split, hipStream_t stream) {
 // With few columns the steps are split over `split` workgroups too (grid.y, `part` steps each):
 // their sums go through memory and the last one adds them up in their order.
 // Bound by memory, and at the smallest sizes by a launch and one round of loads: 16 x 8192 x 8192 9.2 us (36
-// MB, 3.9 TB/s), 16 x 8192 x 28672 27.3 (4.6), 1 x 4096 x 4096 with the coding 5.6 (8.9 MB; the norm
-// of a single row, a launch with one round trip to memory, takes 1.8).
+// MB, 3.9 TB/s), 16 x 8192 x 28672 27.3 (4.6), 1 x 4096 x 4096 4.2 and with the coding 5.6 (8.9 MB; the norm
+// of a single row, a launch with one round trip to memory, takes 1.8).  Past 16 rows its waves wait for their loads:
+// 36 MB take 10.8 us at 24 x 4096 x 16384, 11.0 at 32 x 8192 x 8192, 14.4 at 64 x 8192 x 8192 and 18.9 at 48 x 16384 x 4096,
+// where waves, one a SIMD with one step under way, spend 84 % of their cycles waiting; 64 x 4096 x 4096 8.0.
 template <int DT, int MG, int NF, int WV, bool FUSED, int U, int OCC>
 __global__ __launch_bounds__(64 * WV, OCC) void mxfp4_small_kernel(Mxfp4GemmArgs p, int split, int part) {
     static_assert(!FUSED || MG == 1, "one piece of rows");

@@ -200,7 +200,8 @@ __global__ __launch_bounds__(T, 4) void rmsnorm_kernel(NormArgs p) {
     }
 }
 
-// Rows longer than a workgroup's registers: read twice.
+// Rows longer than a workgroup's registers: read twice (2000 x 65536 with a residual to 16 bits 238 us, 4.4 TB/s, to
+// e4m3 224, to e2m1 213).
 template <int DT, int FORMAT>
 __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs p) {
     constexpr int T = 1024;
@@ -357,7 +358,8 @@ __global__ __launch_bounds__(AHEAD ? 512 : T, AHEAD ? 2 : 4) void rmsnorm_backwa
     }
 }
 
-// Rows longer than a workgroup's registers: read twice; r of each row is kept for dw.
+// Rows longer than a workgroup's registers: read twice, and H and dY once more for dw, for which r of each
+// row is kept: 2000 x 32768 with dh 172 us, of which dw takes 49 and the join 5.
 template <int DT>
 __global__ __launch_bounds__(1024) void rmsnorm_backward_long_kernel(NormBackwardArgs p) {
     constexpr int T = 1024;
@@ -493,7 +495,10 @@ hipError_t backward_launch(const NormBackwardArgs& p, const NormBackwardPlan& pl
 // 8192 with codes 4.6 us with one, 4.8 with two, 5.5 with four); two or four once rows fill the card
 // several times over, so that a unit holds several workgroups (4096 x 8192, residual, to e2m1 53.1, 43.9
 // and 42.0 us, to e4m3 52.1, 45.8 and 45.4, to 16 bits 47.3, 50.2 and 51.5; 16384 x 1024 to e2m1 13.1, 11.0
-// and 14.8; 16384 x 256, residual, to e4m3 9.2, 11.1 and 17.6; 4096 x 16384 two 54.8, four 51.8).
+// and 14.8; 16384 x 256, residual, to e4m3 9.2, 11.1 and 17.6; 4096 x 16384 two 54.8, four 51.8).  From one to two
+// pieces, all with a residual, around the border of 2048 rows: 2047 x 4096 to e4m3 12.3 and 11.4, 2047 x 8192 to e2m1
+// 27.8 and 23.6, to 16 bits 24.5 and 25.6, 2047 x 1024 to e4m3 5.3 and 5.4; below it two are as good or better on wide
+// rows with codes (1024 x 8192 14.3 and 12.1, 512 x 8192 8.9 and 8.2, 256 x 4096 3.9 and 4.2): not used.
 NormPlan rmsnorm_plan(int64_t M, int64_t K, int format) {
     // the columns that a row's codes cover: the codes' padding is written by the threads past K
     const int64_t pieces = ceil_div(format == LLMINT8_CODES_NONE ? K : round_up(K, format == LLMINT8_CODES_MXFP4 ? 256 : 128), 8);
@@ -516,13 +521,17 @@ NormBackwardPlan rmsnorm_backward_plan(int64_t M, int64_t K) {
     while (columns < K) columns *= 2;
     // Few rows: a row over as many threads as it has pieces of 8 columns, and a workgroup a row, since
     // a row takes its own latency (333 x 1040 4.1 us, else 5.6; 100 x 4096 4.6 and 5.2).  So, too, rows that
-    // with the next row ahead would not fit the registers (4096 x 16384 85 us, else 105).
+    // with the next row ahead would not fit the registers (4096 x 16384 85 us, else 105).  There a row's partial sums
+    // outweigh its data up to 511 rows: 511 x 16384 with dh 29.2 us and 22.4 with two rows a workgroup, 300 x 16384 20.2
+    // and 17.6, 512 x 16384 (two) 22.2.
     if (columns > 8192 || M <= 512) {
         const int V = columns > 8192 ? 2 : 1, T = columns / 8 / V;
         return {true, V, T, false, T, M < 512 ? M : (columns > 8192 ? 256 : 512)};
     }
     // Many rows: 512 threads a compute unit, a wave or several a row, the next row's loads under way
-    // (16384 x 1024 20.8 us, 43.7 with a workgroup of 128 threads a row and none ahead).
+    // (16384 x 1024 20.8 us, 43.7 with a workgroup of 128 threads a row and none ahead).  The border, both launches,
+    // a workgroup a row and rows side by side: 256 x 8192 with dh 13.4 and 14.0 us, 512 x 4096 13.1 and 12.0, 512 x 8192
+    // 17.6 and 17.9, 512 x 1040 8.0 and 8.3, 600 x 8192 20.0 and 18.3, 1024 x 8192 30.6 and 21.0.
     const int V = columns <= 2048 ? columns / 512 : 4, T = columns / 8 / V;
     int64_t sides = 512 / T;
     while (sides > 1 && M < 256 * sides) sides /= 2;

@@ -15,7 +15,7 @@ pytestmark = pytest.mark.gpu
 
 DTS = [torch.float16, torch.bfloat16]
 EPS = 1e-5
-# a wave, several, pieces of 8 columns one to eight a thread, and rows longer than registers
+# a wave, several, pieces of 8 columns one to four a thread, and rows longer than registers
 SHAPES = [(1, 16), (3, 64), (2, 144), (37, 528), (5, 1040), (130, 2064), (1, 4096), (9, 8192), (3, 8208), (2, 16400), (2, 32784), (3, 65536), (2, 65552), (1, 131088)]
 BACK = [(1, 16), (3, 64), (70, 144), (333, 1040), (5, 4096), (600, 4112), (9, 8208), (520, 16400), (3, 32768), (3, 32784), (70, 65552)]
 
